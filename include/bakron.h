@@ -52,7 +52,8 @@ extern "C" {
  * 4: bakron_quantize runs the tile wavefront on every device (measured
  * faster than the persistent sweep on every workload); the sweep is
  * bakron_quantize_persistent, and profile class 4 stays 0.
- * 5: adds bakron_wavefront_plan_check. */
+ * 5: adds bakron_wavefront_plan_check.  The layer operators were added to
+ * version 5 without a change to what it had. */
 #define BAKRON_ABI_VERSION 5
 
 typedef enum bakron_status {
@@ -68,6 +69,7 @@ typedef enum bakron_status {
 #define BAKRON_DEV_NONFINITE_W 1 /* W holds a NaN or an infinity */
 #define BAKRON_DEV_BAD_SCALE 2   /* a scale is <= 0, NaN or infinite */
 #define BAKRON_DEV_TIMEOUT 4     /* a bounded device-side wait gave up */
+#define BAKRON_DEV_BAD_TARGET 8  /* a target index is >= the vocabulary's size */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* bakron_status_string(int status);
@@ -397,6 +399,107 @@ int bakron_sweep_plan_check(int64_t m, int64_t n, int64_t* stats);
  * none, BAKRON_ERR_INVALID_ARG for bad arguments, else 1.
  */
 int bakron_wavefront_plan_check(int64_t m, int64_t n, int colpush, int lag, int64_t* stats);
+
+/* --------------------------------------------------------- layer operators
+ * What runs before and after a quantized layer.  Element types are named by
+ * BAKRON_F32 / F16 / BF16; every matrix is row-major with a row stride in
+ * elements (ld..., at least its width) where one is given, else dense.  Rows
+ * that start on 16 bytes are read in 16-byte pieces; others are taken too.
+ * All sums and statistics are held in fp32 (the products of codes in exact
+ * integers), and no result depends on the order in which blocks run.
+ */
+#define BAKRON_F32 0
+#define BAKRON_F16 1
+#define BAKRON_BF16 2
+#define BAKRON_I8 3
+
+/* 8-bit codes of activations X (T x K, fp32, fp16 or bf16), one scale for
+ * each token:
+ *     scales[t] = fp32(max_k |X[t, k]| / 127),
+ *     codes[t, k] = fp32(X[t, k] / scales[t]) rounded to nearest, ties to even,
+ * kept within +-127.  A row of zeros has scale 0 and codes 0; a row that
+ * holds a NaN or an infinity has a NaN scale and codes 0.
+ * codes: T x K, dense.  scales: T.  T, K in 1 .. 2^31 - 1.
+ */
+int bakron_quantize_tokens(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, int8_t* codes, float* scales,
+                           void* stream);
+
+/* Y = X V^T for a layer quantized to 8 bits (codes of bakron_quantize_range,
+ * or of bakron_pack_codes with bits = 8):
+ *     Y[t, o] = x_scale_t scales[o] sum_k c[t, k] codes[o, k] + bias[o].
+ * X: T x K; either values (x_dtype fp32, fp16 or bf16, x_scales NULL), which
+ *    the call quantizes as bakron_quantize_tokens does, or 8-bit codes
+ *    (x_dtype BAKRON_I8) with x_scales (T).
+ * codes: N x K, row stride ldc.  scales: N.  bias: N, or NULL.
+ * Y: T x N of y_dtype (fp32, fp16 or bf16), dense, rounded once.
+ * The sums over k are exact; K in 1 .. 2^17 - 1.
+ * status_dev: 0, or BAKRON_DEV_TIMEOUT.
+ */
+size_t bakron_int8_matmul_workspace_size(int64_t T, int64_t K, int64_t N);
+int bakron_int8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_scales, const int8_t* codes, int64_t ldc,
+                       const float* scales, const float* bias, int64_t T, int64_t K, int64_t N, void* Y, int y_dtype,
+                       void* ws, size_t ws_bytes, int32_t* status_dev, void* stream);
+
+/* The norms around a block, its gate and the residual sum, for the residual
+ * stream X and the block's output H (T x D, element type dtype):
+ *     Y = alpha X + gate * N(H; post, post_bias),
+ *     Z = N(Y; pre, pre_bias),
+ *     N(v; w, b) = (v - m) / sqrt(mean((v - m)^2) + eps) * w + b  for each row,
+ * m = mean(v) (BAKRON_NORM_LAYER) or 0 (BAKRON_NORM_RMS).
+ * H NULL: Y = alpha X (then post, gate are NULL too).  post NULL: no norm
+ * after the block.  gate: groups x D, row g for the tokens g T / groups ..
+ * (g + 1) T / groups - 1 (T a multiple of groups), or NULL.  pre NULL: no
+ * norm of the sum, and no Z.  Weights and biases (D) are fp32; biases go with
+ * layer norms only.
+ * Z is computed from the sum before it is rounded to Y, and is stored either
+ * as values (Z) or as 8-bit codes with a scale for each token (codes,
+ * code_scales: as bakron_quantize_tokens gives, from unrounded values).
+ * Y may be X or H itself.  D in 1 .. 32768.
+ */
+#define BAKRON_NORM_RMS 0
+#define BAKRON_NORM_LAYER 1
+int bakron_norm_residual(const void* X, int64_t ldx, const void* H, int64_t ldh, const float* post,
+                         const float* post_bias, const void* gate, int64_t ldg, int64_t groups, const float* pre,
+                         const float* pre_bias, float alpha, float eps, int kind, int dtype, int64_t T, int64_t D,
+                         void* Y, void* Z, int8_t* codes, float* code_scales, void* stream);
+
+/* Gradients of bakron_norm_residual for the gradients dY, dZ of its results
+ * (either may be NULL: zero), from its Y and H; the statistics are computed
+ * again.  dX, dH: T x D of dtype (dX may be dY or dZ, dH may be H).  The
+ * others are fp32 and may be NULL: dpost, dpre (D), dgate (groups x D), and,
+ * for layer norms, dpost_bias, dpre_bias (D).  Summed in a fixed order.
+ * groups: as in the forward call (0 without a gate), also for the workspace.
+ */
+size_t bakron_norm_residual_backward_workspace_size(int64_t T, int64_t D, int64_t groups);
+int bakron_norm_residual_backward(const void* dY, int64_t lddy, const void* dZ, int64_t lddz, const void* Y, int64_t ldy,
+                                  const void* H, int64_t ldh, const float* post, const float* post_bias,
+                                  const void* gate, int64_t ldg, int64_t groups, const float* pre, float alpha, float eps,
+                                  int kind, int dtype, int64_t T, int64_t D, void* dX, void* dH, float* dpost,
+                                  float* dpost_bias, float* dgate, float* dpre, float* dpre_bias, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Softmax cross entropy of the logits x = H W^T, which are not kept, for
+ * hidden states H (T x D) and an output embedding W (V x D), both fp16 or
+ * both bf16:
+ *     lse[t] = log sum_v exp(x[t, v]),  loss[t] = lse[t] - x[t, targets[t]].
+ * A negative target leaves a token out: loss 0, no gradient.  A target >= V
+ * does too, and sets BAKRON_DEV_BAD_TARGET.  loss, lse: T, fp32.
+ * status_dev: 0, BAKRON_DEV_BAD_TARGET, BAKRON_DEV_TIMEOUT.
+ */
+size_t bakron_linear_cross_entropy_workspace_size(int64_t T, int64_t D, int64_t V, int grad);
+int bakron_linear_cross_entropy(const void* H, int64_t ldh, const void* W, int64_t ldw, int dtype, const int64_t* targets,
+                                int64_t T, int64_t D, int64_t V, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                int32_t* status_dev, void* stream);
+
+/* The same with the gradients of sum_t coef[t] loss[t]:
+ *     G[t, v] = coef[t] (exp(x[t, v] - lse[t]) - [v = targets[t]]),
+ *     dH = G W (T x D),  dW = G^T H (V x D), dense, of the inputs' type.
+ * coef: T, fp32, or NULL for 1 / (number of tokens with a target).
+ */
+int bakron_linear_cross_entropy_grad(const void* H, int64_t ldh, const void* W, int64_t ldw, int dtype,
+                                     const int64_t* targets, const float* coef, int64_t T, int64_t D, int64_t V,
+                                     float* loss, float* lse, void* dH, void* dW, void* ws, size_t ws_bytes,
+                                     int32_t* status_dev, void* stream);
 
 /* --------------------------------------------------------------- self-test
  * Exercises the device-side timeout path on purpose: one thread waits, with

@@ -20,6 +20,14 @@ The calls, each a C ABI entry point of the same name with the prefix bakron_:
   row_scales             App. D scale choice with the MSE shrink search
   pack_codes             b-bit packed codes
   gram, sq_norms, damp   Kronecker factors from samples (Sec. 4.2, App. A.2, App. D)
+and, around a quantized layer (no part of the paper; in _layers.py, which
+imports torch and is loaded by the first use):
+  quantize_tokens        8-bit codes of activations, a scale for each token
+  int8_matmul            the product of quantized activations and weights
+  norm_residual, norm_residual_backward
+                         the norms around a block, its gate and residual sum
+  linear_cross_entropy, linear_cross_entropy_grad
+                         cross entropy over a large vocabulary, its gradients
 """
 
 from __future__ import annotations
@@ -47,7 +55,25 @@ __all__ = [
     "pack_codes",
     "quantize_workspace_size",
     "prepare_workspace_size",
+    "quantize_tokens",
+    "int8_matmul",
+    "norm_residual",
+    "norm_residual_backward",
+    "linear_cross_entropy",
+    "linear_cross_entropy_grad",
 ]
+
+_LAYER_CALLS = ("quantize_tokens", "int8_matmul", "norm_residual", "norm_residual_backward", "linear_cross_entropy",
+                "linear_cross_entropy_grad")
+
+
+def __getattr__(name):
+    if name in _LAYER_CALLS:
+        from . import _layers
+
+        globals().update({n: getattr(_layers, n) for n in _LAYER_CALLS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def load_library():

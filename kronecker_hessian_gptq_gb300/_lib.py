@@ -23,11 +23,13 @@ STATUS_NAMES = {
 DEV_NONFINITE_W = 1
 DEV_BAD_SCALE = 2
 DEV_TIMEOUT = 4
+DEV_BAD_TARGET = 8
 KERNEL_CLASSES = ("setup", "tile_solve", "mid_push", "chunk_push", "sweep")
 
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 _vp = ctypes.c_void_p  # device or host pointers are passed as plain addresses
 
 # name -> (restype, argtypes)
@@ -60,6 +62,20 @@ SIGNATURES = {
     "bakron_quantize_host_workspace_size": (_sz, [_i64, _i64]),
     "bakron_quantize_host": (_int, [_vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _sz, _vp, _vp]),
     "bakron_quantize_noalloc": (_int, [_vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "bakron_quantize_tokens": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "bakron_int8_matmul_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "bakron_int8_matmul": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _sz,
+                                  _vp, _vp]),
+    "bakron_norm_residual": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _f32, _f32, _int, _int,
+                                    _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "bakron_norm_residual_backward_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "bakron_norm_residual_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
+                                             _vp, _f32, _f32, _int, _int, _i64, _i64] + [_vp] * 8 + [_sz, _vp]),
+    "bakron_linear_cross_entropy_workspace_size": (_sz, [_i64, _i64, _i64, _int]),
+    "bakron_linear_cross_entropy": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp,
+                                           _vp]),
+    "bakron_linear_cross_entropy_grad": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _vp, _i64, _i64, _i64] + [_vp] * 5
+                                         + [_sz, _vp, _vp]),
     "bakron_sweep_plan_check": (_int, [_i64, _i64, _vp]),
     "bakron_wavefront_plan_check": (_int, [_i64, _i64, _int, _int, _vp]),
 }

@@ -1,0 +1,104 @@
+// elem.cuh -- element types of the layer operators (fp32, fp16, bf16):
+// conversions from and to fp32, vector loads and stores, and reductions over
+// a team of threads.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace bakron {
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// VEC consecutive elements in one access of VEC * sizeof(T) bytes (at most
+// 16 at a time); p must be aligned to that size.
+template <class T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
+  constexpr int kBytes = VEC * (int)sizeof(T);
+  if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+    for (int q = 0; q < kBytes / 16; ++q) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[q];
+      T e[16 / sizeof(T)];
+      memcpy(e, &u, 16);
+#pragma unroll
+      for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[q * (16 / sizeof(T)) + i] = to_f32<T>(e[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = to_f32<T>(p[i]);
+  }
+}
+template <class T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
+  constexpr int kBytes = VEC * (int)sizeof(T);
+  if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+    for (int q = 0; q < kBytes / 16; ++q) {
+      T e[16 / sizeof(T)];
+#pragma unroll
+      for (int i = 0; i < (int)(16 / sizeof(T)); ++i) e[i] = from_f32<T>(v[q * (16 / sizeof(T)) + i]);
+      uint4 u;
+      memcpy(&u, e, 16);
+      reinterpret_cast<uint4*>(p)[q] = u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+// Sums and maxima over the threads of a block (any multiple of 32, at most
+// 1024): N values at once; `red` holds 32 N floats.
+struct SumOp {
+  static constexpr float kIdentity = 0.f;
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+// A NaN on either side stays: the maximum of a row with a NaN is NaN.
+struct MaxOp {  // of magnitudes
+  static constexpr float kIdentity = 0.f;
+  __device__ __forceinline__ float operator()(float a, float b) const { return a > b || isnan(a) ? a : b; }
+};
+template <class Op>
+__device__ __forceinline__ float warp_reduce(float v, Op op) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int N, class Op>
+__device__ __forceinline__ void block_reduce(float (&v)[N], float* red, Op op) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_reduce(v[k], op);
+  const int nw = blockDim.x >> 5;
+  if (nw == 1) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();  // `red` may still be read by an earlier use
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[k * 32 + warp] = v[k];
+  }
+  __syncthreads();
+  // every warp reduces the warps' values itself, in the same order
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_reduce(lane < nw ? red[k * 32 + lane] : Op::kIdentity, op);
+}
+
+}  // namespace bakron
