@@ -484,9 +484,12 @@ int bakron_norm_residual_backward(const void* dY, int64_t lddy, const void* dZ, 
  *     lse[t] = log sum_v exp(x[t, v]),  loss[t] = lse[t] - x[t, targets[t]].
  * A negative target leaves a token out: loss 0, no gradient.  A target >= V
  * does too, and sets BAKRON_DEV_BAD_TARGET.  loss, lse: T, fp32.
+ * D in 1 .. 2^20, V in 1 .. 2^24.
  * status_dev: 0, BAKRON_DEV_BAD_TARGET, BAKRON_DEV_TIMEOUT.
+ * Workspace: grad = 1 for the gradients too; copies = 1 unless every row of H
+ * and of W starts on 16 bytes (base and stride), for copies that do.
  */
-size_t bakron_linear_cross_entropy_workspace_size(int64_t T, int64_t D, int64_t V, int grad);
+size_t bakron_linear_cross_entropy_workspace_size(int64_t T, int64_t D, int64_t V, int grad, int copies);
 int bakron_linear_cross_entropy(const void* H, int64_t ldh, const void* W, int64_t ldw, int dtype, const int64_t* targets,
                                 int64_t T, int64_t D, int64_t V, float* loss, float* lse, void* ws, size_t ws_bytes,
                                 int32_t* status_dev, void* stream);

@@ -241,6 +241,11 @@ def norm_residual_backward(dY, dZ, Y, H, post=None, gate=None, pre=None, alpha=1
     return out
 
 
+def _copies(H, W):
+    """Whether some row does not start on 16 bytes."""
+    return int(any(t.data_ptr() % 16 or _ld(t) % 8 for t in (H, W)))
+
+
 def _loss_arguments(H, W, targets):
     T, D = _matrix(H, "H", (torch.float16, torch.bfloat16))
     V = _matrix(W, "W", (H.dtype,))[0]
@@ -262,7 +267,7 @@ def linear_cross_entropy(H, W, targets):
     if T == 0:
         return loss, lse, status.zero_()
     lib = _lib.load()
-    ws = _workspace(lib.bakron_linear_cross_entropy_workspace_size(T, D, V, 0), H.device)
+    ws = _workspace(lib.bakron_linear_cross_entropy_workspace_size(T, D, V, 0, _copies(H, W)), H.device)
     st = lib.bakron_linear_cross_entropy(H.data_ptr(), _ld(H), W.data_ptr(), _ld(W), _CODES[H.dtype], targets.data_ptr(),
                                          T, D, V, loss.data_ptr(), lse.data_ptr(), _ptr(ws), ws.numel(),
                                          status.data_ptr(), _stream_of(H))
@@ -284,7 +289,7 @@ def linear_cross_entropy_grad(H, W, targets, coef=None):
     if T == 0:
         return loss, lse, dH, dW.zero_(), status.zero_()
     lib = _lib.load()
-    ws = _workspace(lib.bakron_linear_cross_entropy_workspace_size(T, D, V, 1), H.device)
+    ws = _workspace(lib.bakron_linear_cross_entropy_workspace_size(T, D, V, 1, _copies(H, W)), H.device)
     st = lib.bakron_linear_cross_entropy_grad(H.data_ptr(), _ld(H), W.data_ptr(), _ld(W), _CODES[H.dtype],
                                               targets.data_ptr(), _ptr(coef), T, D, V, loss.data_ptr(), lse.data_ptr(),
                                               dH.data_ptr(), dW.data_ptr(), _ptr(ws), ws.numel(), status.data_ptr(),

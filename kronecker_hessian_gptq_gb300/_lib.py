@@ -71,7 +71,7 @@ SIGNATURES = {
     "bakron_norm_residual_backward_workspace_size": (_sz, [_i64, _i64, _i64]),
     "bakron_norm_residual_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
                                              _vp, _f32, _f32, _int, _int, _i64, _i64] + [_vp] * 8 + [_sz, _vp]),
-    "bakron_linear_cross_entropy_workspace_size": (_sz, [_i64, _i64, _i64, _int]),
+    "bakron_linear_cross_entropy_workspace_size": (_sz, [_i64, _i64, _i64, _int, _int]),
     "bakron_linear_cross_entropy": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp,
                                            _vp]),
     "bakron_linear_cross_entropy_grad": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _vp, _i64, _i64, _i64] + [_vp] * 5

@@ -17,6 +17,7 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;  // tokens: one thread block each in x
+constexpr int64_t kMaxD = (int64_t)1 << 20, kMaxV = (int64_t)1 << 24;
 constexpr int64_t kMaxK = (int64_t)1 << 17;     // 2^14 K stays below 2^31: 32-bit sums are exact
 
 }  // namespace
@@ -111,9 +112,9 @@ int bakron_norm_residual_backward(const void* dY, int64_t lddy, const void* dZ, 
   return from_cuda(bakron::norm_backward_launch(p, ws, (cudaStream_t)stream));
 }
 
-size_t bakron_linear_cross_entropy_workspace_size(int64_t T, int64_t D, int64_t V, int grad) {
-  if (T < 1 || T >= kMaxRows || D < 1 || D >= kMaxRows || V < 1 || V >= kMaxRows) return 0;
-  return bakron::cross_entropy_workspace_bytes(T, D, V, grad != 0);
+size_t bakron_linear_cross_entropy_workspace_size(int64_t T, int64_t D, int64_t V, int grad, int copies) {
+  if (T < 1 || T >= kMaxRows || D < 1 || D > kMaxD || V < 1 || V > kMaxV) return 0;
+  return bakron::cross_entropy_workspace_bytes(T, D, V, grad != 0, copies != 0);
 }
 
 static int cross_entropy(const void* H, int64_t ldh, const void* W, int64_t ldw, int dtype, const int64_t* targets,
@@ -121,13 +122,14 @@ static int cross_entropy(const void* H, int64_t ldh, const void* W, int64_t ldw,
                          void* ws, size_t ws_bytes, int32_t* status_dev, void* stream) {
   if (!H || !W || !targets || !loss || !lse || !status_dev || (dtype != BAKRON_F16 && dtype != BAKRON_BF16))
     return BAKRON_ERR_INVALID_ARG;
-  if (T < 1 || T >= kMaxRows || D < 1 || D >= kMaxRows || V < 1 || V >= kMaxRows || ldh < D || ldw < D)
+  if (T < 1 || T >= kMaxRows || D < 1 || D > kMaxD || V < 1 || V > kMaxV || ldh < D || ldw < D)
     return BAKRON_ERR_INVALID_ARG;
   if (!on_element(H, dtype) || !on_element(W, dtype) || !aligned_to(targets, 8) || loss == lse)
     return BAKRON_ERR_INVALID_ARG;
-  if (!workspace_ok(ws, ws_bytes, bakron::cross_entropy_workspace_bytes(T, D, V, dH != nullptr)))
-    return BAKRON_ERR_WORKSPACE;
   const bakron::CrossEntropy p{H, W, ldh, ldw, dtype, targets, T, D, V, loss, lse, coef, dH, dW};
+  const bool copies = bakron::cross_entropy_needs_copies(p);
+  if (!workspace_ok(ws, ws_bytes, bakron::cross_entropy_workspace_bytes(T, D, V, dH != nullptr, copies)))
+    return BAKRON_ERR_WORKSPACE;
   return from_cuda(bakron::cross_entropy_launch(p, ws, status_dev, (cudaStream_t)stream));
 }
 

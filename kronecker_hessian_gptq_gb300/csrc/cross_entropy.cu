@@ -6,142 +6,409 @@
 //
 // for hidden states H (T x D), output embedding W (V x D) and targets y; a
 // token with a negative target has loss 0 and c_t = 0.
+//
+// The logits come out of the tensor cores a 256 x 256 tile at a time
+// (pair_gemm.cuh).  The epilogue reduces each row's 128 columns to their
+// maximum and the sum of exponentials below it, and a second kernel joins a
+// row's pieces: the loss alone stores 8 bytes for 128 logits.
+//
+// For the gradients a logit is kept, for one piece of the tokens at a time,
+// as the 16-bit fixed-point number round(2048 (m - x) log2 e), m the maximum
+// of its 128 columns: a relative error of exp(x) of at most 1.7e-4 (1e-4 rms,
+// against 1.7e-3 rms of rounding to bf16 or 2.1e-4 to fp16), and a range of
+// 2^-32 below the maximum.  A pass over the piece turns it into G in place,
+// and G, 16-bit, is the operand of the two other products.  This reads and
+// writes 6 bytes for each logit, where computing the logits a second time
+// would cost a third of the products again; a piece holds at most 1 GiB.
 #include <algorithm>
+#include <type_traits>
 
 #include "bakron.h"
 #include "elem.cuh"
 #include "layers.h"
-#include "tile_product.cuh"
+#include "pair_gemm.cuh"
 
 namespace bakron {
 namespace {
 
-// c_t of every token, and the status word: one block.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kChunk = 128;             // columns that share a maximum
+constexpr float kSteps = 2048.f;        // fixed-point steps in a factor of two
+constexpr float kGScale = 32768.f;      // G is stored times this, so that fp16 keeps p down to 2^-29
+constexpr int64_t kPieceBytes = (int64_t)1 << 30;
+constexpr int64_t kPieceTokens = (int64_t)1 << 20;  // keeps the number of tiles and the length of a sum bounded
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// c_t / max |c| of every token, and what the gradients are scaled by in the
+// end, max |c| / kGScale.  One block.
 __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* target, int64_t T, int64_t V, const float* given,
-                                                            float* coef, int32_t* status) {
+                                                            float* coef, float* scale, int32_t* status) {
   __shared__ int with, bad;
+  __shared__ float red[32];
   if (threadIdx.x == 0) with = bad = 0;
   __syncthreads();
   int n = 0, wrong = 0;
+  float top[1] = {0.f};
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
-    if (target[t] >= V) wrong = 1;
-    if (target[t] >= 0 && target[t] < V) ++n;
+    const int64_t y = target[t];
+    if (y >= V) wrong = 1;
+    if (y >= 0 && y < V) {
+      ++n;
+      if (given) top[0] = MaxOp()(fabsf(given[t]), top[0]);
+    }
   }
   if (n) atomicAdd(&with, n);
   if (wrong) atomicOr(&bad, 1);
+  block_reduce<1>(top, red, MaxOp());
   __syncthreads();
-  if (threadIdx.x == 0) *status = bad ? BAKRON_DEV_BAD_TARGET : 0;
+  const float most = given ? top[0] : (with ? 1.f / (float)with : 0.f);
+  if (threadIdx.x == 0) {
+    *status = bad ? BAKRON_DEV_BAD_TARGET : 0;
+    *scale = most / kGScale;
+  }
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const bool has = target[t] >= 0 && target[t] < V;
-    coef[t] = has ? (given ? given[t] : 1.f / (float)with) : 0.f;
+    coef[t] = !has || most == 0.f ? 0.f : given ? given[t] / most : 1.f;
   }
 }
 
-template <class T>
-struct Rows {
-  const T* p;
-  int64_t ld;
-  __device__ float operator()(int64_t r, int64_t c) const { return to_f32<T>(p[r * ld + c]); }
-};
-template <class T>
-struct RowsT {
-  const T* p;
-  int64_t ld;
-  __device__ float operator()(int64_t c, int64_t r) const { return to_f32<T>(p[r * ld + c]); }
-};
-struct Put {
-  float* p;
-  int64_t ld;
-  __device__ void operator()(int64_t r, int64_t c, float v) const { p[r * ld + c] = v; }
-};
-struct Add {
-  float* p;
-  int64_t ld;
-  __device__ void operator()(int64_t r, int64_t c, float v) const { p[r * ld + c] += v; }
-};
-template <class T>
-struct PutAs {
-  T* p;
-  int64_t ld;
-  __device__ void operator()(int64_t r, int64_t c, float v) const { p[r * ld + c] = from_f32<T>(v); }
+// Epilogue of the logits: rows are tokens of the piece, columns the vocabulary.
+template <bool kKeep>
+struct LogitsEpilogue {
+  int64_t rows, V;
+  const int64_t* target;
+  float2* stats;  // rows x chunks: maximum in units of log 2, sum of 2^(x - maximum)
+  int64_t chunks;
+  float* right;    // the target's logit
+  uint16_t* kept;  // rows x ldk
+  int64_t ldk;
+
+  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row, int64_t col, const PairSums& sums) const {
+    if (col >= V) return;
+    const bool whole = col + kChunk <= V;
+    const int left = whole ? kChunk : (int)(V - col);
+    float v[32];
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kChunk; c += 32) {
+      sums.load(c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (whole || c + i < left) m = fmaxf(m, v[i]);
+    }
+    m = m == -INFINITY ? 0.f : m * kLog2e;
+    const bool live = row < rows;
+    const int64_t y = live ? target[row] - col : -1;
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kChunk; c += 32) {
+      sums.load(c, v);
+      if (__any_sync(0xffffffffu, y >= c && y < c + 32)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (y == c + i) right[row] = v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = (whole || c + i < left) ? fmaf(v[i], kLog2e, -m) : -INFINITY;
+      if constexpr (kKeep) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          // a NaN is lost here; its row's sum is NaN, which is what counts
+          const uint32_t lo = (uint32_t)__float2int_rn(fminf(-kSteps * v[2 * i], 65535.f));
+          const uint32_t hi = (uint32_t)__float2int_rn(fminf(-kSteps * v[2 * i + 1], 65535.f));
+          w[i] = lo | (hi << 16);
+        }
+        if (live) {
+          uint16_t* to = kept + row * ldk + col + c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (whole || c + 8 * i < left) reinterpret_cast<uint4*>(to)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s += exp2_approx(v[i]);
+    }
+    if (live) stats[row * chunks + col / kChunk] = make_float2(m, s);
+  }
 };
 
-// One block for each token: lse and loss of its logits, which become G.
-__global__ void __launch_bounds__(256) softmax_kernel(float* x, int64_t V, const int64_t* target, const float* coef,
-                                                      float* loss, float* lse, bool grad) {
-  __shared__ float red[32];
-  float* row = x + (int64_t)blockIdx.x * V;
-  const int64_t y = target[blockIdx.x];
-  const bool has = y >= 0 && y < V;
-  float top = -INFINITY;
-  for (int64_t v = threadIdx.x; v < V; v += 256) top = fmaxf(top, row[v]);
+// Joins a row's chunks: lse and loss.  One block for each token.
+__global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t chunks, int64_t ld, const int64_t* target, int64_t V,
+                                                   const float* right, float* lse, float* loss) {
+  __shared__ float red[64];
+  const float2* row = stats + (int64_t)blockIdx.x * ld;
+  float m = -INFINITY, s = 0.f;
+  for (int64_t c = threadIdx.x; c < chunks; c += 128) {
+    const float2 e = row[c];
+    const float to = fmaxf(m, e.x);
+    s = s * exp2_approx(m - to) + e.y * exp2_approx(e.x - to);
+    m = to;
+  }
+  float top = m;
+#pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  __syncthreads();
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
   __syncthreads();
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
-  float s[1] = {0.f};
-  for (int64_t v = threadIdx.x; v < V; v += 256) s[0] += expf(row[v] - top);
-  block_reduce<1>(s, red, SumOp());
-  const float l = top + logf(s[0]);
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float t[1] = {m == -INFINITY ? 0.f : s * exp2_approx(m - top)};
+  block_reduce<1>(t, red, SumOp());
   if (threadIdx.x == 0) {
+    const float l = (top + log2f(t[0])) * kLn2;
+    const int64_t y = target[blockIdx.x];
     lse[blockIdx.x] = l;
-    loss[blockIdx.x] = has ? l - row[y] : 0.f;
+    loss[blockIdx.x] = y >= 0 && y < V ? l - right[blockIdx.x] : 0.f;
   }
-  if (!grad) return;
-  __syncthreads();
-  const float c = coef[blockIdx.x];
-  for (int64_t v = threadIdx.x; v < V; v += 256) row[v] = c * (expf(row[v] - l) - (has && v == y ? 1.f : 0.f));
 }
 
+// The kept logits of a piece become G, times kGScale: 8 at a time.
 template <class T>
-__global__ void convert_kernel(const float* x, T* y, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
-    y[i] = from_f32<T>(x[i]);
+__global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t ldk, const float2* stats, int64_t chunks,
+                                                       const int64_t* target, int64_t V, const float* coef,
+                                                       const float* lse) {
+  const int64_t row = blockIdx.y;
+  const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (col >= ldk) return;
+  const float c = coef[row];
+  const float off = stats[row * chunks + col / kChunk].x - lse[row] * kLog2e;
+  const int64_t y = target[row] - col;
+  uint16_t* at = kept + row * ldk + col;
+  const uint4 q = *reinterpret_cast<const uint4*>(at);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  float g[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
+    // 65535: too far below; still NaN where the row's sum is
+    const float p = u == 65535u ? off - off : exp2_approx(fmaf((float)u, -1.f / kSteps, off));
+    g[i] = c == 0.f ? 0.f : c * kGScale * (p - (y == i ? 1.f : 0.f));
+  }
+  if (V - col < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= V - col) g[i] = 0.f;
+  }
+  store_vec<T, 8>(reinterpret_cast<T*>(at), g);
 }
 
-constexpr int64_t kPiece = 256;  // tokens whose logits are held at once
+// 32 sums of a row, scaled, to 16 bits.
+template <class T>
+__device__ __forceinline__ void store_row(T* to, int64_t left, bool vec, float scale, const float (&v)[32]) {
+  if (vec && left >= 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = v[8 * i + k] * scale;
+      store_vec<T, 8>(to + 8 * i, e);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < left) to[i] = from_f32<T>(v[i] * scale);
+  }
+}
+
+// Epilogue of the gradients' products.  `part` not null: fp32 sums of the
+// unit's part of K go there (parts x rows x cols).  `acc` not null: sums of
+// earlier pieces are in it, and it takes theirs and these unless this is the
+// last piece.
+template <class T>
+struct GradientEpilogue {
+  int64_t rows, cols;
+  T* out;
+  bool vec;
+  const float* scale;
+  float* part;
+  float* acc;
+  bool first, last;
+  __device__ __forceinline__ void operator()(const PairUnit& q, int64_t row, int64_t col, const PairSums& sums) const {
+    const float sc = *scale;
+#pragma unroll 1
+    for (int c = 0; c < 128 && col + c < cols; c += 32) {
+      float v[32];
+      sums.load(c, v);
+      if (row >= rows) continue;
+      const int64_t left = cols - col - c;
+      const int64_t at = row * cols + col + c;
+      if (part) {
+        float* to = part + (int64_t)q.part * rows * cols + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < left) to[i] = v[i];
+        continue;
+      }
+      if (acc) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < left) {
+            if (!first) v[i] += acc[at + i];
+            if (!last) acc[at + i] = v[i];
+          }
+        if (!last) continue;
+      }
+      store_row<T>(out + at, left, vec, sc, v);
+    }
+  }
+};
+
+// Adds up the parts of a product in their order.
+template <class T>
+__global__ void __launch_bounds__(256) join_parts_kernel(const float* part, int parts, int64_t n, const float* scale, T* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = 0.f;
+  for (int k = 0; k < parts; ++k) s += part[(int64_t)k * n + i];
+  out[i] = from_f32<T>(s * *scale);
+}
+
+// Rows that do not start on 16 bytes, copied to rows that do.
+__global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* x, int64_t ldx, int64_t cols, uint16_t* y, int64_t ldy) {
+  const int64_t row = blockIdx.y;
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c < cols) y[row * ldy + c] = x[row * ldx + c];
+}
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
+int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+int64_t tiles(int64_t x) { return (x + kPairTile - 1) / kPairTile; }
+
+// Tokens of a piece: all, or as many whole tiles as the limits allow.
+int64_t piece_tokens(int64_t T, int64_t V, bool grad) {
+  const int64_t fit = std::max<int64_t>(1, kPieceBytes / (2 * up8(V)) / kPairTile) * kPairTile;
+  return std::min({T, grad ? fit : kPieceTokens, kPieceTokens});
+}
+
+// Parts of K for dH: few tiles over a long K leave pairs of SMs idle, or a
+// last wave nearly empty, so K is cut where the parts' waves are shorter by
+// more than what writing and adding up the parts costs (a step of K is 256 x
+// 256 x 64; a part's tile is written and read in fp32, as long as about 8
+// steps take).
+int dh_parts(int64_t T, int64_t D, int64_t V, int pairs) {
+  const int64_t t = tiles(T) * tiles(D), steps = (V + kPairK - 1) / kPairK;
+  int best = 1;
+  int64_t cost = (t + pairs - 1) / pairs * steps;
+  for (int p = 2; p <= 16 && p <= steps; ++p) {
+    const int64_t c = (t * p + pairs - 1) / pairs * ((steps + p - 1) / p + 8);
+    if (c < cost) best = p, cost = c;
+  }
+  return best;
+}
+
+struct Layout {
+  size_t coef, scale, right, stats, kept, part, acc, h, w, bytes;
+};
+constexpr int kPlanPairs = 76;  // pairs of SMs the workspace is planned for
+Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
+  const int64_t n = piece_tokens(T, V, grad), chunks = tiles(V) * 2;
+  Layout l = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up(bytes);
+    return here;
+  };
+  l.coef = take(T * 4);
+  l.scale = take(4);
+  l.right = take(n * 4);
+  l.stats = take(n * chunks * 8);
+  if (grad) {
+    l.kept = take(n * up8(V) * 2);
+    const int p = dh_parts(n, D, V, kPlanPairs), p2 = T % n ? dh_parts(T % n, D, V, kPlanPairs) : 1;
+    l.part = take(std::max(p > 1 ? (size_t)p * n * D * 4 : 0, p2 > 1 ? (size_t)p2 * (T % n) * D * 4 : 0));
+    l.acc = take(n < T ? V * D * 4 : 0);
+  }
+  if (copies) {
+    l.h = take(T * up8(D) * 2);
+    l.w = take(V * up8(D) * 2);
+  }
+  l.bytes = at;
+  return l;
+}
+
+bool tma_rows(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
 
 template <class T>
-cudaError_t run(const CrossEntropy& p, void* ws, int32_t* status, cudaStream_t stream) {
-  char* at = static_cast<char*>(ws);
-  float* coef = reinterpret_cast<float*>(at);
-  at += up(p.T * 4);
-  float* x = reinterpret_cast<float*>(at);
-  at += up(std::min(kPiece, p.T) * p.V * 4);
-  float* dw = reinterpret_cast<float*>(at);
+cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t stream) {
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const bool grad = p.dH != nullptr;
-  coefficients_kernel<<<1, 1024, 0, stream>>>(p.target, p.T, p.V, p.coef, coef, status);
-  if (grad) {
-    cudaError_t e = cudaMemsetAsync(dw, 0, p.V * p.D * 4, stream);
+  const bool copies = !tma_rows(p.H, p.ldh) || !tma_rows(p.W, p.ldw);
+  const Layout l = layout(p.T, p.D, p.V, grad, copies);
+  const int64_t n = piece_tokens(p.T, p.V, grad), chunks = tiles(p.V) * 2, ldk = up8(p.V);
+  float* coef = reinterpret_cast<float*>(ws + l.coef);
+  float* scale = reinterpret_cast<float*>(ws + l.scale);
+  float* right = reinterpret_cast<float*>(ws + l.right);
+  float2* stats = reinterpret_cast<float2*>(ws + l.stats);
+  uint16_t* kept = reinterpret_cast<uint16_t*>(ws + l.kept);
+  const T *H = static_cast<const T*>(p.H), *W = static_cast<const T*>(p.W);
+  int64_t ldh = p.ldh, ldw = p.ldw;
+  auto align = [&](const T*& x, int64_t& ld, int64_t rows, size_t to) {
+    if (tma_rows(x, ld)) return;
+    uint16_t* y = reinterpret_cast<uint16_t*>(ws + to);
+    for (int64_t r = 0; r < rows; r += 65535)
+      align_rows_kernel<<<dim3((unsigned)((p.D + 255) / 256), (unsigned)std::min<int64_t>(65535, rows - r)), 256, 0, stream>>>(
+          reinterpret_cast<const uint16_t*>(x) + r * ld, ld, p.D, y + r * up8(p.D), up8(p.D));
+    x = reinterpret_cast<const T*>(y), ld = up8(p.D);
+  };
+  align(H, ldh, p.T, l.h);
+  align(W, ldw, p.V, l.w);
+  coefficients_kernel<<<1, 1024, 0, stream>>>(p.target, p.T, p.V, p.coef, coef, scale, status);
+  const bool vec = grad && p.D % 8 == 0 && aligned_to(p.dH, 16) && aligned_to(p.dW, 16);
+  const int dsteps = (int)((p.D + kPairK - 1) / kPairK), vsteps = (int)((p.V + kPairK - 1) / kPairK);
+  for (int64_t t = 0; t < p.T; t += n) {
+    const int64_t m = std::min(n, p.T - t);
+    const T* h = H + t * ldh;
+    const int64_t* target = p.target + t;
+    const PairWork logits{(int)tiles(m), (int)tiles(p.V), 16, dsteps, 1};
+    const PairOperand ph{h, m, ldh}, pw{W, p.V, ldw};
+    cudaError_t e;
+    if (grad) {
+      const LogitsEpilogue<true> epi{m, p.V, target, stats, chunks, right, kept, ldk};
+      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
+    } else {
+      const LogitsEpilogue<false> epi{m, p.V, target, stats, chunks, right, nullptr, 0};
+      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
+    }
+    if (e != cudaSuccess) return e;
+    join_kernel<<<(unsigned)m, 128, 0, stream>>>(stats, (p.V + kChunk - 1) / kChunk, chunks, target, p.V, right, p.lse + t, p.loss + t);
+    if (!grad) continue;
+    for (int64_t r = 0; r < m; r += 65535)
+      gradient_kernel<T><<<dim3((unsigned)((ldk / 8 + 255) / 256), (unsigned)std::min<int64_t>(65535, m - r)), 256, 0, stream>>>(
+          kept + r * ldk, ldk, stats + r * chunks, chunks, target + r, p.V, coef + t + r, p.lse + t + r);
+    const PairOperand pg{kept, m, ldk}, pgt{kept, p.V, ldk}, pwt{W, p.D, ldw}, pht{h, p.D, ldh};
+    T* dH = static_cast<T*>(p.dH) + t * p.D;
+    const int parts = dh_parts(m, p.D, p.V, kPlanPairs);
+    float* part = parts > 1 ? reinterpret_cast<float*>(ws + l.part) : nullptr;
+    e = pair_gemm_launch<false, true, 2, 0>(pg, pwt, p.V, bf16, PairWork{(int)tiles(m), (int)tiles(p.D), 16, vsteps, parts},
+                                            GradientEpilogue<T>{m, p.D, dH, vec, scale, part, nullptr, true, true}, status,
+                                            stream);
+    if (e != cudaSuccess) return e;
+    if (part)
+      join_parts_kernel<T><<<(unsigned)((m * p.D + 255) / 256), 256, 0, stream>>>(part, parts, m * p.D, scale, dH);
+    float* acc = n < p.T ? reinterpret_cast<float*>(ws + l.acc) : nullptr;
+    e = pair_gemm_launch<true, true, 2, 0>(
+        pgt, pht, m, bf16, PairWork{(int)tiles(p.V), (int)tiles(p.D), 16, (int)((m + kPairK - 1) / kPairK), 1},
+        GradientEpilogue<T>{p.V, p.D, static_cast<T*>(p.dW), vec, scale, nullptr, acc, t == 0, t + m == p.T}, status, stream);
     if (e != cudaSuccess) return e;
   }
-  for (int64_t t = 0; t < p.T; t += kPiece) {
-    const int64_t n = std::min(kPiece, p.T - t);
-    const T* H = static_cast<const T*>(p.H) + t * p.ldh;
-    const T* W = static_cast<const T*>(p.W);
-    auto grid = [](int64_t m, int64_t k) { return dim3((unsigned)((k + 63) / 64), (unsigned)((m + 63) / 64)); };
-    tile_product_kernel<float><<<grid(n, p.V), 256, 0, stream>>>(n, p.V, p.D, Rows<T>{H, p.ldh}, RowsT<T>{W, p.ldw}, Put{x, p.V});
-    softmax_kernel<<<(unsigned)n, 256, 0, stream>>>(x, p.V, p.target + t, coef + t, p.loss + t, p.lse + t, grad);
-    if (!grad) continue;
-    tile_product_kernel<float><<<grid(n, p.D), 256, 0, stream>>>(n, p.D, p.V, Rows<float>{x, p.V}, Rows<T>{W, p.ldw},
-                                                                 PutAs<T>{static_cast<T*>(p.dH) + t * p.D, p.D});
-    tile_product_kernel<float><<<grid(p.V, p.D), 256, 0, stream>>>(p.V, p.D, n, RowsT<float>{x, p.V}, Rows<T>{H, p.ldh}, Add{dw, p.D});
-  }
-  if (grad) convert_kernel<T><<<1024, 256, 0, stream>>>(dw, static_cast<T*>(p.dW), p.V * p.D);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t cross_entropy_workspace_bytes(int64_t T, int64_t D, int64_t V, bool grad) {
-  return up(T * 4) + up(std::min(kPiece, T) * V * 4) + (grad ? (size_t)V * D * 4 : 0);
+size_t cross_entropy_workspace_bytes(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
+  return layout(T, D, V, grad, copies).bytes;
 }
+bool cross_entropy_needs_copies(const CrossEntropy& p) { return !tma_rows(p.H, p.ldh) || !tma_rows(p.W, p.ldw); }
 
 cudaError_t cross_entropy_launch(const CrossEntropy& p, void* ws, int32_t* status_dev, cudaStream_t stream) {
-  return p.dtype == kF16 ? run<__half>(p, ws, status_dev, stream) : run<__nv_bfloat16>(p, ws, status_dev, stream);
+  char* at = static_cast<char*>(ws);
+  return p.dtype == kF16 ? run<__half>(p, at, status_dev, stream) : run<__nv_bfloat16>(p, at, status_dev, stream);
 }
 
 }  // namespace bakron

@@ -78,7 +78,10 @@ struct CrossEntropy {
   const float* coef;  // T, or null: 1 / (number of tokens with a target)
   void *dH, *dW;      // null: loss only
 };
-size_t cross_entropy_workspace_bytes(int64_t T, int64_t D, int64_t V, bool grad);
+// copies: with room for aligned copies of H and W, which
+// cross_entropy_needs_copies() tells the need of.
+size_t cross_entropy_workspace_bytes(int64_t T, int64_t D, int64_t V, bool grad, bool copies);
+bool cross_entropy_needs_copies(const CrossEntropy& p);
 cudaError_t cross_entropy_launch(const CrossEntropy& p, void* ws, int32_t* status_dev, cudaStream_t stream);
 
 }  // namespace bakron

@@ -1,0 +1,337 @@
+// pair_gemm.cuh -- C = A B^T in 16-bit floats with fp32 sums on pairs of SMs,
+// for the layer operators whose work is one large matrix product each.
+//
+// A cluster of two blocks computes one 256 x 256 tile at a time: each block
+// keeps 128 rows of A and 128 rows of B for every 64 of K in shared memory
+// (six stages of 32 KB, filled by TMA with the 128-byte swizzle), the even
+// block's MMA thread issues tcgen05.mma with cta_group::2 (M = N = 256,
+// K = 16), which reads both blocks' operands, and each block's tensor memory
+// receives 128 rows of the sums.  Two sums of 256 columns take turns, so that
+// the epilogue warps read one while the MMAs fill the other.  One pair stays
+// on two SMs and walks over the units (tile, part of K) it is given.
+//
+// Either operand may be stored with K contiguous or with its rows (M or N)
+// contiguous: the canonical layouts differ only in the boxes TMA copies and
+// in the descriptors' offsets.
+//
+// With kSegment > 0 the sums are restarted every kSegment steps of 64 and
+// added up in integers by the epilogue, so that products of 8-bit codes stay
+// exact: 1024 products of at most 2^14 reach 2^24, where fp32 integers end.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#include "bakron.h"
+#include "tc.cuh"
+#include "tma.h"
+
+namespace bakron {
+
+constexpr int kPairTile = 256;    // rows and columns of a pair's tile
+constexpr int kPairK = 64;        // K of a stage: 128 bytes
+constexpr int kPairStages = 6;
+constexpr int kPairHalf = 128 * kPairK * 2;        // one block's part of an operand's stage: 16 KB
+constexpr uint32_t kPairStageTx = 4u * kPairHalf;  // bytes of a stage in both blocks
+constexpr int kPairSmem = kPairStages * 2 * kPairHalf + 2048;
+
+// Units of a product: unit u = (tile, part of K); tiles run down groups of
+// `group` tile rows first, so that what runs at the same time shares operands
+// in the L2 cache.
+struct PairWork {
+  int tiles_m, tiles_n, group;
+  int ksteps;  // stages of K
+  int parts;   // parts that K is cut into
+  __host__ __device__ int units() const { return tiles_m * tiles_n * parts; }
+};
+struct PairUnit {
+  int tm, tn, part, k0, k1;
+};
+__host__ __device__ inline PairUnit pair_unit(const PairWork& w, int u) {
+  PairUnit r;
+  const int tiles = w.tiles_m * w.tiles_n;
+  r.part = u / tiles;
+  const int t = u % tiles;
+  const int g = t / (w.group * w.tiles_n), first = g * w.group;
+  const int rows = w.tiles_m - first < w.group ? w.tiles_m - first : w.group;
+  const int in = t - g * w.group * w.tiles_n;
+  r.tm = first + in % rows;
+  r.tn = in / rows;
+  r.k0 = (int)((int64_t)w.ksteps * r.part / w.parts);
+  r.k1 = (int)((int64_t)w.ksteps * (r.part + 1) / w.parts);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+// Address of the even block's copy of a shared variable.
+__device__ __forceinline__ uint32_t in_even_block(const void* p) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// A box into this block's shared memory; its bytes count on the even block's barrier.
+__device__ __forceinline__ void pair_copy(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(mbar)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both blocks once all MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+          smem_u32(mbar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// 32 consecutive columns of this warp's 32 tensor-memory lanes; complete after tmem_wait_ld().
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared memory descriptors with the 128-byte swizzle (layout type 2).  K
+// contiguous: 8-row groups of 1024 bytes (stride offset).  Rows contiguous:
+// 64 rows by 8 of K take 1024 bytes, the next 8 of K follow (stride offset),
+// the next 64 rows are 8 KB on (leading offset).
+template <bool kRows>
+__device__ __forceinline__ uint64_t pair_desc(uint32_t saddr) {
+  const uint64_t lbo = kRows ? 8192 >> 4 : 1, sbo = 1024 >> 4;
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (lbo << 16) | (sbo << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Bytes from one K = 16 step to the next within a stage.
+template <bool kRows>
+__host__ __device__ constexpr uint32_t pair_kstep() { return kRows ? 2048u : 32u; }
+
+struct PairBarriers {
+  uint64_t full[kPairStages], empty[kPairStages], sum_full[2], sum_empty[2];
+  uint32_t tmem;
+};
+
+// The epilogue is called by every thread of 4 kQuads warps for each unit,
+//   epi(unit, row, col, sums)
+// with the thread's row and first column and a source of its 256 / kQuads
+// columns: sums.load(c, v) gives 32 of them from column c on.
+struct PairSums {
+  uint32_t taddr;
+  __device__ __forceinline__ void load(int c, float (&v)[32]) const { tmem_ld32(taddr + (uint32_t)c, v); }
+};
+// With kSegment the columns come as integers, epi(unit, row, col, acc).
+
+template <bool kARows, bool kBRows, int kQuads, int kSegment, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 1)
+    pair_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairWork work,
+                     uint32_t idesc, Epi epi, int32_t* status) {
+  extern __shared__ unsigned char pair_smem_raw[];
+  const uint32_t base = (smem_u32(pair_smem_raw) + 1023u) & ~1023u;
+  __shared__ PairBarriers bar;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pairs = gridDim.x / 2, mine = blockIdx.x / 2, units = work.units();
+  bool broken = false;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(smem_u32(&bar.full[i])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(smem_u32(&bar.empty[i])));
+    }
+    for (int i = 0; i < 2; ++i) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(smem_u32(&bar.sum_full[i])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(&bar.sum_empty[i])), "r"(8 * kQuads));
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&bar.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+
+  if (warp == 0 && lane == 0) {  // copies: 16 KB of A and of B for each stage, in both blocks
+    int n = 0;
+    for (int u = mine; u < units && !broken; u += pairs) {
+      const PairUnit q = pair_unit(work, u);
+      const int a0 = q.tm * kPairTile + (int)rank * 128, b0 = q.tn * kPairTile + (int)rank * 128;
+      for (int k = q.k0; k < q.k1; ++k, ++n) {
+        const int slot = n % kPairStages;
+        if (n >= kPairStages) mbar_wait(&bar.empty[slot], (uint32_t)(n / kPairStages - 1) & 1u, broken);
+        if (broken) break;
+        const uint32_t full = in_even_block(&bar.full[slot]);
+        if (rank == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(&bar.full[slot])),
+                       "r"(kPairStageTx)
+                       : "memory");
+        const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
+        if constexpr (kARows) {
+          pair_copy(a, &map_a, a0, k * kPairK, full);
+          pair_copy(a + 8192, &map_a, a0 + 64, k * kPairK, full);
+        } else {
+          pair_copy(a, &map_a, k * kPairK, a0, full);
+        }
+        if constexpr (kBRows) {
+          pair_copy(b, &map_b, b0, k * kPairK, full);
+          pair_copy(b + 8192, &map_b, b0 + 64, k * kPairK, full);
+        } else {
+          pair_copy(b, &map_b, k * kPairK, b0, full);
+        }
+      }
+    }
+    // No block leaves while copies into it, or arrivals at its barriers, are
+    // on their way: every stage's last use has been released by the MMAs (or,
+    // after a wait that ran out, has at least landed).
+    for (int i = n > kPairStages ? n - kPairStages : 0; i < n; ++i) {
+      bool late = false;
+      if (!broken)
+        mbar_wait(&bar.empty[i % kPairStages], (uint32_t)(i / kPairStages) & 1u, broken);
+      else if (rank == 0)
+        mbar_wait(&bar.full[i % kPairStages], (uint32_t)(i / kPairStages) & 1u, late);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {  // products
+    int n = 0, sums = 0;
+    for (int u = mine; u < units && !broken; u += pairs) {
+      const PairUnit q = pair_unit(work, u);
+      uint32_t acc = 0;
+      for (int k = q.k0; k < q.k1; ++k, ++n) {
+        const int in_segment = kSegment ? (k - q.k0) % kSegment : k - q.k0;
+        if (in_segment == 0) {  // the next of the two sums, once the epilogue has read it
+          acc = tmem + (uint32_t)(sums & 1) * 256u;
+          if (sums >= 2) mbar_wait(&bar.sum_empty[sums & 1], (uint32_t)(sums / 2 - 1) & 1u, broken);
+          tc_fence_after();
+        }
+        const int slot = n % kPairStages;
+        mbar_wait(&bar.full[slot], (uint32_t)(n / kPairStages) & 1u, broken);
+        if (broken) break;
+        tc_fence_after();
+        const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
+#pragma unroll
+        for (int j = 0; j < kPairK / 16; ++j)
+          pair_mma(acc, pair_desc<kARows>(a + j * pair_kstep<kARows>()), pair_desc<kBRows>(b + j * pair_kstep<kBRows>()),
+                   idesc, (in_segment > 0 || j > 0) ? 1u : 0u);
+        pair_commit(&bar.empty[slot]);
+        if (k + 1 == q.k1 || (kSegment && in_segment == kSegment - 1)) {
+          pair_commit(&bar.sum_full[sums & 1]);
+          ++sums;
+        }
+      }
+    }
+  } else if (warp >= 4) {  // epilogue: 32 rows of the block and 256 / kQuads columns for each warp
+    constexpr int kCols = 256 / kQuads;
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)(part * kCols);
+    int sums = 0;
+    for (int u = mine; u < units && !broken; u += pairs) {
+      const PairUnit q = pair_unit(work, u);
+      const int64_t row = (int64_t)q.tm * kPairTile + rank * 128 + 32 * quarter + lane;
+      const int64_t col = (int64_t)q.tn * kPairTile + part * kCols;
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(
+                           in_even_block(&bar.sum_empty[sums & 1]))
+                       : "memory");
+        ++sums;
+      };
+      if constexpr (kSegment == 0) {
+        mbar_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
+        if ((broken = __any_sync(0xffffffffu, broken))) break;
+        tc_fence_after();
+        epi(q, row, col, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes});
+        release();
+      } else {
+        int acc[kCols];
+        for (int k = q.k0; k < q.k1; k += kSegment) {
+          mbar_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
+          if ((broken = __any_sync(0xffffffffu, broken))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            float v[32];
+            tmem_ld32(tmem + (uint32_t)(sums & 1) * 256u + lanes + (uint32_t)c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c + i] = __float2int_rn(v[i]) + (k == q.k0 ? 0 : acc[c + i]);
+          }
+          release();
+        }
+        if (!broken) epi(q, row, col, acc);
+      }
+    }
+  }
+  if (broken) atomicOr(status, BAKRON_DEV_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+}
+
+// An operand: rows x K with K contiguous, or K x rows (`by_rows`), 16-bit.
+struct PairOperand {
+  const void* p;
+  int64_t rows, ld;
+};
+
+// M x N tiles of A (M x K) and B (N x K).  bf16: both bf16, else both fp16.
+// Pairs of SMs on the current device.
+inline int pair_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 1;
+  return std::max(1, sms / 2);
+}
+
+template <bool kARows, bool kBRows, int kQuads, int kSegment, class Epi>
+cudaError_t pair_gemm_launch(PairOperand a, PairOperand b, int64_t K, bool bf16, PairWork work, const Epi& epi,
+                             int32_t* status, cudaStream_t stream) {
+  const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap ma, mb;
+  auto map = [&](CUtensorMap* m, const PairOperand& o, bool rows) {
+    return rows ? make_tensor_map(m, TileMap{o.p, type, K, o.rows, o.ld, kPairK, 64, true})
+                : make_tensor_map(m, TileMap{o.p, type, o.rows, K, o.ld, 128, kPairK, true});
+  };
+  cudaError_t e = map(&ma, a, kARows);
+  if (e == cudaSuccess) e = map(&mb, b, kBRows);
+  if (e != cudaSuccess) return e;
+  auto kernel = pair_gemm_kernel<kARows, kBRows, kQuads, kSegment, Epi>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = 2u * (unsigned)std::min(work.units(), pair_count());
+  // fp32 sums, operand types, which operands have their rows contiguous, N = 256, M = 256
+  const uint32_t t = bf16 ? 1u : 0u;
+  const uint32_t idesc = (1u << 4) | (t << 7) | (t << 10) | ((kARows ? 1u : 0u) << 15) | ((kBRows ? 1u : 0u) << 16) |
+                         ((256u >> 3) << 17) | ((256u >> 4) << 24);
+  kernel<<<grid, 128 + 128 * kQuads, kPairSmem, stream>>>(ma, mb, work, idesc, epi, status);
+  return cudaGetLastError();
+}
+
+}  // namespace bakron

@@ -83,14 +83,15 @@ def test_norm_residual_backward(lib):
 
 def test_linear_cross_entropy(lib):
     size = lib.bakron_linear_cross_entropy_workspace_size
-    assert size(0, 8, 8, 0) == size(4, 0, 8, 0) == size(4, 8, 0, 1) == 0
-    loss, grad = size(4, 64, 100, 0), size(4, 64, 100, 1)
-    assert 0 < loss <= grad
+    assert size(0, 8, 8, 0, 0) == size(4, 0, 8, 0, 0) == size(4, 8, 0, 1, 0) == 0
+    loss, grad = size(4, 64, 100, 0, 0), size(4, 64, 100, 1, 0)
+    assert 0 < loss < grad < size(4, 64, 100, 1, 1)
     good = dict(H=at(0x1000), ldh=64, W=at(0x2000), ldw=64, dtype=BF16, y=at(0x3000), T=4, D=64, V=100, loss=at(0x4000),
                 lse=at(0x5000), ws=at(0x100000), n=loss, status=at(0x6000), stream=None)
     bad = dict(H=[None, at(0x1001)], ldh=[63], W=[None, at(0x2001)], ldw=[63], dtype=[F32, I8], y=[None, at(0x3004)], T=[0],
                D=[0], V=[0], loss=[None], lse=[None, at(0x4000)], status=[None])
     refused(lib.bakron_linear_cross_entropy, good, **bad)
+    refused(lib.bakron_linear_cross_entropy, {**good, "ldh": 65}, 4, n=[loss, size(4, 64, 100, 0, 1) - 1])  # copies
     refused(lib.bakron_linear_cross_entropy, good, 4, ws=[None, at(0x100010)], n=[loss - 1])
     good = {**{k: v for k, v in list(good.items())[:6]}, "coef": None, **{k: good[k] for k in ("T", "D", "V", "loss", "lse")},
             "dH": at(0x7000), "dW": at(0x8000), "ws": at(0x100000), "n": grad, "status": at(0x6000), "stream": None}
