@@ -81,10 +81,8 @@ __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* targe
 template <bool kKeep>
 struct LogitsEpilogue {
   int64_t rows, V;
-  const int64_t* target;
   float2* stats;  // rows x chunks: maximum in units of log 2, sum of 2^(x - maximum)
   int64_t chunks;
-  float* right;    // the target's logit
   uint16_t* kept;  // rows x ldk
   int64_t ldk;
 
@@ -103,16 +101,10 @@ struct LogitsEpilogue {
     }
     m = m == -INFINITY ? 0.f : m * kLog2e;
     const bool live = row < rows;
-    const int64_t y = live ? target[row] - col : -1;
     float s = 0.f;
 #pragma unroll 1
     for (int c = 0; c < kChunk; c += 32) {
       sums.load(c, v);
-      if (__any_sync(0xffffffffu, y >= c && y < c + 32)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (y == c + i) right[row] = v[i];
-      }
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = (whole || c + i < left) ? fmaf(v[i], kLog2e, -m) : -INFINITY;
       if constexpr (kKeep) {
@@ -138,11 +130,18 @@ struct LogitsEpilogue {
   }
 };
 
-// Joins a row's chunks: lse and loss.  One block for each token.
-__global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t chunks, int64_t ld, const int64_t* target, int64_t V,
-                                                   const float* right, float* lse, float* loss) {
+// Joins a row's chunks: lse and loss.  One block for each token.  The target's
+// logit is computed again, in fp32 with 128 sums: the tensor cores round
+// towards zero in their long sums (1e-6 of a logit of 4096 terms), which
+// averages out over a vocabulary but not in the one logit.
+template <class T>
+__global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t chunks, int64_t ld, const int64_t* target,
+                                                   int64_t V, const T* H, int64_t ldh, const T* W, int64_t ldw, int64_t D,
+                                                   float* lse, float* loss) {
   __shared__ float red[64];
   const float2* row = stats + (int64_t)blockIdx.x * ld;
+  const int64_t y = target[blockIdx.x];
+  const bool has = y >= 0 && y < V;
   float m = -INFINITY, s = 0.f;
   for (int64_t c = threadIdx.x; c < chunks; c += 128) {
     const float2 e = row[c];
@@ -156,13 +155,24 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t 
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
   __syncthreads();
   top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float t[1] = {m == -INFINITY ? 0.f : s * exp2_approx(m - top)};
-  block_reduce<1>(t, red, SumOp());
+  float t[2] = {m == -INFINITY ? 0.f : s * exp2_approx(m - top), 0.f};
+  if (has) {
+    const T *h = H + (int64_t)blockIdx.x * ldh, *w = W + y * ldw;
+    const int64_t whole = D / 8 * 8;
+    for (int64_t d = threadIdx.x * 8; d < whole; d += 1024) {
+      float a[8], b[8];
+      load_vec<T, 8>(h + d, a);
+      load_vec<T, 8>(w + d, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[1] = fmaf(a[i], b[i], t[1]);
+    }
+    if (whole + threadIdx.x < D) t[1] = fmaf(to_f32<T>(h[whole + threadIdx.x]), to_f32<T>(w[whole + threadIdx.x]), t[1]);
+  }
+  block_reduce<2>(t, red, SumOp());
   if (threadIdx.x == 0) {
     const float l = (top + log2f(t[0])) * kLn2;
-    const int64_t y = target[blockIdx.x];
     lse[blockIdx.x] = l;
-    loss[blockIdx.x] = y >= 0 && y < V ? l - right[blockIdx.x] : 0.f;
+    loss[blockIdx.x] = has ? l - t[1] : 0.f;
   }
 }
 
@@ -301,7 +311,7 @@ int dh_parts(int64_t T, int64_t D, int64_t V, int pairs) {
 }
 
 struct Layout {
-  size_t coef, scale, right, stats, kept, part, acc, h, w, bytes;
+  size_t coef, scale, stats, kept, part, acc, h, w, bytes;
 };
 constexpr int kPlanPairs = 76;  // pairs of SMs the workspace is planned for
 Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
@@ -315,7 +325,6 @@ Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
   };
   l.coef = take(T * 4);
   l.scale = take(4);
-  l.right = take(n * 4);
   l.stats = take(n * chunks * 8);
   if (grad) {
     l.kept = take(n * up8(V) * 2);
@@ -342,7 +351,6 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
   const int64_t n = piece_tokens(p.T, p.V, grad), chunks = tiles(p.V) * 2, ldk = up8(p.V);
   float* coef = reinterpret_cast<float*>(ws + l.coef);
   float* scale = reinterpret_cast<float*>(ws + l.scale);
-  float* right = reinterpret_cast<float*>(ws + l.right);
   float2* stats = reinterpret_cast<float2*>(ws + l.stats);
   uint16_t* kept = reinterpret_cast<uint16_t*>(ws + l.kept);
   const T *H = static_cast<const T*>(p.H), *W = static_cast<const T*>(p.W);
@@ -368,14 +376,15 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
     const PairOperand ph{h, m, ldh}, pw{W, p.V, ldw};
     cudaError_t e;
     if (grad) {
-      const LogitsEpilogue<true> epi{m, p.V, target, stats, chunks, right, kept, ldk};
+      const LogitsEpilogue<true> epi{m, p.V, stats, chunks, kept, ldk};
       e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
     } else {
-      const LogitsEpilogue<false> epi{m, p.V, target, stats, chunks, right, nullptr, 0};
+      const LogitsEpilogue<false> epi{m, p.V, stats, chunks, nullptr, 0};
       e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
     }
     if (e != cudaSuccess) return e;
-    join_kernel<<<(unsigned)m, 128, 0, stream>>>(stats, (p.V + kChunk - 1) / kChunk, chunks, target, p.V, right, p.lse + t, p.loss + t);
+    join_kernel<T><<<(unsigned)m, 128, 0, stream>>>(stats, (p.V + kChunk - 1) / kChunk, chunks, target, p.V, h, ldh, W, ldw, p.D,
+                                                    p.lse + t, p.loss + t);
     if (!grad) continue;
     for (int64_t r = 0; r < m; r += 65535)
       gradient_kernel<T><<<dim3((unsigned)((ldk / 8 + 255) / 256), (unsigned)std::min<int64_t>(65535, m - r)), 256, 0, stream>>>(
