@@ -80,14 +80,14 @@ __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* targe
 // Epilogue of the logits: rows are tokens of the piece, columns the vocabulary.
 template <bool kKeep>
 struct LogitsEpilogue {
+  CUtensorMap map;  // of the kept logits
   int64_t rows, V;
   float2* stats;  // rows x chunks: maximum in units of log 2, sum of 2^(x - maximum)
   int64_t chunks;
-  uint16_t* kept;  // rows x ldk
-  int64_t ldk;
 
-  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row, int64_t col, const PairSums& sums) const {
-    if (col >= V) return;
+  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, const PairSums& sums,
+                                             const PairBox& box) const {
+    if (col >= V || row0 >= rows) return;
     const bool whole = col + kChunk <= V;
     const int left = whole ? kChunk : (int)(V - col);
     float v[32];
@@ -95,38 +95,47 @@ struct LogitsEpilogue {
 #pragma unroll 1
     for (int c = 0; c < kChunk; c += 32) {
       sums.load(c, v);
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (whole || c + i < left) m = fmaxf(m, v[i]);
+        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < left) m = fmaxf(m, v[i]);
+      }
     }
     m = m == -INFINITY ? 0.f : m * kLog2e;
-    const bool live = row < rows;
     float s = 0.f;
 #pragma unroll 1
     for (int c = 0; c < kChunk; c += 32) {
+      if (c >= left) break;
       sums.load(c, v);
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = (whole || c + i < left) ? fmaf(v[i], kLog2e, -m) : -INFINITY;
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kLog2e, -m);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = c + i < left ? fmaf(v[i], kLog2e, -m) : -INFINITY;
+      }
       if constexpr (kKeep) {
+        // -kSteps v rounded to an integer in the low bits of 1.5 2^23 + it.
+        // A NaN is lost here; its row's sum is NaN, which is what counts.
         uint32_t w[16];
+        constexpr float kMagic = 12582912.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          // a NaN is lost here; its row's sum is NaN, which is what counts
-          const uint32_t lo = (uint32_t)__float2int_rn(fminf(-kSteps * v[2 * i], 65535.f));
-          const uint32_t hi = (uint32_t)__float2int_rn(fminf(-kSteps * v[2 * i + 1], 65535.f));
-          w[i] = lo | (hi << 16);
-        }
-        if (live) {
-          uint16_t* to = kept + row * ldk + col + c;
+        for (int i = 0; i < 16; ++i)
+          w[i] = __byte_perm(__float_as_uint(fminf(fmaf(v[2 * i], -kSteps, kMagic), kMagic + 65535.f)),
+                             __float_as_uint(fminf(fmaf(v[2 * i + 1], -kSteps, kMagic), kMagic + 65535.f)), 0x5410);
+        const int half = (c & 32) >> 3;  // 32 columns are half of a box
+        if (half == 0) box.open();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (whole || c + 8 * i < left) reinterpret_cast<uint4*>(to)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        }
+        for (int j = 0; j < 4; ++j) box.put(half + j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        if (half || c + 32 >= left) box.send(&map, (int)col + (c & ~32), (int)row0);
       }
 #pragma unroll
       for (int i = 0; i < 32; ++i) s += exp2_approx(v[i]);
     }
-    if (live) stats[row * chunks + col / kChunk] = make_float2(m, s);
+    if (row0 + box.lane < rows) stats[(row0 + box.lane) * chunks + col / kChunk] = make_float2(m, s);
   }
 };
 
@@ -206,63 +215,54 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
   store_vec<T, 8>(reinterpret_cast<T*>(at), g);
 }
 
-// 32 sums of a row, scaled, to 16 bits.
-template <class T>
-__device__ __forceinline__ void store_row(T* to, int64_t left, bool vec, float scale, const float (&v)[32]) {
-  if (vec && left >= 32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float e[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] = v[8 * i + k] * scale;
-      store_vec<T, 8>(to + 8 * i, e);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < left) to[i] = from_f32<T>(v[i] * scale);
-  }
-}
-
 // Epilogue of the gradients' products.  `part` not null: fp32 sums of the
 // unit's part of K go there (parts x rows x cols).  `acc` not null: sums of
 // earlier pieces are in it, and it takes theirs and these unless this is the
-// last piece.
+// last piece.  Else the scaled sums go to `out`, by TMA where its rows start
+// on 16 bytes.
 template <class T>
 struct GradientEpilogue {
+  CUtensorMap map;
   int64_t rows, cols;
   T* out;
-  bool vec;
+  bool tma;
   const float* scale;
   float* part;
   float* acc;
   bool first, last;
-  __device__ __forceinline__ void operator()(const PairUnit& q, int64_t row, int64_t col, const PairSums& sums) const {
+  __device__ __forceinline__ void operator()(const PairUnit& q, int64_t row0, int64_t col, const PairSums& sums,
+                                             const PairBox& box) const {
+    if (row0 >= rows) return;
     const float sc = *scale;
+    const int here = (int)(rows - row0 < 32 ? rows - row0 : 32);
 #pragma unroll 1
     for (int c = 0; c < 128 && col + c < cols; c += 32) {
       float v[32];
       sums.load(c, v);
-      if (row >= rows) continue;
-      const int64_t left = cols - col - c;
-      const int64_t at = row * cols + col + c;
-      if (part) {
-        float* to = part + (int64_t)q.part * rows * cols + at;
+      if (tma) {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < left) to[i] = v[i];
+        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i] * sc, v[2 * i + 1] * sc);
+        const int half = (c & 32) >> 3;
+        if (half == 0) box.open();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) box.put(half + j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        if (half || col + c + 32 >= cols) box.send(&map, (int)col + (c & ~32), (int)row0);
         continue;
       }
-      if (acc) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < left) {
-            if (!first) v[i] += acc[at + i];
-            if (!last) acc[at + i] = v[i];
-          }
-        if (!last) continue;
-      }
-      store_row<T>(out + at, left, vec, sc, v);
+      const int64_t at = row0 * cols + col + c + box.lane;
+      const bool in = col + c + box.lane < cols;
+      box.by_row(v, here, [&](int r, float x) {
+        if (!in) return;
+        const int64_t i = at + r * cols;
+        if (part) {
+          part[(int64_t)q.part * rows * cols + i] = x;
+          return;
+        }
+        if (acc && !first) x += acc[i];
+        if (acc && !last) acc[i] = x;
+        else out[i] = from_f32<T>(x * sc);
+      });
     }
   }
 };
@@ -296,15 +296,15 @@ int64_t piece_tokens(int64_t T, int64_t V, bool grad) {
 
 // Parts of K for dH: few tiles over a long K leave pairs of SMs idle, or a
 // last wave nearly empty, so K is cut where the parts' waves are shorter by
-// more than what writing and adding up the parts costs (a step of K is 256 x
-// 256 x 64; a part's tile is written and read in fp32, as long as about 8
-// steps take).
+// more than what writing and adding up the parts costs.  In steps of K of one
+// pair of SMs (256 x 256 x 64, 0.27 us): a tile's epilogue about 8, a tile's
+// part written and read again in fp32 0.3.
 int dh_parts(int64_t T, int64_t D, int64_t V, int pairs) {
   const int64_t t = tiles(T) * tiles(D), steps = (V + kPairK - 1) / kPairK;
   int best = 1;
-  int64_t cost = (t + pairs - 1) / pairs * steps;
+  double cost = (double)((t + pairs - 1) / pairs * (steps + 8));
   for (int p = 2; p <= 16 && p <= steps; ++p) {
-    const int64_t c = (t * p + pairs - 1) / pairs * ((steps + p - 1) / p + 8);
+    const double c = (double)((t * p + pairs - 1) / pairs * ((steps + p - 1) / p + 8)) + 0.3 * (double)(t * p);
     if (c < cost) best = p, cost = c;
   }
   return best;
@@ -367,6 +367,10 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
   align(W, ldw, p.V, l.w);
   coefficients_kernel<<<1, 1024, 0, stream>>>(p.target, p.T, p.V, p.coef, coef, scale, status);
   const bool vec = grad && p.D % 8 == 0 && aligned_to(p.dH, 16) && aligned_to(p.dW, 16);
+  auto out_map = [&](CUtensorMap* map, T* out, int64_t rows) {
+    return make_tensor_map(map, TileMap{out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rows,
+                                        p.D, p.D, 32, 64, true});
+  };
   const int dsteps = (int)((p.D + kPairK - 1) / kPairK), vsteps = (int)((p.V + kPairK - 1) / kPairK);
   for (int64_t t = 0; t < p.T; t += n) {
     const int64_t m = std::min(n, p.T - t);
@@ -376,10 +380,12 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
     const PairOperand ph{h, m, ldh}, pw{W, p.V, ldw};
     cudaError_t e;
     if (grad) {
-      const LogitsEpilogue<true> epi{m, p.V, stats, chunks, kept, ldk};
+      LogitsEpilogue<true> epi{{}, m, p.V, stats, chunks};
+      e = make_tensor_map(&epi.map, TileMap{kept, CU_TENSOR_MAP_DATA_TYPE_UINT16, m, ldk, ldk, 32, 64, true});
+      if (e != cudaSuccess) return e;
       e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
     } else {
-      const LogitsEpilogue<false> epi{m, p.V, stats, chunks, nullptr, 0};
+      const LogitsEpilogue<false> epi{{}, m, p.V, stats, chunks};
       e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
     }
     if (e != cudaSuccess) return e;
@@ -393,16 +399,19 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
     T* dH = static_cast<T*>(p.dH) + t * p.D;
     const int parts = dh_parts(m, p.D, p.V, kPlanPairs);
     float* part = parts > 1 ? reinterpret_cast<float*>(ws + l.part) : nullptr;
+    GradientEpilogue<T> eh{{}, m, p.D, dH, vec && !part, scale, part, nullptr, true, true};
+    if (eh.tma && (e = out_map(&eh.map, dH, m)) != cudaSuccess) return e;
     e = pair_gemm_launch<false, true, 2, 0>(pg, pwt, p.V, bf16, PairWork{(int)tiles(m), (int)tiles(p.D), 16, vsteps, parts},
-                                            GradientEpilogue<T>{m, p.D, dH, vec, scale, part, nullptr, true, true}, status,
-                                            stream);
+                                            eh, status, stream);
     if (e != cudaSuccess) return e;
     if (part)
       join_parts_kernel<T><<<(unsigned)((m * p.D + 255) / 256), 256, 0, stream>>>(part, parts, m * p.D, scale, dH);
     float* acc = n < p.T ? reinterpret_cast<float*>(ws + l.acc) : nullptr;
+    GradientEpilogue<T> ew{{}, p.V, p.D, static_cast<T*>(p.dW), vec && !acc, scale, nullptr, acc, t == 0, t + m == p.T};
+    if (ew.tma && (e = out_map(&ew.map, ew.out, p.V)) != cudaSuccess) return e;
     e = pair_gemm_launch<true, true, 2, 0>(
-        pgt, pht, m, bf16, PairWork{(int)tiles(p.V), (int)tiles(p.D), 16, (int)((m + kPairK - 1) / kPairK), 1},
-        GradientEpilogue<T>{p.V, p.D, static_cast<T*>(p.dW), vec, scale, nullptr, acc, t == 0, t + m == p.T}, status, stream);
+        pgt, pht, m, bf16, PairWork{(int)tiles(p.V), (int)tiles(p.D), 16, (int)((m + kPairK - 1) / kPairK), 1}, ew, status,
+        stream);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();

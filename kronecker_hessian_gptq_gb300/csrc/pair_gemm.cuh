@@ -33,7 +33,9 @@ constexpr int kPairK = 64;        // K of a stage: 128 bytes
 constexpr int kPairStages = 6;
 constexpr int kPairHalf = 128 * kPairK * 2;        // one block's part of an operand's stage: 16 KB
 constexpr uint32_t kPairStageTx = 4u * kPairHalf;  // bytes of a stage in both blocks
-constexpr int kPairSmem = kPairStages * 2 * kPairHalf + 2048;
+constexpr int kPairBox = 4096;  // shared memory of an epilogue warp: 32 rows of 128 bytes
+template <int kQuads>
+constexpr int pair_smem() { return kPairStages * 2 * kPairHalf + 4 * kQuads * kPairBox + 1024; }
 
 // Units of a product: unit u = (tile, part of K); tiles run down groups of
 // `group` tile rows first, so that what runs at the same time shares operands
@@ -133,25 +135,74 @@ struct PairBarriers {
   uint32_t tmem;
 };
 
-// The epilogue is called by every thread of 4 kQuads warps for each unit,
-//   epi(unit, row, col, sums)
-// with the thread's row and first column and a source of its 256 / kQuads
-// columns: sums.load(c, v) gives 32 of them from column c on.
+// The epilogue (which may hold tensor maps: it stays in the parameters) is called by every thread of 4 kQuads warps for each unit,
+//   epi(unit, row0, col, sums, box)
+// with the warp's first row (the thread's own is lane further) and first
+// column and a source of its 256 / kQuads columns: sums.load(c, v) gives 32 of
+// them from column c on.  With kSegment it is an array of integers instead.
 struct PairSums {
   uint32_t taddr;
   __device__ __forceinline__ void load(int c, float (&v)[32]) const { tmem_ld32(taddr + (uint32_t)c, v); }
 };
-// With kSegment the columns come as integers, epi(unit, row, col, acc).
+
+// An epilogue warp's 4 KB of shared memory, 32 rows of 128 bytes, through
+// which its results leave in whole lines: a thread holds one row's sums, so
+// storing them from registers would write 16 bytes of 32 different lines at a
+// time (measured: 11 us for a 256 x 256 tile of 16-bit results, more than the
+// products of 1024 terms take).  The 16-byte pieces of row r are kept at
+// place j ^ (r % 8), the 128-byte swizzle of TMA, free of bank conflicts.
+struct PairBox {
+  uint32_t smem;
+  int lane;
+  __device__ __forceinline__ uint32_t piece(int row, int j) const { return smem + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); }
+  // Before the first put() of a box: the last one's copy has been read.
+  __device__ __forceinline__ void open() const {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+    __syncwarp();
+  }
+  __device__ __forceinline__ void put(int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(piece(lane, j)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+  }
+  // The box to column x and row y of the map's matrix; what lies outside it is left out.
+  __device__ __forceinline__ void send(const CUtensorMap* map, int x, int y) const {
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x),
+                   "r"(y), "r"(smem)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+    }
+  }
+  // 32 fp32 sums of each row, then given back row by row, a column for each
+  // thread: f(r, v) with row r's sum in column `lane`.
+  template <class F>
+  __device__ __forceinline__ void by_row(const float (&v)[32], int rows, F f) const {
+    open();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      put(j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+    __syncwarp();
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) {
+      float x;
+      asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(x) : "r"(piece(r, lane >> 2) + (uint32_t)(lane & 3) * 4u) : "memory");
+      f(r, x);
+    }
+    __syncwarp();
+  }
+};
 
 template <bool kARows, bool kBRows, int kQuads, int kSegment, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 1)
     pair_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairWork work,
-                     uint32_t idesc, Epi epi, int32_t* status) {
+                     uint32_t idesc, const __grid_constant__ Epi epi, int32_t* status) {
   extern __shared__ unsigned char pair_smem_raw[];
   const uint32_t base = (smem_u32(pair_smem_raw) + 1023u) & ~1023u;
   __shared__ PairBarriers bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
+  const uint32_t boxes = base + kPairStages * 2u * kPairHalf;
   const int pairs = gridDim.x / 2, mine = blockIdx.x / 2, units = work.units();
   bool broken = false;
 
@@ -247,10 +298,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
     constexpr int kCols = 256 / kQuads;
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)(part * kCols);
+    const PairBox box{boxes + (uint32_t)(warp - 4) * kPairBox, lane};
     int sums = 0;
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = pair_unit(work, u);
-      const int64_t row = (int64_t)q.tm * kPairTile + rank * 128 + 32 * quarter + lane;
+      const int64_t row = (int64_t)q.tm * kPairTile + rank * 128 + 32 * quarter;
       const int64_t col = (int64_t)q.tn * kPairTile + part * kCols;
       auto release = [&] {
         tc_fence_before();
@@ -265,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
         mbar_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
         if ((broken = __any_sync(0xffffffffu, broken))) break;
         tc_fence_after();
-        epi(q, row, col, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes});
+        epi(q, row, col, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes}, box);
         release();
       } else {
         int acc[kCols];
@@ -282,9 +334,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
           }
           release();
         }
-        if (!broken) epi(q, row, col, acc);
+        if (!broken) epi(q, row, col, acc, box);
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
   if (broken) atomicOr(status, BAKRON_DEV_TIMEOUT);
   __syncwarp();
@@ -323,14 +376,14 @@ cudaError_t pair_gemm_launch(PairOperand a, PairOperand b, int64_t K, bool bf16,
   if (e == cudaSuccess) e = map(&mb, b, kBRows);
   if (e != cudaSuccess) return e;
   auto kernel = pair_gemm_kernel<kARows, kBRows, kQuads, kSegment, Epi>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem<kQuads>());
   if (e != cudaSuccess) return e;
   const unsigned grid = 2u * (unsigned)std::min(work.units(), pair_count());
   // fp32 sums, operand types, which operands have their rows contiguous, N = 256, M = 256
   const uint32_t t = bf16 ? 1u : 0u;
   const uint32_t idesc = (1u << 4) | (t << 7) | (t << 10) | ((kARows ? 1u : 0u) << 15) | ((kBRows ? 1u : 0u) << 16) |
                          ((256u >> 3) << 17) | ((256u >> 4) << 24);
-  kernel<<<grid, 128 + 128 * kQuads, kPairSmem, stream>>>(ma, mb, work, idesc, epi, status);
+  kernel<<<grid, 128 + 128 * kQuads, pair_smem<kQuads>(), stream>>>(ma, mb, work, idesc, epi, status);
   return cudaGetLastError();
 }
 

@@ -9,7 +9,7 @@ namespace bakron {
 
 // A row-major rows x cols matrix of 8- or 16-bit elements with a row stride
 // of ld elements, copied in boxes of box_rows x box_cols into shared memory,
-// swizzled by 128 bytes (box_cols elements are then 128 bytes) or not.
+// swizzled by 128 bytes (a box row is then 128 bytes) or not.
 // The base and the stride have to be multiples of 16 bytes; what a box covers
 // outside the matrix reads as zeros.
 struct TileMap {
