@@ -434,8 +434,10 @@ int bakron_quantize_tokens(const void* X, int dtype, int64_t T, int64_t K, int64
  * Y: T x N of y_dtype (fp32, fp16 or bf16), dense, rounded once.
  * The sums over k are exact; K in 1 .. 2^17 - 1.
  * status_dev: 0, or BAKRON_DEV_TIMEOUT.
+ * Workspace (0 bytes for a few tokens): copies = 1 unless every row of codes
+ * starts on 16 bytes (base and stride), for copies that do.
  */
-size_t bakron_int8_matmul_workspace_size(int64_t T, int64_t K, int64_t N);
+size_t bakron_int8_matmul_workspace_size(int64_t T, int64_t K, int64_t N, int copies);
 int bakron_int8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_scales, const int8_t* codes, int64_t ldc,
                        const float* scales, const float* bias, int64_t T, int64_t K, int64_t N, void* Y, int y_dtype,
                        void* ws, size_t ws_bytes, int32_t* status_dev, void* stream);

@@ -129,7 +129,7 @@ def int8_matmul(X, codes, scales, x_scales=None, bias=None, dtype=None):
     if T == 0:
         return Y, status.zero_()
     lib = _lib.load()
-    ws = _workspace(lib.bakron_int8_matmul_workspace_size(T, K, N), device)
+    ws = _workspace(lib.bakron_int8_matmul_workspace_size(T, K, N, int(codes.data_ptr() % 16 + _ld(codes) % 16 > 0)), device)
     st = lib.bakron_int8_matmul(X.data_ptr(), _CODES.get(X.dtype, 3), _ld(X), _ptr(x_scales), codes.data_ptr(),
                                 _ld(codes), scales.data_ptr(), _ptr(bias), T, K, N, Y.data_ptr(), _CODES[dtype],
                                 _ptr(ws), 0 if ws is None else ws.numel(), status.data_ptr(), _stream_of(X))

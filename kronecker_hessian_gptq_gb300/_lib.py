@@ -63,7 +63,7 @@ SIGNATURES = {
     "bakron_quantize_host": (_int, [_vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _sz, _vp, _vp]),
     "bakron_quantize_noalloc": (_int, [_vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp]),
     "bakron_quantize_tokens": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
-    "bakron_int8_matmul_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "bakron_int8_matmul_workspace_size": (_sz, [_i64, _i64, _i64, _int]),
     "bakron_int8_matmul": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _sz,
                                   _vp, _vp]),
     "bakron_norm_residual": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _f32, _f32, _int, _int,

@@ -32,9 +32,9 @@ int bakron_quantize_tokens(const void* X, int dtype, int64_t T, int64_t K, int64
   return from_cuda(bakron::quantize_tokens_launch(X, dtype, T, K, ldx, codes, K, scales, (cudaStream_t)stream));
 }
 
-size_t bakron_int8_matmul_workspace_size(int64_t T, int64_t K, int64_t N) {
+size_t bakron_int8_matmul_workspace_size(int64_t T, int64_t K, int64_t N, int copies) {
   if (T < 1 || T >= kMaxRows || K < 1 || K >= kMaxK || N < 1 || N >= kMaxRows) return 0;
-  return bakron::int8_matmul_workspace_bytes(T, K, N);
+  return bakron::int8_matmul_workspace_bytes(T, K, N, copies != 0);
 }
 
 int bakron_int8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_scales, const int8_t* codes, int64_t ldc,
@@ -46,8 +46,9 @@ int bakron_int8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_s
   if (x_dtype == BAKRON_I8 ? !x_scales : (x_scales || !float_type(x_dtype) || !on_element(X, x_dtype)))
     return BAKRON_ERR_INVALID_ARG;
   if (!float_type(y_dtype) || !on_element(Y, y_dtype) || Y == X || Y == (const void*)codes) return BAKRON_ERR_INVALID_ARG;
-  if (!workspace_ok(ws, ws_bytes, bakron::int8_matmul_workspace_bytes(T, K, N))) return BAKRON_ERR_WORKSPACE;
   const bakron::Int8Matmul p{X, x_scales, x_dtype, ldx, codes, ldc, scales, bias, T, K, N, Y, y_dtype, N};
+  const bool copies = bakron::int8_matmul_needs_copies(p);
+  if (!workspace_ok(ws, ws_bytes, bakron::int8_matmul_workspace_bytes(T, K, N, copies))) return BAKRON_ERR_WORKSPACE;
   return from_cuda(bakron::int8_matmul_launch(p, ws, status_dev, (cudaStream_t)stream));
 }
 

@@ -286,11 +286,12 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* x, int6
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
 int64_t tiles(int64_t x) { return (x + kPairTile - 1) / kPairTile; }
 
 // Tokens of a piece: all, or as many whole tiles as the limits allow.
 int64_t piece_tokens(int64_t T, int64_t V, bool grad) {
-  const int64_t fit = std::max<int64_t>(1, kPieceBytes / (2 * up8(V)) / kPairTile) * kPairTile;
+  const int64_t fit = std::max<int64_t>(1, kPieceBytes / (2 * up64(V)) / kPairTile) * kPairTile;
   return std::min({T, grad ? fit : kPieceTokens, kPieceTokens});
 }
 
@@ -327,7 +328,7 @@ Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
   l.scale = take(4);
   l.stats = take(n * chunks * 8);
   if (grad) {
-    l.kept = take(n * up8(V) * 2);
+    l.kept = take(n * up64(V) * 2);
     const int p = dh_parts(n, D, V, kPlanPairs), p2 = T % n ? dh_parts(T % n, D, V, kPlanPairs) : 1;
     l.part = take(std::max(p > 1 ? (size_t)p * n * D * 4 : 0, p2 > 1 ? (size_t)p2 * (T % n) * D * 4 : 0));
     l.acc = take(n < T ? V * D * 4 : 0);
@@ -348,7 +349,7 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
   const bool grad = p.dH != nullptr;
   const bool copies = !tma_rows(p.H, p.ldh) || !tma_rows(p.W, p.ldw);
   const Layout l = layout(p.T, p.D, p.V, grad, copies);
-  const int64_t n = piece_tokens(p.T, p.V, grad), chunks = tiles(p.V) * 2, ldk = up8(p.V);
+  const int64_t n = piece_tokens(p.T, p.V, grad), chunks = tiles(p.V) * 2, ldk = up64(p.V);
   float* coef = reinterpret_cast<float*>(ws + l.coef);
   float* scale = reinterpret_cast<float*>(ws + l.scale);
   float2* stats = reinterpret_cast<float2*>(ws + l.stats);

@@ -3,93 +3,468 @@
 // for 8-bit codes c (one scale s_t for each token) and v (one scale w_o for
 // each output), and the codes of activations,
 //     s_t = fp32(max_k |x_tk| / 127), c_tk = rint(fp32(x_tk / s_t)).
-// The integer sums are exact.
+// The integer sums are exact.  Three ways, by the number of tokens:
+//
+//   up to kRowTokens   a warp takes a row of weights in 16-byte pieces and
+//                      multiplies it by every token's codes, which each block
+//                      computes for itself while its first weights are on
+//                      their way (dp4a): one launch, one read of the weights;
+//   up to kPairTokens  int8_pair.cuh: tensor cores, weights converted to fp16
+//                      inside, one read of them for 256 tokens;
+//   above              the weights converted to fp16 once for the call (3
+//                      bytes moved for each), then pair_gemm.cuh, whose
+//                      operands come ready from memory.
 #include <algorithm>
 
 #include "bakron.h"
 #include "elem.cuh"
+#include "int8_pair.cuh"
 #include "layers.h"
 #include "quantize_tokens.cuh"
-#include "tile_product.cuh"
 
 namespace bakron {
 namespace {
 
-template <class T>
-__global__ void __launch_bounds__(256) quantize_tokens_kernel(const T* X, int64_t K, int64_t ldx, int8_t* C, int64_t ldc,
-                                                              float* s) {
+constexpr int kI8 = 3;  // BAKRON_I8
+constexpr int64_t kRowTokens = 8;
+constexpr int64_t kPairTokens = 1024;
+constexpr int kRowThreads = 1024;
+constexpr int64_t kRowSmem = 200 * 1024;  // codes of the tokens that a block keeps
+
+int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
+// Tokens that the row kernel is compiled for.
+int row_tokens(int64_t T) { return T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8; }
+bool by_rows(int64_t T, int64_t K) { return T <= kRowTokens && row_tokens(T) * up16(K) <= kRowSmem; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// ------------------------------------------------------------ codes of tokens
+
+// One block for each token: codes as bytes, or as fp16 for the tensor cores
+// (then also from given bytes), and zeros for what later kernels add to.
+template <class T, class C>
+__global__ void __launch_bounds__(512) quantize_tokens_kernel(const T* X, int64_t K, int64_t ldx, bool vec, C* codes,
+                                                              int64_t ldc, float* s, uint4* zero, int64_t zeros) {
   __shared__ float red[32];
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < zeros; i += (int64_t)gridDim.x * blockDim.x)
+    zero[i] = make_uint4(0, 0, 0, 0);
   const T* x = X + (int64_t)blockIdx.x * ldx;
-  float top[1] = {0.f};
-  for (int64_t k = threadIdx.x; k < K; k += 256) top[0] = MaxOp()(fabsf(to_f32<T>(x[k])), top[0]);
-  block_reduce<1>(top, red, MaxOp());
-  const float scale = token_scale(top[0]), inv = token_inv(scale);
-  if (threadIdx.x == 0) s[blockIdx.x] = scale;
-  int8_t* c = C + (int64_t)blockIdx.x * ldc;
-  for (int64_t k = threadIdx.x; k < K; k += 256) c[k] = (int8_t)token_code(to_f32<T>(x[k]), scale, inv);
+  C* c = codes + (int64_t)blockIdx.x * ldc;
+  auto put = [&](int64_t k, int v) {
+    if constexpr (sizeof(C) == 1)
+      c[k] = (C)v;
+    else
+      c[k] = __int2half_rn(v);
+  };
+  if constexpr (sizeof(T) == 1) {
+    for (int64_t k = threadIdx.x; k < K; k += blockDim.x) put(k, x[k]);
+  } else {
+    constexpr int VEC = 16 / sizeof(T);
+    const int64_t whole = vec ? K / VEC * VEC : 0;
+    float top[1] = {0.f};
+    for (int64_t k = (int64_t)threadIdx.x * VEC; k < whole; k += (int64_t)blockDim.x * VEC) {
+      float v[VEC];
+      load_vec<T, VEC>(x + k, v);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) top[0] = MaxOp()(fabsf(v[i]), top[0]);
+    }
+    for (int64_t k = whole + threadIdx.x; k < K; k += blockDim.x) top[0] = MaxOp()(fabsf(to_f32<T>(x[k])), top[0]);
+    block_reduce<1>(top, red, MaxOp());
+    const float scale = token_scale(top[0]), inv = token_inv(scale);
+    if (threadIdx.x == 0) s[blockIdx.x] = scale;
+    for (int64_t k = (int64_t)threadIdx.x * VEC; k < whole; k += (int64_t)blockDim.x * VEC) {
+      float v[VEC];
+      load_vec<T, VEC>(x + k, v);
+      C e[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int q = token_code(v[i], scale, inv);
+        if constexpr (sizeof(C) == 1)
+          e[i] = (C)q;
+        else
+          e[i] = __int2half_rn(q);
+      }
+      if constexpr (VEC * sizeof(C) % 16 == 0) {
+        uint4 u;
+        memcpy(&u, e, 16);
+        *reinterpret_cast<uint4*>(c + k) = u;
+      } else if constexpr (VEC * sizeof(C) == 8) {
+        uint2 u;
+        memcpy(&u, e, 8);
+        *reinterpret_cast<uint2*>(c + k) = u;
+      } else {
+        uint32_t u;
+        memcpy(&u, e, 4);
+        *reinterpret_cast<uint32_t*>(c + k) = u;
+      }
+    }
+    for (int64_t k = whole + threadIdx.x; k < K; k += blockDim.x) put(k, token_code(to_f32<T>(x[k]), scale, inv));
+  }
 }
 
-struct Codes {
-  const int8_t* p;
-  int64_t ld;
-  __device__ int operator()(int64_t r, int64_t k) const { return p[r * ld + k]; }
-};
-struct CodesT {
-  const int8_t* p;
-  int64_t ld;
-  __device__ int operator()(int64_t k, int64_t r) const { return p[r * ld + k]; }
-};
+template <class C>
+cudaError_t quantize_as(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, C* codes, int64_t ldc, float* s,
+                        uint4* zero, int64_t zeros, cudaStream_t stream) {
+  const unsigned grid = (unsigned)T, threads = (unsigned)std::min<int64_t>(512, std::max<int64_t>(1, (K + 255) / 256) * 32);
+  // whole vectors in and out: rows of X on 16 bytes, rows of codes on a vector's own
+  auto vec = [&](int64_t per) {
+    return aligned_to(X, 16) && ldx % per == 0 && ldc % per == 0 && aligned_to(codes, per * sizeof(C));
+  };
+  switch (dtype) {
+    case kF32:
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const float*)X, K, ldx, vec(4), codes, ldc, s, zero, zeros);
+      break;
+    case kF16:
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __half*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros);
+      break;
+    case kBF16:
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __nv_bfloat16*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros);
+      break;
+    default:
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const int8_t*)X, K, ldx, false, codes, ldc, s, zero, zeros);
+  }
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------ a few tokens
+
+__device__ __forceinline__ float load_value(const void* p, int dtype, int64_t i) {
+  return dtype == kF32   ? static_cast<const float*>(p)[i]
+         : dtype == kF16 ? __half2float(static_cast<const __half*>(p)[i])
+                         : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_value(void* p, int dtype, int64_t i, float v) {
+  if (dtype == kF32)
+    static_cast<float*>(p)[i] = v;
+  else if (dtype == kF16)
+    static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// Codes of TT tokens (those past T are zeros) into shared memory, rows of
+// `pitch` bytes with zeros from K on; 32 / TT warps for each token.  Every
+// block does this for itself: it is a read of the tokens from the L2 cache.
+// The maximum of magnitudes is taken on their bits, which order alike, with
+// NaN above infinity.
+template <int TT, class T>
+__device__ __forceinline__ void tokens_to_shared(const Int8Matmul& p, int8_t* codes, int pitch, float* scales, uint32_t* top) {
+  constexpr int VEC = 16 / sizeof(T), kPer = kRowThreads / TT;
+  const int t = (threadIdx.x >> 5) % TT, id = (threadIdx.x >> 5) / TT * 32 + (threadIdx.x & 31);
+  const int K = (int)p.K;
+  const bool live = t < p.T;
+  const T* x = static_cast<const T*>(p.X) + (live ? t : 0) * p.ldx;
+  const int whole = reinterpret_cast<uintptr_t>(p.X) % 16 == 0 && p.ldx % VEC == 0 ? K / VEC * VEC : 0;
+  if (threadIdx.x < TT) top[threadIdx.x] = 0;
+  __syncthreads();
+  if (live) {
+    float m = 0.f;
+    for (int k = id * VEC; k < whole; k += kPer * VEC) {
+      float v[VEC];
+      load_vec<T, VEC>(x + k, v);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) m = MaxOp()(fabsf(v[i]), m);
+    }
+    for (int k = whole + id; k < K; k += kPer) m = MaxOp()(fabsf(to_f32<T>(x[k])), m);
+    m = warp_reduce(m, MaxOp());
+    if ((threadIdx.x & 31) == 0) atomicMax(top + t, __float_as_uint(m) & 0x7fffffffu);
+  }
+  __syncthreads();
+  int8_t* c = codes + t * pitch;
+  for (int k = (live ? K : 0) + id; k < pitch; k += kPer) c[k] = 0;
+  if (!live) return;
+  const float s = token_scale(__uint_as_float(top[t])), inv = token_inv(s);
+  if (id == 0) scales[t] = s;
+  for (int k = id * VEC; k < whole; k += kPer * VEC) {
+    float v[VEC];
+    load_vec<T, VEC>(x + k, v);
+#pragma unroll
+    for (int q = 0; q < VEC; q += 4) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w |= (uint32_t)(token_code(v[q + i], s, inv) & 255) << (8 * i);
+      *reinterpret_cast<uint32_t*>(c + k + q) = w;
+    }
+  }
+  for (int k = whole + id; k < K; k += kPer) c[k] = (int8_t)token_code(to_f32<T>(x[k]), s, inv);
+}
+
+// A row of weights for each `split` warps of a block (1, or where there are
+// fewer rows than warps a power of two, which share a row and join through
+// shared memory).  kVec: rows start on 16 bytes.
+template <int TT, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(Int8Matmul p, int pitch, int split) {
+  extern __shared__ __align__(16) unsigned char rows_smem[];
+  int8_t* codes = reinterpret_cast<int8_t*>(rows_smem);
+  __shared__ float scales[TT];
+  __shared__ uint32_t top[TT];
+  __shared__ int joined[32][TT];
+  constexpr int kAhead = TT <= 2 ? 8 : 4;  // 16-byte pieces of a lane in flight, 512 bytes of a row each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int K = (int)p.K, groups = (kRowThreads / 32) / split, part = warp % split;
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  const int whole = K / 16 * 16;
+  // this warp's pieces of a row: 512 bytes at lo + 512 i
+  const int pieces = (whole + 511) / 512, lo = (int)((int64_t)pieces * part / split), hi = (int)((int64_t)pieces * (part + 1) / split);
+  int64_t row = (int64_t)blockIdx.x * groups + warp / split;
+  uint4 w[kAhead];
+  auto fetch = [&](int64_t r, int first) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = (first + i) * 512 + lane * 16;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (r < p.N && first + i < hi && k < whole) w[i] = __ldcs(reinterpret_cast<const uint4*>(p.V + r * p.ldv + k));
+    }
+  };
+  if (kVec) fetch(row, lo);  // on its way while the tokens are quantized
+  if (p.x_scales) {
+    const int live = (int)p.T;
+    for (int t = 0; t < TT; ++t) {
+      const int8_t* x = static_cast<const int8_t*>(p.X) + t * p.ldx;
+      for (int k = threadIdx.x; k < pitch; k += kRowThreads) codes[t * pitch + k] = t < live && k < K ? x[k] : (int8_t)0;
+      if (threadIdx.x == 0 && t < live) scales[t] = p.x_scales[t];
+    }
+  } else if (p.x_dtype == kF32) {
+    tokens_to_shared<TT, float>(p, codes, pitch, scales, top);
+  } else if (p.x_dtype == kF16) {
+    tokens_to_shared<TT, __half>(p, codes, pitch, scales, top);
+  } else {
+    tokens_to_shared<TT, __nv_bfloat16>(p, codes, pitch, scales, top);
+  }
+  __syncthreads();
+  for (; row < p.N || split > 1; row += stride) {
+    int acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = 0;
+    if (kVec) {
+      for (int first = lo; first < hi; first += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int k = (first + i) * 512 + lane * 16;
+          if (first + i >= hi || k >= whole) continue;
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const uint4 c = *reinterpret_cast<const uint4*>(codes + t * pitch + k);
+            acc[t] = __dp4a((int)w[i].x, (int)c.x, acc[t]);
+            acc[t] = __dp4a((int)w[i].y, (int)c.y, acc[t]);
+            acc[t] = __dp4a((int)w[i].z, (int)c.z, acc[t]);
+            acc[t] = __dp4a((int)w[i].w, (int)c.w, acc[t]);
+          }
+        }
+        if (first + kAhead < hi) fetch(row, first + kAhead);
+      }
+      if (part == split - 1 && whole + lane < K && row < p.N) {
+        const int v = p.V[row * p.ldv + whole + lane];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[t] += v * codes[t * pitch + whole + lane];
+      }
+      if (split == 1) fetch(row + stride, lo);
+    } else if (row < p.N) {
+      const int8_t* v = p.V + row * p.ldv;
+      for (int k = part * 32 + lane; k < K; k += split * 32) {
+        const int x = v[k];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[t] += x * codes[t * pitch + k];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = __reduce_add_sync(0xffffffffu, acc[t]);
+    if (split > 1) {  // one row for each group of warps, and no more
+      if (lane == 0) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) joined[warp][t] = acc[t];
+      }
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          for (int q = 1; q < split; ++q) acc[t] += joined[warp + q][t];
+      }
+    }
+    if (row < p.N && part == 0 && lane == 0) {
+      const float ws = p.scales[row], bias = p.bias ? p.bias[row] : 0.f;
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        if (t < p.T) store_value(p.Y, p.y_dtype, t * p.ldy + row, fmaf((float)acc[t] * scales[t], ws, bias));
+    }
+    if (split > 1) break;
+  }
+}
+
+template <int TT>
+cudaError_t rows_launch(const Int8Matmul& p, cudaStream_t stream) {
+  const int pitch = (int)up16(p.K), sms = 2 * pair_count();
+  const bool vec = aligned_to(p.V, 16) && p.ldv % 16 == 0;
+  const int64_t warps = (int64_t)sms * (kRowThreads / 32);
+  int split = 1;
+  while (split < 32 && p.N * split * 2 <= warps && p.K >= 1024 * split) split *= 2;
+  const int64_t groups = kRowThreads / 32 / split;
+  const unsigned grid = (unsigned)std::min<int64_t>(sms, (p.N + groups - 1) / groups);
+  const int smem = TT * pitch;
+  auto kernel = vec ? int8_rows_kernel<TT, true> : int8_rows_kernel<TT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kRowThreads, smem, stream>>>(p, pitch, split);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------ many tokens
+
+// Rows of codes to fp16 rows (ldf a multiple of 64), or to aligned bytes.
+template <class C>
+__global__ void __launch_bounds__(256) codes_kernel(const int8_t* V, int64_t ldv, int64_t K, C* F, int64_t ldf) {
+  const int64_t row = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
+  if (k >= K) return;
+  const int8_t* v = V + row * ldv + k;
+  C* f = F + row * ldf + k;
+  alignas(16) int8_t e[16];
+  if (reinterpret_cast<uintptr_t>(v) % 16 == 0 && k + 16 <= K) {
+    *reinterpret_cast<uint4*>(e) = __ldcs(reinterpret_cast<const uint4*>(v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) e[i] = k + i < K ? v[i] : (int8_t)0;
+  }
+  uint32_t w[4];
+  memcpy(w, e, 16);
+  if constexpr (sizeof(C) == 1) {
+    *reinterpret_cast<uint4*>(f) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) i8_to_f16(w[i], h[2 * i], h[2 * i + 1]);
+    reinterpret_cast<uint4*>(f)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4*>(f)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
+template <class C>
+void convert_codes(const int8_t* V, int64_t ldv, int64_t N, int64_t K, C* F, int64_t ldf, cudaStream_t stream) {
+  const int64_t y = 32768;
+  for (int64_t r = 0; r < N; r += y)
+    codes_kernel<C><<<dim3((unsigned)((K + 4095) / 4096), (unsigned)std::min(y, N - r)), 256, 0, stream>>>(
+        V + r * ldv, ldv, K, F + r * ldf, ldf);
+}
+
+// Scales a tile's exact sums and sends them out in whole lines.
 template <class T>
-struct PutScaled {
-  const float *s, *w, *b;
+struct ScaledEpilogue {
+  int64_t tokens, outputs;
+  const float *x_scales, *w_scales, *bias;
   T* y;
-  int64_t ld;
-  __device__ void operator()(int64_t t, int64_t o, int v) const {
-    y[t * ld + o] = from_f32<T>(fmaf((float)v * s[t], w[o], b ? b[o] : 0.f));
+  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, const int (&acc)[64],
+                                             const PairBox& box) const {
+    if (row0 >= tokens) return;
+    const int here = (int)(tokens - row0 < 32 ? tokens - row0 : 32);
+    const float s = box.lane < here ? x_scales[row0 + box.lane] : 0.f;
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      if (col + c >= outputs) break;
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = (float)acc[c + i] * s;
+      const int64_t o = col + c + box.lane;
+      const bool in = o < outputs;
+      const float w = in ? w_scales[o] : 0.f, b = in && bias ? bias[o] : 0.f;
+      T* to = y + row0 * outputs + o;
+      box.by_row(v, here, [&](int r, float x) {
+        if (in) to[r * outputs] = from_f32<T>(fmaf(x, w, b));
+      });
+    }
   }
 };
 
+struct Layout {
+  size_t codes, scales, zeros, arrived, sums, weights, end_zeros, bytes;
+  I8Work work;
+};
+constexpr int kPlanPairs = 76;
+
+// copies: with room for the weights in aligned rows.
+Layout layout(int64_t T, int64_t K, int64_t N, bool copies) {
+  Layout l = {};
+  if (by_rows(T, K)) return l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  l.codes = take(T * up64(K) * 2);
+  l.scales = take(T * 4);
+  if (T <= kPairTokens) {
+    l.work = i8_work(T, K, N, kPlanPairs);
+    l.zeros = at;
+    l.arrived = take(i8_slices(l.work) * 4);
+    l.sums = take(l.work.parts > 1 ? T * N * 4 : 0);
+    l.end_zeros = l.work.parts > 1 ? at : l.zeros;
+    if (copies) l.weights = take(N * up16(K));
+  } else {
+    l.weights = take(N * up64(K) * 2);
+  }
+  l.bytes = at;
+  return l;
+}
+
+bool tma_codes(const Int8Matmul& p) { return aligned_to(p.V, 16) && p.ldv % 16 == 0; }
+
 template <class T>
-void product(const Int8Matmul& p, const int8_t* C, int64_t ldc, const float* s, cudaStream_t stream) {
-  const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.T + 63) / 64));
-  tile_product_kernel<int><<<grid, 256, 0, stream>>>(p.T, p.N, p.K, Codes{C, ldc}, CodesT{p.V, p.ldv},
-                                                     PutScaled<T>{s, p.scales, p.bias, static_cast<T*>(p.Y), p.ldy});
+cudaError_t batch(const Int8Matmul& p, const Layout& l, char* ws, int32_t* status, cudaStream_t stream) {
+  __half* codes = reinterpret_cast<__half*>(ws + l.codes);
+  float* own_scales = reinterpret_cast<float*>(ws + l.scales);
+  const float* s = p.x_scales ? p.x_scales : own_scales;
+  const int64_t ldc = up64(p.K);
+  cudaError_t e = quantize_as<__half>(p.X, p.x_scales ? kI8 : p.x_dtype, p.T, p.K, p.ldx, codes, ldc, own_scales,
+                                      reinterpret_cast<uint4*>(ws + l.zeros), (int64_t)(l.end_zeros - l.zeros) / 16, stream);
+  if (e != cudaSuccess) return e;
+  if (p.T <= kPairTokens) {
+    const int8_t* V = p.V;
+    int64_t ldv = p.ldv;
+    if (!tma_codes(p)) {
+      int8_t* copy = reinterpret_cast<int8_t*>(ws + l.weights);
+      convert_codes<int8_t>(V, ldv, p.N, p.K, copy, up16(p.K), stream);
+      V = copy, ldv = up16(p.K);
+    }
+    const I8Out<T> out{p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y), reinterpret_cast<int32_t*>(ws + l.sums),
+                       reinterpret_cast<uint32_t*>(ws + l.arrived)};
+    return int8_pair_launch<T>(V, ldv, codes, ldc, p.K, l.work, out, status, stream);
+  }
+  __half* weights = reinterpret_cast<__half*>(ws + l.weights);
+  convert_codes<__half>(p.V, p.ldv, p.N, p.K, weights, ldc, stream);
+  const PairWork work{(int)((p.T + 255) / 256), (int)((p.N + 255) / 256), 16, (int)((p.K + kPairK - 1) / kPairK), 1};
+  return pair_gemm_launch<false, false, 4, kI8Steps>(PairOperand{codes, p.T, ldc}, PairOperand{weights, p.N, ldc}, p.K, false,
+                                                     work,
+                                                     ScaledEpilogue<T>{p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y)},
+                                                     status, stream);
 }
 
 }  // namespace
 
 cudaError_t quantize_tokens_launch(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, int8_t* C, int64_t ldc,
                                    float* s, cudaStream_t stream) {
-  const unsigned grid = (unsigned)T;
-  switch (dtype) {
-    case kF32: quantize_tokens_kernel<<<grid, 256, 0, stream>>>((const float*)X, K, ldx, C, ldc, s); break;
-    case kF16: quantize_tokens_kernel<<<grid, 256, 0, stream>>>((const __half*)X, K, ldx, C, ldc, s); break;
-    default: quantize_tokens_kernel<<<grid, 256, 0, stream>>>((const __nv_bfloat16*)X, K, ldx, C, ldc, s);
-  }
-  return cudaGetLastError();
+  return quantize_as<int8_t>(X, dtype, T, K, ldx, C, ldc, s, nullptr, 0, stream);
 }
 
-size_t int8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N) { return (size_t)(T * K + 255) / 256 * 256 + T * 4; }
+size_t int8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies) { return layout(T, K, N, copies).bytes; }
+bool int8_matmul_needs_copies(const Int8Matmul& p) { return !tma_codes(p); }
 
 cudaError_t int8_matmul_launch(const Int8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream) {
   cudaError_t e = cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream);
   if (e != cudaSuccess) return e;
-  const int8_t* C = static_cast<const int8_t*>(p.X);
-  int64_t ldc = p.ldx;
-  const float* s = p.x_scales;
-  if (!s) {
-    int8_t* codes = static_cast<int8_t*>(ws);
-    float* scales = reinterpret_cast<float*>(codes + (p.T * p.K + 255) / 256 * 256);
-    e = quantize_tokens_launch(p.X, p.x_dtype, p.T, p.K, p.ldx, codes, p.K, scales, stream);
-    if (e != cudaSuccess) return e;
-    C = codes, ldc = p.K, s = scales;
+  if (by_rows(p.T, p.K)) {
+    switch (row_tokens(p.T)) {
+      case 1: return rows_launch<1>(p, stream);
+      case 2: return rows_launch<2>(p, stream);
+      case 4: return rows_launch<4>(p, stream);
+      default: return rows_launch<8>(p, stream);
+    }
   }
+  const Layout l = layout(p.T, p.K, p.N, !tma_codes(p));
+  char* at = static_cast<char*>(ws);
   switch (p.y_dtype) {
-    case kF32: product<float>(p, C, ldc, s, stream); break;
-    case kF16: product<__half>(p, C, ldc, s, stream); break;
-    default: product<__nv_bfloat16>(p, C, ldc, s, stream);
+    case kF32: return batch<float>(p, l, at, status_dev, stream);
+    case kF16: return batch<__half>(p, l, at, status_dev, stream);
+    default: return batch<__nv_bfloat16>(p, l, at, status_dev, stream);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace bakron

@@ -30,7 +30,10 @@ struct Int8Matmul {
   int y_dtype;
   int64_t ldy;
 };
-size_t int8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N);
+// copies: with room for the weights' codes in aligned rows, which
+// int8_matmul_needs_copies() tells the need of.
+size_t int8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies);
+bool int8_matmul_needs_copies(const Int8Matmul& p);
 cudaError_t int8_matmul_launch(const Int8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream);
 
 // norm_residual.cu

@@ -3,7 +3,7 @@
 //
 // A cluster of two blocks computes one 256 x 256 tile at a time: each block
 // keeps 128 rows of A and 128 rows of B for every 64 of K in shared memory
-// (six stages of 32 KB, filled by TMA with the 128-byte swizzle), the even
+// (five or six stages of 32 KB, filled by TMA with the 128-byte swizzle), the even
 // block's MMA thread issues tcgen05.mma with cta_group::2 (M = N = 256,
 // K = 16), which reads both blocks' operands, and each block's tensor memory
 // receives 128 rows of the sums.  Two sums of 256 columns take turns, so that
@@ -30,12 +30,14 @@ namespace bakron {
 
 constexpr int kPairTile = 256;    // rows and columns of a pair's tile
 constexpr int kPairK = 64;        // K of a stage: 128 bytes
-constexpr int kPairStages = 6;
 constexpr int kPairHalf = 128 * kPairK * 2;        // one block's part of an operand's stage: 16 KB
 constexpr uint32_t kPairStageTx = 4u * kPairHalf;  // bytes of a stage in both blocks
 constexpr int kPairBox = 4096;  // shared memory of an epilogue warp: 32 rows of 128 bytes
+// Epilogue warps are 4 kQuads; more of them leave room for fewer stages.
 template <int kQuads>
-constexpr int pair_smem() { return kPairStages * 2 * kPairHalf + 4 * kQuads * kPairBox + 1024; }
+__host__ __device__ constexpr int pair_stages() { return kQuads > 2 ? 5 : 6; }
+template <int kQuads>
+constexpr int pair_smem() { return pair_stages<kQuads>() * 2 * kPairHalf + 4 * kQuads * kPairBox + 1024; }
 
 // Units of a product: unit u = (tile, part of K); tiles run down groups of
 // `group` tile rows first, so that what runs at the same time shares operands
@@ -77,6 +79,12 @@ __device__ __forceinline__ uint32_t in_even_block(const void* p) {
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 // A box into this block's shared memory; its bytes count on the even block's barrier.
 __device__ __forceinline__ void pair_copy(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
@@ -131,7 +139,7 @@ template <bool kRows>
 __host__ __device__ constexpr uint32_t pair_kstep() { return kRows ? 2048u : 32u; }
 
 struct PairBarriers {
-  uint64_t full[kPairStages], empty[kPairStages], sum_full[2], sum_empty[2];
+  uint64_t full[6], empty[6], sum_full[2], sum_empty[2];
   uint32_t tmem;
 };
 
@@ -202,6 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
   __shared__ PairBarriers bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
+  constexpr int kPairStages = pair_stages<kQuads>();
   const uint32_t boxes = base + kPairStages * 2u * kPairHalf;
   const int pairs = gridDim.x / 2, mine = blockIdx.x / 2, units = work.units();
   bool broken = false;
@@ -227,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
 
-  if (warp == 0 && lane == 0) {  // copies: 16 KB of A and of B for each stage, in both blocks
+  if (warp == 0) {  // copies: 16 KB of A and of B for each stage, in both blocks
     int n = 0;
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = pair_unit(work, u);
@@ -235,25 +244,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
       for (int k = q.k0; k < q.k1; ++k, ++n) {
         const int slot = n % kPairStages;
         if (n >= kPairStages) mbar_wait(&bar.empty[slot], (uint32_t)(n / kPairStages - 1) & 1u, broken);
-        if (broken) break;
+        if ((broken = __any_sync(0xffffffffu, broken))) break;
         const uint32_t full = in_even_block(&bar.full[slot]);
-        if (rank == 0)
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(&bar.full[slot])),
-                       "r"(kPairStageTx)
-                       : "memory");
         const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
-        if constexpr (kARows) {
-          pair_copy(a, &map_a, a0, k * kPairK, full);
-          pair_copy(a + 8192, &map_a, a0 + 64, k * kPairK, full);
-        } else {
-          pair_copy(a, &map_a, k * kPairK, a0, full);
+        if (elect_one()) {
+          if (rank == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(&bar.full[slot])),
+                         "r"(kPairStageTx)
+                         : "memory");
+          if constexpr (kARows) {
+            pair_copy(a, &map_a, a0, k * kPairK, full);
+            pair_copy(a + 8192, &map_a, a0 + 64, k * kPairK, full);
+          } else {
+            pair_copy(a, &map_a, k * kPairK, a0, full);
+          }
+          if constexpr (kBRows) {
+            pair_copy(b, &map_b, b0, k * kPairK, full);
+            pair_copy(b + 8192, &map_b, b0 + 64, k * kPairK, full);
+          } else {
+            pair_copy(b, &map_b, k * kPairK, b0, full);
+          }
         }
-        if constexpr (kBRows) {
-          pair_copy(b, &map_b, b0, k * kPairK, full);
-          pair_copy(b + 8192, &map_b, b0 + 64, k * kPairK, full);
-        } else {
-          pair_copy(b, &map_b, k * kPairK, b0, full);
-        }
+        __syncwarp();
       }
     }
     // No block leaves while copies into it, or arrivals at its barriers, are
@@ -266,7 +278,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
       else if (rank == 0)
         mbar_wait(&bar.full[i % kPairStages], (uint32_t)(i / kPairStages) & 1u, late);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {  // products
+  } else if (warp == 1 && rank == 0) {  // products
+    // The whole warp walks the loop and one elected thread issues: with the
+    // warp converged the descriptors stay in uniform registers (under a
+    // branch on the lane a step of K took 670 cycles, so 590).
     int n = 0, sums = 0;
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = pair_unit(work, u);
@@ -280,18 +295,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
         }
         const int slot = n % kPairStages;
         mbar_wait(&bar.full[slot], (uint32_t)(n / kPairStages) & 1u, broken);
-        if (broken) break;
+        if ((broken = __any_sync(0xffffffffu, broken))) break;
         tc_fence_after();
         const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
+        const bool sum_done = k + 1 == q.k1 || (kSegment && in_segment == kSegment - 1);
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < kPairK / 16; ++j)
-          pair_mma(acc, pair_desc<kARows>(a + j * pair_kstep<kARows>()), pair_desc<kBRows>(b + j * pair_kstep<kBRows>()),
-                   idesc, (in_segment > 0 || j > 0) ? 1u : 0u);
-        pair_commit(&bar.empty[slot]);
-        if (k + 1 == q.k1 || (kSegment && in_segment == kSegment - 1)) {
-          pair_commit(&bar.sum_full[sums & 1]);
-          ++sums;
+          for (int j = 0; j < kPairK / 16; ++j)
+            pair_mma(acc, pair_desc<kARows>(a + j * pair_kstep<kARows>()),
+                     pair_desc<kBRows>(b + j * pair_kstep<kBRows>()), idesc, (in_segment > 0 || j > 0) ? 1u : 0u);
+          pair_commit(&bar.empty[slot]);
+          if (sum_done) pair_commit(&bar.sum_full[sums & 1]);
         }
+        __syncwarp();
+        if (sum_done) ++sums;
       }
     }
   } else if (warp >= 4) {  // epilogue: 32 rows of the block and 256 / kQuads columns for each warp

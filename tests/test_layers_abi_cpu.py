@@ -37,16 +37,18 @@ def test_quantize_tokens(lib):
 
 
 def test_int8_matmul(lib):
-    need = lib.bakron_int8_matmul_workspace_size(4, 64, 16)
-    assert need > 0
-    for bad in ((0, 64, 16), (4, 0, 16), (4, 64, 0), (4, 1 << 17, 16)):
-        assert lib.bakron_int8_matmul_workspace_size(*bad) == 0
-    good = dict(X=at(0x1000), xt=BF16, ldx=64, xs=None, codes=at(0x2000), ldc=64, scales=at(0x3000), bias=None, T=4, K=64,
+    size = lib.bakron_int8_matmul_workspace_size
+    need, copies = size(40, 64, 16, 0), size(40, 64, 16, 1)
+    assert 0 < need < copies
+    for bad in ((0, 64, 16, 0), (40, 0, 16, 0), (40, 64, 0, 0), (40, 1 << 17, 16, 0)):
+        assert size(*bad) == 0
+    good = dict(X=at(0x1000), xt=BF16, ldx=64, xs=None, codes=at(0x2000), ldc=64, scales=at(0x3000), bias=None, T=40, K=64,
                 N=16, Y=at(0x5000), yt=BF16, ws=at(0x100000), n=need, status=at(0x6000), stream=None)
     call = lib.bakron_int8_matmul
     refused(call, good, X=[None, at(0x1001)], xt=[I8, 9], ldx=[63], xs=[at(0x4000)], codes=[None], ldc=[63], scales=[None],
             T=[0], K=[0, 1 << 17], N=[0], Y=[None, at(0x5001), at(0x1000), at(0x2000)], yt=[I8, -1], status=[None])
     refused(call, good, 4, ws=[None, at(0x100010)], n=[need - 1])
+    refused(call, {**good, "ldc": 65}, 4, n=[need, copies - 1])
 
 
 def test_norm_residual(lib):
