@@ -51,25 +51,6 @@ struct I8Barriers {
   uint32_t tmem;
 };
 
-// As mbar_wait, for what the other block of the pair has written as well.
-__device__ __forceinline__ void pair_wait(uint64_t* mbar, uint32_t parity, bool& broken) {
-  if (broken) return;
-  const uint32_t at = smem_u32(mbar);
-  const long long t0 = clock64();
-  uint32_t done = 0;
-  while (!done) {
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (!done && clock64() - t0 > (1ll << 28)) {
-      broken = true;
-      return;
-    }
-  }
-}
-
 // Four 8-bit integers as fp16: with the sign bit flipped a byte b is the
 // value + 128, and 0x6400 + b is the fp16 number 1024 + b, exactly.
 __device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -122,13 +103,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   };
 
   if (warp == 0) {  // copies: the weights' bytes and half of the tokens' codes
-    int n = 0, tm, tn, k0, k1;
+    int tm, tn, k0, k1;
+    Ring ring;
     for (int u = mine; u < units && !broken; u += pairs) {
       unit(u, tm, tn, k0, k1);
       const int o0 = tm * 256 + (int)rank * 128, t0 = tn * work.nt + (int)rank * (work.nt / 2);
-      for (int k = k0; k < k1; ++k, ++n) {
-        const int slot = n % stages;
-        if (n >= stages) mbar_wait(&bar.empty[slot], (uint32_t)(n / stages - 1) & 1u, broken);
+      for (int k = k0; k < k1; ++k, ring.next(stages)) {
+        const int slot = ring.slot;
+        if (ring.round) ring_wait(&bar.empty[slot], ring.turn ^ 1u, broken);
         if ((broken = __any_sync(0xffffffffu, broken))) break;
         const uint32_t raw = base + (uint32_t)slot * stage, x = raw + kI8Raw + kI8A;
         const uint32_t ready = in_even_block(&bar.ready[slot]);
@@ -150,27 +132,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       }
     }
     // See pair_gemm_kernel: nothing is on its way into a block that leaves.
-    for (int i = n > stages ? n - stages : 0; i < n; ++i) {
+    for (int i = 0; i < stages; ++i, ring.next(stages)) {
+      if (!ring.round) continue;  // this stage's first use would come here
       bool late = false;
       if (!broken) {
-        mbar_wait(&bar.empty[i % stages], (uint32_t)(i / stages) & 1u, broken);
+        ring_wait(&bar.empty[ring.slot], ring.turn ^ 1u, broken);
       } else {
-        mbar_wait(&bar.raw[i % stages], (uint32_t)(i / stages) & 1u, late);
-        if (rank == 0) mbar_wait(&bar.ready[i % stages], (uint32_t)(i / stages) & 1u, late);
+        ring_wait(&bar.raw[ring.slot], ring.turn ^ 1u, late);
+        if (rank == 0) ring_wait(&bar.ready[ring.slot], ring.turn ^ 1u, late);
       }
     }
   } else if (warp == 1 && rank == 0) {  // products
     // fp32 sums of fp16 products, both with K contiguous, M = 256, N = nt
     const uint32_t idesc = (1u << 4) | ((uint32_t)(work.nt >> 3) << 17) | ((256u >> 4) << 24);
-    int n = 0, sums = 0, tm, tn, k0, k1;
+    int sums = 0, tm, tn, k0, k1;
+    Ring ring;
     for (int u = mine; u < units && !broken; u += pairs, ++sums) {
       unit(u, tm, tn, k0, k1);
       const uint32_t acc = tmem + (uint32_t)(sums & 1) * 256u;
-      if (sums >= 2) mbar_wait(&bar.sum_empty[sums & 1], (uint32_t)(sums / 2 - 1) & 1u, broken);
+      if (sums >= 2) ring_wait(&bar.sum_empty[sums & 1], (uint32_t)(sums / 2 - 1) & 1u, broken);
       tc_fence_after();
-      for (int k = k0; k < k1; ++k, ++n) {
-        const int slot = n % stages;
-        pair_wait(&bar.ready[slot], (uint32_t)(n / stages) & 1u, broken);
+      for (int k = k0; k < k1; ++k, ring.next(stages)) {
+        const int slot = ring.slot;
+        ring_wait(&bar.ready[ring.slot], ring.turn, broken);
         if ((broken = __any_sync(0xffffffffu, broken))) break;
         tc_fence_after();
         const uint32_t a = base + (uint32_t)slot * stage + kI8Raw, b = a + kI8A;
@@ -187,12 +171,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   } else if (warp >= 4 && warp < 12) {  // bytes to fp16: 32 rows of every second stage for each warp
     const int group = (warp - 4) >> 2, quarter = (warp - 4) & 3;
     int n = 0, tm, tn, k0, k1;
+    Ring ring;
     for (int u = mine; u < units && !broken; u += pairs) {
       unit(u, tm, tn, k0, k1);
-      for (int k = k0; k < k1; ++k, ++n) {
+      for (int k = k0; k < k1; ++k, ++n, ring.next(stages)) {
         if ((n & 1) != group) continue;
-        const int slot = n % stages;
-        mbar_wait(&bar.raw[slot], (uint32_t)(n / stages) & 1u, broken);
+        const int slot = ring.slot;
+        ring_wait(&bar.raw[slot], ring.turn, broken);
         if ((broken = __any_sync(0xffffffffu, broken))) break;
         const uint32_t raw = base + (uint32_t)slot * stage, a = raw + kI8Raw;
         uint32_t w[4][4];
@@ -214,11 +199,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
                          "r"(h[4 * q]), "r"(h[4 * q + 1]), "r"(h[4 * q + 2]), "r"(h[4 * q + 3])
                          : "memory");
         }
+        // Each thread's fence makes what it wrote visible to the MMAs before
+        // the arrival; a release of cluster scope on top of it would stall the
+        // warp for half a microsecond in every stage.
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
         if (lane == 0)
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.ready[slot]))
-                       : "memory");
+          asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.ready[slot])) : "memory");
       }
     }
   } else if (warp >= 12) {  // epilogue: 32 outputs (lanes) and half of the tokens for each warp
@@ -228,7 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     int sums = 0, tm, tn, k0, k1;
     for (int u = mine; u < units && !broken; u += pairs, ++sums) {
       unit(u, tm, tn, k0, k1);
-      mbar_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
+      ring_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
       if ((broken = __any_sync(0xffffffffu, broken))) break;
       tc_fence_after();
       const int64_t o = (int64_t)tm * 256 + rank * 128 + 32 * quarter + lane;
@@ -255,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.sum_empty[sums & 1]))
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.sum_empty[sums & 1]))
                      : "memory");
       if (work.parts == 1) continue;
       // The last of a slice's parts to arrive reads the joined sums.

@@ -80,6 +80,27 @@ __device__ __forceinline__ uint32_t in_even_block(const void* p) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
+// Place in a ring of stages: the slot, the parity of its barriers in this
+// round, and whether the slot has been used before.
+struct Ring {
+  int slot = 0;
+  uint32_t turn = 0;
+  bool round = false;
+  __device__ __forceinline__ void next(int stages) {
+    if (++slot == stages) slot = 0, turn ^= 1u, round = true;
+  }
+};
+// As mbar_wait, with a first look that costs no clock reading: the loops that
+// feed the tensor cores pass here once for every step of K.
+__device__ __forceinline__ void ring_wait(uint64_t* mbar, uint32_t parity, bool& broken) {
+  if (broken) return;
+  uint32_t done = 0;
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(done)
+               : "r"(smem_u32(mbar)), "r"(parity)
+               : "memory");
+  if (!done) mbar_wait(mbar, parity, broken);
+}
 // One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -237,13 +258,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
   const uint32_t tmem = bar.tmem;
 
   if (warp == 0) {  // copies: 16 KB of A and of B for each stage, in both blocks
-    int n = 0;
+    Ring ring;
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = pair_unit(work, u);
       const int a0 = q.tm * kPairTile + (int)rank * 128, b0 = q.tn * kPairTile + (int)rank * 128;
-      for (int k = q.k0; k < q.k1; ++k, ++n) {
-        const int slot = n % kPairStages;
-        if (n >= kPairStages) mbar_wait(&bar.empty[slot], (uint32_t)(n / kPairStages - 1) & 1u, broken);
+      for (int k = q.k0; k < q.k1; ++k, ring.next(kPairStages)) {
+        const int slot = ring.slot;
+        if (ring.round) ring_wait(&bar.empty[slot], ring.turn ^ 1u, broken);
         if ((broken = __any_sync(0xffffffffu, broken))) break;
         const uint32_t full = in_even_block(&bar.full[slot]);
         const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
@@ -271,30 +292,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
     // No block leaves while copies into it, or arrivals at its barriers, are
     // on their way: every stage's last use has been released by the MMAs (or,
     // after a wait that ran out, has at least landed).
-    for (int i = n > kPairStages ? n - kPairStages : 0; i < n; ++i) {
+    for (int i = 0; i < kPairStages; ++i, ring.next(kPairStages)) {
+      if (!ring.round) continue;  // this stage's first use would come here
       bool late = false;
       if (!broken)
-        mbar_wait(&bar.empty[i % kPairStages], (uint32_t)(i / kPairStages) & 1u, broken);
+        ring_wait(&bar.empty[ring.slot], ring.turn ^ 1u, broken);
       else if (rank == 0)
-        mbar_wait(&bar.full[i % kPairStages], (uint32_t)(i / kPairStages) & 1u, late);
+        ring_wait(&bar.full[ring.slot], ring.turn ^ 1u, late);
     }
   } else if (warp == 1 && rank == 0) {  // products
     // The whole warp walks the loop and one elected thread issues: with the
     // warp converged the descriptors stay in uniform registers (under a
     // branch on the lane a step of K took 670 cycles, so 590).
-    int n = 0, sums = 0;
+    int sums = 0;
+    Ring ring;
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = pair_unit(work, u);
       uint32_t acc = 0;
-      for (int k = q.k0; k < q.k1; ++k, ++n) {
+      for (int k = q.k0; k < q.k1; ++k, ring.next(kPairStages)) {
         const int in_segment = kSegment ? (k - q.k0) % kSegment : k - q.k0;
         if (in_segment == 0) {  // the next of the two sums, once the epilogue has read it
           acc = tmem + (uint32_t)(sums & 1) * 256u;
-          if (sums >= 2) mbar_wait(&bar.sum_empty[sums & 1], (uint32_t)(sums / 2 - 1) & 1u, broken);
+          if (sums >= 2) ring_wait(&bar.sum_empty[sums & 1], (uint32_t)(sums / 2 - 1) & 1u, broken);
           tc_fence_after();
         }
-        const int slot = n % kPairStages;
-        mbar_wait(&bar.full[slot], (uint32_t)(n / kPairStages) & 1u, broken);
+        const int slot = ring.slot;
+        ring_wait(&bar.full[slot], ring.turn, broken);
         if ((broken = __any_sync(0xffffffffu, broken))) break;
         tc_fence_after();
         const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
@@ -331,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
         ++sums;
       };
       if constexpr (kSegment == 0) {
-        mbar_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
+        ring_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
         if ((broken = __any_sync(0xffffffffu, broken))) break;
         tc_fence_after();
         epi(q, row, col, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes}, box);
@@ -339,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
       } else {
         int acc[kCols];
         for (int k = q.k0; k < q.k1; k += kSegment) {
-          mbar_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
+          ring_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
           if ((broken = __any_sync(0xffffffffu, broken))) break;
           tc_fence_after();
 #pragma unroll
