@@ -10,7 +10,7 @@
 //                      computes for itself while its first weights are on
 //                      their way (dp4a): one launch, one read of the weights;
 //   up to kPairTokens  int8_pair.cuh: tensor cores, weights converted to fp16
-//                      inside, one read of them for 256 tokens;
+//                      inside, one read of them for 128 tokens;
 //   above              the weights converted to fp16 once for the call (3
 //                      bytes moved for each), then pair_gemm.cuh, whose
 //                      operands come ready from memory.
@@ -395,8 +395,8 @@ Layout layout(int64_t T, int64_t K, int64_t N, bool copies) {
     l.work = i8_work(T, K, N, kPlanPairs);
     l.zeros = at;
     l.arrived = take(i8_slices(l.work) * 4);
-    l.sums = take(l.work.parts > 1 ? T * N * 4 : 0);
-    l.end_zeros = l.work.parts > 1 ? at : l.zeros;
+    l.sums = take(l.work.shared ? T * N * 4 : 0);
+    l.end_zeros = l.work.shared ? at : l.zeros;
     if (copies) l.weights = take(N * up16(K));
   } else {
     l.weights = take(N * up64(K) * 2);
@@ -431,7 +431,7 @@ cudaError_t batch(const Int8Matmul& p, const Layout& l, char* ws, int32_t* statu
   __half* weights = reinterpret_cast<__half*>(ws + l.weights);
   convert_codes<__half>(p.V, p.ldv, p.N, p.K, weights, ldc, stream);
   const PairWork work{(int)((p.T + 255) / 256), (int)((p.N + 255) / 256), 16, (int)((p.K + kPairK - 1) / kPairK), 1};
-  return pair_gemm_launch<false, false, 4, kI8Steps>(PairOperand{codes, p.T, ldc}, PairOperand{weights, p.N, ldc}, p.K, false,
+  return pair_gemm_launch<false, false, 4, 1024 / kPairK>(PairOperand{codes, p.T, ldc}, PairOperand{weights, p.N, ldc}, p.K, false,
                                                      work,
                                                      ScaledEpilogue<T>{p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y)},
                                                      status, stream);

@@ -90,16 +90,41 @@ struct Ring {
     if (++slot == stages) slot = 0, turn ^= 1u, round = true;
   }
 };
-// As mbar_wait, with a first look that costs no clock reading: the loops that
-// feed the tensor cores pass here once for every step of K.
-__device__ __forceinline__ void ring_wait(uint64_t* mbar, uint32_t parity, bool& broken) {
-  if (broken) return;
-  uint32_t done = 0;
+// A converged warp's wait for the phase of the given parity, for at most about
+// 0.1 s (2^28 cycles); afterwards `broken` is set for the whole warp, and
+// later waits return at once.  Every branch is taken by a vote, so that the
+// compiler knows the warp to stay together: the descriptors of the MMAs then
+// live in uniform registers (45 cycles to issue one, else 110).
+__device__ __forceinline__ uint32_t peek(uint64_t* mbar, uint32_t parity) {
+  uint32_t done;
   asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
                : "=r"(done)
                : "r"(smem_u32(mbar)), "r"(parity)
                : "memory");
-  if (!done) mbar_wait(mbar, parity, broken);
+  return done;
+}
+// A look that does not wait at all (try_wait may hold a thread for a while).
+__device__ __forceinline__ uint32_t glance(uint64_t* mbar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(done)
+               : "r"(smem_u32(mbar)), "r"(parity)
+               : "memory");
+  return done;
+}
+// `seen` is an earlier look at the same phase, whose latency other work has covered.
+__device__ __forceinline__ void warp_wait(uint64_t* mbar, uint32_t parity, bool& broken, uint32_t seen) {
+  if (broken || __all_sync(0xffffffffu, seen)) return;
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, peek(mbar, parity))) {
+    if (__any_sync(0xffffffffu, clock64() - t0 > (1ll << 28))) {
+      broken = true;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void warp_wait(uint64_t* mbar, uint32_t parity, bool& broken) {
+  warp_wait(mbar, parity, broken, peek(mbar, parity));
 }
 // One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -123,11 +148,14 @@ __device__ __forceinline__ void pair_commit(uint64_t* mbar) {
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The operands' descriptors come as their low words, which hold the address in
+// units of 16 bytes, and the high words that all steps share.
+__device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high, uint32_t idesc,
+                                         uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n.reg .pred p;\n.reg .b64 da, db;\nmov.b64 da, {%1, %2};\nmov.b64 db, {%3, %4};\nsetp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(idesc), "r"(acc));
 }
 // 32 consecutive columns of this warp's 32 tensor-memory lanes; complete after tmem_wait_ld().
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -151,13 +179,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 // 64 rows by 8 of K take 1024 bytes, the next 8 of K follow (stride offset),
 // the next 64 rows are 8 KB on (leading offset).
 template <bool kRows>
-__device__ __forceinline__ uint64_t pair_desc(uint32_t saddr) {
-  const uint64_t lbo = kRows ? 8192 >> 4 : 1, sbo = 1024 >> 4;
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (lbo << 16) | (sbo << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-// Bytes from one K = 16 step to the next within a stage.
+__device__ __forceinline__ uint32_t pair_desc_low(uint32_t saddr) { return (saddr >> 4) | ((kRows ? 8192u >> 4 : 1u) << 16); }
+constexpr uint32_t kPairDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride offset, version, swizzle
+// Units of 16 bytes from one K = 16 step to the next within a stage.
 template <bool kRows>
-__host__ __device__ constexpr uint32_t pair_kstep() { return kRows ? 2048u : 32u; }
+__host__ __device__ constexpr uint32_t pair_kstep() { return kRows ? 2048u >> 4 : 32u >> 4; }
 
 struct PairBarriers {
   uint64_t full[6], empty[6], sum_full[2], sum_empty[2];
@@ -264,8 +290,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
       const int a0 = q.tm * kPairTile + (int)rank * 128, b0 = q.tn * kPairTile + (int)rank * 128;
       for (int k = q.k0; k < q.k1; ++k, ring.next(kPairStages)) {
         const int slot = ring.slot;
-        if (ring.round) ring_wait(&bar.empty[slot], ring.turn ^ 1u, broken);
-        if ((broken = __any_sync(0xffffffffu, broken))) break;
+        if (ring.round) warp_wait(&bar.empty[slot], ring.turn ^ 1u, broken);
+        if (broken) break;
         const uint32_t full = in_even_block(&bar.full[slot]);
         const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
         if (elect_one()) {
@@ -296,9 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
       if (!ring.round) continue;  // this stage's first use would come here
       bool late = false;
       if (!broken)
-        ring_wait(&bar.empty[ring.slot], ring.turn ^ 1u, broken);
+        warp_wait(&bar.empty[ring.slot], ring.turn ^ 1u, broken);
       else if (rank == 0)
-        ring_wait(&bar.full[ring.slot], ring.turn ^ 1u, late);
+        warp_wait(&bar.full[ring.slot], ring.turn ^ 1u, late);
     }
   } else if (warp == 1 && rank == 0) {  // products
     // The whole warp walks the loop and one elected thread issues: with the
@@ -313,20 +339,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
         const int in_segment = kSegment ? (k - q.k0) % kSegment : k - q.k0;
         if (in_segment == 0) {  // the next of the two sums, once the epilogue has read it
           acc = tmem + (uint32_t)(sums & 1) * 256u;
-          if (sums >= 2) ring_wait(&bar.sum_empty[sums & 1], (uint32_t)(sums / 2 - 1) & 1u, broken);
+          if (sums >= 2) warp_wait(&bar.sum_empty[sums & 1], (uint32_t)(sums / 2 - 1) & 1u, broken);
           tc_fence_after();
         }
         const int slot = ring.slot;
-        ring_wait(&bar.full[slot], ring.turn, broken);
-        if ((broken = __any_sync(0xffffffffu, broken))) break;
+        warp_wait(&bar.full[slot], ring.turn, broken);
+        if (broken) break;
         tc_fence_after();
-        const uint32_t a = base + (uint32_t)slot * 2u * kPairHalf, b = a + kPairHalf;
+        const uint32_t at = base + (uint32_t)slot * 2u * kPairHalf;
+        const uint32_t a = pair_desc_low<kARows>(at), b = pair_desc_low<kBRows>(at + kPairHalf);
         const bool sum_done = k + 1 == q.k1 || (kSegment && in_segment == kSegment - 1);
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < kPairK / 16; ++j)
-            pair_mma(acc, pair_desc<kARows>(a + j * pair_kstep<kARows>()),
-                     pair_desc<kBRows>(b + j * pair_kstep<kBRows>()), idesc, (in_segment > 0 || j > 0) ? 1u : 0u);
+            pair_mma(acc, a + j * pair_kstep<kARows>(), kPairDescHigh, b + j * pair_kstep<kBRows>(), kPairDescHigh, idesc,
+                     (in_segment > 0 || j > 0) ? 1u : 0u);
           pair_commit(&bar.empty[slot]);
           if (sum_done) pair_commit(&bar.sum_full[sums & 1]);
         }
@@ -354,16 +381,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
         ++sums;
       };
       if constexpr (kSegment == 0) {
-        ring_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
-        if ((broken = __any_sync(0xffffffffu, broken))) break;
+        warp_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
+        if (broken) break;
         tc_fence_after();
         epi(q, row, col, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes}, box);
         release();
       } else {
         int acc[kCols];
         for (int k = q.k0; k < q.k1; k += kSegment) {
-          ring_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
-          if ((broken = __any_sync(0xffffffffu, broken))) break;
+          warp_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
+          if (broken) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < kCols; c += 32) {
