@@ -46,6 +46,15 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
   return u;
 }
 
+// 16 bytes as they come, and as fp32.
+template <class T>
+__device__ __forceinline__ void unpack(const uint4& u, float* v) {
+  T e[16 / sizeof(T)];
+  memcpy(e, &u, 16);
+#pragma unroll
+  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = to_f32<T>(e[i]);
+}
+
 // VEC consecutive elements in one access of VEC * sizeof(T) bytes (at most
 // 16 at a time); p must be aligned to that size.
 template <class T, int VEC>
@@ -117,6 +126,62 @@ __device__ __forceinline__ void block_reduce(float (&v)[N], float* red, Op op) {
   // every warp reduces the warps' values itself, in the same order
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = warp_reduce(lane < nw ? red[k * 32 + lane] : Op::kIdentity, op);
+}
+
+// One value over a block of at most 32 warps with one barrier; `red`: two
+// buffers of 64 floats that successive uses take turns with (see block_sums).
+template <class Op>
+__device__ __forceinline__ float block_one(float v, float* red, int& turn, Op op) {
+  const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+  v = warp_reduce(v, op);
+  float* to = red + 64 * turn;
+  turn ^= 1;
+  if (lane == 0) to[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_reduce(lane < nw ? to[lane] : Op::kIdentity, op);
+}
+
+// Sums of four values over a warp in six exchanges: at each of the first two
+// steps a lane hands on half of its values.  Lane 8 i has the i-th sum.
+__device__ __forceinline__ float warp_sums4(const float (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool high = lane & 16, odd = lane & 8;
+  float a = (high ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, high ? v[0] : v[2], 16);
+  float b = (high ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, high ? v[1] : v[3], 16);
+  float s = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// Sums of two to four values over a block of at most 16 warps with one
+// barrier.  `red`: two buffers of 64 floats, which successive uses take turns
+// with (`turn`), so that a buffer is written again only after a barrier that
+// every reader of it has passed.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float* red, int& turn) {
+  static_assert(N >= 2 && N <= 4, "");
+  const int nw = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = k < N ? v[k] : 0.f;
+  float* to = red + 64 * turn;
+  turn ^= 1;
+  const float s = warp_sums4(w);
+  if ((lane & 7) == 0) to[(lane >> 3) * 16 + warp] = s;
+  __syncthreads();
+  // value lane / 16 (and lane / 16 + 2) of warp lane % 16
+  const bool in = (lane & 15) < nw;
+  float a = in ? to[lane] : 0.f, b = N > 2 && in ? to[32 + lane] : 0.f;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (N > 2) b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  v[0] = __shfl_sync(0xffffffffu, a, 0);
+  v[1] = __shfl_sync(0xffffffffu, a, 16);
+  if (N > 2) v[N > 2 ? 2 : 0] = __shfl_sync(0xffffffffu, b, 0);
+  if (N > 3) v[N > 3 ? 3 : 0] = __shfl_sync(0xffffffffu, b, 16);
 }
 
 }  // namespace bakron

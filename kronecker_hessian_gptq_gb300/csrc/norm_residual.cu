@@ -29,16 +29,20 @@
 namespace bakron {
 namespace {
 
-// One row for each block: thread t holds the NV vectors of VEC elements at
-// columns (i * blockDim.x + t) * VEC.
-template <class T, int VEC, int NV, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_residual_kernel(NormResidual p) {
+constexpr int kSms = 152;
+
+// A block walks over rows with the next one on its way: thread t holds the NV
+// vectors of VEC elements at columns (i * blockDim.x + t) * VEC.  kKeep: the
+// weights stay in registers (RMS norms, 8 elements for each thread), else they
+// are read again for each row, from the L1 cache.
+template <class T, int VEC, int NV, int kThreads, int kBlocks, bool kKeep>
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_residual_kernel(NormResidual p) {
   constexpr int E = VEC * NV;
-  __shared__ float red[64];
-  const int64_t row = blockIdx.x;
+  __shared__ float red[128];
+  int turn = 0;
   const int D = (int)p.D;
   const float invd = 1.f / (float)D;
-  float y[E];
+  const int64_t each = p.T / p.groups;
   int col[NV];
   bool in[NV];
 #pragma unroll
@@ -46,132 +50,162 @@ __global__ void __launch_bounds__(kThreads) norm_residual_kernel(NormResidual p)
     col[i] = (i * (int)blockDim.x + (int)threadIdx.x) * VEC;
     in[i] = col[i] < D;
   }
-  auto load = [&](const void* base, int64_t ld, float(&v)[E]) {
-    const T* r = static_cast<const T*>(base) + row * ld;
+  struct Raw {
+    T e[E];
+  };
+  auto fetch = [&](const void* base, int64_t at, Raw& raw) {
+    const T* r = static_cast<const T*>(base) + at;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float e[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) e[k] = 0.f;
-      if (in[i]) load_vec<T, VEC>(r + col[i], e);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[i * VEC + k] = e[k];
+      if constexpr (VEC * sizeof(T) == 16) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (base && in[i]) u = *reinterpret_cast<const uint4*>(r + col[i]);
+        memcpy(raw.e + i * VEC, &u, 16);
+      } else {
+        raw.e[i] = base && in[i] ? r[col[i]] : from_f32<T>(0.f);
+      }
     }
+  };
+  auto param = [&](const float* w, int i, float none, float(&v)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = none;
+    if (w && in[i]) load_vec<float, VEC>(w + col[i], v);
   };
   // mean and reciprocal deviation of the row held in v
   auto stats = [&](const float(&v)[E], float& m, float& r) {
     m = 0.f;
-    if (p.layer) {
-      float s[1] = {0.f};
+    if (!kKeep && p.layer) {
+      float s = 0.f;
 #pragma unroll
-      for (int k = 0; k < E; ++k) s[0] += v[k];
-      block_reduce<1>(s, red, SumOp());
-      m = s[0] * invd;
+      for (int k = 0; k < E; ++k) s += v[k];
+      m = block_one(s, red, turn, SumOp()) * invd;
     }
-    float s[1] = {0.f};
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (in[i]) {
+      if (kKeep || in[i]) {  // without a mean the zeros beyond the row add nothing
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) s[0] = fmaf(v[i * VEC + k] - m, v[i * VEC + k] - m, s[0]);
+        for (int k = 0; k < VEC; ++k) s = fmaf(v[i * VEC + k] - m, v[i * VEC + k] - m, s);
       }
-    block_reduce<1>(s, red, SumOp());
-    r = rsqrtf(fmaf(s[0], invd, p.eps));
+    r = rsqrtf(fmaf(block_one(s, red, turn, SumOp()), invd, p.eps));
   };
-  load(p.X, p.ldx, y);
-  if (p.H) {
-    float h[E];
-    load(p.H, p.ldh, h);
-    float m = 0.f, r = 1.f;
-    if (p.post) stats(h, m, r);
-    const T* gate = p.gate ? static_cast<const T*>(p.gate) + (row / (p.T / p.groups)) * p.ldg : nullptr;
+  float kept_post[NV][VEC], kept_pre[NV][VEC];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      param(p.post, i, 1.f, kept_post[i]);
+      param(p.pre, i, 1.f, kept_pre[i]);
+    }
+  }
+  Raw rx, rh;
+  fetch(p.X, blockIdx.x * p.ldx, rx);
+  fetch(p.H, blockIdx.x * p.ldh, rh);
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    float y[E], h[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) y[k] = to_f32<T>(rx.e[k]), h[k] = to_f32<T>(rh.e[k]);
+    if (row + gridDim.x < p.T) {
+      fetch(p.X, (row + gridDim.x) * p.ldx, rx);
+      fetch(p.H, (row + gridDim.x) * p.ldh, rh);
+    }
+    if (p.H) {
+      Raw gate;
+      if (p.gate) fetch(p.gate, (row / each) * p.ldg, gate);
+      float m = 0.f, r = 1.f;
+      if (p.post) stats(h, m, r);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float w[VEC], b[VEC];
+        if constexpr (!kKeep) {
+          param(p.post, i, 1.f, w);
+          param(p.post_bias, i, 0.f, b);
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const int e = i * VEC + k;
+          float u = kKeep ? h[e] * r * kept_post[i][k] : fmaf((h[e] - m) * r, w[k], b[k]);
+          if (p.gate) u *= to_f32<T>(gate.e[e]);
+          y[e] = fmaf(p.alpha, y[e], u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) y[k] *= p.alpha;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float e[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        if (!kKeep && !in[i]) y[i * VEC + k] = 0.f;  // a bias may have come in
+        e[k] = y[i * VEC + k];
+      }
+      if (in[i]) store_vec<T, VEC>(static_cast<T*>(p.Y) + row * D + col[i], e);
+    }
+    if (!p.pre) continue;
+    float m, r;
+    stats(y, m, r);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float e[VEC], w[VEC], b[VEC];
+      if constexpr (!kKeep) {
+        param(p.pre, i, 1.f, w);
+        param(p.pre_bias, i, 0.f, b);
+      }
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        e[k] = kKeep ? y[i * VEC + k] * r * kept_pre[i][k] : fmaf((y[i * VEC + k] - m) * r, w[k], b[k]);
+        y[i * VEC + k] = e[k];
+        if (in[i]) top = MaxOp()(fabsf(e[k]), top);
+      }
+      if (!p.C && in[i]) store_vec<T, VEC>(static_cast<T*>(p.Z) + row * D + col[i], e);
+    }
+    if (!p.C) continue;
+    const float s = token_scale(block_one(top, red, turn, MaxOp())), inv = token_inv(s);
+    if (threadIdx.x == 0) p.cs[row] = s;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
+      int8_t* to = p.C + row * D + col[i];
+      uint32_t w[VEC > 4 ? 2 : 1] = {};
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const int c = col[i] + k;
-        float u = h[i * VEC + k];
-        if (p.post) u = fmaf((u - m) * r, __ldg(p.post + c), p.post_bias ? __ldg(p.post_bias + c) : 0.f);
-        if (gate) u *= to_f32<T>(gate[c]);
-        y[i * VEC + k] = fmaf(p.alpha, y[i * VEC + k], u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < E; ++k) y[k] *= p.alpha;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (!in[i]) continue;
-    float e[VEC];
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) e[k] = y[i * VEC + k];
-    store_vec<T, VEC>(static_cast<T*>(p.Y) + row * D + col[i], e);
-  }
-  if (!p.pre) return;
-  float m, r;
-  stats(y, m, r);
-  float top[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (!in[i]) continue;
-    float e[VEC];
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const int c = col[i] + k;
-      e[k] = fmaf((y[i * VEC + k] - m) * r, __ldg(p.pre + c), p.pre_bias ? __ldg(p.pre_bias + c) : 0.f);
-      y[i * VEC + k] = e[k];
-      top[0] = MaxOp()(fabsf(e[k]), top[0]);
-    }
-    if (!p.C) store_vec<T, VEC>(static_cast<T*>(p.Z) + row * D + col[i], e);
-  }
-  if (!p.C) return;
-  block_reduce<1>(top, red, MaxOp());
-  const float s = token_scale(top[0]), inv = token_inv(s);
-  if (threadIdx.x == 0) p.cs[row] = s;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (!in[i]) continue;
-    int8_t c[VEC];
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) c[k] = (int8_t)token_code(y[i * VEC + k], s, inv);
-    int8_t* to = p.C + row * D + col[i];
-    if constexpr (VEC == 8) {
-      uint2 u;
-      memcpy(&u, c, 8);
-      *reinterpret_cast<uint2*>(to) = u;
-    } else if constexpr (VEC == 4) {
-      uint32_t u;
-      memcpy(&u, c, 4);
-      *reinterpret_cast<uint32_t*>(to) = u;
-    } else {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) to[k] = c[k];
+      for (int k = 0; k < VEC; ++k) w[k / 4] |= (uint32_t)(token_code(y[i * VEC + k], s, inv) & 255) << (8 * (k % 4));
+      if constexpr (VEC == 8)
+        *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+      else if constexpr (VEC == 4)
+        *reinterpret_cast<uint32_t*>(to) = w[0];
+      else
+        *to = (int8_t)w[0];
     }
   }
 }
 
+// Threads for a row: enough for 8 elements each up to 8192 columns, for 16 and
+// 32 beyond.  Blocks: as many as fill the SMs, or one for each row.
 template <class T, int VEC>
 cudaError_t norm_residual_typed(const NormResidual& p, cudaStream_t stream) {
   const int64_t nvec = (p.D + VEC - 1) / VEC;
   constexpr int kUnit = 8 / VEC;  // vectors that make up 8 elements
-  auto threads = [&](int64_t per) { return (unsigned)(std::max<int64_t>(1, (nvec + 32 * per - 1) / (32 * per)) * 32); };
-  const unsigned grid = (unsigned)p.T;
-  if (p.D <= 8192) {
-    norm_residual_kernel<T, VEC, kUnit, 1024><<<grid, threads(kUnit), 0, stream>>>(p);
-  } else if (p.D <= 16384) {
-    norm_residual_kernel<T, VEC, 2 * kUnit, 1024><<<grid, threads(2 * kUnit), 0, stream>>>(p);
-  } else {
-    norm_residual_kernel<T, VEC, 4 * kUnit, 1024><<<grid, threads(4 * kUnit), 0, stream>>>(p);
-  }
+  const int64_t per = p.D <= 8192 ? kUnit : p.D <= 16384 ? 2 * kUnit : 4 * kUnit;
+  const int64_t threads = std::max<int64_t>(1, (nvec + 32 * per - 1) / (32 * per)) * 32;
+  const unsigned grid = (unsigned)std::min<int64_t>(p.T, (int64_t)kSms * (1024 / threads));
+  if (p.D <= 4096 && !p.layer)
+    norm_residual_kernel<T, VEC, kUnit, 512, 2, true><<<grid, (unsigned)threads, 0, stream>>>(p);
+  else if (p.D <= 8192 && !p.layer)
+    norm_residual_kernel<T, VEC, kUnit, 1024, 1, true><<<grid, (unsigned)threads, 0, stream>>>(p);
+  else if (p.D <= 8192)
+    norm_residual_kernel<T, VEC, kUnit, 1024, 1, false><<<grid, (unsigned)threads, 0, stream>>>(p);
+  else if (p.D <= 16384)
+    norm_residual_kernel<T, VEC, 2 * kUnit, 1024, 1, false><<<grid, (unsigned)threads, 0, stream>>>(p);
+  else
+    norm_residual_kernel<T, VEC, 4 * kUnit, 1024, 1, false><<<grid, (unsigned)threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ backward
 
 constexpr int kBwdThreads = 512;  // 8 elements each: 4096 columns for one block of a cluster
-constexpr int kBwdBlocks = 152;   // row ranges (times the cluster size: thread blocks)
 
 struct BackwardPlan {
   int64_t groups;  // at least 1
@@ -189,7 +223,7 @@ BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups) {
   while ((int64_t)b.cluster * kBwdThreads * 8 < D) b.cluster *= 2;
   const int64_t per = (D + b.cluster - 1) / b.cluster;
   b.threads = (int)std::max<int64_t>(1, (per + 255) / 256) * 32;
-  const int64_t most = std::max<int64_t>(1, kBwdBlocks * 2 / b.cluster);
+  const int64_t most = std::max<int64_t>(1, kSms * (kBwdThreads / b.threads) / b.cluster);  // that run at once
   if (b.groups <= most) {
     b.bpg = std::max<int64_t>(1, std::min(each, most / b.groups));
     b.nb = b.groups * b.bpg;
@@ -200,16 +234,15 @@ BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups) {
   return b;
 }
 
-// Sum over the whole cluster's threads.  A cluster barrier separates the
+// Sums over the whole cluster's threads.  A cluster barrier separates the
 // writes of a use from its reads, and `slot` alternates, so that a block
 // writes a slot again only after a later barrier, which every reader of it
 // has passed.
 template <int N>
-__device__ __forceinline__ void cluster_reduce(float (&v)[N], float* red, float (*slot)[4], int cluster, int& turn) {
-  block_reduce<N>(v, red, SumOp());
-  if (cluster == 1) return;
+__device__ __forceinline__ void cluster_sums(float (&v)[N], float* red, float (*slot)[4], int cluster, int& turn) {
   float* mine = slot[turn];
-  turn ^= 1;
+  block_sums<N>(v, red, turn);
+  if (cluster == 1) return;
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int k = 0; k < N; ++k) mine[k] = v[k];
@@ -233,10 +266,14 @@ __device__ __forceinline__ void cluster_reduce(float (&v)[N], float* red, float 
 // Planes of the partial column sums, nb x D fp32 each.
 enum Plane { kPost = 0, kPre = 1, kGate = 2, kPostBias = 3, kPreBias = 4, kPlanes = 5 };
 
+// A block (or, for wide rows, a cluster of them) walks over a range of rows
+// with the weights and the columns' sums in registers: 8 columns for each
+// thread.  The next row is on its way while one is worked on; 16 warps with
+// 128 registers fill an SM, and nothing else would cover the loads.
 template <class T, int VEC, bool kLayer>
-__global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(NormBackward p, BackwardPlan plan, float* part) {
+__global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackward p, BackwardPlan plan, float* part) {
   constexpr int E = 8, NV = 8 / VEC;
-  __shared__ float red[4 * 32];
+  __shared__ float red[2 * 64];
   __shared__ float slot[2][4];
   int turn = 0;
   const int cluster = plan.cluster;
@@ -261,17 +298,26 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(NormBackward
     col[i] = ((i * cluster + rank) * (int)blockDim.x + (int)threadIdx.x) * VEC;
     in[i] = col[i] < D;
   }
-  auto load = [&](const void* base, int64_t at, float(&v)[E]) {
+  // A thread's part of a row as it comes: 16-byte vectors, or single elements.
+  struct Raw {
+    T e[E];
+  };
+  auto fetch = [&](const void* base, int64_t at, Raw& raw) {
     const T* r = static_cast<const T*>(base) + at;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float e[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) e[k] = 0.f;
-      if (base && in[i]) load_vec<T, VEC>(r + col[i], e);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[i * VEC + k] = e[k];
+      if constexpr (VEC * sizeof(T) == 16) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (base && in[i]) u = *reinterpret_cast<const uint4*>(r + col[i]);
+        memcpy(raw.e + i * VEC, &u, 16);
+      } else {
+        raw.e[i] = base && in[i] ? r[col[i]] : from_f32<T>(0.f);
+      }
     }
+  };
+  auto open = [&](const Raw& raw, float(&v)[E]) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] = to_f32<T>(raw.e[k]);
   };
   auto store = [&](void* base, int64_t at, const float(&v)[E]) {
 #pragma unroll
@@ -284,10 +330,31 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(NormBackward
   };
   auto param = [&](const float* w, float none, float(&v)[E]) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float e[VEC];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) v[i * VEC + k] = !in[i] ? 0.f : w ? __ldg(w + col[i] + k) : none;
+      for (int k = 0; k < VEC; ++k) e[k] = in[i] ? none : 0.f;
+      if (in[i] && w) load_vec<float, VEC>(w + col[i], e);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) v[i * VEC + k] = e[k];
+    }
   };
+  auto put = [&](float* to, const float(&v)[E]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float e[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) e[k] = v[i * VEC + k];
+      if (in[i]) store_vec<float, VEC>(to + col[i], e);
+    }
+  };
+  const bool masked = !in[NV - 1];  // some columns are beyond the row: their values are zeros
+  float wpre[E], wpost[E], bpost[kLayer ? E : 1], gt[E];
+  param(p.pre, 0.f, wpre);
+  param(p.post, 1.f, wpost);
+  if constexpr (kLayer) param(p.post_bias, 0.f, bpost);
+#pragma unroll
+  for (int k = 0; k < E; ++k) gt[k] = 1.f;
   float apost[E], apre[E], agate[E], apostb[kLayer ? E : 1], apreb[kLayer ? E : 1];
 #pragma unroll
   for (int k = 0; k < E; ++k) apost[k] = apre[k] = agate[k] = 0.f;
@@ -295,61 +362,67 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(NormBackward
 #pragma unroll
     for (int k = 0; k < E; ++k) apostb[k] = apreb[k] = 0.f;
   }
-  auto put = [&](float* to, const float(&v)[E]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        if (in[i]) to[col[i] + k] = v[i * VEC + k];
+  Raw ry, rh, rdy, rdz;
+  auto fetch_row = [&](int64_t row) {
+    if (row >= hi) return;
+    fetch(p.Y, row * p.ldy, ry);
+    fetch(p.H, row * p.ldh, rh);
+    fetch(p.dY, row * p.lddy, rdy);
+    fetch(p.dZ, row * p.lddz, rdz);
   };
-  const bool masked = !in[NV - 1];
+  fetch_row(lo);
+  int64_t group = lo < hi ? lo / each : 0, left = 0;  // rows left in the group
   for (int64_t row = lo; row < hi; ++row) {
-    const int64_t g = row / each;
-    float y[E], h[E], dt[E], dz[E], w[E];
-    load(p.Y, row * p.ldy, y);
-    load(p.H, row * p.ldh, h);
-    load(p.dY, row * p.lddy, dt);
-    load(p.dZ, row * p.lddz, dz);
-    float my = 0.f, mh = 0.f;
+    if (left == 0) {
+      group = row / each;
+      left = (group + 1) * each - row;
+      if (p.gate) {
+        Raw g;
+        fetch(p.gate, group * p.ldg, g);
+        open(g, gt);
+      }
+    }
+    --left;
+    float y[E], h[E], dt[E], dz[E];
+    open(ry, y);
+    open(rh, h);
+    open(rdy, dt);
+    open(rdz, dz);
+    fetch_row(row + 1);
     if constexpr (kLayer) {
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < E; ++k) s[0] += y[k], s[1] += h[k];
-      cluster_reduce<2>(s, red, slot, cluster, turn);
-      my = s[0] * invd, mh = s[1] * invd;
+      cluster_sums<2>(s, red, slot, cluster, turn);
+      const float my = s[0] * invd, mh = p.post ? s[1] * invd : 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
           if (masked && !in[i]) continue;
           y[i * VEC + k] -= my;
-          if (p.post) h[i * VEC + k] -= mh;
+          h[i * VEC + k] -= mh;
         }
     }
-    float ry = 0.f, rh = 1.f;
-    {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      param(p.pre, 0.f, w);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const float q = dz[k] * wpre[k];
+      s[0] = fmaf(y[k], y[k], s[0]);
+      s[1] = fmaf(q, y[k], s[1]);
+      s[2] = fmaf(h[k], h[k], s[2]);
+      if (kLayer) s[3] += q;
+    }
+    cluster_sums<4>(s, red, slot, cluster, turn);
+    if (p.dZ) {
+      const float r = rsqrtf(fmaf(s[0], invd, p.eps)), c1 = r * r * r * s[1] * invd, c0 = r * s[3] * invd;
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        const float kk = dz[k] * w[k];
-        s[0] = fmaf(y[k], y[k], s[0]);
-        s[1] = fmaf(kk, y[k], s[1]);
-        s[2] = fmaf(h[k], h[k], s[2]);
-        if (kLayer) s[3] += kk;
+        const float n = y[k] * r;
+        dt[k] += r * (dz[k] * wpre[k]) - (kLayer ? c0 : 0.f) - c1 * y[k];
+        apre[k] = fmaf(dz[k], n, apre[k]);
+        if constexpr (kLayer) apreb[k] += dz[k];
       }
-      cluster_reduce<4>(s, red, slot, cluster, turn);
-      if (p.pre && p.dZ) {
-        ry = rsqrtf(fmaf(s[0], invd, p.eps));
-        const float c1 = ry * ry * s[1] * invd, c0 = s[3] * invd;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          dt[k] = fmaf(ry, fmaf(dz[k], w[k], -c0) - c1 * y[k], dt[k]);
-          apre[k] = fmaf(dz[k], y[k] * ry, apre[k]);
-          if constexpr (kLayer) apreb[k] += dz[k];
-        }
-      }
-      if (p.post) rh = rsqrtf(fmaf(s[2], invd, p.eps));
     }
     {
       float dx[E];
@@ -358,41 +431,34 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(NormBackward
       store(p.dX, row * p.D, dx);
     }
     if (!p.H) continue;
-    float gt[E];
-    if (p.gate) {
-      load(p.gate, g * p.ldg, gt);
-    } else {
-#pragma unroll
-      for (int k = 0; k < E; ++k) gt[k] = 1.f;
-    }
-    param(p.post, 1.f, w);
-    float wb[E];
-    param(p.post_bias, 0.f, wb);
-    float s[2] = {0.f, 0.f};
+    const float r = p.post ? rsqrtf(fmaf(s[2], invd, p.eps)) : 1.f;
+    float t[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int kk = 0; kk < VEC; ++kk) {
-        const int k = i * VEC + kk;
+      for (int e = 0; e < VEC; ++e) {
+        const int k = i * VEC + e;
         if (masked && !in[i]) dt[k] = 0.f;
-        const float n = h[k] * rh;
-        agate[k] = fmaf(dt[k], fmaf(n, w[k], wb[k]), agate[k]);
+        const float n = h[k] * r;
+        float u = n * wpost[k];
+        if constexpr (kLayer) u += bpost[k];
+        agate[k] = fmaf(dt[k], u, agate[k]);
         const float du = dt[k] * gt[k];
         apost[k] = fmaf(du, n, apost[k]);
         if constexpr (kLayer) apostb[k] += du;
-        dt[k] = du * w[k];
-        s[0] = fmaf(dt[k], n, s[0]);
-        s[1] += dt[k];
+        dt[k] = du * wpost[k];
+        t[0] = fmaf(dt[k], n, t[0]);
+        if (kLayer) t[1] += dt[k];
       }
     if (p.post) {
-      cluster_reduce<2>(s, red, slot, cluster, turn);
-      const float c1 = s[0] * invd * rh, c0 = kLayer ? s[1] * invd : 0.f;
+      cluster_sums<2>(t, red, slot, cluster, turn);
+      const float c1 = t[0] * invd * r * r, c0 = kLayer ? t[1] * invd * r : 0.f;
 #pragma unroll
-      for (int k = 0; k < E; ++k) dt[k] = rh * (dt[k] - c0 - c1 * h[k]);
+      for (int k = 0; k < E; ++k) dt[k] = r * dt[k] - c0 - c1 * h[k];
     }
     store(p.dH, row * p.D, dt);
-    if (p.dgate && row + 1 == (g + 1) * each && plan.bpg == 1) {  // this range holds the whole group
-      put(p.dgate + g * p.D, agate);
+    if (p.dgate && left == 0 && plan.bpg == 1) {  // this range holds the whole group
+      put(p.dgate + group * p.D, agate);
 #pragma unroll
       for (int k = 0; k < E; ++k) agate[k] = 0.f;
     }
@@ -481,11 +547,17 @@ bool vectors(int dtype, int64_t D, std::initializer_list<std::pair<const void*, 
   return true;
 }
 
+bool on16(std::initializer_list<const float*> weights) {
+  for (const float* w : weights)
+    if (!aligned_to(w, 16)) return false;
+  return true;
+}
+
 }  // namespace
 
 cudaError_t norm_residual_launch(const NormResidual& p, cudaStream_t stream) {
   const bool vec = vectors(p.dtype, p.D, {{p.X, p.ldx}, {p.H, p.ldh}, {p.gate, p.ldg}, {p.Y, p.D}, {p.Z, p.D}}) &&
-                   (!p.C || aligned_to(p.C, 8));
+                   (!p.C || aligned_to(p.C, 8)) && on16({p.post, p.post_bias, p.pre, p.pre_bias});
   switch (p.dtype) {
     case kF32: return vec ? norm_residual_typed<float, 4>(p, stream) : norm_residual_typed<float, 1>(p, stream);
     case kF16: return vec ? norm_residual_typed<__half, 8>(p, stream) : norm_residual_typed<__half, 1>(p, stream);
@@ -500,7 +572,8 @@ size_t norm_backward_workspace_bytes(int64_t T, int64_t D, int64_t groups) {
 
 cudaError_t norm_backward_launch(const NormBackward& p, void* ws, cudaStream_t stream) {
   const bool vec = vectors(p.dtype, p.D, {{p.dY, p.lddy}, {p.dZ, p.lddz}, {p.Y, p.ldy}, {p.H, p.ldh}, {p.gate, p.ldg},
-                                          {p.dX, p.D}, {p.dH, p.D}});
+                                          {p.dX, p.D}, {p.dH, p.D}}) &&
+                   on16({p.post, p.post_bias, p.pre, p.dpost, p.dpost_bias, p.dgate, p.dpre, p.dpre_bias});
   float* part = static_cast<float*>(ws);
   switch (p.dtype) {
     case kF32: return vec ? norm_backward_typed<float, 4>(p, part, stream) : norm_backward_typed<float, 1>(p, part, stream);
