@@ -31,146 +31,264 @@ namespace {
 
 constexpr int kSms = 152;
 
-// A block walks over rows with the next one on its way: thread t holds the NV
-// vectors of VEC elements at columns (i * blockDim.x + t) * VEC.  kKeep: the
-// weights stay in registers (RMS norms, 8 elements for each thread), else they
-// are read again for each row, from the L1 cache.
-template <class T, int VEC, int NV, int kThreads, int kBlocks, bool kKeep>
+// Where a thread's 8 N columns of a row lie: vectors of VEC elements at
+// (i * stride + t) * VEC, i.e. 16 bytes where rows start on 16 bytes (eight
+// 16-bit or twice four 32-bit values), else single elements.
+template <class T, int VEC, int N>
+struct Columns {
+  static constexpr int kV = 8 * N / VEC;
+  static constexpr int kWords = 2 * sizeof(T);  // 32-bit words of a Raw8
+  int col[kV];
+  bool in[kV];
+  bool masked;  // some of them are beyond the row
+  __device__ __forceinline__ Columns(int t, int stride, int D) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      col[i] = (i * stride + t) * VEC;
+      in[i] = col[i] < D;
+    }
+    masked = !in[kV - 1];
+  }
+  // Zeros where the row ends, or where there is no array.
+  __device__ __forceinline__ void fetch(const T* row, Raw8<T> (&raw)[N]) const {
+    auto w = [&](int i) -> uint32_t& { return raw[i / kWords].w[i % kWords]; };
+    if constexpr (VEC > 1) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (row && in[i]) u = *reinterpret_cast<const uint4*>(row + col[i]);
+        w(4 * i) = u.x, w(4 * i + 1) = u.y, w(4 * i + 2) = u.z, w(4 * i + 3) = u.w;
+      }
+    } else {
+      constexpr int kW = 4 / sizeof(T);  // elements of a 32-bit word
+#pragma unroll
+      for (int i = 0; i < kV; i += kW) {
+        T e[kW];
+#pragma unroll
+        for (int k = 0; k < kW; ++k) e[k] = row && in[i + k] ? row[col[i + k]] : from_f32<T>(0.f);
+        memcpy(&w(i / kW), e, 4);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(T* row, const Raw8<T> (&raw)[N]) const {
+    auto w = [&](int i) -> const uint32_t& { return raw[i / kWords].w[i % kWords]; };
+    if constexpr (VEC > 1) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (in[i]) *reinterpret_cast<uint4*>(row + col[i]) = make_uint4(w(4 * i), w(4 * i + 1), w(4 * i + 2), w(4 * i + 3));
+    } else {
+      constexpr int kW = 4 / sizeof(T);
+#pragma unroll
+      for (int i = 0; i < kV; i += kW) {
+        T e[kW];
+        memcpy(e, &w(i / kW), 4);
+#pragma unroll
+        for (int k = 0; k < kW; ++k)
+          if (in[i + k]) row[col[i + k]] = e[k];
+      }
+    }
+  }
+  // The same columns of an fp32 array.
+  __device__ __forceinline__ void fetch32(const float* row, float none, F2 (&v)[4 * N]) const {
+    float e[8 * N];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      float f[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) f[k] = in[i] ? none : 0.f;
+      if (row && in[i]) load_vec<float, VEC>(row + col[i], f);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) e[i * VEC + k] = f[k];
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) v[i] = f2(e[2 * i], e[2 * i + 1]);
+  }
+  __device__ __forceinline__ void put32(float* row, const F2 (&v)[4 * N]) const {
+    float e[8 * N];
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) split(v[i], e[2 * i], e[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      float f[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) f[k] = e[i * VEC + k];
+      if (in[i]) store_vec<float, VEC>(row + col[i], f);
+    }
+  }
+  // Zeros beyond the row, where something was added to all columns.
+  __device__ __forceinline__ void mask(F2 (&v)[4 * N]) const {
+    if (!masked) return;
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) {
+      float a, b;
+      split(v[i], a, b);
+      v[i] = f2(in[2 * i / VEC] ? a : 0.f, in[(2 * i + 1) / VEC] ? b : 0.f);
+    }
+  }
+};
+template <class T, int N>
+__device__ __forceinline__ void open_all(const Raw8<T> (&raw)[N], F2 (&v)[4 * N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) open8<T>(raw[i], *reinterpret_cast<F2(*)[4]>(v + 4 * i));
+}
+template <class T, int N>
+__device__ __forceinline__ void close_all(const F2 (&v)[4 * N], Raw8<T> (&raw)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) close8<T>(*reinterpret_cast<const F2(*)[4]>(v + 4 * i), raw[i]);
+}
+
+// A block walks over a range of rows, 8 N columns for each thread, with the
+// next row on its way.  kLayer false: RMS norms, whose weights stay in
+// registers (with the gate's row multiplied in) where N is 1; else they are
+// read again for each row, from the L1 cache.
+template <class T, int VEC, int N, bool kLayer, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) norm_residual_kernel(NormResidual p) {
-  constexpr int E = VEC * NV;
+  constexpr int P = 4 * N;  // pairs
+  constexpr bool kKeep = !kLayer && N == 1;
   __shared__ float red[128];
   int turn = 0;
   const int D = (int)p.D;
   const float invd = 1.f / (float)D;
-  const int64_t each = p.T / p.groups;
-  int col[NV];
-  bool in[NV];
+  const Columns<T, VEC, N> c(threadIdx.x, blockDim.x, D);
+  const int64_t lo = p.T * blockIdx.x / gridDim.x, rows = p.T * (blockIdx.x + 1) / gridDim.x - lo;
+  const uint32_t each = (uint32_t)(p.T / p.groups);
+  uint32_t group = (uint32_t)lo / each, left = each - (uint32_t)lo % each;  // rows left in the group
+  const T* x = static_cast<const T*>(p.X) + lo * p.ldx;
+  const T* hin = p.H ? static_cast<const T*>(p.H) + lo * p.ldh : nullptr;
+  T* yout = static_cast<T*>(p.Y) + lo * D;
+  T* zout = p.Z ? static_cast<T*>(p.Z) + lo * D : nullptr;
+  int8_t* codes = p.C ? p.C + lo * D : nullptr;
+  // mean and reciprocal deviation; v is left without its mean
+  auto stats = [&](F2(&v)[P]) {
+    if constexpr (kLayer) {
+      F2 s = f2(0.f);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    col[i] = (i * (int)blockDim.x + (int)threadIdx.x) * VEC;
-    in[i] = col[i] < D;
-  }
-  struct Raw {
-    T e[E];
+      for (int k = 0; k < P; ++k) s = s + v[k];
+      const F2 m = f2(-block_one(sum(s), red, turn, SumOp()) * invd);
+#pragma unroll
+      for (int k = 0; k < P; ++k) v[k] = v[k] + m;
+      c.mask(v);
+    }
+    F2 s = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < P; ++k) s = fma2(v[k], v[k], s);
+    return rsqrtf(fmaf(block_one(sum(s), red, turn, SumOp()), invd, p.eps));
   };
-  auto fetch = [&](const void* base, int64_t at, Raw& raw) {
-    const T* r = static_cast<const T*>(base) + at;
+  auto gate_row = [&](F2(&g)[P]) {
+    Raw8<T> raw[N];
+    c.fetch(static_cast<const T*>(p.gate) + group * p.ldg, raw);
+    open_all<T, N>(raw, g);
+  };
+  F2 kept_post[kKeep ? P : 1], kept_pre[kKeep ? P : 1];
+  auto keep_post = [&] {  // the weight times the gate
+    if constexpr (kKeep) {
+      c.fetch32(p.post, 1.f, kept_post);
+      if (p.gate) {
+        F2 g[P];
+        gate_row(g);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (VEC * sizeof(T) == 16) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (base && in[i]) u = *reinterpret_cast<const uint4*>(r + col[i]);
-        memcpy(raw.e + i * VEC, &u, 16);
-      } else {
-        raw.e[i] = base && in[i] ? r[col[i]] : from_f32<T>(0.f);
+        for (int k = 0; k < P; ++k) kept_post[k] = kept_post[k] * g[k];
       }
     }
   };
-  auto param = [&](const float* w, int i, float none, float(&v)[VEC]) {
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) v[k] = none;
-    if (w && in[i]) load_vec<float, VEC>(w + col[i], v);
-  };
-  // mean and reciprocal deviation of the row held in v
-  auto stats = [&](const float(&v)[E], float& m, float& r) {
-    m = 0.f;
-    if (!kKeep && p.layer) {
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < E; ++k) s += v[k];
-      m = block_one(s, red, turn, SumOp()) * invd;
+  if constexpr (kKeep) c.fetch32(p.pre, 1.f, kept_pre);
+  keep_post();
+  Raw8<T> rx[N], rh[N];
+  c.fetch(x, rx);
+  c.fetch(hin, rh);
+  const F2 alpha = f2(p.alpha);
+  for (int64_t i = 0; i < rows; ++i) {
+    if (left == 0) {
+      ++group;
+      left = each;
+      if (p.gate) keep_post();
     }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (kKeep || in[i]) {  // without a mean the zeros beyond the row add nothing
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) s = fmaf(v[i * VEC + k] - m, v[i * VEC + k] - m, s);
+    --left;
+    F2 y[P], h[P];
+    open_all<T, N>(rx, y);
+    open_all<T, N>(rh, h);
+    if (i + 1 < rows) {
+      x += p.ldx;
+      c.fetch(x, rx);
+      if (hin) {
+        hin += p.ldh;
+        c.fetch(hin, rh);
       }
-    r = rsqrtf(fmaf(block_one(s, red, turn, SumOp()), invd, p.eps));
-  };
-  float kept_post[NV][VEC], kept_pre[NV][VEC];
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      param(p.post, i, 1.f, kept_post[i]);
-      param(p.pre, i, 1.f, kept_pre[i]);
     }
-  }
-  Raw rx, rh;
-  fetch(p.X, blockIdx.x * p.ldx, rx);
-  fetch(p.H, blockIdx.x * p.ldh, rh);
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    float y[E], h[E];
 #pragma unroll
-    for (int k = 0; k < E; ++k) y[k] = to_f32<T>(rx.e[k]), h[k] = to_f32<T>(rh.e[k]);
-    if (row + gridDim.x < p.T) {
-      fetch(p.X, (row + gridDim.x) * p.ldx, rx);
-      fetch(p.H, (row + gridDim.x) * p.ldh, rh);
-    }
+    for (int k = 0; k < P; ++k) y[k] = y[k] * alpha;
     if (p.H) {
-      Raw gate;
-      if (p.gate) fetch(p.gate, (row / each) * p.ldg, gate);
-      float m = 0.f, r = 1.f;
-      if (p.post) stats(h, m, r);
+      const F2 r = f2(p.post ? stats(h) : 1.f);
+      if constexpr (kKeep) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float w[VEC], b[VEC];
-        if constexpr (!kKeep) {
-          param(p.post, i, 1.f, w);
-          param(p.post_bias, i, 0.f, b);
+        for (int k = 0; k < P; ++k) y[k] = fma2(h[k], r * kept_post[k], y[k]);
+      } else {
+        if (p.post) {
+          F2 w[P];
+          c.fetch32(p.post, 1.f, w);
+#pragma unroll
+          for (int k = 0; k < P; ++k) h[k] = h[k] * (r * w[k]);
+        }
+        if (kLayer && p.post_bias) {
+          F2 w[P];
+          c.fetch32(p.post_bias, 0.f, w);
+#pragma unroll
+          for (int k = 0; k < P; ++k) h[k] = h[k] + w[k];
+        }
+        if (p.gate) {
+          F2 g[P];
+          gate_row(g);
+#pragma unroll
+          for (int k = 0; k < P; ++k) h[k] = h[k] * g[k];
         }
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const int e = i * VEC + k;
-          float u = kKeep ? h[e] * r * kept_post[i][k] : fmaf((h[e] - m) * r, w[k], b[k]);
-          if (p.gate) u *= to_f32<T>(gate.e[e]);
-          y[e] = fmaf(p.alpha, y[e], u);
-        }
+        for (int k = 0; k < P; ++k) y[k] = y[k] + h[k];
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < E; ++k) y[k] *= p.alpha;
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        if (!kKeep && !in[i]) y[i * VEC + k] = 0.f;  // a bias may have come in
-        e[k] = y[i * VEC + k];
-      }
-      if (in[i]) store_vec<T, VEC>(static_cast<T*>(p.Y) + row * D + col[i], e);
+    {
+      Raw8<T> raw[N];
+      close_all<T, N>(y, raw);
+      c.put(yout, raw);
+      yout += D;
     }
     if (!p.pre) continue;
-    float m, r;
-    stats(y, m, r);
-    float top = 0.f;
+    const F2 r = f2(stats(y));
+    if constexpr (kKeep) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e[VEC], w[VEC], b[VEC];
-      if constexpr (!kKeep) {
-        param(p.pre, i, 1.f, w);
-        param(p.pre_bias, i, 0.f, b);
-      }
+      for (int k = 0; k < P; ++k) y[k] = y[k] * (r * kept_pre[k]);
+    } else {
+      F2 w[P];
+      c.fetch32(p.pre, 1.f, w);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        e[k] = kKeep ? y[i * VEC + k] * r * kept_pre[i][k] : fmaf((y[i * VEC + k] - m) * r, w[k], b[k]);
-        y[i * VEC + k] = e[k];
-        if (in[i]) top = MaxOp()(fabsf(e[k]), top);
+      for (int k = 0; k < P; ++k) y[k] = y[k] * (r * w[k]);
+      if (kLayer && p.pre_bias) {
+        c.fetch32(p.pre_bias, 0.f, w);
+#pragma unroll
+        for (int k = 0; k < P; ++k) y[k] = y[k] + w[k];
       }
-      if (!p.C && in[i]) store_vec<T, VEC>(static_cast<T*>(p.Z) + row * D + col[i], e);
     }
-    if (!p.C) continue;
-    const float s = token_scale(block_one(top, red, turn, MaxOp())), inv = token_inv(s);
-    if (threadIdx.x == 0) p.cs[row] = s;
+    if (zout) {
+      Raw8<T> raw[N];
+      close_all<T, N>(y, raw);
+      c.put(zout, raw);
+      zout += D;
+      continue;
+    }
+    float e[2 * P], top = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!in[i]) continue;
-      int8_t* to = p.C + row * D + col[i];
+    for (int k = 0; k < P; ++k) {
+      split(y[k], e[2 * k], e[2 * k + 1]);
+      top = MaxOp()(fabsf(e[2 * k]), MaxOp()(fabsf(e[2 * k + 1]), top));
+    }
+    const float s = token_scale(block_one(top, red, turn, MaxOp())), inv = token_inv(s);
+    if (threadIdx.x == 0) p.cs[lo + i] = s;
+#pragma unroll
+    for (int q = 0; q < Columns<T, VEC, N>::kV; ++q) {
       uint32_t w[VEC > 4 ? 2 : 1] = {};
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) w[k / 4] |= (uint32_t)(token_code(y[i * VEC + k], s, inv) & 255) << (8 * (k % 4));
+      for (int k = 0; k < VEC; ++k) w[k / 4] |= (uint32_t)(token_code(e[q * VEC + k], s, inv) & 255) << (8 * (k % 4));
+      if (!c.in[q]) continue;
+      int8_t* to = codes + c.col[q];
       if constexpr (VEC == 8)
         *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
       else if constexpr (VEC == 4)
@@ -178,29 +296,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_residual_kernel(NormRe
       else
         *to = (int8_t)w[0];
     }
+    codes += D;
   }
 }
 
-// Threads for a row: enough for 8 elements each up to 8192 columns, for 16 and
+// Threads for a row: enough for 8 columns each up to 8192 columns, for 16 and
 // 32 beyond.  Blocks: as many as fill the SMs, or one for each row.
+template <class T, int VEC, bool kLayer>
+cudaError_t norm_residual_typed(const NormResidual& p, cudaStream_t stream) {
+  const int64_t n = p.D <= 8192 ? 1 : p.D <= 16384 ? 2 : 4;
+  const unsigned threads = (unsigned)((p.D + 256 * n - 1) / (256 * n) * 32);
+  const unsigned grid = (unsigned)std::min<int64_t>(p.T, (int64_t)kSms * (1024 / threads));
+  if (p.D <= 4096)
+    norm_residual_kernel<T, VEC, 1, kLayer, 512, 2><<<grid, threads, 0, stream>>>(p);
+  else if (n == 1)
+    norm_residual_kernel<T, VEC, 1, kLayer, 1024, 1><<<grid, threads, 0, stream>>>(p);
+  else if (n == 2)
+    norm_residual_kernel<T, VEC, 2, kLayer, 1024, 1><<<grid, threads, 0, stream>>>(p);
+  else
+    norm_residual_kernel<T, VEC, 4, kLayer, 1024, 1><<<grid, threads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 template <class T, int VEC>
 cudaError_t norm_residual_typed(const NormResidual& p, cudaStream_t stream) {
-  const int64_t nvec = (p.D + VEC - 1) / VEC;
-  constexpr int kUnit = 8 / VEC;  // vectors that make up 8 elements
-  const int64_t per = p.D <= 8192 ? kUnit : p.D <= 16384 ? 2 * kUnit : 4 * kUnit;
-  const int64_t threads = std::max<int64_t>(1, (nvec + 32 * per - 1) / (32 * per)) * 32;
-  const unsigned grid = (unsigned)std::min<int64_t>(p.T, (int64_t)kSms * (1024 / threads));
-  if (p.D <= 4096 && !p.layer)
-    norm_residual_kernel<T, VEC, kUnit, 512, 2, true><<<grid, (unsigned)threads, 0, stream>>>(p);
-  else if (p.D <= 8192 && !p.layer)
-    norm_residual_kernel<T, VEC, kUnit, 1024, 1, true><<<grid, (unsigned)threads, 0, stream>>>(p);
-  else if (p.D <= 8192)
-    norm_residual_kernel<T, VEC, kUnit, 1024, 1, false><<<grid, (unsigned)threads, 0, stream>>>(p);
-  else if (p.D <= 16384)
-    norm_residual_kernel<T, VEC, 2 * kUnit, 1024, 1, false><<<grid, (unsigned)threads, 0, stream>>>(p);
-  else
-    norm_residual_kernel<T, VEC, 4 * kUnit, 1024, 1, false><<<grid, (unsigned)threads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.layer ? norm_residual_typed<T, VEC, true>(p, stream) : norm_residual_typed<T, VEC, false>(p, stream);
 }
 
 // ------------------------------------------------------------------ backward
@@ -272,7 +391,6 @@ enum Plane { kPost = 0, kPre = 1, kGate = 2, kPostBias = 3, kPreBias = 4, kPlane
 // 128 registers fill an SM, and nothing else would cover the loads.
 template <class T, int VEC, bool kLayer>
 __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackward p, BackwardPlan plan, float* part) {
-  constexpr int E = 8, NV = 8 / VEC;
   __shared__ float red[2 * 64];
   __shared__ float slot[2][4];
   int turn = 0;
@@ -291,186 +409,147 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackw
     lo = b * plan.groups / plan.nb * each;
     hi = (b + 1) * plan.groups / plan.nb * each;
   }
-  int col[NV];
-  bool in[NV];
+  const Columns<T, VEC, 1> c(rank * (int)blockDim.x + (int)threadIdx.x, cluster * (int)blockDim.x, D);
+  F2 wpre[4], wpost[4], bpost[kLayer ? 4 : 1], gt[4];
+  c.fetch32(p.pre, 0.f, wpre);
+  c.fetch32(p.post, 1.f, wpost);
+  if constexpr (kLayer) c.fetch32(p.post_bias, 0.f, bpost);
+  F2 apost[4], apre[4], agate[4], apostb[kLayer ? 4 : 1], apreb[kLayer ? 4 : 1];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    col[i] = ((i * cluster + rank) * (int)blockDim.x + (int)threadIdx.x) * VEC;
-    in[i] = col[i] < D;
+  for (int k = 0; k < 4; ++k) {
+    gt[k] = f2(1.f);
+    apost[k] = apre[k] = agate[k] = f2(0.f);
+    if constexpr (kLayer) apostb[k] = apreb[k] = f2(0.f);
   }
-  // A thread's part of a row as it comes: 16-byte vectors, or single elements.
-  struct Raw {
-    T e[E];
+  const T *py = static_cast<const T*>(p.Y) + lo * p.ldy, *ph = p.H ? static_cast<const T*>(p.H) + lo * p.ldh : nullptr;
+  const T* pdy = p.dY ? static_cast<const T*>(p.dY) + lo * p.lddy : nullptr;
+  const T* pdz = p.dZ ? static_cast<const T*>(p.dZ) + lo * p.lddz : nullptr;
+  T *px = static_cast<T*>(p.dX) + lo * D, *pdh = p.dH ? static_cast<T*>(p.dH) + lo * D : nullptr;
+  Raw8<T> ry[1], rh[1], rdy[1], rdz[1];
+  auto fetch_row = [&] {
+    c.fetch(py, ry);
+    c.fetch(ph, rh);
+    c.fetch(pdy, rdy);
+    c.fetch(pdz, rdz);
   };
-  auto fetch = [&](const void* base, int64_t at, Raw& raw) {
-    const T* r = static_cast<const T*>(base) + at;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (VEC * sizeof(T) == 16) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (base && in[i]) u = *reinterpret_cast<const uint4*>(r + col[i]);
-        memcpy(raw.e + i * VEC, &u, 16);
-      } else {
-        raw.e[i] = base && in[i] ? r[col[i]] : from_f32<T>(0.f);
-      }
-    }
-  };
-  auto open = [&](const Raw& raw, float(&v)[E]) {
-#pragma unroll
-    for (int k = 0; k < E; ++k) v[k] = to_f32<T>(raw.e[k]);
-  };
-  auto store = [&](void* base, int64_t at, const float(&v)[E]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) e[k] = v[i * VEC + k];
-      if (in[i]) store_vec<T, VEC>(static_cast<T*>(base) + at + col[i], e);
-    }
-  };
-  auto param = [&](const float* w, float none, float(&v)[E]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) e[k] = in[i] ? none : 0.f;
-      if (in[i] && w) load_vec<float, VEC>(w + col[i], e);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[i * VEC + k] = e[k];
-    }
-  };
-  auto put = [&](float* to, const float(&v)[E]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float e[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) e[k] = v[i * VEC + k];
-      if (in[i]) store_vec<float, VEC>(to + col[i], e);
-    }
-  };
-  const bool masked = !in[NV - 1];  // some columns are beyond the row: their values are zeros
-  float wpre[E], wpost[E], bpost[kLayer ? E : 1], gt[E];
-  param(p.pre, 0.f, wpre);
-  param(p.post, 1.f, wpost);
-  if constexpr (kLayer) param(p.post_bias, 0.f, bpost);
-#pragma unroll
-  for (int k = 0; k < E; ++k) gt[k] = 1.f;
-  float apost[E], apre[E], agate[E], apostb[kLayer ? E : 1], apreb[kLayer ? E : 1];
-#pragma unroll
-  for (int k = 0; k < E; ++k) apost[k] = apre[k] = agate[k] = 0.f;
-  if constexpr (kLayer) {
-#pragma unroll
-    for (int k = 0; k < E; ++k) apostb[k] = apreb[k] = 0.f;
-  }
-  Raw ry, rh, rdy, rdz;
-  auto fetch_row = [&](int64_t row) {
-    if (row >= hi) return;
-    fetch(p.Y, row * p.ldy, ry);
-    fetch(p.H, row * p.ldh, rh);
-    fetch(p.dY, row * p.lddy, rdy);
-    fetch(p.dZ, row * p.lddz, rdz);
-  };
-  fetch_row(lo);
+  if (lo < hi) fetch_row();
   int64_t group = lo < hi ? lo / each : 0, left = 0;  // rows left in the group
   for (int64_t row = lo; row < hi; ++row) {
     if (left == 0) {
       group = row / each;
       left = (group + 1) * each - row;
       if (p.gate) {
-        Raw g;
-        fetch(p.gate, group * p.ldg, g);
-        open(g, gt);
+        Raw8<T> g[1];
+        c.fetch(static_cast<const T*>(p.gate) + group * p.ldg, g);
+        open_all<T, 1>(g, gt);
       }
     }
     --left;
-    float y[E], h[E], dt[E], dz[E];
-    open(ry, y);
-    open(rh, h);
-    open(rdy, dt);
-    open(rdz, dz);
-    fetch_row(row + 1);
-    if constexpr (kLayer) {
-      float s[2] = {0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < E; ++k) s[0] += y[k], s[1] += h[k];
-      cluster_sums<2>(s, red, slot, cluster, turn);
-      const float my = s[0] * invd, mh = p.post ? s[1] * invd : 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          if (masked && !in[i]) continue;
-          y[i * VEC + k] -= my;
-          h[i * VEC + k] -= mh;
-        }
+    F2 y[4], h[4], dt[4], dz[4];
+    open_all<T, 1>(ry, y);
+    open_all<T, 1>(rh, h);
+    open_all<T, 1>(rdy, dt);
+    open_all<T, 1>(rdz, dz);
+    if (row + 1 < hi) {
+      py += p.ldy;
+      if (ph) ph += p.ldh;
+      if (pdy) pdy += p.lddy;
+      if (pdz) pdz += p.lddz;
+      fetch_row();
     }
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (kLayer) {
+      F2 sy = f2(0.f), sh = f2(0.f);
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      const float q = dz[k] * wpre[k];
-      s[0] = fmaf(y[k], y[k], s[0]);
-      s[1] = fmaf(q, y[k], s[1]);
-      s[2] = fmaf(h[k], h[k], s[2]);
-      if (kLayer) s[3] += q;
+      for (int k = 0; k < 4; ++k) sy = sy + y[k], sh = sh + h[k];
+      float s[2] = {sum(sy), sum(sh)};
+      cluster_sums<2>(s, red, slot, cluster, turn);
+      const F2 my = f2(-s[0] * invd), mh = f2(p.post ? -s[1] * invd : 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = y[k] + my, h[k] = h[k] + mh;
+      c.mask(y);
+      c.mask(h);
+    }
+    float s[4];
+    F2 q[4];
+    {
+      F2 yy = f2(0.f), qy = f2(0.f), hh = f2(0.f), qq = f2(0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        q[k] = dz[k] * wpre[k];
+        yy = fma2(y[k], y[k], yy);
+        qy = fma2(q[k], y[k], qy);
+        hh = fma2(h[k], h[k], hh);
+        if constexpr (kLayer) qq = qq + q[k];
+      }
+      s[0] = sum(yy), s[1] = sum(qy), s[2] = sum(hh), s[3] = kLayer ? sum(qq) : 0.f;
     }
     cluster_sums<4>(s, red, slot, cluster, turn);
     if (p.dZ) {
-      const float r = rsqrtf(fmaf(s[0], invd, p.eps)), c1 = r * r * r * s[1] * invd, c0 = r * s[3] * invd;
+      const float r = rsqrtf(fmaf(s[0], invd, p.eps));
+      const F2 r2 = f2(r), c1 = f2(-r * r * r * s[1] * invd), c0 = f2(-r * s[3] * invd);
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        const float n = y[k] * r;
-        dt[k] += r * (dz[k] * wpre[k]) - (kLayer ? c0 : 0.f) - c1 * y[k];
-        apre[k] = fmaf(dz[k], n, apre[k]);
-        if constexpr (kLayer) apreb[k] += dz[k];
+      for (int k = 0; k < 4; ++k) {
+        dt[k] = fma2(y[k], c1, fma2(q[k], r2, dt[k]));
+        if constexpr (kLayer) dt[k] = dt[k] + c0;
+        apre[k] = fma2(dz[k], y[k] * r2, apre[k]);
+        if constexpr (kLayer) apreb[k] = apreb[k] + dz[k];
       }
+      if constexpr (kLayer) c.mask(dt);
     }
+    Raw8<T> out[1];
     {
-      float dx[E];
+      F2 dx[4];
 #pragma unroll
-      for (int k = 0; k < E; ++k) dx[k] = p.alpha * dt[k];
-      store(p.dX, row * p.D, dx);
+      for (int k = 0; k < 4; ++k) dx[k] = dt[k] * f2(p.alpha);
+      close_all<T, 1>(dx, out);
+      c.put(px, out);
+      px += D;
     }
     if (!p.H) continue;
     const float r = p.post ? rsqrtf(fmaf(s[2], invd, p.eps)) : 1.f;
-    float t[2] = {0.f, 0.f};
+    F2 tn = f2(0.f), tq = f2(0.f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int k = i * VEC + e;
-        if (masked && !in[i]) dt[k] = 0.f;
-        const float n = h[k] * r;
-        float u = n * wpost[k];
-        if constexpr (kLayer) u += bpost[k];
-        agate[k] = fmaf(dt[k], u, agate[k]);
-        const float du = dt[k] * gt[k];
-        apost[k] = fmaf(du, n, apost[k]);
-        if constexpr (kLayer) apostb[k] += du;
-        dt[k] = du * wpost[k];
-        t[0] = fmaf(dt[k], n, t[0]);
-        if (kLayer) t[1] += dt[k];
+    for (int k = 0; k < 4; ++k) {
+      const F2 n = h[k] * f2(r);
+      const F2 du = dt[k] * gt[k];
+      if constexpr (kLayer) {
+        agate[k] = fma2(dt[k], fma2(n, wpost[k], bpost[k]), agate[k]);
+        apostb[k] = apostb[k] + du;
+      } else {
+        agate[k] = fma2(dt[k], n * wpost[k], agate[k]);
       }
-    if (p.post) {
-      cluster_sums<2>(t, red, slot, cluster, turn);
-      const float c1 = t[0] * invd * r * r, c0 = kLayer ? t[1] * invd * r : 0.f;
-#pragma unroll
-      for (int k = 0; k < E; ++k) dt[k] = r * dt[k] - c0 - c1 * h[k];
+      apost[k] = fma2(du, n, apost[k]);
+      dt[k] = du * wpost[k];
+      tn = fma2(dt[k], n, tn);
+      if constexpr (kLayer) tq = tq + dt[k];
     }
-    store(p.dH, row * p.D, dt);
-    if (p.dgate && left == 0 && plan.bpg == 1) {  // this range holds the whole group
-      put(p.dgate + group * p.D, agate);
+    if (p.post) {
+      float t[2] = {sum(tn), kLayer ? sum(tq) : 0.f};
+      cluster_sums<2>(t, red, slot, cluster, turn);
+      const F2 c1 = f2(-t[0] * invd * r * r), c0 = f2(-t[1] * invd * r);
 #pragma unroll
-      for (int k = 0; k < E; ++k) agate[k] = 0.f;
+      for (int k = 0; k < 4; ++k) {
+        dt[k] = fma2(h[k], c1, dt[k] * f2(r));
+        if constexpr (kLayer) dt[k] = dt[k] + c0;
+      }
+    }
+    close_all<T, 1>(dt, out);
+    c.put(pdh, out);
+    pdh += D;
+    if (p.dgate && left == 0 && plan.bpg == 1) {  // this range holds the whole group
+      c.put32(p.dgate + group * p.D, agate);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) agate[k] = f2(0.f);
     }
   }
   const int64_t plane = plan.nb * p.D;
   float* mine = part + b * p.D;
-  if (p.dpost) put(mine + kPost * plane, apost);
-  if (p.dpre) put(mine + kPre * plane, apre);
-  if (p.dgate && plan.bpg > 1) put(mine + kGate * plane, agate);
+  if (p.dpost) c.put32(mine + kPost * plane, apost);
+  if (p.dpre) c.put32(mine + kPre * plane, apre);
+  if (p.dgate && plan.bpg > 1) c.put32(mine + kGate * plane, agate);
   if constexpr (kLayer) {
-    if (p.dpost_bias) put(mine + kPostBias * plane, apostb);
-    if (p.dpre_bias) put(mine + kPreBias * plane, apreb);
+    if (p.dpost_bias) c.put32(mine + kPostBias * plane, apostb);
+    if (p.dpre_bias) c.put32(mine + kPreBias * plane, apreb);
   }
   if (cluster > 1)  // the others may still read this block's slots
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
