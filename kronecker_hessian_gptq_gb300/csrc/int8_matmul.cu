@@ -44,8 +44,9 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // (then also from given bytes), and zeros for what later kernels add to.
 template <class T, class C>
 __global__ void __launch_bounds__(512) quantize_tokens_kernel(const T* X, int64_t K, int64_t ldx, bool vec, C* codes,
-                                                              int64_t ldc, float* s, uint4* zero, int64_t zeros) {
+                                                              int64_t ldc, float* s, uint4* zero, int64_t zeros, int32_t* status) {
   __shared__ float red[32];
+  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < zeros; i += (int64_t)gridDim.x * blockDim.x)
     zero[i] = make_uint4(0, 0, 0, 0);
   const T* x = X + (int64_t)blockIdx.x * ldx;
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(512) quantize_tokens_kernel(const T* X, int64_
 
 template <class C>
 cudaError_t quantize_as(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, C* codes, int64_t ldc, float* s,
-                        uint4* zero, int64_t zeros, cudaStream_t stream) {
+                        uint4* zero, int64_t zeros, int32_t* status, cudaStream_t stream) {
   const unsigned grid = (unsigned)T, threads = (unsigned)std::min<int64_t>(512, std::max<int64_t>(1, (K + 255) / 256) * 32);
   // whole vectors in and out: rows of X on 16 bytes, rows of codes on a vector's own
   auto vec = [&](int64_t per) {
@@ -112,16 +113,16 @@ cudaError_t quantize_as(const void* X, int dtype, int64_t T, int64_t K, int64_t 
   };
   switch (dtype) {
     case kF32:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const float*)X, K, ldx, vec(4), codes, ldc, s, zero, zeros);
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const float*)X, K, ldx, vec(4), codes, ldc, s, zero, zeros, status);
       break;
     case kF16:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __half*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros);
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __half*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros, status);
       break;
     case kBF16:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __nv_bfloat16*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros);
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __nv_bfloat16*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros, status);
       break;
     default:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const int8_t*)X, K, ldx, false, codes, ldc, s, zero, zeros);
+      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const int8_t*)X, K, ldx, false, codes, ldc, s, zero, zeros, status);
   }
   return cudaGetLastError();
 }
@@ -193,9 +194,10 @@ __device__ __forceinline__ void tokens_to_shared(const Int8Matmul& p, int8_t* co
 // fewer rows than warps a power of two, which share a row and join through
 // shared memory).  kVec: rows start on 16 bytes.
 template <int TT, bool kVec>
-__global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(Int8Matmul p, int pitch, int split) {
+__global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(Int8Matmul p, int pitch, int split, int32_t* status) {
   extern __shared__ __align__(16) unsigned char rows_smem[];
   int8_t* codes = reinterpret_cast<int8_t*>(rows_smem);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   __shared__ float scales[TT];
   __shared__ uint32_t top[TT];
   __shared__ int joined[32][TT];
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(Int8Matmul p, in
 }
 
 template <int TT>
-cudaError_t rows_launch(const Int8Matmul& p, cudaStream_t stream) {
+cudaError_t rows_launch(const Int8Matmul& p, int32_t* status, cudaStream_t stream) {
   const int pitch = (int)up16(p.K), sms = 2 * pair_count();
   const bool vec = aligned_to(p.V, 16) && p.ldv % 16 == 0;
   const int64_t warps = (int64_t)sms * (kRowThreads / 32);
@@ -304,7 +306,7 @@ cudaError_t rows_launch(const Int8Matmul& p, cudaStream_t stream) {
   auto kernel = vec ? int8_rows_kernel<TT, true> : int8_rows_kernel<TT, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kRowThreads, smem, stream>>>(p, pitch, split);
+  kernel<<<grid, kRowThreads, smem, stream>>>(p, pitch, split, status);
   return cudaGetLastError();
 }
 
@@ -414,7 +416,8 @@ cudaError_t batch(const Int8Matmul& p, const Layout& l, char* ws, int32_t* statu
   const float* s = p.x_scales ? p.x_scales : own_scales;
   const int64_t ldc = up64(p.K);
   cudaError_t e = quantize_as<__half>(p.X, p.x_scales ? kI8 : p.x_dtype, p.T, p.K, p.ldx, codes, ldc, own_scales,
-                                      reinterpret_cast<uint4*>(ws + l.zeros), (int64_t)(l.end_zeros - l.zeros) / 16, stream);
+                                      reinterpret_cast<uint4*>(ws + l.zeros), (int64_t)(l.end_zeros - l.zeros) / 16, status,
+                                      stream);
   if (e != cudaSuccess) return e;
   if (p.T <= kPairTokens) {
     const int8_t* V = p.V;
@@ -441,21 +444,19 @@ cudaError_t batch(const Int8Matmul& p, const Layout& l, char* ws, int32_t* statu
 
 cudaError_t quantize_tokens_launch(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, int8_t* C, int64_t ldc,
                                    float* s, cudaStream_t stream) {
-  return quantize_as<int8_t>(X, dtype, T, K, ldx, C, ldc, s, nullptr, 0, stream);
+  return quantize_as<int8_t>(X, dtype, T, K, ldx, C, ldc, s, nullptr, 0, nullptr, stream);
 }
 
 size_t int8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies) { return layout(T, K, N, copies).bytes; }
 bool int8_matmul_needs_copies(const Int8Matmul& p) { return !tma_codes(p); }
 
 cudaError_t int8_matmul_launch(const Int8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream);
-  if (e != cudaSuccess) return e;
   if (by_rows(p.T, p.K)) {
     switch (row_tokens(p.T)) {
-      case 1: return rows_launch<1>(p, stream);
-      case 2: return rows_launch<2>(p, stream);
-      case 4: return rows_launch<4>(p, stream);
-      default: return rows_launch<8>(p, stream);
+      case 1: return rows_launch<1>(p, status_dev, stream);
+      case 2: return rows_launch<2>(p, status_dev, stream);
+      case 4: return rows_launch<4>(p, status_dev, stream);
+      default: return rows_launch<8>(p, status_dev, stream);
     }
   }
   const Layout l = layout(p.T, p.K, p.N, !tma_codes(p));
