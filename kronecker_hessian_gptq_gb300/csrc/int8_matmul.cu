@@ -25,7 +25,6 @@
 namespace bakron {
 namespace {
 
-constexpr int kI8 = 3;  // BAKRON_I8
 constexpr int64_t kRowTokens = 8;
 constexpr int64_t kPairTokens = 1024;
 constexpr int kRowThreads = 1024;
@@ -40,89 +39,171 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // ------------------------------------------------------------ codes of tokens
 
-// One block for each token: codes as bytes, or as fp16 for the tensor cores
-// (then also from given bytes), and zeros for what later kernels add to.
-template <class T, class C>
-__global__ void __launch_bounds__(512) quantize_tokens_kernel(const T* X, int64_t K, int64_t ldx, bool vec, C* codes,
-                                                              int64_t ldc, float* s, uint4* zero, int64_t zeros, int32_t* status) {
-  __shared__ float red[32];
-  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < zeros; i += (int64_t)gridDim.x * blockDim.x)
-    zero[i] = make_uint4(0, 0, 0, 0);
-  const T* x = X + (int64_t)blockIdx.x * ldx;
-  C* c = codes + (int64_t)blockIdx.x * ldc;
-  auto put = [&](int64_t k, int v) {
-    if constexpr (sizeof(C) == 1)
-      c[k] = (C)v;
-    else
-      c[k] = __int2half_rn(v);
-  };
-  if constexpr (sizeof(T) == 1) {
-    for (int64_t k = threadIdx.x; k < K; k += blockDim.x) put(k, x[k]);
-  } else {
-    constexpr int VEC = 16 / sizeof(T);
-    const int64_t whole = vec ? K / VEC * VEC : 0;
-    float top[1] = {0.f};
-    for (int64_t k = (int64_t)threadIdx.x * VEC; k < whole; k += (int64_t)blockDim.x * VEC) {
-      float v[VEC];
-      load_vec<T, VEC>(x + k, v);
+constexpr int kPrepareThreads = 512;
+
+// What a product does before its main kernel, in one launch: a block for each
+// token takes its scale and its codes, as bytes or as fp16 for the tensor
+// cores; the blocks after them rewrite codes that were given (as fp16, or as
+// bytes in rows that start on 16 bytes), 16 at a time; all of them clear what
+// the main kernel adds to.
+struct Rewrite {
+  const int8_t* from;
+  int64_t ld, rows, cols;
+  void* to;  // rows of ldt
+  int64_t ldt;
+  bool f16;
+};
+struct Prepare {
+  const void* X;  // tokens x K values, or null
+  int64_t tokens, K, ldx;
+  bool vec;  // rows of X on 16 bytes, rows of the codes on a vector's own
+  void* codes;
+  int64_t ldc;
+  float* scales;
+  Rewrite rewrite[2];
+  uint4* zero;
+  int64_t zeros;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void rewrite_codes(const Rewrite& w, int64_t at, int64_t step) {
+  const int64_t per = (w.cols + 15) / 16, all = w.rows * per;
+  for (; at < all; at += step) {
+    const int64_t row = (uint64_t)at < (1ull << 32) && per < (1ll << 32) ? (uint32_t)at / (uint32_t)per : at / per;
+    const int64_t k = (at - row * per) * 16;
+    const int8_t* v = w.from + row * w.ld + k;
+    uint32_t e[4] = {0, 0, 0, 0};
+    if (reinterpret_cast<uintptr_t>(v) % 16 == 0 && k + 16 <= w.cols) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(v));
+      e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
+    } else {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) top[0] = MaxOp()(fabsf(v[i]), top[0]);
+      for (int i = 0; i < 16; ++i)
+        if (k + i < w.cols) e[i / 4] |= (uint32_t)(uint8_t)v[i] << (8 * (i % 4));
     }
-    for (int64_t k = whole + threadIdx.x; k < K; k += blockDim.x) top[0] = MaxOp()(fabsf(to_f32<T>(x[k])), top[0]);
-    block_reduce<1>(top, red, MaxOp());
-    const float scale = token_scale(top[0]), inv = token_inv(scale);
-    if (threadIdx.x == 0) s[blockIdx.x] = scale;
-    for (int64_t k = (int64_t)threadIdx.x * VEC; k < whole; k += (int64_t)blockDim.x * VEC) {
-      float v[VEC];
-      load_vec<T, VEC>(x + k, v);
-      C e[VEC];
+    if (w.f16) {
+      uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int q = token_code(v[i], scale, inv);
-        if constexpr (sizeof(C) == 1)
-          e[i] = (C)q;
-        else
-          e[i] = __int2half_rn(q);
-      }
-      if constexpr (VEC * sizeof(C) % 16 == 0) {
-        uint4 u;
-        memcpy(&u, e, 16);
-        *reinterpret_cast<uint4*>(c + k) = u;
-      } else if constexpr (VEC * sizeof(C) == 8) {
-        uint2 u;
-        memcpy(&u, e, 8);
-        *reinterpret_cast<uint2*>(c + k) = u;
-      } else {
-        uint32_t u;
-        memcpy(&u, e, 4);
-        *reinterpret_cast<uint32_t*>(c + k) = u;
-      }
+      for (int i = 0; i < 4; ++i) i8_to_f16(e[i], h[2 * i], h[2 * i + 1]);
+      uint4* f = reinterpret_cast<uint4*>(static_cast<__half*>(w.to) + row * w.ldt + k);
+      f[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      f[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<int8_t*>(w.to) + row * w.ldt + k) = make_uint4(e[0], e[1], e[2], e[3]);
     }
-    for (int64_t k = whole + threadIdx.x; k < K; k += blockDim.x) put(k, token_code(to_f32<T>(x[k]), scale, inv));
   }
 }
 
 template <class C>
-cudaError_t quantize_as(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, C* codes, int64_t ldc, float* s,
-                        uint4* zero, int64_t zeros, int32_t* status, cudaStream_t stream) {
-  const unsigned grid = (unsigned)T, threads = (unsigned)std::min<int64_t>(512, std::max<int64_t>(1, (K + 255) / 256) * 32);
-  // whole vectors in and out: rows of X on 16 bytes, rows of codes on a vector's own
-  auto vec = [&](int64_t per) {
-    return aligned_to(X, 16) && ldx % per == 0 && ldc % per == 0 && aligned_to(codes, per * sizeof(C));
-  };
+__device__ __forceinline__ void put8(C* to, const float (&v)[8], float s, float inv) {
+  uint32_t w[4];
+  if constexpr (sizeof(C) == 1) {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i / 4] |= (uint32_t)(token_code(v[i], s, inv) & 255) << (8 * (i % 4));
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<__half>((float)token_code(v[2 * i], s, inv), (float)token_code(v[2 * i + 1], s, inv));
+    *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// NV > 0: a thread keeps its NV runs of 8 values in registers (K up to 4096
+// NV), so that they are read once; 0: any K, read twice.
+template <class T, class C, int NV>
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Prepare p) {
+  __shared__ float red[32];
+  asm volatile("griddepcontrol.launch_dependents;\n");  // see int8_pair_kernel
+  if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.zeros; i += (int64_t)gridDim.x * blockDim.x)
+    p.zero[i] = make_uint4(0, 0, 0, 0);
+  if ((int64_t)blockIdx.x >= p.tokens) {
+    const int64_t at = ((int64_t)blockIdx.x - p.tokens) * blockDim.x + threadIdx.x;
+    const int64_t step = ((int64_t)gridDim.x - p.tokens) * blockDim.x;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+      if (p.rewrite[i].from) rewrite_codes(p.rewrite[i], at, step);
+    return;
+  }
+  const T* x = static_cast<const T*>(p.X) + (int64_t)blockIdx.x * p.ldx;
+  C* c = static_cast<C*>(p.codes) + (int64_t)blockIdx.x * p.ldc;
+  const int64_t whole = p.vec ? p.K / 8 * 8 : 0;
+  const int64_t stride = (int64_t)blockDim.x * 8;
+  float v[NV ? NV : 1][8];
+  float top[1] = {0.f};
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t k = threadIdx.x * 8 + i * stride;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      if (k < whole) load_vec<T, 8>(x + k, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top[0] = MaxOp()(fabsf(v[i][e]), top[0]);
+  } else {
+    for (int64_t k = threadIdx.x * 8; k < whole; k += stride) {
+      load_vec<T, 8>(x + k, v[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top[0] = MaxOp()(fabsf(v[0][e]), top[0]);
+    }
+  }
+  for (int64_t k = whole + threadIdx.x; k < p.K; k += blockDim.x) top[0] = MaxOp()(fabsf(to_f32<T>(x[k])), top[0]);
+  block_reduce<1>(top, red, MaxOp());
+  const float scale = token_scale(top[0]), inv = token_inv(scale);
+  if (threadIdx.x == 0) p.scales[blockIdx.x] = scale;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t k = threadIdx.x * 8 + i * stride;
+      if (k < whole) put8(c + k, v[i], scale, inv);
+    }
+  } else {
+    for (int64_t k = threadIdx.x * 8; k < whole; k += stride) {
+      load_vec<T, 8>(x + k, v[0]);
+      put8(c + k, v[0], scale, inv);
+    }
+  }
+  for (int64_t k = whole + threadIdx.x; k < p.K; k += blockDim.x) {
+    const int q = token_code(to_f32<T>(x[k]), scale, inv);
+    if constexpr (sizeof(C) == 1)
+      c[k] = (C)q;
+    else
+      c[k] = __int2half_rn(q);
+  }
+}
+
+template <class T, class C>
+void prepare_typed(const Prepare& p, unsigned grid, cudaStream_t stream) {
+  const unsigned threads = (unsigned)std::min<int64_t>(kPrepareThreads, std::max<int64_t>(1, (p.K + 255) / 256) * 32);
+  const int64_t one = (int64_t)threads * 8;
+  if (!p.vec || p.K > 4 * one)
+    prepare_kernel<T, C, 0><<<grid, threads, 0, stream>>>(p);
+  else if (p.K <= one)
+    prepare_kernel<T, C, 1><<<grid, threads, 0, stream>>>(p);
+  else if (p.K <= 2 * one)
+    prepare_kernel<T, C, 2><<<grid, threads, 0, stream>>>(p);
+  else
+    prepare_kernel<T, C, 4><<<grid, threads, 0, stream>>>(p);
+}
+template <class C>
+cudaError_t prepare_launch(Prepare p, int dtype, cudaStream_t stream) {
+  if (!p.X) p.tokens = 0;
+  int64_t blocks = 0;  // of the rewriting: eight turns each, at most a few for each SM
+  for (const Rewrite& w : p.rewrite)
+    if (w.from) blocks += (w.rows * ((w.cols + 15) / 16) + kPrepareThreads * 8 - 1) / (kPrepareThreads * 8);
+  blocks = std::min<int64_t>(blocks, 152 * 8);
+  const unsigned grid = (unsigned)std::max<int64_t>(1, p.tokens + blocks);
+  p.vec = aligned_to(p.X, 16) && p.ldx % (16 / (int64_t)elem_size(dtype)) == 0 && p.ldc % 8 == 0 &&
+          aligned_to(p.codes, 8 * sizeof(C));
+  if (!p.X) p.K = kPrepareThreads * 8;  // whole blocks for the rewriting
   switch (dtype) {
-    case kF32:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const float*)X, K, ldx, vec(4), codes, ldc, s, zero, zeros, status);
-      break;
-    case kF16:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __half*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros, status);
-      break;
-    case kBF16:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const __nv_bfloat16*)X, K, ldx, vec(8), codes, ldc, s, zero, zeros, status);
-      break;
-    default:
-      quantize_tokens_kernel<<<grid, threads, 0, stream>>>((const int8_t*)X, K, ldx, false, codes, ldc, s, zero, zeros, status);
+    case kF32: prepare_typed<float, C>(p, grid, stream); break;
+    case kF16: prepare_typed<__half, C>(p, grid, stream); break;
+    default: prepare_typed<__nv_bfloat16, C>(p, grid, stream);
   }
   return cudaGetLastError();
 }
@@ -312,41 +393,6 @@ cudaError_t rows_launch(const Int8Matmul& p, int32_t* status, cudaStream_t strea
 
 // ------------------------------------------------------------ many tokens
 
-// Rows of codes to fp16 rows (ldf a multiple of 64), or to aligned bytes.
-template <class C>
-__global__ void __launch_bounds__(256) codes_kernel(const int8_t* V, int64_t ldv, int64_t K, C* F, int64_t ldf) {
-  const int64_t row = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
-  if (k >= K) return;
-  const int8_t* v = V + row * ldv + k;
-  C* f = F + row * ldf + k;
-  alignas(16) int8_t e[16];
-  if (reinterpret_cast<uintptr_t>(v) % 16 == 0 && k + 16 <= K) {
-    *reinterpret_cast<uint4*>(e) = __ldcs(reinterpret_cast<const uint4*>(v));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) e[i] = k + i < K ? v[i] : (int8_t)0;
-  }
-  uint32_t w[4];
-  memcpy(w, e, 16);
-  if constexpr (sizeof(C) == 1) {
-    *reinterpret_cast<uint4*>(f) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    uint32_t h[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) i8_to_f16(w[i], h[2 * i], h[2 * i + 1]);
-    reinterpret_cast<uint4*>(f)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    reinterpret_cast<uint4*>(f)[1] = make_uint4(h[4], h[5], h[6], h[7]);
-  }
-}
-template <class C>
-void convert_codes(const int8_t* V, int64_t ldv, int64_t N, int64_t K, C* F, int64_t ldf, cudaStream_t stream) {
-  const int64_t y = 32768;
-  for (int64_t r = 0; r < N; r += y)
-    codes_kernel<C><<<dim3((unsigned)((K + 4095) / 4096), (unsigned)std::min(y, N - r)), 256, 0, stream>>>(
-        V + r * ldv, ldv, K, F + r * ldf, ldf);
-}
-
 // Scales a tile's exact sums and sends them out in whole lines.
 template <class T>
 struct ScaledEpilogue {
@@ -415,36 +461,41 @@ cudaError_t batch(const Int8Matmul& p, const Layout& l, char* ws, int32_t* statu
   float* own_scales = reinterpret_cast<float*>(ws + l.scales);
   const float* s = p.x_scales ? p.x_scales : own_scales;
   const int64_t ldc = up64(p.K);
-  cudaError_t e = quantize_as<__half>(p.X, p.x_scales ? kI8 : p.x_dtype, p.T, p.K, p.ldx, codes, ldc, own_scales,
-                                      reinterpret_cast<uint4*>(ws + l.zeros), (int64_t)(l.end_zeros - l.zeros) / 16, status,
-                                      stream);
+  const bool pairs = p.T <= kPairTokens, copy = !tma_codes(p);
+  Prepare a = {};
+  a.K = p.K;
+  a.status = status;
+  a.zero = reinterpret_cast<uint4*>(ws + l.zeros), a.zeros = (int64_t)(l.end_zeros - l.zeros) / 16;
+  if (p.x_scales) {
+    a.rewrite[0] = Rewrite{static_cast<const int8_t*>(p.X), p.ldx, p.T, p.K, codes, ldc, true};
+  } else {
+    a.X = p.X, a.tokens = p.T, a.ldx = p.ldx, a.codes = codes, a.ldc = ldc, a.scales = own_scales;
+  }
+  if (!pairs)
+    a.rewrite[1] = Rewrite{p.V, p.ldv, p.N, p.K, ws + l.weights, ldc, true};
+  else if (copy)
+    a.rewrite[1] = Rewrite{p.V, p.ldv, p.N, p.K, ws + l.weights, up16(p.K), false};
+  cudaError_t e = prepare_launch<__half>(a, p.x_scales ? kF32 : p.x_dtype, stream);
   if (e != cudaSuccess) return e;
-  if (p.T <= kPairTokens) {
-    const int8_t* V = p.V;
-    int64_t ldv = p.ldv;
-    if (!tma_codes(p)) {
-      int8_t* copy = reinterpret_cast<int8_t*>(ws + l.weights);
-      convert_codes<int8_t>(V, ldv, p.N, p.K, copy, up16(p.K), stream);
-      V = copy, ldv = up16(p.K);
-    }
+  if (pairs) {
     const I8Out<T> out{p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y), reinterpret_cast<int32_t*>(ws + l.sums),
                        reinterpret_cast<uint32_t*>(ws + l.arrived)};
-    return int8_pair_launch<T>(V, ldv, codes, ldc, p.K, l.work, out, status, stream);
+    return int8_pair_launch<T>(copy ? reinterpret_cast<int8_t*>(ws + l.weights) : p.V, copy ? up16(p.K) : p.ldv, codes, ldc,
+                               p.K, l.work, out, !copy, status, stream);
   }
-  __half* weights = reinterpret_cast<__half*>(ws + l.weights);
-  convert_codes<__half>(p.V, p.ldv, p.N, p.K, weights, ldc, stream);
   const PairWork work{(int)((p.T + 255) / 256), (int)((p.N + 255) / 256), 16, (int)((p.K + kPairK - 1) / kPairK), 1};
-  return pair_gemm_launch<false, false, 4, 1024 / kPairK>(PairOperand{codes, p.T, ldc}, PairOperand{weights, p.N, ldc}, p.K, false,
-                                                     work,
-                                                     ScaledEpilogue<T>{p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y)},
-                                                     status, stream);
+  return pair_gemm_launch<false, false, 4, 1024 / kPairK>(
+      PairOperand{codes, p.T, ldc}, PairOperand{ws + l.weights, p.N, ldc}, p.K, false, work,
+      ScaledEpilogue<T>{p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y)}, status, stream);
 }
 
 }  // namespace
 
 cudaError_t quantize_tokens_launch(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, int8_t* C, int64_t ldc,
                                    float* s, cudaStream_t stream) {
-  return quantize_as<int8_t>(X, dtype, T, K, ldx, C, ldc, s, nullptr, 0, nullptr, stream);
+  Prepare a = {};
+  a.X = X, a.tokens = T, a.K = K, a.ldx = ldx, a.codes = C, a.ldc = ldc, a.scales = s;
+  return prepare_launch<int8_t>(a, dtype, stream);
 }
 
 size_t int8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies) { return layout(T, K, N, copies).bytes; }

@@ -157,6 +157,9 @@ template <class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, I8Work work,
                      I8Out<T> out, int32_t* status) {
+  // The kernel may start before the one that prepares the tokens' codes, their
+  // scales and the zeros has ended: the weights are read at once, and who
+  // needs the others waits (griddepcontrol.wait).
   extern __shared__ unsigned char i8_smem_raw[];
   __shared__ I8Barriers bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -222,6 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       if (ring.round) warp_wait(&bar.raw_full[ring.slot], ring.turn ^ 1u, late);
     }
   } else if (warp == 3) {  // the tokens' codes
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     Ring ring;
     while (!broken && q.next(work)) {
       const int t0 = q.tn * work.nt + (int)rank * (work.nt / 2);
@@ -322,6 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     const int cols = work.nt / 2, c0 = part * cols;
     const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0;
     const uint32_t kept = tmem + lanes;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     int sums = 0;
     while (!broken && q.next(work)) {
       const int64_t o = (int64_t)q.tm * 256 + rank * 128 + 32 * quarter + lane;
@@ -384,7 +389,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       }
     }
   }
-  if (broken) atomicOr(status, BAKRON_DEV_TIMEOUT);
+  if (broken) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    atomicOr(status, BAKRON_DEV_TIMEOUT);
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -416,9 +424,10 @@ inline I8Work i8_work(int64_t T, int64_t K, int64_t N, int pairs) {
 }
 inline int64_t i8_slices(const I8Work& w) { return (int64_t)w.tiles_m * w.tiles_n * 16; }
 
+// early: the weights are not written by the kernel before, so this one may start during it.
 template <class T>
 cudaError_t int8_pair_launch(const int8_t* V, int64_t ldv, const void* codes, int64_t ldc, int64_t K, const I8Work& w,
-                             const I8Out<T>& out, int32_t* status, cudaStream_t stream) {
+                             const I8Out<T>& out, bool early, int32_t* status, cudaStream_t stream) {
   CUtensorMap mw, mx;
   cudaError_t e = make_tensor_map(&mw, TileMap{V, CU_TENSOR_MAP_DATA_TYPE_UINT8, out.outputs, K, ldv, 128, kI8K, true});
   if (e == cudaSuccess)
@@ -426,9 +435,17 @@ cudaError_t int8_pair_launch(const int8_t* V, int64_t ldv, const void* codes, in
   const int smem = w.ops * w.op_bytes() + w.raws * kI8Raw + 1024;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(int8_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8SmemMost + 1024);
   if (e != cudaSuccess) return e;
-  const unsigned grid = 2u * (unsigned)w.pairs;
-  int8_pair_kernel<T><<<grid, kI8Threads, smem, stream>>>(mw, mx, w, out, status);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)w.pairs);
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, int8_pair_kernel<T>, mw, mx, w, out, status);
 }
 
 }  // namespace bakron
