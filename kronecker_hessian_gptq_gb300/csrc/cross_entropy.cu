@@ -45,32 +45,28 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // c_t / max |c| of every token, and what the gradients are scaled by in the
-// end, max |c| / kGScale.  One block.
+// end, max |c| / kGScale.  One block.  (Targets that are too large are
+// reported by join_kernel.)
 __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* target, int64_t T, int64_t V, const float* given,
-                                                            float* coef, float* scale, int32_t* status) {
-  __shared__ int with, bad;
+                                                            float* coef, float* scale) {
+  __shared__ int with;
   __shared__ float red[32];
-  if (threadIdx.x == 0) with = bad = 0;
+  if (threadIdx.x == 0) with = 0;
   __syncthreads();
-  int n = 0, wrong = 0;
+  int n = 0;
   float top[1] = {0.f};
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const int64_t y = target[t];
-    if (y >= V) wrong = 1;
     if (y >= 0 && y < V) {
       ++n;
       if (given) top[0] = MaxOp()(fabsf(given[t]), top[0]);
     }
   }
   if (n) atomicAdd(&with, n);
-  if (wrong) atomicOr(&bad, 1);
   block_reduce<1>(top, red, MaxOp());
   __syncthreads();
   const float most = given ? top[0] : (with ? 1.f / (float)with : 0.f);
-  if (threadIdx.x == 0) {
-    *status = bad ? BAKRON_DEV_BAD_TARGET : 0;
-    *scale = most / kGScale;
-  }
+  if (threadIdx.x == 0) *scale = most / kGScale;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const bool has = target[t] >= 0 && target[t] < V;
     coef[t] = !has || most == 0.f ? 0.f : given ? given[t] / most : 1.f;
@@ -146,11 +142,27 @@ struct LogitsEpilogue {
 template <class T>
 __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t chunks, int64_t ld, const int64_t* target,
                                                    int64_t V, const T* H, int64_t ldh, const T* W, int64_t ldw, int64_t D,
-                                                   float* lse, float* loss) {
+                                                   float* lse, float* loss, int32_t* status) {
   __shared__ float red[64];
-  const float2* row = stats + (int64_t)blockIdx.x * ld;
+  // Launched while the logits are made: the target's logit needs only H and W.
   const int64_t y = target[blockIdx.x];
   const bool has = y >= 0 && y < V;
+  float t[2] = {0.f, 0.f};
+  if (has) {
+    const T *h = H + (int64_t)blockIdx.x * ldh, *w = W + y * ldw;
+    const int64_t whole = D / 8 * 8;
+    for (int64_t d = threadIdx.x * 8; d < whole; d += 1024) {
+      float a[8], b[8];
+      load_vec<T, 8>(h + d, a);
+      load_vec<T, 8>(w + d, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[1] = fmaf(a[i], b[i], t[1]);
+    }
+    if (whole + threadIdx.x < D) t[1] = fmaf(to_f32<T>(h[whole + threadIdx.x]), to_f32<T>(w[whole + threadIdx.x]), t[1]);
+  }
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (y >= V && threadIdx.x == 0) atomicOr(status, BAKRON_DEV_BAD_TARGET);
+  const float2* row = stats + (int64_t)blockIdx.x * ld;
   float m = -INFINITY, s = 0.f;
   for (int64_t c = threadIdx.x; c < chunks; c += 128) {
     const float2 e = row[c];
@@ -164,19 +176,7 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t 
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
   __syncthreads();
   top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float t[2] = {m == -INFINITY ? 0.f : s * exp2_approx(m - top), 0.f};
-  if (has) {
-    const T *h = H + (int64_t)blockIdx.x * ldh, *w = W + y * ldw;
-    const int64_t whole = D / 8 * 8;
-    for (int64_t d = threadIdx.x * 8; d < whole; d += 1024) {
-      float a[8], b[8];
-      load_vec<T, 8>(h + d, a);
-      load_vec<T, 8>(w + d, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[1] = fmaf(a[i], b[i], t[1]);
-    }
-    if (whole + threadIdx.x < D) t[1] = fmaf(to_f32<T>(h[whole + threadIdx.x]), to_f32<T>(w[whole + threadIdx.x]), t[1]);
-  }
+  t[0] = m == -INFINITY ? 0.f : s * exp2_approx(m - top);
   block_reduce<2>(t, red, SumOp());
   if (threadIdx.x == 0) {
     const float l = (top + log2f(t[0])) * kLn2;
@@ -366,7 +366,7 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
   };
   align(H, ldh, p.T, l.h);
   align(W, ldw, p.V, l.w);
-  coefficients_kernel<<<1, 1024, 0, stream>>>(p.target, p.T, p.V, p.coef, coef, scale, status);
+  if (grad) coefficients_kernel<<<1, 1024, 0, stream>>>(p.target, p.T, p.V, p.coef, coef, scale);
   const bool vec = grad && p.D % 8 == 0 && aligned_to(p.dH, 16) && aligned_to(p.dW, 16);
   auto out_map = [&](CUtensorMap* map, T* out, int64_t rows) {
     return make_tensor_map(map, TileMap{out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rows,
@@ -384,14 +384,24 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
       LogitsEpilogue<true> epi{{}, m, p.V, stats, chunks};
       e = make_tensor_map(&epi.map, TileMap{kept, CU_TENSOR_MAP_DATA_TYPE_UINT16, m, ldk, ldk, 32, 64, true});
       if (e != cudaSuccess) return e;
-      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
+      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
     } else {
       const LogitsEpilogue<false> epi{{}, m, p.V, stats, chunks};
-      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream);
+      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
     }
     if (e != cudaSuccess) return e;
-    join_kernel<T><<<(unsigned)m, 128, 0, stream>>>(stats, (p.V + kChunk - 1) / kChunk, chunks, target, p.V, h, ldh, W, ldw, p.D,
-                                                    p.lse + t, p.loss + t);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)m);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, join_kernel<T>, (const float2*)stats, (p.V + kChunk - 1) / kChunk, chunks, target, p.V, h, ldh,
+                           W, ldw, p.D, p.lse + t, p.loss + t, status);
+    if (e != cudaSuccess) return e;
     if (!grad) continue;
     for (int64_t r = 0; r < m; r += 65535)
       gradient_kernel<T><<<dim3((unsigned)((ldk / 8 + 255) / 256), (unsigned)std::min<int64_t>(65535, m - r)), 256, 0, stream>>>(

@@ -66,31 +66,58 @@ struct Prepare {
   int32_t* status;
 };
 
+// The 16 codes at v, of which `bytes` are there, zeros for the others.  Rows
+// may start anywhere: the codes come in the 32-bit words that hold them,
+// shifted into place.
+__device__ __forceinline__ uint4 load_codes(const int8_t* v, int bytes) {
+  const int off = (int)(reinterpret_cast<uintptr_t>(v) & 3);
+  const uint32_t* word = reinterpret_cast<const uint32_t*>(v - off);
+  uint32_t f[5], e[4];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) f[i] = 4 * i < off + bytes ? word[i] : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = __funnelshift_r(f[i], f[i + 1], 8 * off);
+    const int here = bytes - 4 * i;
+    if (here < 4) e[i] = here <= 0 ? 0u : e[i] & ((1u << (8 * here)) - 1u);
+  }
+  return make_uint4(e[0], e[1], e[2], e[3]);
+}
+__device__ __forceinline__ void store_codes(void* to, int64_t at, bool f16, const uint4& u) {
+  if (f16) {
+    uint32_t h[8];
+    i8_to_f16(u.x, h[0], h[1]);
+    i8_to_f16(u.y, h[2], h[3]);
+    i8_to_f16(u.z, h[4], h[5]);
+    i8_to_f16(u.w, h[6], h[7]);
+    uint4* f = reinterpret_cast<uint4*>(static_cast<__half*>(to) + at);
+    f[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    f[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<int8_t*>(to) + at) = u;
+  }
+}
 __device__ __forceinline__ void rewrite_codes(const Rewrite& w, int64_t at, int64_t step) {
   const int64_t per = (w.cols + 15) / 16, all = w.rows * per;
+  if (w.ld == w.cols && w.ldt == w.cols && reinterpret_cast<uintptr_t>(w.from) % 16 == 0 && w.cols % 16 == 0) {
+    // Dense on both sides: four loads of a thread on their way at once.
+    const uint4* from = reinterpret_cast<const uint4*>(w.from);
+    for (; at < all; at += 4 * step) {
+      uint4 u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = at + i * step < all ? __ldcs(from + at + i * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (at + i * step < all) store_codes(w.to, (at + i * step) * 16, w.f16, u[i]);
+    }
+    return;
+  }
   for (; at < all; at += step) {
-    const int64_t row = (uint64_t)at < (1ull << 32) && per < (1ll << 32) ? (uint32_t)at / (uint32_t)per : at / per;
-    const int64_t k = (at - row * per) * 16;
+    const int64_t row = at < (1ll << 32) ? (int64_t)((uint32_t)at / (uint32_t)per) : at / per;  // per < 2^13
+    const int64_t k = (at - row * per) * 16, left = w.cols - k;
     const int8_t* v = w.from + row * w.ld + k;
-    uint32_t e[4] = {0, 0, 0, 0};
-    if (reinterpret_cast<uintptr_t>(v) % 16 == 0 && k + 16 <= w.cols) {
-      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(v));
-      e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (k + i < w.cols) e[i / 4] |= (uint32_t)(uint8_t)v[i] << (8 * (i % 4));
-    }
-    if (w.f16) {
-      uint32_t h[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) i8_to_f16(e[i], h[2 * i], h[2 * i + 1]);
-      uint4* f = reinterpret_cast<uint4*>(static_cast<__half*>(w.to) + row * w.ldt + k);
-      f[0] = make_uint4(h[0], h[1], h[2], h[3]);
-      f[1] = make_uint4(h[4], h[5], h[6], h[7]);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<int8_t*>(w.to) + row * w.ldt + k) = make_uint4(e[0], e[1], e[2], e[3]);
-    }
+    const bool whole = left >= 16 && reinterpret_cast<uintptr_t>(v) % 16 == 0;
+    store_codes(w.to, row * w.ldt + k, w.f16, whole ? __ldcs(reinterpret_cast<const uint4*>(v)) : load_codes(v, left < 16 ? (int)left : 16));
   }
 }
 
@@ -192,10 +219,10 @@ void prepare_typed(const Prepare& p, unsigned grid, cudaStream_t stream) {
 template <class C>
 cudaError_t prepare_launch(Prepare p, int dtype, cudaStream_t stream) {
   if (!p.X) p.tokens = 0;
-  int64_t blocks = 0;  // of the rewriting: eight turns each, at most a few for each SM
+  int64_t blocks = 0;  // of the rewriting: 16 codes for each thread, at most what fills the SMs four times
   for (const Rewrite& w : p.rewrite)
-    if (w.from) blocks += (w.rows * ((w.cols + 15) / 16) + kPrepareThreads * 8 - 1) / (kPrepareThreads * 8);
-  blocks = std::min<int64_t>(blocks, 152 * 8);
+    if (w.from) blocks += (w.rows * ((w.cols + 15) / 16) + kPrepareThreads - 1) / kPrepareThreads;
+  blocks = std::min<int64_t>(blocks, 2 * pair_count() * 16);
   const unsigned grid = (unsigned)std::max<int64_t>(1, p.tokens + blocks);
   p.vec = aligned_to(p.X, 16) && p.ldx % (16 / (int64_t)elem_size(dtype)) == 0 && p.ldc % 8 == 0 &&
           aligned_to(p.codes, 8 * sizeof(C));
@@ -210,11 +237,6 @@ cudaError_t prepare_launch(Prepare p, int dtype, cudaStream_t stream) {
 
 // ------------------------------------------------------------ a few tokens
 
-__device__ __forceinline__ float load_value(const void* p, int dtype, int64_t i) {
-  return dtype == kF32   ? static_cast<const float*>(p)[i]
-         : dtype == kF16 ? __half2float(static_cast<const __half*>(p)[i])
-                         : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
 __device__ __forceinline__ void store_value(void* p, int dtype, int64_t i, float v) {
   if (dtype == kF32)
     static_cast<float*>(p)[i] = v;

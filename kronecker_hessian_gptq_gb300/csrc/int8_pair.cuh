@@ -382,10 +382,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       if (before + 1 != (uint32_t)pieces) continue;
       __threadfence();
       if (!in) continue;
-#pragma unroll 8
-      for (int c = 0; c < live; ++c) {
-        const int64_t t = t0 + c, at = t * out.outputs + o;
-        out.y[at] = from_f32<T>(fmaf((float)__ldcg(out.sums + at) * out.x_scales[t], ws, bias));
+      const int32_t* from = out.sums + t0 * out.outputs + o;
+      T* to = out.y + t0 * out.outputs + o;
+      for (int c = 0; c < live; c += 16) {  // 16 reads on their way at once
+        int v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = c + i < live ? __ldcg(from + (int64_t)(c + i) * out.outputs) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < live)
+            to[(int64_t)(c + i) * out.outputs] = from_f32<T>(fmaf((float)v[i] * out.x_scales[t0 + c + i], ws, bias));
       }
     }
   }

@@ -251,7 +251,7 @@ struct PairBox {
 template <bool kARows, bool kBRows, int kQuads, int kSegment, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 1)
     pair_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairWork work,
-                     uint32_t idesc, const __grid_constant__ Epi epi, int32_t* status) {
+                     uint32_t idesc, const __grid_constant__ Epi epi, int32_t* status, int32_t first_status) {
   extern __shared__ unsigned char pair_smem_raw[];
   const uint32_t base = (smem_u32(pair_smem_raw) + 1023u) & ~1023u;
   __shared__ PairBarriers bar;
@@ -262,6 +262,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
   const int pairs = gridDim.x / 2, mine = blockIdx.x / 2, units = work.units();
   bool broken = false;
 
+  asm volatile("griddepcontrol.launch_dependents;\n");
+  // This early nothing can have been reported.
+  if (first_status >= 0 && blockIdx.x == 0 && threadIdx.x == 0) *status = first_status;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(smem_u32(&bar.full[i])));
@@ -422,6 +425,7 @@ struct PairOperand {
 };
 
 // M x N tiles of A (M x K) and B (N x K).  bf16: both bf16, else both fp16.
+// first_status >= 0: the status word is set to it first.
 // Pairs of SMs on the current device.
 inline int pair_count() {
   int dev = 0, sms = 0;
@@ -432,7 +436,7 @@ inline int pair_count() {
 
 template <bool kARows, bool kBRows, int kQuads, int kSegment, class Epi>
 cudaError_t pair_gemm_launch(PairOperand a, PairOperand b, int64_t K, bool bf16, PairWork work, const Epi& epi,
-                             int32_t* status, cudaStream_t stream) {
+                             int32_t* status, cudaStream_t stream, int32_t first_status = -1) {
   const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap ma, mb;
   auto map = [&](CUtensorMap* m, const PairOperand& o, bool rows) {
@@ -450,7 +454,7 @@ cudaError_t pair_gemm_launch(PairOperand a, PairOperand b, int64_t K, bool bf16,
   const uint32_t t = bf16 ? 1u : 0u;
   const uint32_t idesc = (1u << 4) | (t << 7) | (t << 10) | ((kARows ? 1u : 0u) << 15) | ((kBRows ? 1u : 0u) << 16) |
                          ((256u >> 3) << 17) | ((256u >> 4) << 24);
-  kernel<<<grid, 128 + 128 * kQuads, pair_smem<kQuads>(), stream>>>(ma, mb, work, idesc, epi, status);
+  kernel<<<grid, 128 + 128 * kQuads, pair_smem<kQuads>(), stream>>>(ma, mb, work, idesc, epi, status, first_status);
   return cudaGetLastError();
 }
 
