@@ -415,17 +415,41 @@ cudaError_t rows_launch(const Int8Matmul& p, int32_t* status, cudaStream_t strea
 
 // ------------------------------------------------------------ many tokens
 
-// Scales a tile's exact sums and sends them out in whole lines.
+// Scales a tile's exact sums and sends them out in whole lines: 16-bit results
+// whose rows start on 16 bytes by TMA, others row by row.
 template <class T>
 struct ScaledEpilogue {
+  CUtensorMap map;
   int64_t tokens, outputs;
   const float *x_scales, *w_scales, *bias;
   T* y;
+  bool tma;  // then outputs is a multiple of 8 and the vectors start on 16 bytes
   __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, const int (&acc)[64],
                                              const PairBox& box) const {
-    if (row0 >= tokens) return;
+    if (row0 >= tokens || col >= outputs) return;
     const int here = (int)(tokens - row0 < 32 ? tokens - row0 : 32);
     const float s = box.lane < here ? x_scales[row0 + box.lane] : 0.f;
+    if constexpr (sizeof(T) == 2) {
+      if (tma) {
+        box.open();
+#pragma unroll
+        for (int c = 0; c < 64; c += 8) {
+          float w[8], b[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = b[i] = 0.f;
+          if (col + c < outputs) {
+            load_vec<float, 8>(w_scales + col + c, w);
+            if (bias) load_vec<float, 8>(bias + col + c, b);
+          }
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = fmaf((float)acc[c + i] * s, w[i], b[i]);
+          box.put(c / 8, pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+        }
+        box.send(&map, (int)col, (int)row0);
+        return;
+      }
+    }
 #pragma unroll
     for (int c = 0; c < 64; c += 32) {
       if (col + c >= outputs) break;
@@ -506,9 +530,14 @@ cudaError_t batch(const Int8Matmul& p, const Layout& l, char* ws, int32_t* statu
                                p.K, l.work, out, !copy, status, stream);
   }
   const PairWork work{(int)((p.T + 255) / 256), (int)((p.N + 255) / 256), 16, (int)((p.K + kPairK - 1) / kPairK), 1};
-  return pair_gemm_launch<false, false, 4, 1024 / kPairK>(
-      PairOperand{codes, p.T, ldc}, PairOperand{ws + l.weights, p.N, ldc}, p.K, false, work,
-      ScaledEpilogue<T>{p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y)}, status, stream);
+  ScaledEpilogue<T> epi{{}, p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y), false};
+  epi.tma = sizeof(T) == 2 && p.N % 8 == 0 && aligned_to(p.Y, 16) && aligned_to(p.scales, 16) && aligned_to(p.bias, 16);
+  if (epi.tma)
+    e = make_tensor_map(&epi.map, TileMap{p.Y, p.y_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                          p.T, p.N, p.N, 32, 64, true});
+  if (e != cudaSuccess) return e;
+  return pair_gemm_launch<false, false, 4, 1024 / kPairK>(PairOperand{codes, p.T, ldc}, PairOperand{ws + l.weights, p.N, ldc},
+                                                          p.K, false, work, epi, status, stream);
 }
 
 }  // namespace
