@@ -8,13 +8,13 @@
 // token with a negative target has loss 0 and c_t = 0.
 //
 // The logits come out of the tensor cores a 256 x 256 tile at a time
-// (pair_gemm.cuh).  The epilogue reduces each row's 128 columns to their
+// (pair_gemm.cuh).  The epilogue reduces each row's 64 columns to their
 // maximum and the sum of exponentials below it, and a second kernel joins a
-// row's pieces: the loss alone stores 8 bytes for 128 logits.
+// row's pieces: the loss alone stores 8 bytes for 64 logits.
 //
 // For the gradients a logit is kept, for one piece of the tokens at a time,
 // as the 16-bit fixed-point number round(2048 (m - x) log2 e), m the maximum
-// of its 128 columns: a relative error of exp(x) of at most 1.7e-4 (1e-4 rms,
+// of its 64 columns: a relative error of exp(x) of at most 1.7e-4 (1e-4 rms,
 // against 1.7e-3 rms of rounding to bf16 or 2.1e-4 to fp16), and a range of
 // 2^-32 below the maximum.  A pass over the piece turns it into G in place,
 // and G, 16-bit, is the operand of the two other products.  This reads and
@@ -32,7 +32,7 @@ namespace bakron {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kChunk = 128;             // columns that share a maximum
+constexpr int kChunk = 64;              // columns that share a maximum
 constexpr float kSteps = 2048.f;        // fixed-point steps in a factor of two
 constexpr float kGScale = 32768.f;      // G is stored times this, so that fp16 keeps p down to 2^-29
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;
@@ -83,54 +83,43 @@ struct LogitsEpilogue {
 
   __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, const PairSums& sums,
                                              const PairBox& box) const {
-    if (col >= V || row0 >= rows) return;
-    const bool whole = col + kChunk <= V;
-    const int left = whole ? kChunk : (int)(V - col);
-    float v[32];
+    if (row0 >= rows) return;
+#pragma unroll 1
+    for (int c = 0; c < 128 && col + c < V; c += kChunk) chunk(row0, col + c, c, sums, box);
+  }
+  __device__ __forceinline__ void chunk(int64_t row0, int64_t col, int at, const PairSums& sums, const PairBox& box) const {
+    const int left = V - col < kChunk ? (int)(V - col) : kChunk;
+    float v[2][32];
+    sums.load(at, v[0]);
+    sums.load(at + 32, v[1]);
+    if (left < kChunk) {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i >= left) v[i / 32][i % 32] = -INFINITY;
+    }
     float m = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < kChunk; c += 32) {
-      sums.load(c, v);
-      if (whole) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < left) m = fmaxf(m, v[i]);
-      }
-    }
+    for (int i = 0; i < kChunk; ++i) m = fmaxf(m, v[i / 32][i % 32]);
     m = m == -INFINITY ? 0.f : m * kLog2e;
+    if constexpr (kKeep) box.open();
     float s = 0.f;
-#pragma unroll 1
-    for (int c = 0; c < kChunk; c += 32) {
-      if (c >= left) break;
-      sums.load(c, v);
-      if (whole) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], kLog2e, -m);
-      } else {
+    for (int j = 0; j < kChunk; j += 8) {
+      uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = c + i < left ? fmaf(v[i], kLog2e, -m) : -INFINITY;
-      }
-      if constexpr (kKeep) {
-        // -kSteps v rounded to an integer in the low bits of 1.5 2^23 + it.
+      for (int i = 0; i < 8; ++i) {
+        const float x = fmaf(v[j / 32][j % 32 + i], kLog2e, -m);
+        // -kSteps x rounded to an integer in the low bits of 1.5 2^23 + it.
         // A NaN is lost here; its row's sum is NaN, which is what counts.
-        uint32_t w[16];
         constexpr float kMagic = 12582912.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = __byte_perm(__float_as_uint(fminf(fmaf(v[2 * i], -kSteps, kMagic), kMagic + 65535.f)),
-                             __float_as_uint(fminf(fmaf(v[2 * i + 1], -kSteps, kMagic), kMagic + 65535.f)), 0x5410);
-        const int half = (c & 32) >> 3;  // 32 columns are half of a box
-        if (half == 0) box.open();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) box.put(half + j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        if (half || c + 32 >= left) box.send(&map, (int)col + (c & ~32), (int)row0);
+        if constexpr (kKeep) w[i] = __float_as_uint(fminf(fmaf(x, -kSteps, kMagic), kMagic + 65535.f));
+        s += exp2_approx(x);
       }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s += exp2_approx(v[i]);
+      if constexpr (kKeep)
+        box.put(j / 8, __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[4], w[5], 0x5410),
+                __byte_perm(w[6], w[7], 0x5410));
     }
+    if constexpr (kKeep) box.send(&map, (int)col, (int)row0);
     if (row0 + box.lane < rows) stats[(row0 + box.lane) * chunks + col / kChunk] = make_float2(m, s);
   }
 };
@@ -316,7 +305,7 @@ struct Layout {
 };
 constexpr int kPlanPairs = 76;  // pairs of SMs the workspace is planned for
 Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
-  const int64_t n = piece_tokens(T, V, grad), chunks = tiles(V) * 2;
+  const int64_t n = piece_tokens(T, V, grad), chunks = tiles(V) * 4;
   Layout l = {};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -333,10 +322,8 @@ Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
     l.part = take(std::max(p > 1 ? (size_t)p * n * D * 4 : 0, p2 > 1 ? (size_t)p2 * (T % n) * D * 4 : 0));
     l.acc = take(n < T ? V * D * 4 : 0);
   }
-  if (copies) {
-    l.h = take(T * up8(D) * 2);
-    l.w = take(V * up8(D) * 2);
-  }
+  l.h = take(D % 64 || copies ? T * up64(D) * 2 : 0);
+  if (copies) l.w = take(V * up8(D) * 2);
   l.bytes = at;
   return l;
 }
@@ -349,23 +336,26 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
   const bool grad = p.dH != nullptr;
   const bool copies = !tma_rows(p.H, p.ldh) || !tma_rows(p.W, p.ldw);
   const Layout l = layout(p.T, p.D, p.V, grad, copies);
-  const int64_t n = piece_tokens(p.T, p.V, grad), chunks = tiles(p.V) * 2, ldk = up64(p.V);
+  const int64_t n = piece_tokens(p.T, p.V, grad), chunks = tiles(p.V) * 4, ldk = up64(p.V);
   float* coef = reinterpret_cast<float*>(ws + l.coef);
   float* scale = reinterpret_cast<float*>(ws + l.scale);
   float2* stats = reinterpret_cast<float2*>(ws + l.stats);
   uint16_t* kept = reinterpret_cast<uint16_t*>(ws + l.kept);
   const T *H = static_cast<const T*>(p.H), *W = static_cast<const T*>(p.W);
   int64_t ldh = p.ldh, ldw = p.ldw;
-  auto align = [&](const T*& x, int64_t& ld, int64_t rows, size_t to) {
-    if (tma_rows(x, ld)) return;
+  auto copy = [&](const T*& x, int64_t& ld, int64_t rows, size_t to, int64_t ldt) {
     uint16_t* y = reinterpret_cast<uint16_t*>(ws + to);
     for (int64_t r = 0; r < rows; r += 65535)
       align_rows_kernel<<<dim3((unsigned)((p.D + 255) / 256), (unsigned)std::min<int64_t>(65535, rows - r)), 256, 0, stream>>>(
-          reinterpret_cast<const uint16_t*>(x) + r * ld, ld, p.D, y + r * up8(p.D), up8(p.D));
-    x = reinterpret_cast<const T*>(y), ld = up8(p.D);
+          reinterpret_cast<const uint16_t*>(x) + r * ld, ld, p.D, y + r * ldt, ldt);
+    x = reinterpret_cast<const T*>(y), ld = ldt;
   };
-  align(H, ldh, p.T, l.h);
-  align(W, ldw, p.V, l.w);
+  // Rows of 16-bit values that do not start on 128 bytes make TMA fetch more
+  // lines (1021 x 1000 times 1000 x 50021: 88 us, from 60 with rows of 1024).
+  // H is small and read by two products, so it is copied then; W only where
+  // TMA cannot read it at all.
+  if (copies || (p.D % 64 && !(aligned_to(H, 128) && ldh % 64 == 0))) copy(H, ldh, p.T, l.h, up64(p.D));
+  if (!tma_rows(W, ldw)) copy(W, ldw, p.V, l.w, up8(p.D));
   if (grad) coefficients_kernel<<<1, 1024, 0, stream>>>(p.target, p.T, p.V, p.coef, coef, scale);
   const bool vec = grad && p.D % 8 == 0 && aligned_to(p.dH, 16) && aligned_to(p.dW, 16);
   auto out_map = [&](CUtensorMap* map, T* out, int64_t rows) {
