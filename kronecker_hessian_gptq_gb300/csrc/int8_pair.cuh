@@ -335,6 +335,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       const int live = (int)(out.tokens - t0 < cols ? out.tokens - t0 : cols);  // may be negative
       const bool in = o < out.outputs;
       const float ws = in ? out.w_scales[o] : 0.f, bias = in && out.bias ? out.bias[o] : 0.f;
+      // scales of the slice's tokens, one for each lane, handed out by shuffles
+      const float xs[2] = {lane < live ? out.x_scales[t0 + lane] : 0.f, 32 + lane < live ? out.x_scales[t0 + 32 + lane] : 0.f};
+      auto finish = [&](int c, const int(&v)[16]) {  // 16 tokens' results
+        T* to = out.y + (t0 + c) * out.outputs + o;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float s = __shfl_sync(0xffffffffu, c < 32 ? xs[0] : xs[1], (c & 16) + i);
+          if (in && c + i < live) to[i * out.outputs] = from_f32<T>(fmaf((float)v[i] * s, ws, bias));
+        }
+      };
       for (int k = q.k0; k < q.k1; k += kI8Segment, ++sums) {
         warp_wait(&bar.sum_full[sums & two], (uint32_t)(sums >> two) & 1u, broken);
         if (broken) break;
@@ -354,16 +364,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           }
           if (!last) {
             tmem_st16(kept + (uint32_t)c, v);
+          } else if (pieces == 1) {
+            finish(c, v);
           } else if (in) {
+            int32_t* to = out.sums + (t0 + c) * out.outputs + o;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (c + i >= live) break;
-              const int64_t t = t0 + c + i, at = t * out.outputs + o;
-              if (pieces == 1)
-                out.y[at] = from_f32<T>(fmaf((float)v[i] * out.x_scales[t], ws, bias));
-              else
-                atomicAdd(out.sums + at, v[i]);
-            }
+            for (int i = 0; i < 16; ++i)
+              if (c + i < live) atomicAdd(to + i * out.outputs, v[i]);
           }
         }
         tc_fence_before();
@@ -381,17 +388,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       before = __shfl_sync(0xffffffffu, before, 0);
       if (before + 1 != (uint32_t)pieces) continue;
       __threadfence();
-      if (!in) continue;
-      const int32_t* from = out.sums + t0 * out.outputs + o;
-      T* to = out.y + t0 * out.outputs + o;
+      const int32_t* sum = out.sums + t0 * out.outputs + o;
       for (int c = 0; c < live; c += 16) {  // 16 reads on their way at once
         int v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = c + i < live ? __ldcg(from + (int64_t)(c + i) * out.outputs) : 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < live)
-            to[(int64_t)(c + i) * out.outputs] = from_f32<T>(fmaf((float)v[i] * out.x_scales[t0 + c + i], ws, bias));
+        for (int i = 0; i < 16; ++i) v[i] = in && c + i < live ? __ldcg(sum + (c + i) * out.outputs) : 0;
+        finish(c, v);
       }
     }
   }
