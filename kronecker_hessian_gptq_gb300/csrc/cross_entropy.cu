@@ -241,17 +241,19 @@ struct GradientEpilogue {
       }
       const int64_t at = row0 * cols + col + c + box.lane;
       const bool in = col + c + box.lane < cols;
-      box.by_row(v, here, [&](int r, float x) {
-        if (!in) return;
-        const int64_t i = at + r * cols;
-        if (part) {
-          part[(int64_t)q.part * rows * cols + i] = x;
-          return;
-        }
-        if (acc && !first) x += acc[i];
-        if (acc && !last) acc[i] = x;
-        else out[i] = from_f32<T>(x * sc);
-      });
+      if (part) {
+        float* to = part + (int64_t)q.part * rows * cols + at;
+        box.by_row(v, here, in, [&](int r, float x) { to[r * cols] = x; });
+      } else if (!acc) {
+        box.by_row(v, here, in, [&](int r, float x) { out[at + r * cols] = from_f32<T>(x * sc); });
+      } else {
+        box.by_row(v, here, in, [&](int r, float x) {
+          const int64_t i = at + r * cols;
+          if (!first) x += acc[i];
+          if (!last) acc[i] = x;
+          else out[i] = from_f32<T>(x * sc);
+        });
+      }
     }
   }
 };

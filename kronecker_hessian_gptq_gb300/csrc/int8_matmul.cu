@@ -460,9 +460,7 @@ struct ScaledEpilogue {
       const bool in = o < outputs;
       const float w = in ? w_scales[o] : 0.f, b = in && bias ? bias[o] : 0.f;
       T* to = y + row0 * outputs + o;
-      box.by_row(v, here, [&](int r, float x) {
-        if (in) to[r * outputs] = from_f32<T>(fmaf(x, w, b));
-      });
+      box.by_row(v, here, in, [&](int r, float x) { to[r * outputs] = from_f32<T>(fmaf(x, w, b)); });
     }
   }
 };

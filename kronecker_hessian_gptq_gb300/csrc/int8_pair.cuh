@@ -123,16 +123,24 @@ __device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi
   asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(hi) : "r"(b), "r"(off));
 }
 
-// Columns of 32 lanes from and to tensor memory, complete on return (32
-// columns: after the wait for stores).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, int (&v)[16]) {
+// 32 columns of 32 lanes from and to tensor memory; several may be under way,
+// complete after the wait for loads or stores.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
+        "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr)
       : "memory");
+}
+// The loads of v are complete (and nothing that reads v moves ahead of this).
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -144,12 +152,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[30]), "r"(v[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const int (&v)[16]) {
+// 16 of v, from the kFrom-th on.
+template <int kFrom>
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
-      "tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(v[kFrom]), "r"(v[kFrom + 1]), "r"(v[kFrom + 2]), "r"(v[kFrom + 3]), "r"(v[kFrom + 4]), "r"(v[kFrom + 5]),
+      "r"(v[kFrom + 6]), "r"(v[kFrom + 7]), "r"(v[kFrom + 8]), "r"(v[kFrom + 9]), "r"(v[kFrom + 10]), "r"(v[kFrom + 11]),
+      "r"(v[kFrom + 12]), "r"(v[kFrom + 13]), "r"(v[kFrom + 14]), "r"(v[kFrom + 15])
       : "memory");
 }
 
@@ -337,12 +347,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       const float ws = in ? out.w_scales[o] : 0.f, bias = in && out.bias ? out.bias[o] : 0.f;
       // scales of the slice's tokens, one for each lane, handed out by shuffles
       const float xs[2] = {lane < live ? out.x_scales[t0 + lane] : 0.f, 32 + lane < live ? out.x_scales[t0 + 32 + lane] : 0.f};
-      auto finish = [&](int c, const int(&v)[16]) {  // 16 tokens' results
-        T* to = out.y + (t0 + c) * out.outputs + o;
+      auto finish = [&](int c, uint32_t(&v)[32]) {  // 32 tokens' results
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float s = __shfl_sync(0xffffffffu, c < 32 ? xs[0] : xs[1], (c & 16) + i);
-          if (in && c + i < live) to[i * out.outputs] = from_f32<T>(fmaf((float)v[i] * s, ws, bias));
+        for (int i = 0; i < 32; ++i)
+          v[i] = __float_as_uint(fmaf((float)(int)v[i] * __shfl_sync(0xffffffffu, xs[c >> 5], i), ws, bias));
+        if (!in) return;
+        T* to = out.y + (t0 + c) * out.outputs + o;
+        if (c + 32 <= live) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i, to += out.outputs) *to = from_f32<T>(__uint_as_float(v[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i, to += out.outputs)
+            if (c + i < live) *to = from_f32<T>(__uint_as_float(v[i]));
         }
       };
       for (int k = q.k0; k < q.k1; k += kI8Segment, ++sums) {
@@ -351,28 +368,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         tc_fence_after();
         const uint32_t from = kept + (1 + (uint32_t)(sums & two)) * nt;
         const bool last = k + kI8Segment >= q.k1;
-        for (int c = 0; c < live; c += 16) {  // the same for the whole warp
-          int v[16];
-          tmem_ld16(from + (uint32_t)c, v);
+        // 32 tokens at a time, the same for the whole warp; a load from tensor
+        // memory takes hundreds of cycles, so both are under way together.
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float2int_rn(__int_as_float(v[i]));
+        for (int c = 0; c < kI8Tokens / 2; c += 32) {
+          if (c >= live) break;
+          uint32_t v[32], w[32];
+          tmem_ld32_async(from + (uint32_t)c, v);
           if (k > q.k0) {
-            int w[16];
-            tmem_ld16(kept + (uint32_t)c, w);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += w[i];
+            tmem_ld32_async(kept + (uint32_t)c, w);
+            tmem_wait(w);
           }
+          tmem_wait(v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = (uint32_t)__float2int_rn(__uint_as_float(v[i])) + (k > q.k0 ? w[i] : 0u);
           if (!last) {
-            tmem_st16(kept + (uint32_t)c, v);
+            tmem_st16<0>(kept + (uint32_t)c, v);
+            if (c + 16 < cols) tmem_st16<16>(kept + (uint32_t)c + 16, v);  // what follows is the other warps'
           } else if (pieces == 1) {
             finish(c, v);
           } else if (in) {
             int32_t* to = out.sums + (t0 + c) * out.outputs + o;
+            if (c + 32 <= live) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i < live) atomicAdd(to + i * out.outputs, v[i]);
+              for (int i = 0; i < 32; ++i, to += out.outputs) atomicAdd(to, (int)v[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i, to += out.outputs)
+                if (c + i < live) atomicAdd(to, (int)v[i]);
+            }
           }
         }
+        if (!last) asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0)
@@ -388,11 +415,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       before = __shfl_sync(0xffffffffu, before, 0);
       if (before + 1 != (uint32_t)pieces) continue;
       __threadfence();
-      const int32_t* sum = out.sums + t0 * out.outputs + o;
-      for (int c = 0; c < live; c += 16) {  // 16 reads on their way at once
-        int v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = in && c + i < live ? __ldcg(sum + (c + i) * out.outputs) : 0;
+      for (int c = 0; c < kI8Tokens / 2; c += 32) {
+        if (c >= live) break;
+        const int32_t* sum = out.sums + (t0 + c) * out.outputs + o;
+        uint32_t v[32];  // 32 reads on their way at once
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          v[i] = in && c + i < live ? (uint32_t)__ldcg(sum) : 0u;
+          sum += out.outputs;
+        }
         finish(c, v);
       }
     }

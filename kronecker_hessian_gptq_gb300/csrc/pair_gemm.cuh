@@ -230,19 +230,29 @@ struct PairBox {
     }
   }
   // 32 fp32 sums of each row, then given back row by row, a column for each
-  // thread: f(r, v) with row r's sum in column `lane`.
+  // thread: f(r, v) with row r's sum in column `lane`, for the threads with
+  // `in`.  One branch for all rows: a branch in each row would cost more than
+  // the row.
   template <class F>
-  __device__ __forceinline__ void by_row(const float (&v)[32], int rows, F f) const {
+  __device__ __forceinline__ void by_row(const float (&v)[32], int rows, bool in, F f) const {
     open();
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       put(j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
     __syncwarp();
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-      float x;
-      asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(x) : "r"(piece(r, lane >> 2) + (uint32_t)(lane & 3) * 4u) : "memory");
-      f(r, x);
+    if (in) {
+      float x[32];
+#pragma unroll
+      for (int r = 0; r < 32; ++r)
+        asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(x[r]) : "r"(piece(r, lane >> 2) + (uint32_t)(lane & 3) * 4u) : "memory");
+      if (rows == 32) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) f(r, x[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+          if (r < rows) f(r, x[r]);
+      }
     }
     __syncwarp();
   }
