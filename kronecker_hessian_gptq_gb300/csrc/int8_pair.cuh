@@ -425,7 +425,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           v[i] = in && c + i < live ? (uint32_t)__ldcg(sum) : 0u;
           sum += out.outputs;
         }
-        finish(c, v);
+        T* to = out.y + (t0 + c) * out.outputs + o;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float s = __shfl_sync(0xffffffffu, xs[c >> 5], i);
+          if (in && c + i < live) *to = from_f32<T>(fmaf((float)(int)v[i] * s, ws, bias));
+          to += out.outputs;
+        }
       }
     }
   }
