@@ -24,13 +24,29 @@ _I8 = 3
 _KINDS = {"rms": 0, "layer": 1}
 _empty = torch.empty
 _current_device = torch.cuda.current_device
-_current_stream = torch.cuda.current_stream
+_entries = {}
+
+
+def _entry(name):
+    """The C entry point `name`, looked up once."""
+    f = _entries.get(name)
+    if f is None:
+        f = _entries[name] = getattr(_lib.load(), name)
+    return f
+
 
 def _call(name, *args):
-    """The C entry point `name` on `args`; the signatures are attached by load()."""
-    st = getattr(_lib.load(), name)(*args)
+    st = _entry(name)(*args)
     if st:
         _lib.check(st, name)
+
+
+def _handle(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The same without the Stream object around it, where torch offers it.
+_handle = getattr(torch._C, "_cuda_getCurrentRawStream", _handle)
 
 
 def _on(stream, call, *args, **kw):
@@ -84,7 +100,7 @@ def _vector(t, name, dtype, n, device):
 def _stream_on(device):
     if device != _current_device():
         raise ValueError(f"the tensors are on cuda:{device}, which is not the current device")
-    return _current_stream(device).cuda_stream
+    return _handle(device)
 
 
 def quantize_tokens(X, stream=None):
@@ -143,7 +159,7 @@ def int8_matmul(X, codes, scales, x_scales=None, bias=None, dtype=None, stream=N
     if T == 0:
         return Y, status.zero_()
     p = codes.data_ptr()
-    nbytes = _lib.load().bakron_int8_matmul_workspace_size(T, K, N, 1 if p % 16 or ldc % 16 else 0)
+    nbytes = _entry("bakron_int8_matmul_workspace_size")(T, K, N, 1 if p % 16 or ldc % 16 else 0)
     ws = _empty(nbytes, dtype=torch.uint8, device=at).data_ptr() if nbytes else None
     _call("bakron_int8_matmul", X.data_ptr(), kind, ldx, xs, p, ldc, w, b, T, K, N, Y.data_ptr(), out, ws, nbytes,
           status.data_ptr(), _stream_on(device))
@@ -249,7 +265,7 @@ def norm_residual_backward(dY, dZ, Y, H, post=None, gate=None, pre=None, alpha=1
             if t is not None:
                 t.zero_()
         return out
-    nbytes = _lib.load().bakron_norm_residual_backward_workspace_size(T, D, groups)
+    nbytes = _entry("bakron_norm_residual_backward_workspace_size")(T, D, groups)
     ws = _empty(nbytes, dtype=torch.uint8, device=at)
     to = {k: None if t is None else t.data_ptr() for k, t in out.items()}
     _call("bakron_norm_residual_backward", None if dY is None else dY.data_ptr(), lddy,
@@ -280,7 +296,7 @@ def _loss(name, H, W, targets, coef, grad):
         return (loss, lse, *out, status.zero_())
     h, w = H.data_ptr(), W.data_ptr()
     copies = 1 if h % 16 or w % 16 or ldh % 8 or ldw % 8 else 0  # some row does not start on 16 bytes
-    nbytes = _lib.load().bakron_linear_cross_entropy_workspace_size(T, D, V, grad, copies)
+    nbytes = _entry("bakron_linear_cross_entropy_workspace_size")(T, D, V, grad, copies)
     ws = _empty(nbytes, dtype=torch.uint8, device=at)
     more = (c,) if grad else ()
     _call(name, h, ldh, w, ldw, _CODES[dtype], y, *more, T, D, V, loss.data_ptr(), lse.data_ptr(),
