@@ -187,7 +187,8 @@ __device__ __forceinline__ void block_reduce(float (&v)[N], float* red, Op op) {
 }
 
 // One value over a block of at most 32 warps with one barrier; `red`: two
-// buffers of 64 floats that successive uses take turns with (see block_sums).
+// buffers of 64 floats that successive uses take turns with, so that one is
+// written again only after a barrier that every reader of it has passed.
 template <class Op>
 __device__ __forceinline__ float block_one(float v, float* red, int& turn, Op op) {
   const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -212,34 +213,29 @@ __device__ __forceinline__ float warp_sums4(const float (&v)[4]) {
   return s;
 }
 
-// Sums of two to four values over a block of at most 16 warps with one
-// barrier.  `red`: two buffers of 64 floats, which successive uses take turns
-// with (`turn`), so that a buffer is written again only after a barrier that
-// every reader of it has passed.
+// Sums of up to four values over a block of at most 32 warps with one barrier.
+// `red`: two buffers of 128 floats, zero at first, which successive uses take
+// turns with (`turn`), so that a buffer is written again only after a barrier
+// that every reader of it has passed.
 template <int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float* red, int& turn) {
-  static_assert(N >= 2 && N <= 4, "");
-  const int nw = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(N <= 4, "");
+  const int lane = threadIdx.x & 31;
   float w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) w[k] = k < N ? v[k] : 0.f;
-  float* to = red + 64 * turn;
+  float* to = red + 128 * turn;
   turn ^= 1;
   const float s = warp_sums4(w);
-  if ((lane & 7) == 0) to[(lane >> 3) * 16 + warp] = s;
+  if ((lane & 7) == 0) to[(lane >> 3) * 32 + (threadIdx.x >> 5)] = s;
   __syncthreads();
-  // value lane / 16 (and lane / 16 + 2) of warp lane % 16
-  const bool in = (lane & 15) < nw;
-  float a = in ? to[lane] : 0.f, b = N > 2 && in ? to[32 + lane] : 0.f;
+  // value lane / 8 of four warps
+  const float4 f = *reinterpret_cast<const float4*>(to + lane * 4);
+  float t = (f.x + f.y) + (f.z + f.w);
 #pragma unroll
-  for (int o = 8; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (N > 2) b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  v[0] = __shfl_sync(0xffffffffu, a, 0);
-  v[1] = __shfl_sync(0xffffffffu, a, 16);
-  if (N > 2) v[N > 2 ? 2 : 0] = __shfl_sync(0xffffffffu, b, 0);
-  if (N > 3) v[N > 3 ? 3 : 0] = __shfl_sync(0xffffffffu, b, 16);
+  for (int o = 4; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, t, 8 * k);
 }
 
 }  // namespace bakron

@@ -324,7 +324,11 @@ cudaError_t norm_residual_typed(const NormResidual& p, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ backward
 
-constexpr int kBwdThreads = 512;  // 8 elements each: 4096 columns for one block of a cluster
+// Values a column keeps in a block: the weights pre, post and the gate's row,
+// the sums of their gradients; the same of the biases.
+constexpr int bwd_held(bool layer) { return layer ? 9 : 6; }
+constexpr int kBwdRegisterD = 4096;  // columns up to which they are in registers, 512 threads of 8
+constexpr int kBwdPerSm = 8;         // blocks of an SM at most
 
 struct BackwardPlan {
   int64_t groups;  // at least 1
@@ -332,17 +336,24 @@ struct BackwardPlan {
   int64_t bpg;     // ranges that share a group; 1 where a range holds whole groups
   int cluster;     // thread blocks that share a row range, each with a part of the columns
   int threads;
+  bool shared;
+  int smem;
 };
 
-BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups) {
+BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups, bool layer) {
   BackwardPlan b;
   b.groups = std::max<int64_t>(1, groups);
+  b.shared = D > kBwdRegisterD;
   const int64_t each = T / b.groups;
+  // columns of a block: 32 bytes of shared memory hold a value for 8 of them
+  const int64_t most_cols = !b.shared ? kBwdRegisterD : std::min(1024, 220 * 1024 / 32 / bwd_held(layer) / 32 * 32) * 8;
   b.cluster = 1;
-  while ((int64_t)b.cluster * kBwdThreads * 8 < D) b.cluster *= 2;
+  while (b.cluster * most_cols < D) b.cluster *= 2;
   const int64_t per = (D + b.cluster - 1) / b.cluster;
-  b.threads = (int)std::max<int64_t>(1, (per + 255) / 256) * 32;
-  const int64_t most = std::max<int64_t>(1, kSms * (kBwdThreads / b.threads) / b.cluster);  // that run at once
+  b.threads = (int)((per + 255) / 256) * 32;
+  b.smem = b.shared ? b.threads * 32 * bwd_held(layer) : 0;
+  // ranges that run at once
+  const int64_t most = std::max<int64_t>(1, kSms * (b.shared ? 1 : std::min(512 / b.threads, kBwdPerSm)) / b.cluster);
   if (b.groups <= most) {
     b.bpg = std::max<int64_t>(1, std::min(each, most / b.groups));
     b.nb = b.groups * b.bpg;
@@ -385,14 +396,71 @@ __device__ __forceinline__ void cluster_sums(float (&v)[N], float* red, float (*
 // Planes of the partial column sums, nb x D fp32 each.
 enum Plane { kPost = 0, kPre = 1, kGate = 2, kPostBias = 3, kPreBias = 4, kPlanes = 5 };
 
-// A block (or, for wide rows, a cluster of them) walks over a range of rows
-// with the weights and the columns' sums in registers: 8 columns for each
-// thread.  The next row is on its way while one is worked on; 16 warps with
-// 128 registers fill an SM, and nothing else would cover the loads.
-template <class T, int VEC, bool kLayer>
-__global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackward p, BackwardPlan plan, float* part) {
-  __shared__ float red[2 * 64];
+// An fp32 value for each of a thread's 8 columns: in registers, or in shared
+// memory as two vectors of four that lie `blockDim.x` vectors apart, free of
+// bank conflicts.
+template <bool kShared>
+struct Held {
+  F2 v[kShared ? 1 : 4];
+  float4* p;
+  __device__ __forceinline__ Held(float* base, int which)
+      : p(kShared ? reinterpret_cast<float4*>(base) + which * 2 * blockDim.x + threadIdx.x : nullptr) {}
+  __device__ __forceinline__ void get(F2 (&x)[4]) const {
+    if constexpr (kShared) {
+      const float4 a = p[0], b = p[blockDim.x];
+      x[0] = f2(a.x, a.y), x[1] = f2(a.z, a.w), x[2] = f2(b.x, b.y), x[3] = f2(b.z, b.w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = v[k];
+    }
+  }
+  __device__ __forceinline__ void set(const F2 (&x)[4]) {
+    if constexpr (kShared) {
+      float e[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) split(x[k], e[2 * k], e[2 * k + 1]);
+      p[0] = make_float4(e[0], e[1], e[2], e[3]);
+      p[blockDim.x] = make_float4(e[4], e[5], e[6], e[7]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = x[k];
+    }
+  }
+  __device__ __forceinline__ void fill(float x) {
+    const F2 e[4] = {f2(x), f2(x), f2(x), f2(x)};
+    set(e);
+  }
+  // += a b
+  __device__ __forceinline__ void add(const F2 (&a)[4], const F2 (&b)[4]) {
+    F2 x[4];
+    get(x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = fma2(a[k], b[k], x[k]);
+    set(x);
+  }
+  __device__ __forceinline__ void add(const F2 (&a)[4]) {
+    F2 x[4];
+    get(x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = x[k] + a[k];
+    set(x);
+  }
+};
+
+// A block (or, for the widest rows, a cluster of them) walks over a range of
+// rows, 8 columns for each thread, with the next row on its way.  The weights
+// and the columns' sums are each thread's own: in registers up to 4096 columns
+// (16384 x 4096 in bf16: 172 us; 222 with them in shared memory, which adds
+// instructions to a kernel that is bound by issuing them), in shared memory
+// for wider rows, which halves the blocks that share a row and wait for one
+// another twice in each (4096 x 14336 in bf16: 279 us, 550 with registers).
+template <class T, int VEC, bool kLayer, bool kShared>
+__global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(NormBackward p, BackwardPlan plan, float* part) {
+  extern __shared__ __align__(16) float bwd_smem[];
+  __shared__ __align__(16) float red[2 * 128];
   __shared__ float slot[2][4];
+  for (int i = threadIdx.x; i < 2 * 128; i += blockDim.x) red[i] = 0.f;
+  __syncthreads();
   int turn = 0;
   const int cluster = plan.cluster;
   const int64_t b = blockIdx.x / cluster;
@@ -410,16 +478,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackw
     hi = (b + 1) * plan.groups / plan.nb * each;
   }
   const Columns<T, VEC, 1> c(rank * (int)blockDim.x + (int)threadIdx.x, cluster * (int)blockDim.x, D);
-  F2 wpre[4], wpost[4], bpost[kLayer ? 4 : 1], gt[4];
-  c.fetch32(p.pre, 0.f, wpre);
-  c.fetch32(p.post, 1.f, wpost);
-  if constexpr (kLayer) c.fetch32(p.post_bias, 0.f, bpost);
-  F2 apost[4], apre[4], agate[4], apostb[kLayer ? 4 : 1], apreb[kLayer ? 4 : 1];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    gt[k] = f2(1.f);
-    apost[k] = apre[k] = agate[k] = f2(0.f);
-    if constexpr (kLayer) apostb[k] = apreb[k] = f2(0.f);
+  Held<kShared> wpre(bwd_smem, 0), wpost(bwd_smem, 1), gate(bwd_smem, 2), apre(bwd_smem, 3), apost(bwd_smem, 4),
+      agate(bwd_smem, 5), bpost(bwd_smem, 6), apreb(bwd_smem, 7), apostb(bwd_smem, 8);  // the last three: layer norms only
+  {
+    F2 v[4];
+    c.fetch32(p.pre, 0.f, v);
+    wpre.set(v);
+    c.fetch32(p.post, 1.f, v);
+    wpost.set(v);
+    gate.fill(1.f);
+    apre.fill(0.f);
+    apost.fill(0.f);
+    agate.fill(0.f);
+    if constexpr (kLayer) {
+      apreb.fill(0.f);
+      apostb.fill(0.f);
+      c.fetch32(p.post_bias, 0.f, v);
+      bpost.set(v);
+    }
   }
   const T *py = static_cast<const T*>(p.Y) + lo * p.ldy, *ph = p.H ? static_cast<const T*>(p.H) + lo * p.ldh : nullptr;
   const T* pdy = p.dY ? static_cast<const T*>(p.dY) + lo * p.lddy : nullptr;
@@ -433,15 +509,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackw
     c.fetch(pdz, rdz);
   };
   if (lo < hi) fetch_row();
-  int64_t group = lo < hi ? lo / each : 0, left = 0;  // rows left in the group
+  int64_t group = 0, left = 0;  // rows left in the group
   for (int64_t row = lo; row < hi; ++row) {
     if (left == 0) {
       group = row / each;
       left = (group + 1) * each - row;
       if (p.gate) {
         Raw8<T> g[1];
+        F2 v[4];
         c.fetch(static_cast<const T*>(p.gate) + group * p.ldg, g);
-        open_all<T, 1>(g, gt);
+        open_all<T, 1>(g, v);
+        gate.set(v);
       }
     }
     --left;
@@ -468,32 +546,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackw
       for (int k = 0; k < 4; ++k) y[k] = y[k] + my, h[k] = h[k] + mh;
       c.mask(y);
       c.mask(h);
+      if (p.dZ) apreb.add(dz);
     }
     float s[4];
-    F2 q[4];
+    F2 w[4];
+    wpre.get(w);
     {
       F2 yy = f2(0.f), qy = f2(0.f), hh = f2(0.f), qq = f2(0.f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        q[k] = dz[k] * wpre[k];
+        w[k] = dz[k] * w[k];
         yy = fma2(y[k], y[k], yy);
-        qy = fma2(q[k], y[k], qy);
+        qy = fma2(w[k], y[k], qy);
         hh = fma2(h[k], h[k], hh);
-        if constexpr (kLayer) qq = qq + q[k];
+        if constexpr (kLayer) qq = qq + w[k];
       }
       s[0] = sum(yy), s[1] = sum(qy), s[2] = sum(hh), s[3] = kLayer ? sum(qq) : 0.f;
     }
     cluster_sums<4>(s, red, slot, cluster, turn);
     if (p.dZ) {
       const float r = rsqrtf(fmaf(s[0], invd, p.eps));
-      const F2 r2 = f2(r), c1 = f2(-r * r * r * s[1] * invd), c0 = f2(-r * s[3] * invd);
+      const F2 r2 = f2(r), c1 = f2(-r * r * s[1] * invd), c0 = f2(-r * s[3] * invd);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        dt[k] = fma2(y[k], c1, fma2(q[k], r2, dt[k]));
+        y[k] = y[k] * r2;
+        dt[k] = fma2(y[k], c1, fma2(w[k], r2, dt[k]));
         if constexpr (kLayer) dt[k] = dt[k] + c0;
-        apre[k] = fma2(dz[k], y[k] * r2, apre[k]);
-        if constexpr (kLayer) apreb[k] = apreb[k] + dz[k];
       }
+      apre.add(dz, y);
       if constexpr (kLayer) c.mask(dt);
     }
     Raw8<T> out[1];
@@ -507,26 +587,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackw
     }
     if (!p.H) continue;
     const float r = p.post ? rsqrtf(fmaf(s[2], invd, p.eps)) : 1.f;
-    F2 tn = f2(0.f), tq = f2(0.f);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const F2 n = h[k] * f2(r);
-      const F2 du = dt[k] * gt[k];
+    for (int k = 0; k < 4; ++k) h[k] = h[k] * f2(r);  // the unit row
+    wpost.get(w);
+    if (p.dgate) {
+      F2 u[4];
       if constexpr (kLayer) {
-        agate[k] = fma2(dt[k], fma2(n, wpost[k], bpost[k]), agate[k]);
-        apostb[k] = apostb[k] + du;
+        bpost.get(u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = fma2(h[k], w[k], u[k]);
       } else {
-        agate[k] = fma2(dt[k], n * wpost[k], agate[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = h[k] * w[k];
       }
-      apost[k] = fma2(du, n, apost[k]);
-      dt[k] = du * wpost[k];
-      tn = fma2(dt[k], n, tn);
-      if constexpr (kLayer) tq = tq + dt[k];
+      agate.add(dt, u);
+    }
+    if (p.gate) {
+      F2 g[4];
+      gate.get(g);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dt[k] = dt[k] * g[k];
     }
     if (p.post) {
+      apost.add(dt, h);
+      if constexpr (kLayer) apostb.add(dt);
+      F2 tn = f2(0.f), tq = f2(0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        dt[k] = dt[k] * w[k];
+        tn = fma2(dt[k], h[k], tn);
+        if constexpr (kLayer) tq = tq + dt[k];
+      }
       float t[2] = {sum(tn), kLayer ? sum(tq) : 0.f};
       cluster_sums<2>(t, red, slot, cluster, turn);
-      const F2 c1 = f2(-t[0] * invd * r * r), c0 = f2(-t[1] * invd * r);
+      const F2 c1 = f2(-t[0] * invd * r), c0 = f2(-t[1] * invd * r);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         dt[k] = fma2(h[k], c1, dt[k] * f2(r));
@@ -537,19 +631,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(NormBackw
     c.put(pdh, out);
     pdh += D;
     if (p.dgate && left == 0 && plan.bpg == 1) {  // this range holds the whole group
-      c.put32(p.dgate + group * p.D, agate);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) agate[k] = f2(0.f);
+      F2 v[4];
+      agate.get(v);
+      c.put32(p.dgate + group * p.D, v);
+      agate.fill(0.f);
     }
   }
   const int64_t plane = plan.nb * p.D;
   float* mine = part + b * p.D;
-  if (p.dpost) c.put32(mine + kPost * plane, apost);
-  if (p.dpre) c.put32(mine + kPre * plane, apre);
-  if (p.dgate && plan.bpg > 1) c.put32(mine + kGate * plane, agate);
+  auto put = [&](const float* want, const Held<kShared>& from, int q) {
+    if (!want) return;
+    F2 v[4];
+    from.get(v);
+    c.put32(mine + q * plane, v);
+  };
+  put(p.dpost, apost, kPost);
+  put(p.dpre, apre, kPre);
+  put(plan.bpg > 1 ? p.dgate : nullptr, agate, kGate);
   if constexpr (kLayer) {
-    if (p.dpost_bias) c.put32(mine + kPostBias * plane, apostb);
-    if (p.dpre_bias) c.put32(mine + kPreBias * plane, apreb);
+    put(p.dpost_bias, apostb, kPostBias);
+    put(p.dpre_bias, apreb, kPreBias);
   }
   if (cluster > 1)  // the others may still read this block's slots
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -588,18 +689,22 @@ __global__ void __launch_bounds__(512) column_sums_kernel(ColumnSums a) {
 
 template <class T, int VEC>
 cudaError_t norm_backward_typed(const NormBackward& p, float* part, cudaStream_t stream) {
-  const BackwardPlan plan = backward_plan(p.T, p.D, p.groups);
+  const BackwardPlan plan = backward_plan(p.T, p.D, p.groups, p.layer);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(plan.nb * plan.cluster));
   cfg.blockDim = dim3((unsigned)plan.threads);
+  cfg.dynamicSmemBytes = (size_t)plan.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)plan.cluster, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = p.layer ? cudaLaunchKernelEx(&cfg, norm_backward_kernel<T, VEC, true>, p, plan, part)
-                          : cudaLaunchKernelEx(&cfg, norm_backward_kernel<T, VEC, false>, p, plan, part);
+  auto kernel = plan.shared ? (p.layer ? norm_backward_kernel<T, VEC, true, true> : norm_backward_kernel<T, VEC, false, true>)
+                            : (p.layer ? norm_backward_kernel<T, VEC, true, false> : norm_backward_kernel<T, VEC, false, false>);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, kernel, p, plan, part);
   if (e != cudaSuccess) return e;
   ColumnSums a = {};
   a.part = part;
@@ -646,7 +751,7 @@ cudaError_t norm_residual_launch(const NormResidual& p, cudaStream_t stream) {
 }
 
 size_t norm_backward_workspace_bytes(int64_t T, int64_t D, int64_t groups) {
-  return (size_t)kPlanes * backward_plan(T, D, groups).nb * D * 4;
+  return (size_t)kPlanes * std::max(backward_plan(T, D, groups, false).nb, backward_plan(T, D, groups, true).nb) * D * 4;
 }
 
 cudaError_t norm_backward_launch(const NormBackward& p, void* ws, cudaStream_t stream) {
