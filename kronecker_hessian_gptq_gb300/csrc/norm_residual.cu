@@ -657,34 +657,36 @@ __global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(
 }
 
 // Sums the ranges' partial rows in a fixed order: 32 columns for each block,
-// 16 threads for each column.
+// 32 threads for each column.
 struct ColumnSums {
   float* out[kPlanes];
   const float* part;
-  int64_t nb, bpg, groups, D;
+  int64_t nb, bpg, D;
   int first[kPlanes + 1];  // blockIdx.y of a plane's first output row
 };
-__global__ void __launch_bounds__(512) column_sums_kernel(ColumnSums a) {
-  __shared__ float red[16][33];
-  int q = 0;
-  while ((int)blockIdx.y >= a.first[q + 1]) ++q;
-  const int64_t r = (int64_t)blockIdx.y - a.first[q];
-  const int64_t from = q == kGate ? r * a.bpg : 0, n = q == kGate ? a.bpg : a.nb;
+__global__ void __launch_bounds__(1024) column_sums_kernel(ColumnSums a) {
+  __shared__ float red[32][33];
+  const int row = (int)blockIdx.y;
+  int q = 0, first = 0;
+  float* out = a.out[0];
+#pragma unroll
+  for (int k = 1; k < kPlanes; ++k)
+    if (row >= a.first[k]) q = k, first = a.first[k], out = a.out[k];
+  const int64_t r = row - first;
+  const int n = (int)(q == kGate ? a.bpg : a.nb);
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (c < a.D) {
-    const float* x = a.part + (q * a.nb + from) * a.D + c;
+    const float* x = a.part + (q * a.nb + (q == kGate ? r * a.bpg : 0) + threadIdx.y) * a.D + c;
 #pragma unroll 4
-    for (int64_t i = threadIdx.y; i < n; i += 16) s += x[i * a.D];
+    for (int i = threadIdx.y; i < n; i += 32, x += 32 * a.D) s += *x;
   }
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && c < a.D) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t += red[i][threadIdx.x];
-    a.out[q][r * a.D + c] = t;
-  }
+  // a warp for each column, a lane for each of its threads' sums
+  s = warp_reduce(red[threadIdx.x][threadIdx.y], SumOp());
+  const int64_t to = (int64_t)blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && to < a.D) out[r * a.D + to] = s;
 }
 
 template <class T, int VEC>
@@ -708,7 +710,7 @@ cudaError_t norm_backward_typed(const NormBackward& p, float* part, cudaStream_t
   if (e != cudaSuccess) return e;
   ColumnSums a = {};
   a.part = part;
-  a.nb = plan.nb, a.bpg = plan.bpg, a.groups = plan.groups, a.D = p.D;
+  a.nb = plan.nb, a.bpg = plan.bpg, a.D = p.D;
   float* outs[kPlanes] = {p.dpost, p.dpre, plan.bpg > 1 ? p.dgate : nullptr, p.dpost_bias, p.dpre_bias};
   int rows = 0;
   for (int q = 0; q < kPlanes; ++q) {
@@ -717,7 +719,7 @@ cudaError_t norm_backward_typed(const NormBackward& p, float* part, cudaStream_t
     if (outs[q]) rows += q == kGate ? (int)plan.groups : 1;
   }
   a.first[kPlanes] = rows;
-  if (rows) column_sums_kernel<<<dim3((unsigned)((p.D + 31) / 32), (unsigned)rows), dim3(32, 16), 0, stream>>>(a);
+  if (rows) column_sums_kernel<<<dim3((unsigned)((p.D + 31) / 32), (unsigned)rows), dim3(32, 32), 0, stream>>>(a);
   return cudaGetLastError();
 }
 
