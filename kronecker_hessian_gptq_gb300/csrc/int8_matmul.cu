@@ -25,15 +25,21 @@
 namespace bakron {
 namespace {
 
-constexpr int64_t kRowTokens = 8;
-constexpr int64_t kPairTokens = 1024;
+// Where the next way becomes the faster one (us on the GPU for 4096 -> 4096,
+// 4096 -> 14336 and 14336 -> 4096): 4 tokens by rows 9, 17, 24 and 8 tokens 14,
+// 26, 39, where the tensor cores take 16, 20, 24 for either; 768 tokens without
+// the conversion 41, 99, 102, with it 42, 109, 123, and 1024 tokens 45, 125, 131
+// against 44, 110, 129.
+constexpr int64_t kRowTokens = 4;
+constexpr int64_t kPairTokens = 768;
+constexpr int kPlanPairs = 76;  // pairs of SMs that work is planned for
 constexpr int kRowThreads = 1024;
 constexpr int64_t kRowSmem = 200 * 1024;  // codes of the tokens that a block keeps
 
 int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
 int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
 // Tokens that the row kernel is compiled for.
-int row_tokens(int64_t T) { return T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8; }
+int row_tokens(int64_t T) { return T <= 1 ? 1 : T <= 2 ? 2 : 4; }
 bool by_rows(int64_t T, int64_t K) { return T <= kRowTokens && row_tokens(T) * up16(K) <= kRowSmem; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -469,7 +475,6 @@ struct Layout {
   size_t codes, scales, zeros, arrived, sums, weights, end_zeros, bytes;
   I8Work work;
 };
-constexpr int kPlanPairs = 76;
 
 // copies: with room for the weights in aligned rows.
 Layout layout(int64_t T, int64_t K, int64_t N, bool copies) {
@@ -528,14 +533,14 @@ cudaError_t batch(const Int8Matmul& p, const Layout& l, char* ws, int32_t* statu
                                p.K, l.work, out, !copy, status, stream);
   }
   const PairWork work{(int)((p.T + 255) / 256), (int)((p.N + 255) / 256), 16, (int)((p.K + kPairK - 1) / kPairK), 1};
+  const PairOperand pc{codes, p.T, ldc}, pw{ws + l.weights, p.N, ldc};
   ScaledEpilogue<T> epi{{}, p.T, p.N, s, p.scales, p.bias, static_cast<T*>(p.Y), false};
   epi.tma = sizeof(T) == 2 && p.N % 8 == 0 && aligned_to(p.Y, 16) && aligned_to(p.scales, 16) && aligned_to(p.bias, 16);
   if (epi.tma)
     e = make_tensor_map(&epi.map, TileMap{p.Y, p.y_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                                           p.T, p.N, p.N, 32, 64, true});
   if (e != cudaSuccess) return e;
-  return pair_gemm_launch<false, false, 4, 1024 / kPairK>(PairOperand{codes, p.T, ldc}, PairOperand{ws + l.weights, p.N, ldc},
-                                                          p.K, false, work, epi, status, stream);
+  return pair_gemm_launch<false, false, 4, 1024 / kPairK>(pc, pw, p.K, false, work, epi, status, stream);
 }
 
 }  // namespace
@@ -555,8 +560,7 @@ cudaError_t int8_matmul_launch(const Int8Matmul& p, void* ws, int32_t* status_de
     switch (row_tokens(p.T)) {
       case 1: return rows_launch<1>(p, status_dev, stream);
       case 2: return rows_launch<2>(p, status_dev, stream);
-      case 4: return rows_launch<4>(p, status_dev, stream);
-      default: return rows_launch<8>(p, status_dev, stream);
+      default: return rows_launch<4>(p, status_dev, stream);
     }
   }
   const Layout l = layout(p.T, p.K, p.N, !tma_codes(p));

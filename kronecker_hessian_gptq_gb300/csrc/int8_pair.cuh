@@ -4,7 +4,7 @@
 // The chip has no fast 8-bit integer products (tcgen05 kind::i8 is absent from
 // sm_103a), but an 8-bit integer is exact in fp16, its products are exact in
 // fp32, and sums of 1024 of them stay below 2^24: so the weights are read as
-// bytes, converted on their way through shared memory, and multiplied with
+// bytes, converted on their way to the tensor cores and multiplied with
 // kind::f16, and sums of at most 1024 terms are joined as 32-bit integers.
 //
 // A cluster of two blocks takes 256 outputs (the MMA's rows, 128 for each
@@ -451,7 +451,9 @@ inline I8Work i8_work(int64_t T, int64_t K, int64_t N, int pairs) {
   I8Work w;
   w.tiles_m = (int)((N + 255) / 256);
   w.tiles_n = (int)((T + kI8Tokens - 1) / kI8Tokens);
-  w.nt = (int)(((T + w.tiles_n - 1) / w.tiles_n + 31) / 32 * 32);
+  // At least 64: an MMA takes no less time for 32 (24 tokens 4096 -> 14336: 25
+  // us, so 21).
+  w.nt = std::max(64, (int)(((T + w.tiles_n - 1) / w.tiles_n + 31) / 32 * 32));
   w.tiles_n = (int)((T + w.nt - 1) / w.nt);
   w.ksteps = (int)((K + kI8K - 1) / kI8K);
   // Whole tiles, or equal shares of all steps?  In steps of K: a tile's end

@@ -94,37 +94,25 @@ struct Ring {
 // 0.1 s (2^28 cycles); afterwards `broken` is set for the whole warp, and
 // later waits return at once.  Every branch is taken by a vote, so that the
 // compiler knows the warp to stay together: the descriptors of the MMAs then
-// live in uniform registers (45 cycles to issue one, else 110).
-__device__ __forceinline__ uint32_t peek(uint64_t* mbar, uint32_t parity) {
+// live in uniform registers (issuing four with the wait takes 360 to 480
+// cycles, so 480 to 600 without), and the first look costs no clock reading.
+__device__ __forceinline__ bool phase_done(uint64_t* mbar, uint32_t parity) {
   uint32_t done;
   asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
                : "=r"(done)
                : "r"(smem_u32(mbar)), "r"(parity)
                : "memory");
-  return done;
+  return __all_sync(0xffffffffu, done) != 0;
 }
-// A look that does not wait at all (try_wait may hold a thread for a while).
-__device__ __forceinline__ uint32_t glance(uint64_t* mbar, uint32_t parity) {
-  uint32_t done;
-  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(done)
-               : "r"(smem_u32(mbar)), "r"(parity)
-               : "memory");
-  return done;
-}
-// `seen` is an earlier look at the same phase, whose latency other work has covered.
-__device__ __forceinline__ void warp_wait(uint64_t* mbar, uint32_t parity, bool& broken, uint32_t seen) {
-  if (broken || __all_sync(0xffffffffu, seen)) return;
+__device__ __forceinline__ void warp_wait(uint64_t* mbar, uint32_t parity, bool& broken) {
+  if (broken || phase_done(mbar, parity)) return;
   const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, peek(mbar, parity))) {
+  while (!phase_done(mbar, parity)) {
     if (__any_sync(0xffffffffu, clock64() - t0 > (1ll << 28))) {
       broken = true;
       return;
     }
   }
-}
-__device__ __forceinline__ void warp_wait(uint64_t* mbar, uint32_t parity, bool& broken) {
-  warp_wait(mbar, parity, broken, peek(mbar, parity));
 }
 // One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -241,17 +229,23 @@ struct PairBox {
       put(j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
     __syncwarp();
     if (in) {
-      float x[32];
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 8) {
+        float x[8];
 #pragma unroll
-      for (int r = 0; r < 32; ++r)
-        asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(x[r]) : "r"(piece(r, lane >> 2) + (uint32_t)(lane & 3) * 4u) : "memory");
-      if (rows == 32) {
+        for (int r = 0; r < 8; ++r)
+          asm volatile("ld.shared.f32 %0, [%1];\n"
+                       : "=f"(x[r])
+                       : "r"(piece(r0 + r, lane >> 2) + (uint32_t)(lane & 3) * 4u)
+                       : "memory");
+        if (r0 + 8 <= rows) {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) f(r, x[r]);
-      } else {
+          for (int r = 0; r < 8; ++r) f(r0 + r, x[r]);
+        } else {
 #pragma unroll
-        for (int r = 0; r < 32; ++r)
-          if (r < rows) f(r, x[r]);
+          for (int r = 0; r < 8; ++r)
+            if (r0 + r < rows) f(r0 + r, x[r]);
+        }
       }
     }
     __syncwarp();
