@@ -213,29 +213,53 @@ __device__ __forceinline__ float warp_sums4(const float (&v)[4]) {
   return s;
 }
 
-// Sums of up to four values over a block of at most 32 warps with one barrier.
-// `red`: two buffers of 128 floats, zero at first, which successive uses take
-// turns with (`turn`), so that a buffer is written again only after a barrier
-// that every reader of it has passed.
+// Sums of eight values over a warp in nine exchanges; lane 4 i has the i-th sum.
+__device__ __forceinline__ float warp_sums8(const float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  const bool high = lane & 16, mid = lane & 8, odd = lane & 4;
+  float a[4], b[2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    a[k] = (high ? v[k + 4] : v[k]) + __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 4], 16);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) b[k] = (mid ? a[k + 2] : a[k]) + __shfl_xor_sync(0xffffffffu, mid ? a[k] : a[k + 2], 8);
+  float s = (odd ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, odd ? b[0] : b[1], 4);
+#pragma unroll
+  for (int o = 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// Sums of up to eight values over a block of at most 32 warps with one
+// barrier.  `red`: two buffers of 256 floats, zero at first, which successive
+// uses take turns with (`turn`), so that a buffer is written again only after
+// a barrier that every reader of it has passed.
 template <int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float* red, int& turn) {
-  static_assert(N <= 4, "");
+  static_assert(N <= 8, "");
+  constexpr int kEach = N <= 4 ? 8 : 4;  // lanes that share a value
   const int lane = threadIdx.x & 31;
-  float w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = k < N ? v[k] : 0.f;
-  float* to = red + 128 * turn;
+  float* to = red + 256 * turn;
   turn ^= 1;
-  const float s = warp_sums4(w);
-  if ((lane & 7) == 0) to[(lane >> 3) * 32 + (threadIdx.x >> 5)] = s;
+  float w[32 / kEach], s;
+#pragma unroll
+  for (int k = 0; k < 32 / kEach; ++k) w[k] = k < N ? v[k] : 0.f;
+  if constexpr (N <= 4)
+    s = warp_sums4(w);
+  else
+    s = warp_sums8(w);
+  if (lane % kEach == 0) to[lane / kEach * 32 + (threadIdx.x >> 5)] = s;
   __syncthreads();
-  // value lane / 8 of four warps
-  const float4 f = *reinterpret_cast<const float4*>(to + lane * 4);
-  float t = (f.x + f.y) + (f.z + f.w);
+  // value lane / kEach of 32 / kEach warps
+  float t = 0.f;
 #pragma unroll
-  for (int o = 4; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  for (int k = 0; k < 8 / kEach; ++k) {
+    const float4 f = *reinterpret_cast<const float4*>(to + lane / kEach * 32 + (k * kEach + lane % kEach) * 4);
+    t += (f.x + f.y) + (f.z + f.w);
+  }
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, t, 8 * k);
+  for (int o = kEach / 2; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, t, kEach * k);
 }
 
 }  // namespace bakron

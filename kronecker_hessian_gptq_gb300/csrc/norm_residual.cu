@@ -38,17 +38,15 @@ template <class T, int VEC, int N>
 struct Columns {
   static constexpr int kV = 8 * N / VEC;
   static constexpr int kWords = 2 * sizeof(T);  // 32-bit words of a Raw8
-  int col[kV];
-  bool in[kV];
-  bool masked;  // some of them are beyond the row
-  __device__ __forceinline__ Columns(int t, int stride, int D) {
+  int first, step;  // the first vector's column, columns from one vector to the next
+  int have;         // vectors within the row
+  __device__ __forceinline__ Columns(int t, int stride, int D) : first(t * VEC), step(stride * VEC) {
+    have = 0;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      col[i] = (i * stride + t) * VEC;
-      in[i] = col[i] < D;
-    }
-    masked = !in[kV - 1];
+    for (int i = 0; i < kV; ++i) have += first + i * step < D;
   }
+  __device__ __forceinline__ bool in(int i) const { return i < have; }
+  __device__ __forceinline__ int64_t col(int i) const { return first + i * step; }
   // Zeros where the row ends, or where there is no array.
   __device__ __forceinline__ void fetch(const T* row, Raw8<T> (&raw)[N]) const {
     auto w = [&](int i) -> uint32_t& { return raw[i / kWords].w[i % kWords]; };
@@ -56,7 +54,7 @@ struct Columns {
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (row && in[i]) u = *reinterpret_cast<const uint4*>(row + col[i]);
+        if (row && in(i)) u = *reinterpret_cast<const uint4*>(row + col(i));
         w(4 * i) = u.x, w(4 * i + 1) = u.y, w(4 * i + 2) = u.z, w(4 * i + 3) = u.w;
       }
     } else {
@@ -65,7 +63,7 @@ struct Columns {
       for (int i = 0; i < kV; i += kW) {
         T e[kW];
 #pragma unroll
-        for (int k = 0; k < kW; ++k) e[k] = row && in[i + k] ? row[col[i + k]] : from_f32<T>(0.f);
+        for (int k = 0; k < kW; ++k) e[k] = row && in(i + k) ? row[col(i + k)] : from_f32<T>(0.f);
         memcpy(&w(i / kW), e, 4);
       }
     }
@@ -75,7 +73,7 @@ struct Columns {
     if constexpr (VEC > 1) {
 #pragma unroll
       for (int i = 0; i < kV; ++i)
-        if (in[i]) *reinterpret_cast<uint4*>(row + col[i]) = make_uint4(w(4 * i), w(4 * i + 1), w(4 * i + 2), w(4 * i + 3));
+        if (in(i)) *reinterpret_cast<uint4*>(row + col(i)) = make_uint4(w(4 * i), w(4 * i + 1), w(4 * i + 2), w(4 * i + 3));
     } else {
       constexpr int kW = 4 / sizeof(T);
 #pragma unroll
@@ -84,9 +82,38 @@ struct Columns {
         memcpy(e, &w(i / kW), 4);
 #pragma unroll
         for (int k = 0; k < kW; ++k)
-          if (in[i + k]) row[col[i + k]] = e[k];
+          if (in(i + k)) row[col(i + k)] = e[k];
       }
     }
+  }
+  // The row's columns on their way into shared memory: a vector for each
+  // thread and `i`, `threads` vectors apart, zeros where the row ends.
+  // (32-bit elements only: the copies are of 4 or 16 bytes.)
+  __device__ __forceinline__ void fetch_async(const T* row, T* to, int t, int threads) const {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to + (i * threads + t) * VEC);
+      const T* src = in(i) ? row + col(i) : row;
+      if constexpr (VEC == 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(in(i) ? 16 : 0) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(in(i) ? 4 : 0) : "memory");
+    }
+  }
+  __device__ __forceinline__ void fetched(const T* from, int t, int threads, F2 (&v)[4 * N]) const {
+    static_assert(N == 1, "");
+    Raw8<T> raw[1];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const T* at = from + (i * threads + t) * VEC;
+      if constexpr (VEC == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(at);
+        raw[0].w[4 * i] = u.x, raw[0].w[4 * i + 1] = u.y, raw[0].w[4 * i + 2] = u.z, raw[0].w[4 * i + 3] = u.w;
+      } else {
+        raw[0].w[i] = *reinterpret_cast<const uint32_t*>(at);
+      }
+    }
+    open8<T>(raw[0], v);
   }
   // The same columns of an fp32 array.
   __device__ __forceinline__ void fetch32(const float* row, float none, F2 (&v)[4 * N]) const {
@@ -95,8 +122,8 @@ struct Columns {
     for (int i = 0; i < kV; ++i) {
       float f[VEC];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) f[k] = in[i] ? none : 0.f;
-      if (row && in[i]) load_vec<float, VEC>(row + col[i], f);
+      for (int k = 0; k < VEC; ++k) f[k] = in(i) ? none : 0.f;
+      if (row && in(i)) load_vec<float, VEC>(row + col(i), f);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) e[i * VEC + k] = f[k];
     }
@@ -112,17 +139,17 @@ struct Columns {
       float f[VEC];
 #pragma unroll
       for (int k = 0; k < VEC; ++k) f[k] = e[i * VEC + k];
-      if (in[i]) store_vec<float, VEC>(row + col[i], f);
+      if (in(i)) store_vec<float, VEC>(row + col(i), f);
     }
   }
   // Zeros beyond the row, where something was added to all columns.
   __device__ __forceinline__ void mask(F2 (&v)[4 * N]) const {
-    if (!masked) return;
+    if (have == kV) return;
 #pragma unroll
     for (int i = 0; i < 4 * N; ++i) {
       float a, b;
       split(v[i], a, b);
-      v[i] = f2(in[2 * i / VEC] ? a : 0.f, in[(2 * i + 1) / VEC] ? b : 0.f);
+      v[i] = f2(in(2 * i / VEC) ? a : 0.f, in((2 * i + 1) / VEC) ? b : 0.f);
     }
   }
 };
@@ -287,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_residual_kernel(NormRe
       uint32_t w[VEC > 4 ? 2 : 1] = {};
 #pragma unroll
       for (int k = 0; k < VEC; ++k) w[k / 4] |= (uint32_t)(token_code(e[q * VEC + k], s, inv) & 255) << (8 * (k % 4));
-      if (!c.in[q]) continue;
-      int8_t* to = codes + c.col[q];
+      if (!c.in(q)) continue;
+      int8_t* to = codes + c.col(q);
       if constexpr (VEC == 8)
         *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
       else if constexpr (VEC == 4)
@@ -329,6 +356,12 @@ cudaError_t norm_residual_typed(const NormResidual& p, cudaStream_t stream) {
 constexpr int bwd_held(bool layer) { return layer ? 9 : 6; }
 constexpr int kBwdRegisterD = 4096;  // columns up to which they are in registers, 512 threads of 8
 constexpr int kBwdPerSm = 8;         // blocks of an SM at most
+// Rows on their way in shared memory: of 32-bit elements, whose 32 registers
+// for the next row would be spilled as they arrive (1531 x 1999: 47 -> 29 us).
+// 16-bit elements come straight into registers (16384 x 4096 in bf16: 173 us,
+// 189 through shared memory).
+template <class T>
+constexpr int kBwdStages = sizeof(T) == 4 ? 2 : 0;
 
 struct BackwardPlan {
   int64_t groups;  // at least 1
@@ -340,7 +373,7 @@ struct BackwardPlan {
   int smem;
 };
 
-BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups, bool layer) {
+BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups, bool layer, int staged_bytes = 0) {
   BackwardPlan b;
   b.groups = std::max<int64_t>(1, groups);
   b.shared = D > kBwdRegisterD;
@@ -351,7 +384,7 @@ BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups, bool layer) {
   while (b.cluster * most_cols < D) b.cluster *= 2;
   const int64_t per = (D + b.cluster - 1) / b.cluster;
   b.threads = (int)((per + 255) / 256) * 32;
-  b.smem = b.shared ? b.threads * 32 * bwd_held(layer) : 0;
+  b.smem = b.shared ? b.threads * 32 * bwd_held(layer) : b.threads * 32 * staged_bytes;
   // ranges that run at once
   const int64_t most = std::max<int64_t>(1, kSms * (b.shared ? 1 : std::min(512 / b.threads, kBwdPerSm)) / b.cluster);
   if (b.groups <= most) {
@@ -369,7 +402,7 @@ BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups, bool layer) {
 // writes a slot again only after a later barrier, which every reader of it
 // has passed.
 template <int N>
-__device__ __forceinline__ void cluster_sums(float (&v)[N], float* red, float (*slot)[4], int cluster, int& turn) {
+__device__ __forceinline__ void cluster_sums(float (&v)[N], float* red, float (*slot)[8], int cluster, int& turn) {
   float* mine = slot[turn];
   block_sums<N>(v, red, turn);
   if (cluster == 1) return;
@@ -450,16 +483,18 @@ struct Held {
 // A block (or, for the widest rows, a cluster of them) walks over a range of
 // rows, 8 columns for each thread, with the next row on its way.  The weights
 // and the columns' sums are each thread's own: in registers up to 4096 columns
-// (16384 x 4096 in bf16: 172 us; 222 with them in shared memory, which adds
-// instructions to a kernel that is bound by issuing them), in shared memory
-// for wider rows, which halves the blocks that share a row and wait for one
-// another twice in each (4096 x 14336 in bf16: 279 us, 550 with registers).
+// (16384 x 4096 in bf16: 168 us; 222 with them in shared memory, which adds
+// instructions to a kernel that issues one in 57% of the cycles with 4 warps
+// on a scheduler), in shared memory for wider rows, which halves the blocks
+// that share a row and wait for one another twice in each (4096 x 14336 in
+// bf16: 270 us, 550 with registers).
 template <class T, int VEC, bool kLayer, bool kShared>
 __global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(NormBackward p, BackwardPlan plan, float* part) {
   extern __shared__ __align__(16) float bwd_smem[];
-  __shared__ __align__(16) float red[2 * 128];
-  __shared__ float slot[2][4];
-  for (int i = threadIdx.x; i < 2 * 128; i += blockDim.x) red[i] = 0.f;
+  __shared__ __align__(16) float red[2 * 256];
+  __shared__ float slot[2][8];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  for (int i = threadIdx.x; i < 2 * 256; i += blockDim.x) red[i] = 0.f;
   __syncthreads();
   int turn = 0;
   const int cluster = plan.cluster;
@@ -502,13 +537,50 @@ __global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(
   const T* pdz = p.dZ ? static_cast<const T*>(p.dZ) + lo * p.lddz : nullptr;
   T *px = static_cast<T*>(p.dX) + lo * D, *pdh = p.dH ? static_cast<T*>(p.dH) + lo * D : nullptr;
   Raw8<T> ry[1], rh[1], rdy[1], rdz[1];
+  constexpr int kStages = kShared ? 0 : kBwdStages<T>;
+  const int t = (int)threadIdx.x, n = (int)blockDim.x;
+  T* const staged = reinterpret_cast<T*>(bwd_smem);
+  int stage = 0;
   auto fetch_row = [&] {
-    c.fetch(py, ry);
-    c.fetch(ph, rh);
-    c.fetch(pdy, rdy);
-    c.fetch(pdz, rdz);
+    if constexpr (kStages > 0) {
+      T* to = staged + stage * 32 * n;
+      c.fetch_async(py, to, t, n);
+      if (ph) c.fetch_async(ph, to + 8 * n, t, n);
+      if (pdy) c.fetch_async(pdy, to + 16 * n, t, n);
+      if (pdz) c.fetch_async(pdz, to + 24 * n, t, n);
+    } else {
+      c.fetch(py, ry);
+      c.fetch(ph, rh);
+      c.fetch(pdy, rdy);
+      c.fetch(pdz, rdz);
+    }
   };
-  if (lo < hi) fetch_row();
+  auto advance = [&] {
+    py += p.ldy;
+    if (ph) ph += p.ldh;
+    if (pdy) pdy += p.lddy;
+    if (pdz) pdz += p.lddz;
+  };
+  if constexpr (kStages > 0) {
+    for (stage = 0; stage < kStages; ++stage) {
+      if (lo + stage < hi) fetch_row();
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+      advance();
+    }
+    stage = 0;
+  } else if (lo < hi) {
+    fetch_row();
+  }
+  // A later row into the place of the row at hand, after a barrier of its
+  // sums, which follows all reads of that place.
+  auto fetch_over = [&](int64_t row) {
+    if constexpr (kStages > 0) {
+      if (row + kStages < hi) fetch_row();
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+      advance();
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+  };
   int64_t group = 0, left = 0;  // rows left in the group
   for (int64_t row = lo; row < hi; ++row) {
     if (left == 0) {
@@ -524,16 +596,24 @@ __global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(
     }
     --left;
     F2 y[4], h[4], dt[4], dz[4];
-    open_all<T, 1>(ry, y);
-    open_all<T, 1>(rh, h);
-    open_all<T, 1>(rdy, dt);
-    open_all<T, 1>(rdz, dz);
-    if (row + 1 < hi) {
-      py += p.ldy;
-      if (ph) ph += p.ldh;
-      if (pdy) pdy += p.lddy;
-      if (pdz) pdz += p.lddz;
-      fetch_row();
+    if constexpr (kStages > 0) {
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
+      const T* from = staged + stage * 32 * n;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = dt[k] = dz[k] = f2(0.f);
+      c.fetched(from, t, n, y);
+      if (ph) c.fetched(from + 8 * n, t, n, h);
+      if (pdy) c.fetched(from + 16 * n, t, n, dt);
+      if (pdz) c.fetched(from + 24 * n, t, n, dz);
+    } else {
+      open_all<T, 1>(ry, y);
+      open_all<T, 1>(rh, h);
+      open_all<T, 1>(rdy, dt);
+      open_all<T, 1>(rdz, dz);
+      if (row + 1 < hi) {
+        advance();
+        fetch_row();
+      }
     }
     if constexpr (kLayer) {
       F2 sy = f2(0.f), sh = f2(0.f);
@@ -548,11 +628,27 @@ __global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(
       c.mask(h);
       if (p.dZ) apreb.add(dz);
     }
-    float s[4];
+    // One exchange for all sums of a row where that pays: with q = g * post,
+    // mean(q dt n_h) is linear in dt = dy + r_y k + c n_y, whose c comes from
+    // the same exchange (16384 x 4096 in bf16: 168 us, 173 with two).  Layer
+    // norms would need four sums more; the wide form has no registers left
+    // for it (4096 x 14336: 270 us, 328 with one exchange).
+    constexpr bool kOne = !kLayer && !kShared;
+    float s[kOne ? 6 : 4];
     F2 w[4];
     wpre.get(w);
     {
-      F2 yy = f2(0.f), qy = f2(0.f), hh = f2(0.f), qq = f2(0.f);
+      F2 yy = f2(0.f), qy = f2(0.f), hh = f2(0.f), qq = f2(0.f), hd = f2(0.f), hk = f2(0.f), hy = f2(0.f);
+      F2 q[4];
+      if constexpr (kOne) {
+        wpost.get(q);
+        if (p.gate) {
+          F2 g[4];
+          gate.get(g);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[k] = q[k] * g[k];
+        }
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         w[k] = dz[k] * w[k];
@@ -560,13 +656,26 @@ __global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(
         qy = fma2(w[k], y[k], qy);
         hh = fma2(h[k], h[k], hh);
         if constexpr (kLayer) qq = qq + w[k];
+        if constexpr (kOne) {
+          q[k] = q[k] * h[k];
+          hd = fma2(q[k], dt[k], hd);
+          hk = fma2(q[k], w[k], hk);
+          hy = fma2(q[k], y[k], hy);
+        }
       }
-      s[0] = sum(yy), s[1] = sum(qy), s[2] = sum(hh), s[3] = kLayer ? sum(qq) : 0.f;
+      s[0] = sum(yy), s[1] = sum(qy), s[2] = sum(hh);
+      if constexpr (!kOne)
+        s[3] = kLayer ? sum(qq) : 0.f;
+      else
+        s[3] = sum(hd), s[4] = sum(hk), s[5] = sum(hy);
     }
-    cluster_sums<4>(s, red, slot, cluster, turn);
+    cluster_sums<kOne ? 6 : 4>(s, red, slot, cluster, turn);
+    fetch_over(row);
     if (p.dZ) {
       const float r = rsqrtf(fmaf(s[0], invd, p.eps));
-      const F2 r2 = f2(r), c1 = f2(-r * r * s[1] * invd), c0 = f2(-r * s[3] * invd);
+      const float cn = -r * r * s[1] * invd;
+      const F2 r2 = f2(r), c1 = f2(cn), c0 = f2(kLayer ? -r * s[3] * invd : 0.f);
+      if constexpr (kOne) s[3] = fmaf(cn * r, s[5], fmaf(r, s[4], s[3]));
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         y[k] = y[k] * r2;
@@ -611,15 +720,18 @@ __global__ void __launch_bounds__(kShared ? 1024 : 512, 1) norm_backward_kernel(
     if (p.post) {
       apost.add(dt, h);
       if constexpr (kLayer) apostb.add(dt);
+      float t[2] = {s[3] * r, 0.f};
       F2 tn = f2(0.f), tq = f2(0.f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         dt[k] = dt[k] * w[k];
-        tn = fma2(dt[k], h[k], tn);
+        if constexpr (!kOne) tn = fma2(dt[k], h[k], tn);
         if constexpr (kLayer) tq = tq + dt[k];
       }
-      float t[2] = {sum(tn), kLayer ? sum(tq) : 0.f};
-      cluster_sums<2>(t, red, slot, cluster, turn);
+      if constexpr (!kOne) {
+        t[0] = sum(tn), t[1] = kLayer ? sum(tq) : 0.f;
+        cluster_sums<2>(t, red, slot, cluster, turn);
+      }
       const F2 c1 = f2(-t[0] * invd * r), c0 = f2(-t[1] * invd * r);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -666,6 +778,7 @@ struct ColumnSums {
 };
 __global__ void __launch_bounds__(1024) column_sums_kernel(ColumnSums a) {
   __shared__ float red[32][33];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // it may have been launched before the rows were done
   const int row = (int)blockIdx.y;
   int q = 0, first = 0;
   float* out = a.out[0];
@@ -691,7 +804,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(ColumnSums a) {
 
 template <class T, int VEC>
 cudaError_t norm_backward_typed(const NormBackward& p, float* part, cudaStream_t stream) {
-  const BackwardPlan plan = backward_plan(p.T, p.D, p.groups, p.layer);
+  const BackwardPlan plan = backward_plan(p.T, p.D, p.groups, p.layer, kBwdStages<T> * (int)sizeof(T));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(plan.nb * plan.cluster));
   cfg.blockDim = dim3((unsigned)plan.threads);
@@ -719,8 +832,13 @@ cudaError_t norm_backward_typed(const NormBackward& p, float* part, cudaStream_t
     if (outs[q]) rows += q == kGate ? (int)plan.groups : 1;
   }
   a.first[kPlanes] = rows;
-  if (rows) column_sums_kernel<<<dim3((unsigned)((p.D + 31) / 32), (unsigned)rows), dim3(32, 32), 0, stream>>>(a);
-  return cudaGetLastError();
+  if (!rows) return cudaSuccess;
+  cfg.gridDim = dim3((unsigned)((p.D + 31) / 32), (unsigned)rows);
+  cfg.blockDim = dim3(32, 32);
+  cfg.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, column_sums_kernel, a);
 }
 
 // Vectors of 16 bytes where every row of every array starts on 16 bytes and
