@@ -152,6 +152,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// A store and an integer sum to memory under a predicate: as a branch for each
+// value they cost a warp 150 cycles a value.
+__device__ __forceinline__ void store_if(bool p, float* to, float x) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p st.global.f32 [%0], %1;\n}\n" ::"l"(to), "f"(x), "r"((int)p)
+               : "memory");
+}
+template <class T>
+__device__ __forceinline__ void store_if(bool p, T* to, float x) {
+  const T v = from_f32<T>(x);
+  uint16_t bits;
+  memcpy(&bits, &v, 2);
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p st.global.b16 [%0], %1;\n}\n" ::"l"(to), "h"(bits), "r"((int)p)
+               : "memory");
+}
+__device__ __forceinline__ void add_if(bool p, int32_t* to, int x) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p red.global.add.s32 [%0], %1;\n}\n" ::"l"(to), "r"(x), "r"((int)p)
+               : "memory");
+}
+
 // 16 of v, from the kFrom-th on.
 template <int kFrom>
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -351,16 +370,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           v[i] = __float_as_uint(fmaf((float)(int)v[i] * __shfl_sync(0xffffffffu, xs[c >> 5], i), ws, bias));
-        if (!in) return;
         T* to = out.y + (t0 + c) * out.outputs + o;
-        if (c + 32 <= live) {
+        const int rows = in ? live - c : 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i, to += out.outputs) *to = from_f32<T>(__uint_as_float(v[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i, to += out.outputs)
-            if (c + i < live) *to = from_f32<T>(__uint_as_float(v[i]));
-        }
+        for (int i = 0; i < 32; ++i, to += out.outputs) store_if(i < rows, to, __uint_as_float(v[i]));
       };
       for (int k = q.k0; k < q.k1; k += kI8Segment, ++sums) {
         warp_wait(&bar.sum_full[sums & two], (uint32_t)(sums >> two) & 1u, broken);
@@ -387,16 +400,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
             if (c + 16 < cols) tmem_st16<16>(kept + (uint32_t)c + 16, v);  // what follows is the other warps'
           } else if (pieces == 1) {
             finish(c, v);
-          } else if (in) {
+          } else {
             int32_t* to = out.sums + (t0 + c) * out.outputs + o;
-            if (c + 32 <= live) {
+            const int rows = in ? live - c : 0;
 #pragma unroll
-              for (int i = 0; i < 32; ++i, to += out.outputs) atomicAdd(to, (int)v[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i, to += out.outputs)
-                if (c + i < live) atomicAdd(to, (int)v[i]);
-            }
+            for (int i = 0; i < 32; ++i, to += out.outputs) add_if(i < rows, to, (int)v[i]);
           }
         }
         if (!last) asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
@@ -418,20 +426,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 #pragma unroll
       for (int c = 0; c < kI8Tokens / 2; c += 32) {
         if (c >= live) break;
-        const int32_t* sum = out.sums + (t0 + c) * out.outputs + o;
-        uint32_t v[32];  // 32 reads on their way at once
+        // 32 reads on their way at once; beyond the tokens or the outputs the last one's
+        const int rows = live - c;
+        const int32_t* sum = out.sums + (t0 + c) * out.outputs + (in ? o : out.outputs - 1);
+        uint32_t v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          v[i] = in && c + i < live ? (uint32_t)__ldcg(sum) : 0u;
-          sum += out.outputs;
+          v[i] = (uint32_t)__ldcg(sum);
+          if (i + 1 < rows) sum += out.outputs;
         }
-        T* to = out.y + (t0 + c) * out.outputs + o;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float s = __shfl_sync(0xffffffffu, xs[c >> 5], i);
-          if (in && c + i < live) *to = from_f32<T>(fmaf((float)(int)v[i] * s, ws, bias));
-          to += out.outputs;
-        }
+        finish(c, v);
       }
     }
   }
