@@ -23,7 +23,7 @@
 // Every 1024 of K the epilogue adds the fp32 sums to integers, which stay in
 // tensor memory while a piece is longer than that.  A pair of SMs is given
 // either whole tiles or, where that would leave too many pairs idle, an equal
-// share of all tiles' steps; then the pieces of a tile are joined in memory
+// part of one tile or an equal share of all tiles' steps; then the pieces of a tile are joined in memory
 // with integer atomics, whose order does not matter, and the last to arrive
 // scales a slice's sums and writes the results.
 #pragma once
@@ -467,6 +467,15 @@ inline I8Work i8_work(int64_t T, int64_t K, int64_t N, int pairs) {
   const int64_t whole = (tiles + pairs - 1) / pairs * (w.ksteps + 2), share = (all + pairs - 1) / pairs + 6 + w.nt / 16;
   w.shared = share < whole;
   w.pairs = (int)std::min<int64_t>(w.shared ? all : tiles, pairs);
+  // A share that ends one tile and begins another has two ends to wait for.
+  // As many pairs for each tile have one, at 2 steps and 1 for every 32 tokens
+  // less (128 tokens 4096 -> 4096: 17.0 us, 20.3 with 76 pairs for 16 tiles;
+  // 256: 21.0, 23.8; 200 tokens 14336 -> 4096, 56 steps for 48: 42.2, 42.5).
+  if (w.shared && tiles < pairs) {
+    const int64_t each = pairs / tiles;
+    if ((w.ksteps + each - 1) / each <= (all + pairs - 1) / pairs + 2 + w.nt / 32)
+      w.pairs = (int)std::min(all, tiles * each);
+  }
   // 512 columns: with 64 tokens two sums leave room for all operands, and with
   // more a wait at the end of a segment costs less than an operand's.
   w.bufs = w.nt <= 64 ? 2 : 1;
