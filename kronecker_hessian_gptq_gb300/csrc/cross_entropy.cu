@@ -35,6 +35,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kChunk = 64;              // columns that share a maximum
 constexpr float kSteps = 2048.f;        // fixed-point steps in a factor of two
 constexpr float kGScale = 32768.f;      // G is stored times this, so that fp16 keeps p down to 2^-29
+constexpr int kSumTerms = 512;          // terms that the tensor cores sum at a stretch, and
+constexpr int64_t kFewLogits = 8192;    // the vocabulary up to which: see logits_launch()
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;
 constexpr int64_t kPieceTokens = (int64_t)1 << 20;  // keeps the number of tiles and the length of a sum bounded
 
@@ -76,6 +78,7 @@ __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* targe
 // Epilogue of the logits: rows are tokens of the piece, columns the vocabulary.
 template <bool kKeep>
 struct LogitsEpilogue {
+  using Sum = float;
   CUtensorMap map;  // of the kept logits
   int64_t rows, V;
   float2* stats;  // rows x chunks: maximum in units of log 2, sum of 2^(x - maximum)
@@ -85,21 +88,27 @@ struct LogitsEpilogue {
                                              const PairBox& box) const {
     if (row0 >= rows) return;
 #pragma unroll 1
-    for (int c = 0; c < 128 && col + c < V; c += kChunk) chunk(row0, col + c, c, sums, box);
+    for (int c = 0; c < 128 && col + c < V; c += kChunk) {
+      float v[kChunk];
+      sums.load(c, *reinterpret_cast<float(*)[32]>(v));
+      sums.load(c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+      chunk(row0, col + c, v, box);
+    }
   }
-  __device__ __forceinline__ void chunk(int64_t row0, int64_t col, int at, const PairSums& sums, const PairBox& box) const {
+  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, float (&v)[kChunk],
+                                             const PairBox& box) const {
+    if (row0 < rows && col < V) chunk(row0, col, v, box);
+  }
+  __device__ __forceinline__ void chunk(int64_t row0, int64_t col, float (&v)[kChunk], const PairBox& box) const {
     const int left = V - col < kChunk ? (int)(V - col) : kChunk;
-    float v[2][32];
-    sums.load(at, v[0]);
-    sums.load(at + 32, v[1]);
     if (left < kChunk) {
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
-        if (i >= left) v[i / 32][i % 32] = -INFINITY;
+        if (i >= left) v[i] = -INFINITY;
     }
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) m = fmaxf(m, v[i / 32][i % 32]);
+    for (int i = 0; i < kChunk; ++i) m = fmaxf(m, v[i]);
     m = m == -INFINITY ? 0.f : m * kLog2e;
     if constexpr (kKeep) box.open();
     float s = 0.f;
@@ -108,7 +117,7 @@ struct LogitsEpilogue {
       uint32_t w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float x = fmaf(v[j / 32][j % 32 + i], kLog2e, -m);
+        const float x = fmaf(v[j + i], kLog2e, -m);
         // -kSteps x rounded to an integer in the low bits of 1.5 2^23 + it.
         // A NaN is lost here; its row's sum is NaN, which is what counts.
         constexpr float kMagic = 12582912.f;
@@ -332,6 +341,21 @@ Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
 
 bool tma_rows(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
 
+// The tensor cores round towards zero as they sum, so long sums come out small
+// by up to 1e-6 of 4096 terms.  Over a large vocabulary that averages out; over
+// a small one lse is little else than its few largest logits.  There the sums
+// are restarted every 512 terms and added up in fp32 (error of 20 tokens'
+// losses, 4096 x 1000: 1.9e-6 of them without, 2e-7 with it).  It costs most
+// of half the product's time (1024 tokens, 4096 x 32000: 239 us, 147 without),
+// and the error there is 7e-7 without.
+template <bool kKeep>
+cudaError_t logits_launch(const PairOperand& h, const PairOperand& w, int64_t D, bool bf16, const PairWork& work,
+                          const LogitsEpilogue<kKeep>& epi, int32_t* status, cudaStream_t stream, int first_status) {
+  return D > kSumTerms && epi.V <= kFewLogits
+             ? pair_gemm_launch<false, false, 4, kSumTerms / kPairK>(h, w, D, bf16, work, epi, status, stream, first_status)
+             : pair_gemm_launch<false, false, 2, 0>(h, w, D, bf16, work, epi, status, stream, first_status);
+}
+
 template <class T>
 cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t stream) {
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -376,10 +400,10 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
       LogitsEpilogue<true> epi{{}, m, p.V, stats, chunks};
       e = make_tensor_map(&epi.map, TileMap{kept, CU_TENSOR_MAP_DATA_TYPE_UINT16, m, ldk, ldk, 32, 64, true});
       if (e != cudaSuccess) return e;
-      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
+      e = logits_launch(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
     } else {
       const LogitsEpilogue<false> epi{{}, m, p.V, stats, chunks};
-      e = pair_gemm_launch<false, false, 2, 0>(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
+      e = logits_launch(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
     }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -425,6 +425,7 @@ cudaError_t rows_launch(const Int8Matmul& p, int32_t* status, cudaStream_t strea
 // whose rows start on 16 bytes by TMA, others row by row.
 template <class T>
 struct ScaledEpilogue {
+  using Sum = int;
   CUtensorMap map;
   int64_t tokens, outputs;
   const float *x_scales, *w_scales, *bias;

@@ -15,12 +15,14 @@
 // in the descriptors' offsets.
 //
 // With kSegment > 0 the sums are restarted every kSegment steps of 64 and
-// added up in integers by the epilogue, so that products of 8-bit codes stay
-// exact: 1024 products of at most 2^14 reach 2^24, where fp32 integers end.
+// added up by the epilogue: in integers, so that products of 8-bit codes stay
+// exact (1024 products of at most 2^14 reach 2^24, where fp32 integers end), or
+// in fp32, rounded to nearest where the tensor cores round towards zero.
 #pragma once
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "bakron.h"
 #include "tc.cuh"
@@ -182,7 +184,7 @@ struct PairBarriers {
 //   epi(unit, row0, col, sums, box)
 // with the warp's first row (the thread's own is lane further) and first
 // column and a source of its 256 / kQuads columns: sums.load(c, v) gives 32 of
-// them from column c on.  With kSegment it is an array of integers instead.
+// them from column c on.  With kSegment it is an array of Epi::Sum instead.
 struct PairSums {
   uint32_t taddr;
   __device__ __forceinline__ void load(int c, float (&v)[32]) const { tmem_ld32(taddr + (uint32_t)c, v); }
@@ -394,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
         epi(q, row, col, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes}, box);
         release();
       } else {
-        int acc[kCols];
+        typename Epi::Sum acc[kCols];
         for (int k = q.k0; k < q.k1; k += kSegment) {
           warp_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
           if (broken) break;
@@ -404,7 +406,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
             float v[32];
             tmem_ld32(tmem + (uint32_t)(sums & 1) * 256u + lanes + (uint32_t)c, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c + i] = __float2int_rn(v[i]) + (k == q.k0 ? 0 : acc[c + i]);
+            for (int i = 0; i < 32; ++i) {
+              if constexpr (std::is_same<typename Epi::Sum, int>::value)
+                acc[c + i] = __float2int_rn(v[i]) + (k == q.k0 ? 0 : acc[c + i]);
+              else
+                acc[c + i] = k == q.k0 ? v[i] : acc[c + i] + v[i];
+            }
           }
           release();
         }
