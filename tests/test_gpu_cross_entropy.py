@@ -266,3 +266,25 @@ def test_refusals(bk):
                  lambda: bk.linear_cross_entropy_grad(h, w, y, coef=torch.ones(5, device="cuda"))):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("t,d,v", [(20, 4096, 1000), (5, 4096, 8192), (130, 3000, 777)])
+def test_log_sums_of_few_large_logits(bk, t, d, v, dtype):
+    """Targets far above the rest, in a small vocabulary: lse is little else
+    than the target's logit, so an error of its sum does not average out.  Sums
+    that round towards zero every 16 terms lose half a unit (2^-24) of the sum
+    so far each time, which is on average half of what it ends as: 2^-26 of
+    the logit for every 16 terms.  Restarted every 512 terms that is 4.8e-7;
+    over 4096 it would be 3.8e-6.  Twice the former, with 2^-22 for the
+    exponentials' sum and the logarithm, is allowed over all tokens."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(t + d + v)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    w = (rand(v, d) * d ** -0.5).to(getattr(torch, dtype))
+    y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+    h = (rand(t, d) + 12 * w[y].float()).to(w.dtype)
+    lse = bk.linear_cross_entropy(h, w, y)[1].double()
+    want = torch.logsumexp(h.double() @ w.double().t(), 1)
+    assert float((lse - want).norm() / want.norm()) <= 2 * 512 / 16 * 2.0 ** -26 + 2.0 ** -22
