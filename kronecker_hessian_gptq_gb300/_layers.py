@@ -160,9 +160,11 @@ def int8_matmul(X, codes, scales, x_scales=None, bias=None, dtype=None, stream=N
         return Y, status.zero_()
     p = codes.data_ptr()
     nbytes = _entry("bakron_int8_matmul_workspace_size")(T, K, N, 1 if p % 16 or ldc % 16 else 0)
-    ws = _empty(nbytes, dtype=torch.uint8, device=at).data_ptr() if nbytes else None
-    _call("bakron_int8_matmul", X.data_ptr(), kind, ldx, xs, p, ldc, w, b, T, K, N, Y.data_ptr(), out, ws, nbytes,
-          status.data_ptr(), _stream_on(device))
+    # Held until the call has returned: what is given back before the launches
+    # may by then be another thread's.
+    ws = _empty(nbytes, dtype=torch.uint8, device=at) if nbytes else None
+    _call("bakron_int8_matmul", X.data_ptr(), kind, ldx, xs, p, ldc, w, b, T, K, N, Y.data_ptr(), out,
+          ws.data_ptr() if nbytes else None, nbytes, status.data_ptr(), _stream_on(device))
     return Y, status
 
 
