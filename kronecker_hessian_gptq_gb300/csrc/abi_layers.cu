@@ -1,6 +1,8 @@
 // abi_layers.cu -- the extern "C" entry points of the layer operators
 // (declared in bakron.h): arguments are checked on the host before anything
 // is enqueued.
+#include <initializer_list>
+
 #include "bakron.h"
 #include "internal.h"
 #include "layers.h"
@@ -12,6 +14,12 @@ using bakron::aligned_to;
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA; }
 bool float_type(int dtype) { return dtype == BAKRON_F32 || dtype == BAKRON_F16 || dtype == BAKRON_BF16; }
 bool on_element(const void* p, int dtype) { return aligned_to(p, bakron::elem_size(dtype)); }
+// Arrays of 32-bit elements (null: not there).
+bool on_words(std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays)
+    if (!aligned_to(p, 4)) return false;
+  return true;
+}
 bool workspace_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && aligned_to(ws, bakron::kAlign) && have >= need);
 }
@@ -45,6 +53,7 @@ int bakron_int8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_s
     return BAKRON_ERR_INVALID_ARG;
   if (x_dtype == BAKRON_I8 ? !x_scales : (x_scales || !float_type(x_dtype) || !on_element(X, x_dtype)))
     return BAKRON_ERR_INVALID_ARG;
+  if (!on_words({x_scales, scales, bias, status_dev})) return BAKRON_ERR_INVALID_ARG;
   if (!float_type(y_dtype) || !on_element(Y, y_dtype) || Y == X || Y == (const void*)codes) return BAKRON_ERR_INVALID_ARG;
   const bakron::Int8Matmul p{X, x_scales, x_dtype, ldx, codes, ldc, scales, bias, T, K, N, Y, y_dtype, N};
   const bool copies = bakron::int8_matmul_needs_copies(p);
@@ -67,7 +76,7 @@ int bakron_norm_residual(const void* X, int64_t ldx, const void* H, int64_t ldh,
           : (Z || codes || code_scales))
     return BAKRON_ERR_INVALID_ARG;
   if (!on_element(X, dtype) || !on_element(H, dtype) || !on_element(gate, dtype) || !on_element(Y, dtype) ||
-      !on_element(Z, dtype))
+      !on_element(Z, dtype) || !on_words({post, post_bias, pre, pre_bias, code_scales}))
     return BAKRON_ERR_INVALID_ARG;
   if (Z == Y || (Z && (Z == X || Z == H)) || (codes && (codes == X || codes == H || codes == Y)))
     return BAKRON_ERR_INVALID_ARG;
@@ -101,6 +110,7 @@ int bakron_norm_residual_backward(const void* dY, int64_t lddy, const void* dZ, 
   if (gate && (groups < 1 || T % groups || ldg < D)) return BAKRON_ERR_INVALID_ARG;
   for (const void* q : {dY, dZ, Y, H, gate, (const void*)dX, (const void*)dH})
     if (!on_element(q, dtype)) return BAKRON_ERR_INVALID_ARG;
+  if (!on_words({post, post_bias, pre, dpost, dpost_bias, dgate, dpre, dpre_bias})) return BAKRON_ERR_INVALID_ARG;
   for (const void* q : {Y, H, gate, (const void*)dH})
     if (q && q == dX) return BAKRON_ERR_INVALID_ARG;
   for (const void* q : {dY, dZ, Y, gate})
@@ -125,7 +135,8 @@ static int cross_entropy(const void* H, int64_t ldh, const void* W, int64_t ldw,
     return BAKRON_ERR_INVALID_ARG;
   if (T < 1 || T >= kMaxRows || D < 1 || D > kMaxD || V < 1 || V > kMaxV || ldh < D || ldw < D)
     return BAKRON_ERR_INVALID_ARG;
-  if (!on_element(H, dtype) || !on_element(W, dtype) || !aligned_to(targets, 8) || loss == lse)
+  if (!on_element(H, dtype) || !on_element(W, dtype) || !aligned_to(targets, 8) || loss == lse ||
+      !on_words({coef, loss, lse, status_dev}))
     return BAKRON_ERR_INVALID_ARG;
   const bakron::CrossEntropy p{H, W, ldh, ldw, dtype, targets, T, D, V, loss, lse, coef, dH, dW};
   const bool copies = bakron::cross_entropy_needs_copies(p);

@@ -100,3 +100,29 @@ def test_linear_cross_entropy(lib):
     refused(lib.bakron_linear_cross_entropy_grad, good, **bad, dH=[None, at(0x1000), at(0x2000), at(0x7001)],
             dW=[None, at(0x7000), at(0x1000), at(0x2000), at(0x8001)])
     refused(lib.bakron_linear_cross_entropy_grad, good, 4, ws=[None, at(0x100010)], n=[grad - 1])
+
+
+def test_arrays_of_32_bits_off_their_elements(lib):
+    """Weights, scales, gradients, losses and status words that do not start on 4 bytes."""
+    off = at(0x9002)
+    good = dict(X=at(0x1000), xt=I8, ldx=64, xs=at(0x4000), codes=at(0x2000), ldc=64, scales=at(0x3000), bias=None, T=40, K=64,
+                N=16, Y=at(0x5000), yt=BF16, ws=at(0x100000), n=1 << 30, status=at(0x6000), stream=None)
+    refused(lib.bakron_int8_matmul, good, xs=[off], scales=[off], bias=[off], status=[off])
+    p = {k: at(0x1000 * (i + 1)) for i, k in enumerate("XHYZCsgwb")}
+    good = dict(X=p["X"], ldx=64, H=p["H"], ldh=64, post=p["w"], post_bias=p["b"], gate=p["g"], ldg=64, groups=2, pre=p["w"],
+                pre_bias=p["b"], alpha=1.0, eps=1e-6, kind=1, dtype=BF16, T=4, D=64, Y=p["Y"], Z=None, codes=p["C"],
+                code_scales=p["s"], stream=None)
+    refused(lib.bakron_norm_residual, good, post=[off], post_bias=[off], pre=[off], pre_bias=[off], code_scales=[off])
+    p = {k: at(0x1000 * (i + 1)) for i, k in enumerate(["dY", "dZ", "Y", "H", "w", "b", "g", "dX", "dH", "f1", "f2", "f3", "f4", "f5"])}
+    good = dict(dY=p["dY"], lddy=64, dZ=p["dZ"], lddz=64, Y=p["Y"], ldy=64, H=p["H"], ldh=64, post=p["w"], post_bias=p["b"],
+                gate=p["g"], ldg=64, groups=2, pre=p["w"], alpha=1.0, eps=1e-6, kind=1, dtype=BF16, T=4, D=64, dX=p["dX"],
+                dH=p["dH"], dpost=p["f1"], dpost_bias=p["f2"], dgate=p["f3"], dpre=p["f4"], dpre_bias=p["f5"],
+                ws=at(0x100000), n=1 << 30, stream=None)
+    refused(lib.bakron_norm_residual_backward, good, post=[off], post_bias=[off], pre=[off], dpost=[off], dpost_bias=[off],
+            dgate=[off], dpre=[off], dpre_bias=[off])
+    good = dict(H=at(0x1000), ldh=64, W=at(0x2000), ldw=64, dtype=BF16, y=at(0x3000), coef=at(0x3800), T=4, D=64, V=100,
+                loss=at(0x4000), lse=at(0x5000), dH=at(0x7000), dW=at(0x8000), ws=at(0x100000), n=1 << 30, status=at(0x6000),
+                stream=None)
+    refused(lib.bakron_linear_cross_entropy_grad, good, coef=[off], loss=[off], lse=[off], status=[off])
+    good = {k: v for k, v in good.items() if k not in ("coef", "dH", "dW")}
+    refused(lib.bakron_linear_cross_entropy, good, loss=[off], lse=[off], status=[off])
