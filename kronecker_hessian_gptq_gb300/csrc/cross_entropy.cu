@@ -12,6 +12,16 @@
 // maximum and the sum of exponentials below it, and a second kernel joins a
 // row's pieces: the loss alone stores 8 bytes for 64 logits.
 //
+// The target is left out of these sums, and its logit is summed again, in fp32:
+// with r_t the log-sum of the other words and d_t = r_t - x_t,y(t),
+//     loss_t = log(1 + exp(d_t)),  lse_t = x_t,y(t) + loss_t,
+//     G_t,y(t) = -c_t (1 - exp(-loss_t)).
+// The tensor cores round towards zero in their long sums (up to 4e-6 of a logit
+// of 4096 terms).  Over the other words that is an error of their log-sum,
+// which counts with their share 1 - p; as a difference between two versions of
+// the target's logit it would count in full, and a loss near zero would come
+// out below it.
+//
 // For the gradients a logit is kept, for one piece of the tokens at a time,
 // as the 16-bit fixed-point number round(2048 (m - x) log2 e), m the maximum
 // of its 64 columns: a relative error of exp(x) of at most 1.7e-4 (1e-4 rms,
@@ -81,25 +91,42 @@ struct LogitsEpilogue {
   using Sum = float;
   CUtensorMap map;  // of the kept logits
   int64_t rows, V;
-  float2* stats;  // rows x chunks: maximum in units of log 2, sum of 2^(x - maximum)
+  const int64_t* target;
+  float2* stats;  // rows x chunks, of all words but the target: maximum in units of log 2, sum of 2^(x - maximum)
   int64_t chunks;
 
+  // The thread's row's target, as a column from `col` on.
+  __device__ __forceinline__ int64_t target_from(int64_t row0, int64_t col, const PairBox& box) const {
+    return row0 + box.lane < rows ? target[row0 + box.lane] - col : -1;
+  }
   __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, const PairSums& sums,
                                              const PairBox& box) const {
     if (row0 >= rows) return;
+    const int64_t y = target_from(row0, col, box);
 #pragma unroll 1
     for (int c = 0; c < 128 && col + c < V; c += kChunk) {
       float v[kChunk];
       sums.load(c, *reinterpret_cast<float(*)[32]>(v));
       sums.load(c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
-      chunk(row0, col + c, v, box);
+      chunk(row0, col + c, y - c, v, box);
     }
   }
   __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, float (&v)[kChunk],
                                              const PairBox& box) const {
-    if (row0 < rows && col < V) chunk(row0, col, v, box);
+    if (row0 < rows && col < V) chunk(row0, col, target_from(row0, col, box), v, box);
   }
-  __device__ __forceinline__ void chunk(int64_t row0, int64_t col, float (&v)[kChunk], const PairBox& box) const {
+  __device__ __forceinline__ void chunk(int64_t row0, int64_t col, int64_t y, float (&v)[kChunk], const PairBox& box) const {
+    // One branch for the warp: few chunks hold the target of any of its rows.
+    // By a bit for each column: a comparison with the index would become an
+    // indexed store, and v would live in local memory.
+    const bool here = y >= 0 && y < kChunk;
+    if (__any_sync(0xffffffffu, here)) {
+      const uint64_t bit = here ? 1ull << y : 0;
+      const uint32_t lo = (uint32_t)bit, hi = (uint32_t)(bit >> 32);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if ((i < 32 ? lo >> i : hi >> (i - 32)) & 1u) v[i] = -INFINITY;
+    }
     const int left = V - col < kChunk ? (int)(V - col) : kChunk;
     if (left < kChunk) {
 #pragma unroll
@@ -133,10 +160,8 @@ struct LogitsEpilogue {
   }
 };
 
-// Joins a row's chunks: lse and loss.  One block for each token.  The target's
-// logit is computed again, in fp32 with 128 sums: the tensor cores round
-// towards zero in their long sums (1e-6 of a logit of 4096 terms), which
-// averages out over a vocabulary but not in the one logit.
+// Joins a row's chunks and its target's logit, summed in fp32 with 128 sums:
+// lse and loss.  One block for each token.
 template <class T>
 __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t chunks, int64_t ld, const int64_t* target,
                                                    int64_t V, const T* H, int64_t ldh, const T* W, int64_t ldw, int64_t D,
@@ -177,9 +202,11 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t 
   t[0] = m == -INFINITY ? 0.f : s * exp2_approx(m - top);
   block_reduce<2>(t, red, SumOp());
   if (threadIdx.x == 0) {
-    const float l = (top + log2f(t[0])) * kLn2;
-    lse[blockIdx.x] = l;
-    loss[blockIdx.x] = has ? l - t[1] : 0.f;
+    const float rest = (top + log2f(t[0])) * kLn2, d = rest - t[1];
+    // Either way the larger of the two with what the smaller one adds to it.
+    const float more = log1pf(expf(-fabsf(d)));
+    lse[blockIdx.x] = !has ? rest : d > 0.f ? rest + more : t[1] + more;
+    loss[blockIdx.x] = !has ? 0.f : d > 0.f ? d + more : more;
   }
 }
 
@@ -187,13 +214,14 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t 
 template <class T>
 __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t ldk, const float2* stats, int64_t chunks,
                                                        const int64_t* target, int64_t V, const float* coef,
-                                                       const float* lse) {
+                                                       const float* lse, const float* loss) {
   const int64_t row = blockIdx.y;
   const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (col >= ldk) return;
   const float c = coef[row];
   const float off = stats[row * chunks + col / kChunk].x - lse[row] * kLog2e;
   const int64_t y = target[row] - col;
+  const float wrong = y >= 0 && y < 8 ? expm1f(-loss[row]) : 0.f;  // p - 1 of the target
   uint16_t* at = kept + row * ldk + col;
   const uint4 q = *reinterpret_cast<const uint4*>(at);
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -203,7 +231,7 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
     const uint32_t u = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
     // 65535: too far below; still NaN where the row's sum is
     const float p = u == 65535u ? off - off : exp2_approx(fmaf((float)u, -1.f / kSteps, off));
-    g[i] = c == 0.f ? 0.f : c * kGScale * (p - (y == i ? 1.f : 0.f));
+    g[i] = c == 0.f ? 0.f : c * kGScale * (y == i ? wrong : p);
   }
   if (V - col < 8) {
 #pragma unroll
@@ -397,12 +425,12 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
     const PairOperand ph{h, m, ldh}, pw{W, p.V, ldw};
     cudaError_t e;
     if (grad) {
-      LogitsEpilogue<true> epi{{}, m, p.V, stats, chunks};
+      LogitsEpilogue<true> epi{{}, m, p.V, target, stats, chunks};
       e = make_tensor_map(&epi.map, TileMap{kept, CU_TENSOR_MAP_DATA_TYPE_UINT16, m, ldk, ldk, 32, 64, true});
       if (e != cudaSuccess) return e;
       e = logits_launch(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
     } else {
-      const LogitsEpilogue<false> epi{{}, m, p.V, stats, chunks};
+      const LogitsEpilogue<false> epi{{}, m, p.V, target, stats, chunks};
       e = logits_launch(ph, pw, p.D, bf16, logits, epi, status, stream, t == 0 ? 0 : -1);
     }
     if (e != cudaSuccess) return e;
@@ -421,7 +449,8 @@ cudaError_t run(const CrossEntropy& p, char* ws, int32_t* status, cudaStream_t s
     if (!grad) continue;
     for (int64_t r = 0; r < m; r += 65535)
       gradient_kernel<T><<<dim3((unsigned)((ldk / 8 + 255) / 256), (unsigned)std::min<int64_t>(65535, m - r)), 256, 0, stream>>>(
-          kept + r * ldk, ldk, stats + r * chunks, chunks, target + r, p.V, coef + t + r, p.lse + t + r);
+          kept + r * ldk, ldk, stats + r * chunks, chunks, target + r, p.V, coef + t + r, p.lse + t + r,
+          p.loss + t + r);
     const PairOperand pg{kept, m, ldk}, pgt{kept, p.V, ldk}, pwt{W, p.D, ldw}, pht{h, p.D, ldh};
     T* dH = static_cast<T*>(p.dH) + t * p.D;
     const int parts = dh_parts(m, p.D, p.V, kPlanPairs);

@@ -1,0 +1,121 @@
+"""Cross entropy where logits are large, masked or decided, with few tokens' coefficients of another size, and in several
+pieces, against fp64.
+
+Most inputs here are made so that a logit is one exact product (of whole numbers and powers of two in a few columns): the tensor cores'
+sums then have no error, and what is left is the operator's own.  Tolerances, for logits that are exact: a row's sum of
+exponentials is good to 2^-13 (1024 additions along any path, an exponential to 2^-21), which moves lse and loss by as
+much, besides 2^-22 of their and the logits' sizes.  An entry of G is within p (2^-12 + 2^-13 + 2^-22 max |x|) + 2^-31 of
+its coefficient before it is rounded to 16 bits: a step of the kept logarithms, the sum's error, and the rounding of
+lse to fp32, which for large logits is what p is known to."""
+
+import pytest
+
+from test_gpu_cross_entropy import U, _close, bk  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _exact(h, w, y, coef):
+    """fp64 (loss, tolerance), (lse, tolerance), G and its error for exact logits."""
+    import torch
+
+    x = h.double() @ w.double().t()
+    has = (y >= 0) & (y < len(w))
+    at = y.clamp(0, len(w) - 1)[:, None]
+    lse = torch.logsumexp(x, 1)
+    size = torch.where(x > lse[:, None] - 100, x.abs(), 0.0).amax(1)  # of the logits that count
+    right = x.gather(1, at)[:, 0]
+    # log-sum of the others, so that a loss near zero keeps its digits
+    rest = torch.logsumexp(x.scatter(1, at, -float("inf")), 1)
+    loss = torch.where(has, torch.nn.functional.softplus(rest - right), 0.0)
+    loss = torch.where(has & (rest == -float("inf")), 0.0, loss)
+    tol = 2.0 ** -13 + 2.0 ** -22 * size
+    p = torch.exp(x - lse[:, None])
+    hot = torch.zeros_like(p).scatter_(1, at, has.double()[:, None])
+    c = torch.where(has, coef.double(), 0.0)[:, None]
+    return (loss, tol * torch.clamp(loss, max=1.0) + 2.0 ** -22 * loss + 1e-30), (lse, tol), c * (p - hot), \
+        c.abs() * (p * (2.0 ** -12 + tol[:, None]) + 2.0 ** -31)
+
+
+def _check(bk, h, w, y, coef=None, finite=True):
+    """Both calls against fp64, gradients too."""
+    import torch
+
+    dtype = str(h.dtype).replace("torch.", "")
+    has = (y >= 0) & (y < len(w))
+    given = has.float() / has.sum().clamp(min=1) if coef is None else coef
+    loss, lse, g, err = _exact(h, w, y, given)
+    got = bk.linear_cross_entropy(h, w, y)
+    assert int(got[2].item()) == 0
+    _close(got[0], *loss)
+    _close(got[1], *lse)
+    l2, s2, dh, dw, st = bk.linear_cross_entropy_grad(h, w, y, coef=coef)
+    assert int(st.item()) == 0
+    _close(l2, *loss)
+    _close(s2, *lse)
+    if finite:
+        e = err + U[dtype] * (g.abs() + err)
+        for out, a, b, ea in ((dh, g, w.double(), e), (dw, g.t(), h.double(), e.t())):
+            ref = a @ b
+            tol = ea @ b.abs() + (2 * a.shape[1] + 16) * 2.0 ** -24 * ((a.abs() + ea) @ b.abs())
+            _close(out, ref, tol + U[dtype] * (ref.abs() + tol) + (2.0 ** -24 if dtype == "float16" else 1e-38))
+    return loss[0], dh, dw
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("v", [1000, 8193, 32000])
+@pytest.mark.parametrize("logit", [5.0, 15.0, 30.0])
+def test_losses_of_confident_tokens(bk, logit, v, dtype):  # noqa: F811
+    """4096 terms for each logit, the target's about `logit`.  A loss is never negative, and its error is that of the
+    others' log-sum below the target's logit: the tensor cores' sums of 4096 terms come out up to 2^-16 (256 steps of
+    16 terms, 2^-24 each) of their size too small, of the others' about 5, the target's own sum is good to 2^-18 of it
+    (128 sums of 32 terms, their magnitudes several times the logit), and all of it counts with 1 - p."""
+    import torch
+
+    t, d = 64, 4096
+    gen = torch.Generator(device="cuda").manual_seed(v)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    w = (rand(v, d) * d ** -0.5).to(getattr(torch, dtype))
+    y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+    h = (rand(t, d) + logit * w[y].float()).to(w.dtype)
+    x = h.double() @ w.double().t()
+    right = x.gather(1, y[:, None])[:, 0]
+    rest = torch.logsumexp(x.scatter(1, y[:, None], -float("inf")), 1)
+    want = torch.nn.functional.softplus(rest - right)
+    tol = -torch.expm1(-want) * (2.0 ** -16 * 5 + 2.0 ** -18 * right.abs()) + 2.0 ** -21 * want
+    for loss, lse in (bk.linear_cross_entropy(h, w, y)[:2], bk.linear_cross_entropy_grad(h, w, y)[:2]):
+        assert bool((loss >= 0).all()), float(loss.min())
+        _close(loss, want, tol)
+        _close(lse, want + right, tol + 2.0 ** -18 * right.abs())
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("logit", [10.0, 40.0])
+def test_gradients_of_confident_tokens(bk, logit, dtype):  # noqa: F811
+    """dH of a token that is right: c (p_y - 1) w_y and the others' p w, both of them about 1 - p."""
+    import torch
+
+    t, d, v = 32, 64, 500
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    h, w = torch.zeros((t, d), device="cuda"), torch.zeros((v, d), device="cuda")
+    w[:, 0] = torch.randint(-3, 4, (v,), generator=gen, device="cuda").float()
+    w[:, 1 + t:] = torch.randint(-8, 9, (v, d - 1 - t), generator=gen, device="cuda").float()
+    y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+    each = torch.arange(t, device="cuda")
+    w[y, 1 + each] = 1  # a column for each token, which its target alone answers to
+    h[:, 0] = 0.25
+    h[each, 1 + each] = logit
+    h, w = h.to(getattr(torch, dtype)), w.to(getattr(torch, dtype))
+    coef = torch.exp(torch.full((t,), min(logit, 20.0), device="cuda"))  # so that fp16 results are not below their steps
+    _check(bk, h, w, y, coef)
+    _, _, dh, _, _ = bk.linear_cross_entropy_grad(h, w, y, coef=coef)
+    x = h.double() @ w.double().t()
+    x, right = x.scatter(1, y[:, None], -float("inf")), x.gather(1, y[:, None])
+    q = torch.sigmoid(torch.logsumexp(x, 1, keepdim=True) - right)  # 1 - p
+    part = (torch.softmax(x, 1) * q).scatter(1, y[:, None], -q) * coef.double()[:, None]
+    ref = part @ w.double()
+    # Relative to 1 - p: a kept logarithm's step (2^-12), the sum of exponentials (2^-13), 500 terms' sum (2^-14), G's and
+    # the result's rounding.  No word lies below the kept range here; G in fp16 ends 2^-39 below the largest coefficient.
+    floor = 2.0 ** -39 * float(coef.max()) if dtype == "float16" else 0.0
+    tol = (part.abs() * (2.0 ** -10 + U[dtype]) + floor) @ w.double().abs()
+    _close(dh, ref, tol + U[dtype] * ref.abs() + 2.0 ** -24)
