@@ -16,8 +16,8 @@
 // with r_t the log-sum of the other words and d_t = r_t - x_t,y(t),
 //     loss_t = log(1 + exp(d_t)),  lse_t = x_t,y(t) + loss_t,
 //     G_t,y(t) = -c_t (1 - exp(-loss_t)).
-// The tensor cores round towards zero in their long sums (up to 4e-6 of a logit
-// of 4096 terms).  Over the other words that is an error of their log-sum,
+// The tensor cores round towards zero in their long sums (3e-4 of a logit of 30
+// over 4096 terms).  Over the other words that is an error of their log-sum,
 // which counts with their share 1 - p; as a difference between two versions of
 // the target's logit it would count in full, and a loss near zero would come
 // out below it.
@@ -26,7 +26,9 @@
 // as the 16-bit fixed-point number round(2048 (m - x) log2 e), m the maximum
 // of its 64 columns: a relative error of exp(x) of at most 1.7e-4 (1e-4 rms,
 // against 1.7e-3 rms of rounding to bf16 or 2.1e-4 to fp16), and a range of
-// 2^-32 below the maximum.  A pass over the piece turns it into G in place,
+// 2^-32 below the maximum.  (The difference is taken first and then scaled: a
+// rounded m log2 e in place of m would leave its remainder, which for logits
+// in the thousands is more than a step, and for a mask's value is anything.)  A pass over the piece turns it into G in place,
 // and G, 16-bit, is the operand of the two other products.  This reads and
 // writes 6 bytes for each logit, where computing the logits a second time
 // would cost a third of the products again; a piece holds at most 1 GiB.
@@ -41,7 +43,7 @@
 namespace bakron {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kChunk = 64;              // columns that share a maximum
 constexpr float kSteps = 2048.f;        // fixed-point steps in a factor of two
 constexpr float kGScale = 32768.f;      // G is stored times this, so that fp16 keeps p down to 2^-29
@@ -54,6 +56,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+
+// exp(from - to), 1 where both are the same infinity.
+__device__ __forceinline__ float exp_diff(float from, float to) {
+  return from == to ? 1.f : exp2_approx((from - to) * kLog2e);
 }
 
 // c_t / max |c| of every token, and what the gradients are scaled by in the
@@ -92,7 +99,7 @@ struct LogitsEpilogue {
   CUtensorMap map;  // of the kept logits
   int64_t rows, V;
   const int64_t* target;
-  float2* stats;  // rows x chunks, of all words but the target: maximum in units of log 2, sum of 2^(x - maximum)
+  float2* stats;  // rows x chunks, of all words but the target: maximum, sum of exp(x - maximum)
   int64_t chunks;
 
   // The thread's row's target, as a column from `col` on.
@@ -136,20 +143,28 @@ struct LogitsEpilogue {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) m = fmaxf(m, v[i]);
-    m = m == -INFINITY ? 0.f : m * kLog2e;
+    if (m == -INFINITY) m = 0.f;
+    const F2 minus_m = f2(-m), log2e = f2(kLog2e);
     if constexpr (kKeep) box.open();
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < kChunk; j += 8) {
       uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = fmaf(v[j + i], kLog2e, -m);
-        // -kSteps x rounded to an integer in the low bits of 1.5 2^23 + it.
-        // A NaN is lost here; its row's sum is NaN, which is what counts.
-        constexpr float kMagic = 12582912.f;
-        if constexpr (kKeep) w[i] = __float_as_uint(fminf(fmaf(x, -kSteps, kMagic), kMagic + 65535.f));
-        s += exp2_approx(x);
+      for (int i = 0; i < 8; i += 2) {
+        const F2 x = (f2(v[j + i], v[j + i + 1]) + minus_m) * log2e;  // at most 0
+        if constexpr (kKeep) {
+          // -kSteps x rounded to an integer in the low bits of 1.5 2^23 + it.
+          // A NaN is lost here; its row's sum is NaN, which is what counts.
+          constexpr float kMagic = 12582912.f;
+          float a, b;
+          split(fma2(x, f2(-kSteps), f2(kMagic)), a, b);
+          w[i] = __float_as_uint(fminf(a, kMagic + 65535.f)), w[i + 1] = __float_as_uint(fminf(b, kMagic + 65535.f));
+        }
+        float a, b;
+        split(x, a, b);
+        s += exp2_approx(a);
+        s += exp2_approx(b);
       }
       if constexpr (kKeep)
         box.put(j / 8, __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[4], w[5], 0x5410),
@@ -190,7 +205,7 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t 
   for (int64_t c = threadIdx.x; c < chunks; c += 128) {
     const float2 e = row[c];
     const float to = fmaxf(m, e.x);
-    s = s * exp2_approx(m - to) + e.y * exp2_approx(e.x - to);
+    s = s * exp_diff(m, to) + e.y * exp_diff(e.x, to);
     m = to;
   }
   float top = m;
@@ -199,10 +214,10 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t 
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
   __syncthreads();
   top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  t[0] = m == -INFINITY ? 0.f : s * exp2_approx(m - top);
+  t[0] = s * exp_diff(m, top);
   block_reduce<2>(t, red, SumOp());
   if (threadIdx.x == 0) {
-    const float rest = (top + log2f(t[0])) * kLn2, d = rest - t[1];
+    const float sum = logf(t[0]), rest = top + sum, d = (top - t[1]) + sum;
     // Either way the larger of the two with what the smaller one adds to it.
     const float more = log1pf(expf(-fabsf(d)));
     lse[blockIdx.x] = !has ? rest : d > 0.f ? rest + more : t[1] + more;
@@ -219,7 +234,7 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
   const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (col >= ldk) return;
   const float c = coef[row];
-  const float off = stats[row * chunks + col / kChunk].x - lse[row] * kLog2e;
+  const float off = (stats[row * chunks + col / kChunk].x - lse[row]) * kLog2e;
   const int64_t y = target[row] - col;
   const float wrong = y >= 0 && y < 8 ? expm1f(-loss[row]) : 0.f;  // p - 1 of the target
   uint16_t* at = kept + row * ldk + col;

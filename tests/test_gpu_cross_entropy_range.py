@@ -62,6 +62,75 @@ def _check(bk, h, w, y, coef=None, finite=True):
     return loss[0], dh, dw
 
 
+def _one_column(t, d, v, dtype, sizes, seed=0):
+    """Logits h[t, 0] w[v, 0] + h[t, 1] w[v, 1]: a whole number of up to 8 bits times one of up to 3, or the like."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    h = torch.zeros((t, d), device="cuda")
+    w = torch.zeros((v, d), device="cuda")
+    pick = torch.tensor(sizes, device="cuda", dtype=torch.float32)
+    h[:, 0] = pick[torch.randint(0, len(sizes), (t,), generator=gen, device="cuda")]
+    w[:, 0] = 1
+    w[:, 1] = torch.randint(-6, 7, (v,), generator=gen, device="cuda").float()
+    h[:, 1] = 1
+    y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+    to = getattr(torch, dtype)
+    return h.to(to), w.to(to), y
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("v", [300, 9000])
+def test_large_logits_of_a_row(bk, v, sign, dtype):  # noqa: F811
+    """A row's logits all near +-5000 to 30000: what counts are their differences, 0 to 12."""
+    sizes = [sign * s for s in (5120, 5760, 6016, 7168, 8192, 9984, 11008, 14336, 16256, 20480, 23040, 26624, 30720)]
+    h, w, y = _one_column(150, 24, v, dtype, sizes)
+    _check(bk, h, w, y)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("v", [200, 9000])
+def test_a_row_decided_by_one_large_logit(bk, v, dtype):  # noqa: F811
+    """One word far above the rest of its row, at the sizes where a rounded maximum leaves a remainder: p = 1 there, for the
+    target (no gradient left) or for another word (all of it)."""
+    import torch
+
+    t = 120
+    h = torch.zeros((t, 16), device="cuda")
+    h[:, 0] = 5700 + 128 * torch.arange(t, device="cuda")
+    w = torch.zeros((v, 16), device="cuda")
+    w[v // 3, 0] = 1
+    y = torch.full((t,), v // 3, device="cuda")
+    y[::2] = v - 1
+    to = getattr(torch, dtype)
+    _check(bk, h.to(to), w.to(to), y)
+    _check(bk, -h.to(to), w.to(to), y)
+
+
+@pytest.mark.parametrize("mask", [-1e4, -6e4, -1e9, -1e30, -3.3895e38])
+@pytest.mark.parametrize("v,masked", [(700, 200), (700, 640), (9000, 8000), (65, 1)])
+def test_masked_words(bk, v, masked, mask):  # noqa: F811
+    """A column of ones in H and a mask's value in W leave words out, here whole runs of 64 of them, with the other logits
+    far below zero too (an all-masked run is then the largest number about if it is taken for zero)."""
+    import torch
+
+    for low in (0.0, -120.0, -1000.0):
+        gen = torch.Generator(device="cuda").manual_seed(v + masked)
+        h = torch.zeros((40, 32), device="cuda")
+        w = torch.zeros((v, 32), device="cuda")
+        h[:, 0] = 1
+        h[:, 1] = torch.randint(-4, 5, (40,), generator=gen, device="cuda").float()
+        w[:, 0] = low
+        w[v - masked:, 0] = mask
+        w[:v - masked, 1] = torch.randint(-2, 3, (v - masked,), generator=gen, device="cuda").float()
+        y = torch.randint(0, v - masked, (40,), generator=gen, device="cuda")
+        y[::7] = -100
+        loss, dh, dw = _check(bk, h.bfloat16(), w.bfloat16(), y, finite=mask > -float("inf"))
+        assert torch.isfinite(loss).all()
+        assert not dw[v - masked:].any()  # no token's probability reaches them
+
+
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("v", [1000, 8193, 32000])
 @pytest.mark.parametrize("logit", [5.0, 15.0, 30.0])
