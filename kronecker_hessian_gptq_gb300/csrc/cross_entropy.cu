@@ -143,8 +143,8 @@ struct LogitsEpilogue {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) m = fmaxf(m, v[i]);
-    if (m == -INFINITY) m = 0.f;
-    const F2 minus_m = f2(-m), log2e = f2(kLog2e);
+    // All of them -infinity: their sum is 0, and so it stays below any other maximum.
+    const F2 minus_m = f2(m == -INFINITY ? 0.f : -m), log2e = f2(kLog2e);
     if constexpr (kKeep) box.open();
     float s = 0.f;
 #pragma unroll
@@ -217,10 +217,12 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* stats, int64_t 
   t[0] = s * exp_diff(m, top);
   block_reduce<2>(t, red, SumOp());
   if (threadIdx.x == 0) {
-    const float sum = logf(t[0]), rest = top + sum, d = (top - t[1]) + sum;
+    const float sum = logf(t[0]), rest = top + sum;
+    const float d = t[1] < INFINITY ? (top - t[1]) + sum : NAN;
     // Either way the larger of the two with what the smaller one adds to it.
     const float more = log1pf(expf(-fabsf(d)));
-    lse[blockIdx.x] = !has ? rest : d > 0.f ? rest + more : t[1] + more;
+    const float both = d > 0.f ? rest + more : t[1] + more;
+    lse[blockIdx.x] = !has || (rest == -INFINITY && t[1] == -INFINITY) ? rest : both;
     loss[blockIdx.x] = !has ? 0.f : d > 0.f ? d + more : more;
   }
 }
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
   const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (col >= ldk) return;
   const float c = coef[row];
-  const float off = (stats[row * chunks + col / kChunk].x - lse[row]) * kLog2e;
+  const float l = lse[row], off = (stats[row * chunks + col / kChunk].x - l) * kLog2e;
   const int64_t y = target[row] - col;
   const float wrong = y >= 0 && y < 8 ? expm1f(-loss[row]) : 0.f;  // p - 1 of the target
   uint16_t* at = kept + row * ldk + col;
@@ -244,8 +246,8 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t u = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
-    // 65535: too far below; still NaN where the row's sum is
-    const float p = u == 65535u ? off - off : exp2_approx(fmaf((float)u, -1.f / kSteps, off));
+    // 65535: too far below, or -infinity; still NaN where the row's sum is
+    const float p = u == 65535u ? l - l : exp2_approx(fmaf((float)u, -1.f / kSteps, off));
     g[i] = c == 0.f ? 0.f : c * kGScale * (y == i ? wrong : p);
   }
   if (V - col < 8) {

@@ -108,7 +108,7 @@ def test_a_row_decided_by_one_large_logit(bk, v, dtype):  # noqa: F811
     _check(bk, -h.to(to), w.to(to), y)
 
 
-@pytest.mark.parametrize("mask", [-1e4, -6e4, -1e9, -1e30, -3.3895e38])
+@pytest.mark.parametrize("mask", [-1e4, -6e4, -1e9, -1e30, -3.3895e38, -float("inf")])
 @pytest.mark.parametrize("v,masked", [(700, 200), (700, 640), (9000, 8000), (65, 1)])
 def test_masked_words(bk, v, masked, mask):  # noqa: F811
     """A column of ones in H and a mask's value in W leave words out, here whole runs of 64 of them, with the other logits
@@ -129,6 +129,39 @@ def test_masked_words(bk, v, masked, mask):  # noqa: F811
         loss, dh, dw = _check(bk, h.bfloat16(), w.bfloat16(), y, finite=mask > -float("inf"))
         assert torch.isfinite(loss).all()
         assert not dw[v - masked:].any()  # no token's probability reaches them
+
+
+def test_a_masked_target_and_a_row_without_words(bk):  # noqa: F811
+    import torch
+
+    inf = float("inf")
+    h = torch.zeros((4, 16), device="cuda")
+    h[:, 0] = 1
+    w = torch.zeros((200, 16), device="cuda")
+    w[100:, 0] = -inf
+    y = torch.tensor([3, 150, -1, 199], device="cuda")
+    loss, lse, _ = bk.linear_cross_entropy(h.bfloat16(), w.bfloat16(), y)
+    want = torch.log(torch.tensor(100.0, device="cuda"))
+    assert torch.isposinf(loss[[1, 3]]).all() and loss[2] == 0 and (loss[0] - want).abs() < 1e-4
+    assert ((lse - want).abs() < 1e-4).all()
+    w[:, 0] = -inf
+    for target in (-1, 5):
+        loss, lse, _ = bk.linear_cross_entropy(h.bfloat16(), w.bfloat16(), torch.full((4,), target, device="cuda"))
+        assert torch.isneginf(lse).all() and (torch.isnan(loss).all() if target >= 0 else not loss.any())
+
+
+def test_an_infinite_logit_of_the_target(bk):  # noqa: F811
+    """lse - x is infinity less infinity, whether or not another word is infinite too."""
+    import torch
+
+    h = torch.zeros((3, 16), device="cuda")
+    h[:, 0] = 1
+    w = torch.zeros((200, 16), device="cuda")
+    w[70, 0] = float("inf")
+    for words in (1, 2):
+        w[69 + words, 0] = float("inf")
+        loss, lse, dh, _, _ = bk.linear_cross_entropy_grad(h.bfloat16(), w.bfloat16(), torch.tensor([70, 3, -1], device="cuda"))
+        assert torch.isnan(loss[:2]).all() and torch.isnan(lse).all() and loss[2] == 0 and torch.isnan(dh[:2]).any(1).all()
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
