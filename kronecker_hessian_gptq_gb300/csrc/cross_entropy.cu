@@ -64,8 +64,9 @@ __device__ __forceinline__ float exp_diff(float from, float to) {
 }
 
 // c_t / max |c| of every token, and what the gradients are scaled by in the
-// end, max |c| / kGScale.  One block.  (Targets that are too large are
-// reported by join_kernel.)
+// end, max |c| / kGScale.  The largest of the finite ones: another stays what
+// it is and reaches its own row of G only.  One block.  (Targets that are too
+// large are reported by join_kernel.)
 __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* target, int64_t T, int64_t V, const float* given,
                                                             float* coef, float* scale) {
   __shared__ int with;
@@ -78,17 +79,17 @@ __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* targe
     const int64_t y = target[t];
     if (y >= 0 && y < V) {
       ++n;
-      if (given) top[0] = MaxOp()(fabsf(given[t]), top[0]);
+      if (given && isfinite(given[t])) top[0] = fmaxf(fabsf(given[t]), top[0]);
     }
   }
   if (n) atomicAdd(&with, n);
   block_reduce<1>(top, red, MaxOp());
   __syncthreads();
-  const float most = given ? top[0] : (with ? 1.f / (float)with : 0.f);
+  const float most = !given ? 1.f / (float)max(with, 1) : top[0] > 0.f ? top[0] : 1.f;
   if (threadIdx.x == 0) *scale = most / kGScale;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const bool has = target[t] >= 0 && target[t] < V;
-    coef[t] = !has || most == 0.f ? 0.f : given ? given[t] / most : 1.f;
+    coef[t] = !has ? 0.f : given ? given[t] / most : 1.f;
   }
 }
 

@@ -10,7 +10,7 @@ lse to fp32, which for large logits is what p is known to."""
 
 import pytest
 
-from test_gpu_cross_entropy import U, _close, bk  # noqa: F401
+from test_gpu_cross_entropy import U, _close, _make, bk  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +221,25 @@ def test_gradients_of_confident_tokens(bk, logit, dtype):  # noqa: F811
     floor = 2.0 ** -39 * float(coef.max()) if dtype == "float16" else 0.0
     tol = (part.abs() * (2.0 ** -10 + U[dtype]) + floor) @ w.double().abs()
     _close(dh, ref, tol + U[dtype] * ref.abs() + 2.0 ** -24)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_a_coefficient_that_is_not_finite_keeps_to_its_token(bk, dtype, bad):  # noqa: F811
+    """G[t] = coef[t] (p - hot): only row t of dH is touched (dW is a sum over all rows)."""
+    import torch
+
+    h, w, y = _make(140, 64, 400, dtype)
+    y[:5] = 7
+    coef = torch.rand(140, device="cuda") + 0.5
+    clean = bk.linear_cross_entropy_grad(h, w, y, coef=coef)
+    coef[3] = bad
+    loss, lse, dh, dw, st = bk.linear_cross_entropy_grad(h, w, y, coef=coef)
+    rest = torch.arange(140, device="cuda") != 3
+    assert int(st.item()) == 0 and torch.equal(loss, clean[0]) and torch.equal(lse, clean[1])
+    assert not torch.isfinite(dh[3]).any() and torch.isfinite(dh[rest]).all()
+    # the largest coefficient, by which all are divided, may have been the third
+    assert torch.allclose(dh[rest].float(), clean[2][rest].float(), rtol=4 * U[dtype], atol=4 * U[dtype] * float(clean[2].abs().max()))
+    assert not torch.isfinite(dw).all()
+    zero = bk.linear_cross_entropy_grad(h, w, y, coef=torch.where(rest, 0.0, coef))
+    assert not zero[2][rest].any() and not torch.isfinite(zero[2][3]).any()
