@@ -31,7 +31,8 @@
 // in the thousands is more than a step, and for a mask's value is anything.)  A pass over the piece turns it into G in place,
 // and G, 16-bit, is the operand of the two other products.  This reads and
 // writes 6 bytes for each logit, where computing the logits a second time
-// would cost a third of the products again; a piece holds at most 1 GiB.
+// would cost a third of the products again.  A piece's logits take at most 1
+// GiB, and for the loss alone its statistics 256 MiB, or what 256 tokens take.
 #include <algorithm>
 #include <type_traits>
 
@@ -49,7 +50,8 @@ constexpr float kSteps = 2048.f;        // fixed-point steps in a factor of two
 constexpr float kGScale = 32768.f;      // G is stored times this, so that fp16 keeps p down to 2^-29
 constexpr int kSumTerms = 512;          // terms that the tensor cores sum at a stretch, and
 constexpr int64_t kFewLogits = 8192;    // the vocabulary up to which: see logits_launch()
-constexpr int64_t kPieceBytes = (int64_t)1 << 30;
+constexpr int64_t kPieceBytes = (int64_t)1 << 30;       // of kept logits
+constexpr int64_t kPieceStatsBytes = (int64_t)1 << 28;  // of statistics, for the loss alone
 constexpr int64_t kPieceTokens = (int64_t)1 << 20;  // keeps the number of tiles and the length of a sum bounded
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -337,8 +339,8 @@ int64_t tiles(int64_t x) { return (x + kPairTile - 1) / kPairTile; }
 
 // Tokens of a piece: all, or as many whole tiles as the limits allow.
 int64_t piece_tokens(int64_t T, int64_t V, bool grad) {
-  const int64_t fit = std::max<int64_t>(1, kPieceBytes / (2 * up64(V)) / kPairTile) * kPairTile;
-  return std::min({T, grad ? fit : kPieceTokens, kPieceTokens});
+  const int64_t token = grad ? 2 * up64(V) : tiles(V) * 4 * 8, most = grad ? kPieceBytes : kPieceStatsBytes;
+  return std::min({T, std::max<int64_t>(1, most / token / kPairTile) * kPairTile, kPieceTokens});
 }
 
 // Parts of K for dH: few tiles over a long K leave pairs of SMs idle, or a
@@ -370,10 +372,10 @@ Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
     at += up(bytes);
     return here;
   };
-  l.coef = take(T * 4);
-  l.scale = take(4);
   l.stats = take(n * chunks * 8);
   if (grad) {
+    l.coef = take(T * 4);
+    l.scale = take(4);
     l.kept = take(n * up64(V) * 2);
     const int p = dh_parts(n, D, V, kPlanPairs), p2 = T % n ? dh_parts(T % n, D, V, kPlanPairs) : 1;
     l.part = take(std::max(p > 1 ? (size_t)p * n * D * 4 : 0, p2 > 1 ? (size_t)p2 * (T % n) * D * 4 : 0));

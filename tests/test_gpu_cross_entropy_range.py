@@ -10,7 +10,7 @@ lse to fp32, which for large logits is what p is known to."""
 
 import pytest
 
-from test_gpu_cross_entropy import U, _close, _make, bk  # noqa: F401
+from test_gpu_cross_entropy import U, _close, _make, _reference, bk  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +243,20 @@ def test_a_coefficient_that_is_not_finite_keeps_to_its_token(bk, dtype, bad):  #
     assert not torch.isfinite(dw).all()
     zero = bk.linear_cross_entropy_grad(h, w, y, coef=torch.where(rest, 0.0, coef))
     assert not zero[2][rest].any() and not torch.isfinite(zero[2][3]).any()
+
+
+def test_losses_of_more_tokens_than_one_piece_holds(bk):  # noqa: F811
+    """The loss alone, over a vocabulary so large that its statistics are taken in pieces of the tokens."""
+    import torch
+
+    h, w, y = _make(2600, 16, 1000003, "bfloat16")
+    y[2500] = 1000003
+    loss, lse, st = bk.linear_cross_entropy(h, w, y)
+    assert int(st.item()) == 8
+    for lo, hi in ((0, 700), (1900, 2200), (2300, 2600)):
+        part = bk.linear_cross_entropy(h[lo:hi], w, y[lo:hi])
+        assert torch.equal(part[0], loss[lo:hi]) and torch.equal(part[1], lse[lo:hi])
+    for q in (slice(0, 20), slice(2040, 2060), slice(2590, 2600)):
+        r = _reference(h[q], w, y[q])
+        _close(loss[q], *r["loss"])
+        _close(lse[q], *r["lse"])

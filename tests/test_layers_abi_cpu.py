@@ -126,3 +126,10 @@ def test_arrays_of_32_bits_off_their_elements(lib):
     refused(lib.bakron_linear_cross_entropy_grad, good, coef=[off], loss=[off], lse=[off], status=[off])
     good = {k: v for k, v in good.items() if k not in ("coef", "dH", "dW")}
     refused(lib.bakron_linear_cross_entropy, good, loss=[off], lse=[off], status=[off])
+
+
+def test_statistics_of_the_loss_are_bounded(lib):
+    """8 bytes for 64 logits: taken in pieces of the tokens, of 256 MiB or 256 tokens, whatever the tokens' number."""
+    size = lib.bakron_linear_cross_entropy_workspace_size
+    for T, V in ((1 << 18, 1 << 17), (1 << 16, 1 << 24), ((1 << 31) - 1, 32000)):
+        assert size(T, 64, V, 0, 0) <= max(1 << 28, 256 * V // 8) + 4 * T + 4096
