@@ -95,7 +95,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         )
     lib = ctypes.CDLL(path)
     for name, (res, args) in SIGNATURES.items():
-        fn = getattr(lib, name)
+        fn = getattr(lib, name, None)
+        if fn is None:
+            raise RuntimeError(
+                f"{path} has no {name}: it is of an older version than this package, build it again "
+                "(python -c 'import __graft_entry__ as g; g.build()')"
+            )
         fn.restype = res
         fn.argtypes = args
     _lib = lib

@@ -74,3 +74,15 @@ def test_the_workspace_lives_until_the_call_has_returned(entries, name, call):
     """Memory that is given back before the launches can be handed to another thread, or unmapped, meanwhile."""
     call()
     assert entries == [(name, True)]
+
+
+def test_a_library_without_an_entry_point_is_named(monkeypatch):
+    """An older libbakron.so than the package's own: the error says which file and what it lacks."""
+    from kronecker_hessian_gptq_gb300 import _lib
+    from kronecker_hessian_gptq_gb300 import build as b
+
+    b.build()
+    monkeypatch.setattr(_lib, "_lib", None)
+    monkeypatch.setitem(_lib.SIGNATURES, "bakron_of_a_later_version", (None, []))
+    with pytest.raises(RuntimeError, match="libbakron.so.*bakron_of_a_later_version.*build it again"):
+        _lib.load()
