@@ -49,7 +49,7 @@ constexpr int kChunk = 64;              // columns that share a maximum
 constexpr float kSteps = 2048.f;        // fixed-point steps in a factor of two
 constexpr float kGScale = 32768.f;      // G is stored times this, so that fp16 keeps p down to 2^-29
 constexpr int kSumTerms = 512;          // terms that the tensor cores sum at a stretch, and
-constexpr int64_t kFewLogits = 8192;    // the vocabulary up to which: see logits_launch()
+constexpr int64_t kFewLogits = 8192;    // the vocabulary up to which they do: see logits_launch()
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;       // of kept logits
 constexpr int64_t kPieceStatsBytes = (int64_t)1 << 28;  // of statistics, for the loss alone
 constexpr int64_t kPieceTokens = (int64_t)1 << 20;  // keeps the number of tiles and the length of a sum bounded
@@ -389,13 +389,18 @@ Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
 
 bool tma_rows(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
 
-// The tensor cores round towards zero as they sum, so long sums come out small
-// by up to 1e-6 of 4096 terms.  Over a large vocabulary that averages out; over
-// a small one lse is little else than its few largest logits.  There the sums
-// are restarted every 512 terms and added up in fp32 (error of 20 tokens'
-// losses, 4096 x 1000: 1.9e-6 of them without, 2e-7 with it).  It costs most
-// of half the product's time (1024 tokens, 4096 x 32000: 239 us, 147 without),
-// and the error there is 7e-7 without.
+// The tensor cores round towards zero as they sum, about 1e-9 of a logit for
+// each of its terms.  The target's own is summed apart; what is left of 4096
+// terms is an error of 4e-6 of a loss that another word makes alone, and of 1e-6
+// (1000 words) to 5e-7 (131072) where the words share it; the plain product in
+// fp32 is 8e-7 and 4e-7 to 8e-7 off.  Restarted every 512 terms and added up in
+// fp32 the sums are good to 5e-7 and 1e-7, whatever their length and whatever
+// the vocabulary.  They cost about 60% of the product, and so the limit is one
+// of price: 1024 tokens 25 -> 38 us at 1000 words, 28 -> 41 at 4096, 46 -> 76 at
+// 8192, but 147 -> 239 at 32768 and 569 -> 893 at 131072.  (Every 1024 or 2048
+// terms: 28 and 17% over large vocabularies, for a quarter and a half of the
+// error.)  It is one of the vocabulary and not of the work, so that a token's loss
+// does not depend on how many others are in the call.
 template <bool kKeep>
 cudaError_t logits_launch(const PairOperand& h, const PairOperand& w, int64_t D, bool bf16, const PairWork& work,
                           const LogitsEpilogue<kKeep>& epi, int32_t* status, cudaStream_t stream, int first_status) {
