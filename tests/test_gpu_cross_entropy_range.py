@@ -260,3 +260,31 @@ def test_losses_of_more_tokens_than_one_piece_holds(bk):  # noqa: F811
         r = _reference(h[q], w, y[q])
         _close(loss[q], *r["loss"])
         _close(lse[q], *r["lse"])
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("ratio", [1e-2, 1e-4, 1e-6])
+@pytest.mark.parametrize("v", [500, 40000])
+def test_gradients_of_tokens_with_small_coefficients(bk, v, ratio, dtype):  # noqa: F811
+    """Tokens whose coefficient is `ratio` of the largest, which is such that their dH is well above fp16's steps.  In
+    units of its coefficient a G is within p (2^-12 + 2^-13) + 2^-31, and 2^-40 / ratio besides: half of fp16's smallest
+    step where the largest coefficient stands for 2^15 (bf16 has no such step here).  Roundings of G do not agree over
+    the words: their sum over v is within six times its root of squares (the kept logarithms' and the sum's own part is
+    taken in full)."""
+    import torch
+
+    t, d = 64, 48
+    h, w, y = _make(t, d, v, dtype)
+    y = y.clamp(min=0)
+    coef = torch.full((t,), 1e-2 / ratio, device="cuda")
+    coef[1::2] = 1e-2
+    dh = bk.linear_cross_entropy_grad(h, w, y, coef=coef)[2][1::2].double()
+    r = _reference(h, w, y, coef)
+    small = slice(1, None, 2)
+    g, err = r["g"][small], r["gerr"][small]
+    step = 1e-2 * 2.0 ** -40 / ratio if dtype == "float16" else 0.0
+    wd = w.double()
+    ref = g @ wd
+    tol = err @ wd.abs() + 6 * (((U[dtype] * g.abs() + step) ** 2) @ wd ** 2).sqrt() + (2 * v + 16) * 2.0 ** -24 * (g.abs() @ wd.abs())
+    _close(dh, ref, tol + U[dtype] * ref.abs() + 2.0 ** -25)
+    assert float((dh - ref).norm()) <= 8 * U[dtype] * float(ref.norm())
