@@ -405,8 +405,10 @@ int bakron_wavefront_plan_check(int64_t m, int64_t n, int colpush, int lag, int6
  * BAKRON_F32 / F16 / BF16; every matrix is row-major with a row stride in
  * elements (ld..., at least its width) where one is given, else dense.  Rows
  * that start on 16 bytes are read in 16-byte pieces; others are taken too.
- * All sums and statistics are held in fp32 (the products of codes in exact
- * integers), and no result depends on the order in which blocks run.
+ * Sums and statistics are held in fp32 (the products of codes in exact
+ * integers), and no result depends on the order in which blocks run.  What is
+ * held in fewer bits on the way stands at its call.  All arrays start on their
+ * elements; a workspace lives until the stream has passed the call.
  */
 #define BAKRON_F32 0
 #define BAKRON_F16 1
@@ -431,8 +433,10 @@ int bakron_quantize_tokens(const void* X, int dtype, int64_t T, int64_t K, int64
  *    the call quantizes as bakron_quantize_tokens does, or 8-bit codes
  *    (x_dtype BAKRON_I8) with x_scales (T).
  * codes: N x K, row stride ldc.  scales: N.  bias: N, or NULL.
- * Y: T x N of y_dtype (fp32, fp16 or bf16), dense, rounded once.
- * The sums over k are exact; K in 1 .. 2^17 - 1.
+ * Y: T x N of y_dtype (fp32, fp16 or bf16), dense.
+ * The sums over k are exact; K in 1 .. 2^17 - 1.  A sum is rounded to fp32 and
+ * scaled in it (by the token's scale, then by the output's with the bias in one
+ * step), and the result is rounded to y_dtype.
  * status_dev: 0, or BAKRON_DEV_TIMEOUT.
  * Workspace (0 bytes for a few tokens): copies = 1 unless every row of codes
  * starts on 16 bytes (base and stride), for copies that do.
@@ -484,6 +488,12 @@ int bakron_norm_residual_backward(const void* dY, int64_t lddy, const void* dZ, 
  * hidden states H (T x D) and an output embedding W (V x D), both fp16 or
  * both bf16:
  *     lse[t] = log sum_v exp(x[t, v]),  loss[t] = lse[t] - x[t, targets[t]].
+ * The target's logit is summed in fp32 and apart from the others, so a loss is
+ * never negative and keeps its digits near zero.  The others are sums of the
+ * tensor cores, which round towards zero: about 1e-9 of a logit for each of its
+ * D terms (over at most 8192 words 5e-7 in all).  Logits may have any size, and
+ * words may be masked by any number, or for the loss alone by -infinity (whose
+ * product with G = 0 is a NaN in dH).
  * A negative target leaves a token out: loss 0, no gradient.  A target >= V
  * does too, and sets BAKRON_DEV_BAD_TARGET.  loss, lse: T, fp32.
  * D in 1 .. 2^20, V in 1 .. 2^24.
@@ -499,7 +509,13 @@ int bakron_linear_cross_entropy(const void* H, int64_t ldh, const void* W, int64
 /* The same with the gradients of sum_t coef[t] loss[t]:
  *     G[t, v] = coef[t] (exp(x[t, v] - lse[t]) - [v = targets[t]]),
  *     dH = G W (T x D),  dW = G^T H (V x D), dense, of the inputs' type.
- * coef: T, fp32, or NULL for 1 / (number of tokens with a target).
+ * coef: T, fp32, or NULL for 1 / (number of tokens with a target).  One that is
+ * NaN or infinite reaches its own row of dH, and dW.
+ * For these the logits are kept, in pieces of the tokens (1 GiB at most, or what
+ * 256 tokens take), as 16-bit logarithms below the maximum of 64 words: 1.7e-4
+ * of exp(x), 0 from 2^-32 of that maximum.  G is rounded to the inputs' type,
+ * in fp16 with a smallest step of 2^-39 of the largest coefficient; the sums
+ * over V and T are the tensor cores', in fp32 towards zero.
  */
 int bakron_linear_cross_entropy_grad(const void* H, int64_t ldh, const void* W, int64_t ldw, int dtype,
                                      const int64_t* targets, const float* coef, int64_t T, int64_t D, int64_t V,

@@ -6,7 +6,8 @@ Like the rest of the package these marshal torch tensors into the C ABI and
 enqueue on the current stream.  With stream=s a call runs as under
 ``with torch.cuda.stream(s)``: results and workspace belong to s, and the
 inputs are kept from reuse until s has passed the call.  Zero tokens are
-allowed everywhere and launch nothing.
+allowed everywhere and launch nothing.  Like the rest of the package the calls
+are not recorded by autograd: gradients come from the calls that return them.
 
 A call for one token takes less time on the GPU than a handful of torch calls
 take on the host, so the checks here read each attribute once.

@@ -362,7 +362,7 @@ int dh_parts(int64_t T, int64_t D, int64_t V, int pairs) {
 struct Layout {
   size_t coef, scale, stats, kept, part, acc, h, w, bytes;
 };
-constexpr int kPlanPairs = 76;  // pairs of SMs the workspace is planned for
+constexpr int kPlanPairs = 76;  // pairs of SMs that parts of K are planned for: a whole GB300
 Layout layout(int64_t T, int64_t D, int64_t V, bool grad, bool copies) {
   const int64_t n = piece_tokens(T, V, grad), chunks = tiles(V) * 4;
   Layout l = {};

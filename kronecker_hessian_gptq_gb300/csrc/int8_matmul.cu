@@ -27,12 +27,15 @@ namespace {
 
 // Where the next way becomes the faster one (us on the GPU for 4096 -> 4096,
 // 4096 -> 14336 and 14336 -> 4096): 4 tokens by rows 9, 17, 24 and 8 tokens 14,
-// 26, 39, where the tensor cores take 12, 19, 22 for either; 768 tokens without
+// 26, 39, where the tensor cores take 12, 19, 22 for either: up to 4 tokens, for
+// the first two of the three.  768 tokens without
 // the conversion 41, 99, 102, with it 42, 109, 123, and 1024 tokens 45, 125, 131
 // against 44, 110, 129.
 constexpr int64_t kRowTokens = 4;
 constexpr int64_t kPairTokens = 768;
-constexpr int kPlanPairs = 76;  // pairs of SMs that work is planned for
+// Pairs of SMs that work is planned for: a whole GB300.  With fewer the results
+// are the same (no pair waits for another), and some pairs work for two.
+constexpr int kPlanPairs = 76;
 constexpr int kRowThreads = 1024;
 constexpr int64_t kRowSmem = 200 * 1024;  // codes of the tokens that a block keeps
 

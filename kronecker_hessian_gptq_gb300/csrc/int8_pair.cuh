@@ -309,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         if (sum_done) ++sums, in_segment = 0;
       }
     }
-  } else if (warp >= 4 && warp < 4 + kI8Convert) {  // bytes to fp16: 32 rows of every third step for each warp
+  } else if (warp >= 4 && warp < 4 + kI8Convert) {  // bytes to fp16: 32 rows of every second step for each warp
     const int group = (warp - 4) >> 2, quarter = (warp - 4) & 3;
     // A thread takes a row; its 16-byte pieces lie where the 128-byte swizzle
     // of TMA puts them, so that eight rows' pieces touch all banks.

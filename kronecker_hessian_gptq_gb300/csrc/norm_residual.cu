@@ -29,7 +29,7 @@
 namespace bakron {
 namespace {
 
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // that rows are shared out over: a whole GB300; with fewer, some blocks wait their turn
 
 // Where a thread's 8 N columns of a row lie: vectors of VEC elements at
 // (i * stride + t) * VEC, i.e. 16 bytes where rows start on 16 bytes (eight

@@ -429,14 +429,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
   if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
 }
 
-// An operand: rows x K with K contiguous, or K x rows (`by_rows`), 16-bit.
+// An operand, 16-bit: rows x K with K contiguous, or K x rows with its rows
+// contiguous (kARows, kBRows).
 struct PairOperand {
   const void* p;
   int64_t rows, ld;
 };
 
-// M x N tiles of A (M x K) and B (N x K).  bf16: both bf16, else both fp16.
-// first_status >= 0: the status word is set to it first.
 // Pairs of SMs on the current device.
 inline int pair_count() {
   int dev = 0, sms = 0;
@@ -445,6 +444,8 @@ inline int pair_count() {
   return std::max(1, sms / 2);
 }
 
+// M x N tiles of A (M x K) and B (N x K).  bf16: both bf16, else both fp16.
+// first_status >= 0: the status word is set to it first.
 template <bool kARows, bool kBRows, int kQuads, int kSegment, class Epi>
 cudaError_t pair_gemm_launch(PairOperand a, PairOperand b, int64_t K, bool bf16, PairWork work, const Epi& epi,
                              int32_t* status, cudaStream_t stream, int32_t first_status = -1) {
