@@ -99,37 +99,42 @@ __global__ void __launch_bounds__(1024) coefficients_kernel(const int64_t* targe
 template <bool kKeep>
 struct LogitsEpilogue {
   using Sum = float;
+  static constexpr bool kAhead = true;
   CUtensorMap map;  // of the kept logits
   int64_t rows, V;
   const int64_t* target;
   float2* stats;  // rows x chunks, of all words but the target: maximum, sum of exp(x - maximum)
   int64_t chunks;
 
-  // The thread's row's target, as a column from `col` on.
-  __device__ __forceinline__ int64_t target_from(int64_t row0, int64_t col, const PairBox& box) const {
-    return row0 + box.lane < rows ? target[row0 + box.lane] - col : -1;
+  // The target's column among a unit's 128 or 64, -1 without one there.
+  __device__ __forceinline__ static int column(int64_t y) { return (uint64_t)y < 128u ? (int)y : -1; }
+  // The target of a row, as it is: looked at, it would be waited for.
+  __device__ __forceinline__ int64_t ahead(int64_t row) const {
+    int64_t y = -1;
+    if (row < rows) y = target[row];
+    return y;
   }
-  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, const PairSums& sums,
+  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, int64_t y, const PairSums& sums,
                                              const PairBox& box) const {
     if (row0 >= rows) return;
-    const int64_t y = target_from(row0, col, box);
+    const int at = column(y - col);
 #pragma unroll 1
     for (int c = 0; c < 128 && col + c < V; c += kChunk) {
       float v[kChunk];
       sums.load(c, *reinterpret_cast<float(*)[32]>(v));
       sums.load(c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
-      chunk(row0, col + c, y - c, v, box);
+      chunk(row0, col + c, at - c, v, box);
     }
   }
-  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, float (&v)[kChunk],
+  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, int64_t y, float (&v)[kChunk],
                                              const PairBox& box) const {
-    if (row0 < rows && col < V) chunk(row0, col, target_from(row0, col, box), v, box);
+    if (row0 < rows && col < V) chunk(row0, col, column(y - col), v, box);
   }
-  __device__ __forceinline__ void chunk(int64_t row0, int64_t col, int64_t y, float (&v)[kChunk], const PairBox& box) const {
+  __device__ __forceinline__ void chunk(int64_t row0, int64_t col, int y, float (&v)[kChunk], const PairBox& box) const {
     // One branch for the warp: few chunks hold the target of any of its rows.
     // By a bit for each column: a comparison with the index would become an
     // indexed store, and v would live in local memory.
-    const bool here = y >= 0 && y < kChunk;
+    const bool here = (uint32_t)y < (uint32_t)kChunk;
     if (__any_sync(0xffffffffu, here)) {
       const uint64_t bit = here ? 1ull << y : 0;
       const uint32_t lo = (uint32_t)bit, hi = (uint32_t)(bit >> 32);
@@ -149,7 +154,7 @@ struct LogitsEpilogue {
     // All of them -infinity: their sum is 0, and so it stays below any other maximum.
     const F2 minus_m = f2(m == -INFINITY ? 0.f : -m), log2e = f2(kLog2e);
     if constexpr (kKeep) box.open();
-    float s = 0.f;
+    F2 s = f2(0.f);
 #pragma unroll
     for (int j = 0; j < kChunk; j += 8) {
       uint32_t w[8];
@@ -166,15 +171,14 @@ struct LogitsEpilogue {
         }
         float a, b;
         split(x, a, b);
-        s += exp2_approx(a);
-        s += exp2_approx(b);
+        s = s + f2(exp2_approx(a), exp2_approx(b));
       }
       if constexpr (kKeep)
         box.put(j / 8, __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[4], w[5], 0x5410),
                 __byte_perm(w[6], w[7], 0x5410));
     }
     if constexpr (kKeep) box.send(&map, (int)col, (int)row0);
-    if (row0 + box.lane < rows) stats[(row0 + box.lane) * chunks + col / kChunk] = make_float2(m, s);
+    if (row0 + box.lane < rows) stats[(row0 + box.lane) * chunks + col / kChunk] = make_float2(m, sum(s));
   }
 };
 
@@ -238,10 +242,9 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
   const int64_t row = blockIdx.y;
   const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (col >= ldk) return;
-  const float c = coef[row];
+  const float c = coef[row], nll = loss[row];
   const float l = lse[row], off = (stats[row * chunks + col / kChunk].x - l) * kLog2e;
   const int64_t y = target[row] - col;
-  const float wrong = y >= 0 && y < 8 ? expm1f(-loss[row]) : 0.f;  // p - 1 of the target
   uint16_t* at = kept + row * ldk + col;
   const uint4 q = *reinterpret_cast<const uint4*>(at);
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -251,7 +254,12 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
     const uint32_t u = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
     // 65535: too far below, or -infinity; still NaN where the row's sum is
     const float p = u == 65535u ? l - l : exp2_approx(fmaf((float)u, -1.f / kSteps, off));
-    g[i] = c == 0.f ? 0.f : c * kGScale * (y == i ? wrong : p);
+    g[i] = c == 0.f ? 0.f : c * kGScale * p;
+  }
+  if (y >= 0 && y < 8 && c != 0.f) {  // (late, when what it depends on has come)
+    const float wrong = c * kGScale * expm1f(-nll);  // p - 1
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = (1u << y) >> i & 1u ? wrong : g[i];
   }
   if (V - col < 8) {
 #pragma unroll
@@ -268,6 +276,7 @@ __global__ void __launch_bounds__(256) gradient_kernel(uint16_t* kept, int64_t l
 // on 16 bytes.
 template <class T>
 struct GradientEpilogue {
+  static constexpr bool kAhead = false;
   CUtensorMap map;
   int64_t rows, cols;
   T* out;
@@ -276,7 +285,7 @@ struct GradientEpilogue {
   float* part;
   float* acc;
   bool first, last;
-  __device__ __forceinline__ void operator()(const PairUnit& q, int64_t row0, int64_t col, const PairSums& sums,
+  __device__ __forceinline__ void operator()(const PairUnit& q, int64_t row0, int64_t col, int64_t, const PairSums& sums,
                                              const PairBox& box) const {
     if (row0 >= rows) return;
     const float sc = *scale;

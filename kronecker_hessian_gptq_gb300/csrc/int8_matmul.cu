@@ -428,13 +428,14 @@ cudaError_t rows_launch(const Int8Matmul& p, int32_t* status, cudaStream_t strea
 // whose rows start on 16 bytes by TMA, others row by row.
 template <class T>
 struct ScaledEpilogue {
+  static constexpr bool kAhead = false;
   using Sum = int;
   CUtensorMap map;
   int64_t tokens, outputs;
   const float *x_scales, *w_scales, *bias;
   T* y;
   bool tma;  // then outputs is a multiple of 8 and the vectors start on 16 bytes
-  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, const int (&acc)[64],
+  __device__ __forceinline__ void operator()(const PairUnit&, int64_t row0, int64_t col, int64_t, const int (&acc)[64],
                                              const PairBox& box) const {
     if (row0 >= tokens || col >= outputs) return;
     const int here = (int)(tokens - row0 < 32 ? tokens - row0 : 32);

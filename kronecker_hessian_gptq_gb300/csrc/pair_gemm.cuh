@@ -181,10 +181,12 @@ struct PairBarriers {
 };
 
 // The epilogue (which may hold tensor maps: it stays in the parameters) is called by every thread of 4 kQuads warps for each unit,
-//   epi(unit, row0, col, sums, box)
+//   epi(unit, row0, col, ahead, sums, box)
 // with the warp's first row (the thread's own is lane further) and first
-// column and a source of its 256 / kQuads columns: sums.load(c, v) gives 32 of
-// them from column c on.  With kSegment it is an array of Epi::Sum instead.
+// column, what epi.ahead(row) read for the thread's row while the unit before
+// was at hand (Epi::kAhead: 0 without it), and a source of its 256 / kQuads
+// columns: sums.load(c, v) gives 32 of them from column c on.  With kSegment it
+// is an array of Epi::Sum instead.
 struct PairSums {
   uint32_t taddr;
   __device__ __forceinline__ void load(int c, float (&v)[32]) const { tmem_ld32(taddr + (uint32_t)c, v); }
@@ -376,9 +378,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
     const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)(part * kCols);
     const PairBox box{boxes + (uint32_t)(warp - 4) * kPairBox, lane};
     int sums = 0;
+    auto row_of = [&](const PairUnit& q) { return (int64_t)q.tm * kPairTile + rank * 128 + 32 * quarter; };
+    PairUnit q = pair_unit(work, mine), next = q;
+    int64_t read = 0, ahead = 0;
+    if constexpr (Epi::kAhead) ahead = epi.ahead(row_of(q) + lane);
     for (int u = mine; u < units && !broken; u += pairs) {
-      const PairUnit q = pair_unit(work, u);
-      const int64_t row = (int64_t)q.tm * kPairTile + rank * 128 + 32 * quarter;
+      if constexpr (Epi::kAhead) {
+        q = next, read = ahead;
+        if (u + pairs < units) {
+          next = pair_unit(work, u + pairs);
+          ahead = epi.ahead(row_of(next) + lane);
+        }
+      } else {
+        q = pair_unit(work, u);
+      }
+      const int64_t row = row_of(q);
       const int64_t col = (int64_t)q.tn * kPairTile + part * kCols;
       auto release = [&] {
         tc_fence_before();
@@ -393,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
         warp_wait(&bar.sum_full[sums & 1], (uint32_t)(sums / 2) & 1u, broken);
         if (broken) break;
         tc_fence_after();
-        epi(q, row, col, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes}, box);
+        epi(q, row, col, read, PairSums{tmem + (uint32_t)(sums & 1) * 256u + lanes}, box);
         release();
       } else {
         typename Epi::Sum acc[kCols];
@@ -415,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 128 * kQuads, 
           }
           release();
         }
-        if (!broken) epi(q, row, col, acc, box);
+        if (!broken) epi(q, row, col, read, acc, box);
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
