@@ -70,6 +70,7 @@ typedef enum bakron_status {
 #define BAKRON_DEV_BAD_SCALE 2   /* a scale is <= 0, NaN or infinite */
 #define BAKRON_DEV_TIMEOUT 4     /* a bounded device-side wait gave up */
 #define BAKRON_DEV_BAD_TARGET 8  /* a target index is >= the vocabulary's size */
+#define BAKRON_DEV_NONFINITE_GRAD 16 /* a gradient holds a NaN or an infinity */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* bakron_status_string(int status);
@@ -521,6 +522,135 @@ int bakron_linear_cross_entropy_grad(const void* H, int64_t ldh, const void* W, 
                                      const int64_t* targets, const float* coef, int64_t T, int64_t D, int64_t V,
                                      float* loss, float* lse, void* dH, void* dW, void* ws, size_t ws_bytes,
                                      int32_t* status_dev, void* stream);
+
+/* ------------------------------------------ a projection in 8-bit floats
+ * The product with e4m3 codes and a scale for each block of 128, the norms of
+ * queries and keys with the position rotation behind it, and the AdamW step
+ * over many tensors.  Conventions as above.
+ */
+#define BAKRON_E4M3 4
+
+/* e4m3 codes of X (T x K, fp32, fp16 or bf16), one scale for each block of
+ * rows x cols values: 1 x 128 (tokens), 128 x 128 (weights) or 128 x 1
+ * (operands of a sum over tokens); the last block of a row or column may be
+ * shorter.  For each block, all in fp32,
+ *     scale = max |X| / 448,  r = 1 / scale,
+ *     code = X r rounded to nearest in e4m3, ties to even, within +-448.
+ * A block of zeros, or whose scale is below 2^-126, has scale 0 and codes 0;
+ * one that holds a NaN or an infinity has a NaN scale and codes 0.
+ * codes: T x K, row stride ldc.  scales: ceil(T / rows) x ceil(K / cols), dense.
+ * T, K in 1 .. 2^31 - 1.
+ */
+int bakron_quantize_blocks(const void* X, int dtype, int64_t T, int64_t K, int64_t ldx, int rows, int cols, uint8_t* codes,
+                           int64_t ldc, float* scales, void* stream);
+
+/* Y = X V^T for a layer in e4m3 with a scale for each block of 128 x 128:
+ *     Y[t, o] = sum_b sx[t, b] scales[o / 128, b] sum_{k in b} c[t, k] codes[o, k] + bias[o].
+ * X: T x K; either values (x_dtype fp32, fp16 or bf16, x_scales NULL), which the
+ *    call quantizes as bakron_quantize_blocks does with blocks of 1 x 128, or
+ *    codes (x_dtype BAKRON_E4M3) with x_scales (T x ceil(K / 128)).
+ * codes: N x K, row stride ldc.  scales: ceil(N / 128) x ceil(K / 128).
+ * bias: N, or NULL.  Y: T x N of y_dtype, dense.
+ * A block's products are summed by the tensor cores (fp32, towards zero); the
+ * sums are scaled and added up in fp32 and rounded to y_dtype.  No result
+ * depends on the other tokens, but on their number: it decides how K is split.
+ * T in 1 .. 2^24, K, N in 1 .. 2^20.
+ * status_dev: 0, or BAKRON_DEV_TIMEOUT.
+ * Workspace: copies = 1 unless every row of codes starts on 16 bytes (base and
+ * stride), for copies that do.
+ */
+size_t bakron_fp8_matmul_workspace_size(int64_t T, int64_t K, int64_t N, int x_dtype, int copies);
+int bakron_fp8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_scales, const uint8_t* codes, int64_t ldc,
+                      const float* scales, const float* bias, int64_t T, int64_t K, int64_t N, void* Y, int y_dtype,
+                      void* ws, size_t ws_bytes, int32_t* status_dev, void* stream);
+
+/* Gradients of that product for the gradient dY (T x N) of its result, with
+ * dY and X (T x K) quantized for each sum:
+ *     dX = Q(dY) V            blocks of 1 x 128 of dY,
+ *     dW = Q(dY)^T Q(X)       blocks of 128 x 1: 128 tokens of a column,
+ *     dbias[o] = sum_t dY[t, o].
+ * dX: T x K, dW: N x K (of the values that the codes stand for), dense, of
+ * dtype (that of dY and X: fp32, fp16 or bf16); dbias: N, fp32.  Each may be
+ * NULL, not both dX and dW.  X may be NULL without dW; codes and scales
+ * without dX.  Workspace: want = 1 for dX + 2 for dW + 4 for dbias; copies as
+ * above (1 needed with dX only).
+ */
+size_t bakron_fp8_matmul_backward_workspace_size(int64_t T, int64_t K, int64_t N, int want, int copies);
+int bakron_fp8_matmul_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int dtype, const uint8_t* codes,
+                               int64_t ldc, const float* scales, int64_t T, int64_t K, int64_t N, void* dX, void* dW,
+                               float* dbias, void* ws, size_t ws_bytes, int32_t* status_dev, void* stream);
+
+/* The norms of queries Q (T x Hq heads of D) and keys K (T x Hk heads of D)
+ * for each head, and the rotation of their first R values by the position:
+ *     n = x / sqrt(mean(x^2) + eps) * w   (without a weight: n = x),
+ *     y[a] = n[a] cos(p f_i) - n[b] sin(p f_i),
+ *     y[b] = n[b] cos(p f_i) + n[a] sin(p f_i),   i < R / 2,
+ * (a, b) = (i, i + R / 2) for BAKRON_PAIRS_HALVES, (2 i, 2 i + 1) for
+ * BAKRON_PAIRS_NEIGHBOURS; y = n beyond R.
+ * Q, K: element type dtype, strides (in elements) of tokens and of heads, the
+ * D values of a head side by side (so both may lie in one buffer with the
+ * values'); K NULL with Hk = 0.  q_weight, k_weight: D, fp32, or NULL.
+ * positions: T (any 64-bit numbers).  freqs: R / 2, fp64, radians for each
+ * position.  R even, 0 (no rotation; positions and freqs NULL) to D; D in 1 ..
+ * 1024; Hq, Hk in 0 .. 65535, Hq + Hk at least 1.
+ * YQ, YK: T x heads x D, dense; rounded once.  Angles are exact to |p| 2^-54
+ * turns before they are rounded to fp32.
+ */
+#define BAKRON_PAIRS_HALVES 0
+#define BAKRON_PAIRS_NEIGHBOURS 1
+int bakron_head_norm_rotary(const void* Q, int64_t q_token, int64_t q_head, int64_t Hq, const void* K, int64_t k_token,
+                            int64_t k_head, int64_t Hk, const float* q_weight, const float* k_weight,
+                            const int64_t* positions, const double* freqs, int64_t R, int pairs, float eps, int dtype,
+                            int64_t T, int64_t D, void* YQ, void* YK, void* stream);
+
+/* Its gradients for the gradients dYQ, dYK of its results (strided like Q and
+ * K), from Q and K.  dQ, dK: T x heads x D, dense, of dtype; dq_weight,
+ * dk_weight: D, fp32, or NULL, summed over tokens and heads in a fixed order.
+ * Without its weight a side's Q or K is not read and may be NULL.
+ */
+size_t bakron_head_norm_rotary_backward_workspace_size(int64_t T, int64_t D);
+int bakron_head_norm_rotary_backward(const void* dYQ, int64_t dq_token, int64_t dq_head, const void* dYK, int64_t dk_token,
+                                     int64_t dk_head, const void* Q, int64_t q_token, int64_t q_head, int64_t Hq,
+                                     const void* K, int64_t k_token, int64_t k_head, int64_t Hk, const float* q_weight,
+                                     const float* k_weight, const int64_t* positions, const double* freqs, int64_t R,
+                                     int pairs, float eps, int dtype, int64_t T, int64_t D, void* dQ, void* dK,
+                                     float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* One AdamW step over `count` tensors, in place.  With g = grad_scale grad:
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *     param = (1 - lr weight_decay) param
+ *             - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * (0 where m is 0), computed in fp32 and rounded to the parameter's type;
+ * copy, where given, gets the same value in its type.
+ * bits = 32: m and v are fp32.  bits = 8: m and v hold e4m3 codes of m and of
+ * sqrt(v) with a scale (max / 448) for each 256 values of the tensor, the last
+ * may be fewer.  They are rounded up or down at random, by the share that is cut
+ * off; the 16 bits for each come from the seed, the step, the tensor's place in
+ * the list and the value's in the tensor alone.  A root that is not 0 stays so.
+ * A value whose gradient, or its square, is not finite in fp32 is left as it
+ * is, and BAKRON_DEV_NONFINITE_GRAD is set.
+ * tensors: host, read in the call.  Arrays are dense, start on their elements
+ * and do not overlap; param: param_dtype (fp32, fp16, bf16), grad: grad_dtype,
+ * copy: copy_dtype (fp16 or bf16), or NULL.  n may be 0.
+ * step: from 1 on.  lr_dev, step_dev, grad_scale_dev: device, in place of the
+ * numbers, or NULL; skip: device, a number that is not 0 leaves everything as
+ * it is, or NULL.  (A captured call reads these when it is replayed.)
+ * 0 <= beta < 1; eps >= 0.  ws: 256 bytes, device.  status_dev: device.
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void *m, *v;
+  float *m_scales, *v_scales;
+  void* copy;
+  int64_t n;
+  int param_dtype, grad_dtype, copy_dtype;
+} bakron_adamw_tensor;
+size_t bakron_adamw_workspace_size(void);
+int bakron_adamw(const bakron_adamw_tensor* tensors, int64_t count, int bits, double lr, const float* lr_dev, int64_t step,
+                 const int64_t* step_dev, double beta1, double beta2, double eps, double weight_decay, double grad_scale,
+                 const float* grad_scale_dev, const int32_t* skip, uint64_t seed, void* ws, size_t ws_bytes,
+                 int32_t* status_dev, void* stream);
 
 /* --------------------------------------------------------------- self-test
  * Exercises the device-side timeout path on purpose: one thread waits, with

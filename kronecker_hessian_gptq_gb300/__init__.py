@@ -28,6 +28,14 @@ imports torch and is loaded by the first use):
                          the norms around a block, its gate and residual sum
   linear_cross_entropy, linear_cross_entropy_grad
                          cross entropy over a large vocabulary, its gradients
+and for a projection in 8-bit floats (in _projection.py, likewise):
+  quantize_blocks        e4m3 codes with a scale for each block of 128
+  fp8_matmul, fp8_matmul_backward
+                         the product of such codes, its gradients
+  head_norm_rotary, head_norm_rotary_backward
+                         norms of queries and keys for each head and the
+                         position rotation, their gradients
+  adamw, adamw_states    the AdamW step over many tensors, states in 8 or 32 bits
 """
 
 from __future__ import annotations
@@ -61,10 +69,19 @@ __all__ = [
     "norm_residual_backward",
     "linear_cross_entropy",
     "linear_cross_entropy_grad",
+    "quantize_blocks",
+    "fp8_matmul",
+    "fp8_matmul_backward",
+    "head_norm_rotary",
+    "head_norm_rotary_backward",
+    "adamw",
+    "adamw_states",
 ]
 
 _LAYER_CALLS = ("quantize_tokens", "int8_matmul", "norm_residual", "norm_residual_backward", "linear_cross_entropy",
                 "linear_cross_entropy_grad")
+_PROJECTION_CALLS = ("quantize_blocks", "fp8_matmul", "fp8_matmul_backward", "head_norm_rotary",
+                     "head_norm_rotary_backward", "adamw", "adamw_states")
 
 
 def __getattr__(name):
@@ -72,6 +89,11 @@ def __getattr__(name):
         from . import _layers
 
         globals().update({n: getattr(_layers, n) for n in _LAYER_CALLS})
+        return globals()[name]
+    if name in _PROJECTION_CALLS:
+        from . import _projection
+
+        globals().update({n: getattr(_projection, n) for n in _PROJECTION_CALLS})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

@@ -24,12 +24,14 @@ DEV_NONFINITE_W = 1
 DEV_BAD_SCALE = 2
 DEV_TIMEOUT = 4
 DEV_BAD_TARGET = 8
+DEV_NONFINITE_GRAD = 16
 KERNEL_CLASSES = ("setup", "tile_solve", "mid_push", "chunk_push", "sweep")
 
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _int = ctypes.c_int
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 _vp = ctypes.c_void_p  # device or host pointers are passed as plain addresses
 
 # name -> (restype, argtypes)
@@ -76,6 +78,21 @@ SIGNATURES = {
                                            _vp]),
     "bakron_linear_cross_entropy_grad": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _vp, _i64, _i64, _i64] + [_vp] * 5
                                          + [_sz, _vp, _vp]),
+    "bakron_quantize_blocks": (_int, [_vp, _int, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _vp]),
+    "bakron_fp8_matmul_workspace_size": (_sz, [_i64, _i64, _i64, _int, _int]),
+    "bakron_fp8_matmul": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _sz, _vp,
+                                 _vp]),
+    "bakron_fp8_matmul_backward_workspace_size": (_sz, [_i64, _i64, _i64, _int, _int]),
+    "bakron_fp8_matmul_backward": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _i64, _i64] + [_vp] * 4
+                                   + [_sz, _vp, _vp]),
+    "bakron_head_norm_rotary": (_int, [_vp, _i64, _i64, _i64] * 2 + [_vp] * 4 + [_i64, _int, _f32, _int, _i64, _i64, _vp,
+                                                                                 _vp, _vp]),
+    "bakron_head_norm_rotary_backward_workspace_size": (_sz, [_i64, _i64]),
+    "bakron_head_norm_rotary_backward": (_int, [_vp, _i64, _i64] * 2 + [_vp, _i64, _i64, _i64] * 2 + [_vp] * 4
+                                         + [_i64, _int, _f32, _int, _i64, _i64] + [_vp] * 5 + [_sz, _vp]),
+    "bakron_adamw_workspace_size": (_sz, []),
+    "bakron_adamw": (_int, [_vp, _i64, _int, _f64, _vp, _i64, _vp, _f64, _f64, _f64, _f64, _f64, _vp, _vp,
+                            ctypes.c_uint64, _vp, _sz, _vp, _vp]),
     "bakron_sweep_plan_check": (_int, [_i64, _i64, _vp]),
     "bakron_wavefront_plan_check": (_int, [_i64, _i64, _int, _int, _vp]),
 }

@@ -1,0 +1,428 @@
+// fp8_pair.cuh -- products of e4m3 codes with one scale for each 128 of K, on
+// pairs of SMs:
+//     C[m, n] = sum over blocks b of sa[m, b] sb[n, b] sum_{k in b} A[m, k] B[n, k].
+//
+// A cluster of two blocks computes a tile of 256 x kN.  A stage holds one block
+// of K: 128 codes of 128 rows of A and of kN / 2 rows of B in each block of the
+// pair (TMA, 128-byte swizzle), four tcgen05.mma of kind::f8f6f4 with
+// cta_group::2.  The tensor cores sum one block of K alone; the sums (fp32, in
+// tensor memory, two or four in turn) are read by 16 epilogue warps, scaled and
+// added to sums in registers, a thread for a row and kN / 4 columns, while the
+// next block is multiplied.  For kN = 256 the tensor cores take 512 cycles for a
+// block of K; the epilogue's 64 columns a thread are 64 scaled additions, at 128
+// a cycle 256 cycles, where the columns share a scale (weights: one for 128 x
+// 128), and twice as many where they do not (kColumns).
+//
+// Either operand may be stored with K contiguous or with its rows contiguous
+// (a weight's gradient sums over tokens, a row each).  Where there are fewer
+// tiles than pairs of SMs, K is cut into parts whose sums meet in memory: the
+// last part of a tile to arrive adds them up in their order.
+//
+// One warp copies the weights' side, one the other, which a kernel before may
+// still be writing (griddepcontrol): the weights are then on their way already.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#include "pair_gemm.cuh"
+
+namespace bakron {
+
+constexpr int kF8K = 128;  // K of a stage, and of a scale
+constexpr int kF8Warps = 16;
+constexpr int kF8Threads = 128 + 32 * kF8Warps;
+constexpr int kF8MostStages = 10;
+constexpr int kF8Ring = 4;  // columns' scales on their way
+constexpr int kF8Smem = 226 * 1024;
+
+// Shared memory of a variant: stages, boxes for results in whole lines, scales.
+template <int kN, bool kColumns, bool kBoxes>
+struct F8Shape {
+  static constexpr int kA = 128 * kF8K, kB = kN / 2 * kF8K, kStage = kA + kB;
+  static constexpr int kBufs = kN > 128 ? 2 : 4;
+  static constexpr int kCols = kN / 4;  // of a thread
+  static constexpr int kScales = kColumns ? kF8Ring * kN * 4 : 0;
+  static constexpr int kOther = (kBoxes ? kF8Warps * kPairBox : 0) + kScales + 1024;
+  static constexpr int kFit = (kF8Smem - kOther) / kStage;
+  static constexpr int kStages = kFit < kF8MostStages ? kFit : kF8MostStages;
+  static constexpr int kBytes = kStages * kStage + kOther;
+};
+
+struct F8Scales {
+  // of row r in block b: a[(r >> a_shift) a_row + b a_k]
+  const float* a;
+  int64_t a_row, a_k, rows;
+  int a_shift;
+  // of column c: one for 128 columns, b[(c >> 7) b_col + b b_k]; kColumns: b[b b_k + c],
+  // b_k a multiple of 4 and at least the columns of all tiles
+  const float* b;
+  int64_t b_col, b_k, cols;
+};
+struct F8Join {
+  float* sums;        // a tile's parts: [part][tile][block of the pair][warp][column][lane]
+  uint32_t* arrived;  // for each tile, block and warp, zero
+};
+
+struct F8Barriers {
+  uint64_t full[kF8MostStages], empty[kF8MostStages], sum_full[4], sum_empty[4], scale_full[kF8Ring], scale_empty[kF8Ring];
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ void pair_mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 da, db;\nmov.b64 da, {%1, %2};\nmov.b64 db, {%3, %2};\nsetp.ne.b32 p, %5, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(kPairDescHigh), "r"(b), "r"(idesc), "r"(acc));
+}
+// 16 bytes' units from one K = 32 to the next within a stage: 32 bytes of a
+// row, or 32 rows of 128 bytes.
+template <bool kRows>
+__host__ __device__ constexpr uint32_t f8_kstep() { return kRows ? 4096u >> 4 : 32u >> 4; }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// kWeightsA: A is what no kernel before writes (the weights), else B.
+template <bool kARows, bool kBRows, int kN, bool kColumns, bool kWeightsA, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairWork work,
+                    F8Scales sc, F8Join join, const __grid_constant__ Epi epi, int32_t* status, int32_t first_status) {
+  using Shape = F8Shape<kN, kColumns, Epi::kBoxes>;
+  constexpr int kStages = Shape::kStages, kBufs = Shape::kBufs, kCols = Shape::kCols;
+  constexpr int kChunk = kCols < 32 ? kCols : 32;
+  extern __shared__ unsigned char f8_smem_raw[];
+  const uint32_t base = (smem_u32(f8_smem_raw) + 1023u) & ~1023u;
+  const uint32_t boxes = base + kStages * Shape::kStage;
+  const uint32_t scales = boxes + (Epi::kBoxes ? kF8Warps * kPairBox : 0);
+  __shared__ F8Barriers bar;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pairs = gridDim.x / 2, mine = blockIdx.x / 2, units = work.units();
+  bool broken = false;
+
+  // This early nothing can have been reported.
+  if (first_status >= 0 && blockIdx.x == 0 && threadIdx.x == 0) *status = first_status;
+  if (threadIdx.x == 0) {
+    auto init = [](uint64_t* b, int n) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n));
+    };
+    for (int i = 0; i < kStages; ++i) init(&bar.full[i], 1), init(&bar.empty[i], 1);
+    for (int i = 0; i < kBufs; ++i) init(&bar.sum_full[i], 1), init(&bar.sum_empty[i], 2 * kF8Warps);
+    for (int i = 0; i < kF8Ring; ++i) init(&bar.scale_full[i], 1), init(&bar.scale_empty[i], kF8Warps);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&bar.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+
+  if (warp == 0 || warp == 3) {  // copies: warp 0 the weights' side, warp 3 the other
+    const bool is_a = (warp == 0) == kWeightsA;
+    if (warp == 3) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    Ring ring;
+    for (int u = mine; u < units && !broken; u += pairs) {
+      const PairUnit q = pair_unit(work, u);
+      const int row = is_a ? q.tm * 256 + (int)rank * 128 : q.tn * kN + (int)rank * (kN / 2);
+      for (int k = q.k0; k < q.k1; ++k, ring.next(kStages)) {
+        const int slot = ring.slot;
+        if (ring.round) warp_wait(&bar.empty[slot], ring.turn ^ 1u, broken);
+        if (broken) break;
+        const uint32_t full = in_even_block(&bar.full[slot]);
+        const uint32_t at = base + (uint32_t)slot * Shape::kStage + (is_a ? 0u : (uint32_t)Shape::kA);
+        if (elect_one()) {
+          // The other warp's bytes may be counted before they are expected.
+          if (warp == 0 && rank == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(&bar.full[slot])),
+                         "r"(2u * Shape::kStage)
+                         : "memory");
+          if (is_a)
+            pair_copy(at, &map_a, kARows ? row : k * kF8K, kARows ? k * kF8K : row, full);
+          else
+            pair_copy(at, &map_b, kBRows ? row : k * kF8K, kBRows ? k * kF8K : row, full);
+        }
+        __syncwarp();
+      }
+    }
+    // No block leaves while copies into it, or arrivals at its barriers, are on their way (see pair_gemm_kernel).
+    for (int i = 0; i < kStages; ++i, ring.next(kStages)) {
+      if (!ring.round) continue;
+      bool late = false;
+      if (!broken)
+        warp_wait(&bar.empty[ring.slot], ring.turn ^ 1u, broken);
+      else if (rank == 0)
+        warp_wait(&bar.full[ring.slot], ring.turn ^ 1u, late);
+    }
+  } else if (warp == 1 && rank == 0) {  // products
+    // fp32 sums of e4m3 products, which operands have their rows contiguous, N = kN, M = 256
+    constexpr uint32_t idesc = (1u << 4) | ((kARows ? 1u : 0u) << 15) | ((kBRows ? 1u : 0u) << 16) | ((uint32_t)(kN >> 3) << 17) |
+                               ((256u >> 4) << 24);
+    int sums = 0;
+    Ring ring;
+    for (int u = mine; u < units && !broken; u += pairs) {
+      const PairUnit q = pair_unit(work, u);
+      for (int k = q.k0; k < q.k1; ++k, ring.next(kStages), ++sums) {
+        const int buf = sums % kBufs;
+        if (sums >= kBufs) warp_wait(&bar.sum_empty[buf], (uint32_t)(sums / kBufs - 1) & 1u, broken);
+        warp_wait(&bar.full[ring.slot], ring.turn, broken);
+        if (broken) break;
+        tc_fence_after();
+        const uint32_t at = base + (uint32_t)ring.slot * Shape::kStage, acc = tmem + (uint32_t)(buf * kN);
+        const uint32_t a = pair_desc_low<kARows>(at), b = pair_desc_low<kBRows>(at + Shape::kA);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < kF8K / 32; ++j) pair_mma_f8(acc, a + j * f8_kstep<kARows>(), b + j * f8_kstep<kBRows>(), idesc, j > 0);
+          pair_commit(&bar.empty[ring.slot]);
+          pair_commit(&bar.sum_full[buf]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 2 && kColumns) {  // the columns' scales
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    Ring ring;
+    for (int u = mine; u < units && !broken; u += pairs) {
+      const PairUnit q = pair_unit(work, u);
+      for (int k = q.k0; k < q.k1; ++k, ring.next(kF8Ring)) {
+        if (ring.round) warp_wait(&bar.scale_empty[ring.slot], ring.turn ^ 1u, broken);
+        if (broken) break;
+        if (elect_one()) {
+          const uint32_t full = smem_u32(&bar.scale_full[ring.slot]);
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full), "r"(kN * 4) : "memory");
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                           scales + (uint32_t)(ring.slot * kN * 4)),
+                       "l"(sc.b + k * sc.b_k + (int64_t)q.tn * kN), "r"(kN * 4), "r"(full)
+                       : "memory");
+        }
+        __syncwarp();
+      }
+    }
+    for (int i = 0; i < kF8Ring; ++i, ring.next(kF8Ring)) {
+      bool late = false;
+      if (ring.round) warp_wait(&bar.scale_full[ring.slot], ring.turn ^ 1u, late);
+    }
+  } else if (warp >= 4) {  // epilogue: 32 rows of the block and kCols columns for each warp
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)(part * kCols);
+    const PairBox box{boxes + (uint32_t)(warp - 4) * kPairBox, lane};
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    int sums = 0;
+    Ring ring;
+    for (int u = mine; u < units && !broken; u += pairs) {
+      const PairUnit q = pair_unit(work, u);
+      const int64_t row0 = (int64_t)q.tm * 256 + rank * 128 + 32 * quarter, col = (int64_t)q.tn * kN + part * kCols;
+      // Beyond the matrix the last row's and column's scales: sums are 0 there.
+      const int64_t row = row0 + lane < sc.rows ? row0 + lane : sc.rows - 1;
+      const float* sa = sc.a + (row >> sc.a_shift) * sc.a_row;
+      const float* sb = kColumns ? nullptr : sc.b + ((col < sc.cols ? col : sc.cols - 1) >> 7) * sc.b_col;
+      F2 acc[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = f2(0.f);
+      float a_next = sa[q.k0 * sc.a_k], b_next = kColumns ? 1.f : sb[q.k0 * sc.b_k];
+      for (int k = q.k0; k < q.k1; ++k, ++sums) {
+        const int buf = sums % kBufs;
+        const float a = a_next, b = b_next;
+        if (k + 1 < q.k1) {
+          a_next = sa[(k + 1) * sc.a_k];
+          if (!kColumns) b_next = sb[(k + 1) * sc.b_k];
+        }
+        if (kColumns) warp_wait(&bar.scale_full[ring.slot], ring.turn, broken);
+        warp_wait(&bar.sum_full[buf], (uint32_t)(sums / kBufs) & 1u, broken);
+        if (broken) break;
+        tc_fence_after();
+        const F2 s = f2(a * b);
+        const uint32_t from = scales + (uint32_t)(ring.slot * kN + part * kCols) * 4u;
+#pragma unroll
+        for (int c = 0; c < kCols; c += kChunk) {
+          float v[kChunk];
+          if constexpr (kChunk == 16)
+            tmem_ld16(tmem + (uint32_t)(buf * kN + c) + lanes, v);
+          else
+            tmem_ld32(tmem + (uint32_t)(buf * kN + c) + lanes, v);
+          if (c + kChunk == kCols) {  // all read: the buffer may be filled again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+              asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.sum_empty[buf]))
+                           : "memory");
+          }
+#pragma unroll
+          for (int i = 0; i < kChunk; i += 4) {
+            F2 x = f2(v[i], v[i + 1]), y = f2(v[i + 2], v[i + 3]);
+            if constexpr (kColumns) {
+              float w[4];
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                           : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3])
+                           : "r"(from + (uint32_t)(c + i) * 4u)
+                           : "memory");
+              x = x * f2(w[0], w[1]);
+              y = y * f2(w[2], w[3]);
+            }
+            acc[(c + i) / 2] = fma2(x, s, acc[(c + i) / 2]);
+            acc[(c + i) / 2 + 1] = fma2(y, s, acc[(c + i) / 2 + 1]);
+          }
+        }
+        if (kColumns) {
+          __syncwarp();
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(&bar.scale_empty[ring.slot])) : "memory");
+          ring.next(kF8Ring);
+        }
+      }
+      if (broken) break;
+      float out[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) split(acc[i], out[2 * i], out[2 * i + 1]);
+      if (work.parts > 1) {
+        if (row0 >= epi.rows() || col >= epi.cols()) continue;  // for every part alike
+        const int64_t tile = (int64_t)q.tm * work.tiles_n + q.tn, tiles = (int64_t)work.tiles_m * work.tiles_n;
+        const int64_t slice = (tile * 2 + rank) * kF8Warps + (warp - 4), stride = tiles * 2 * kF8Warps * 32 * kCols;
+        float* to = join.sums + slice * (32 * kCols) + lane;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) to[q.part * stride + 32 * i] = out[i];
+        __threadfence();
+        __syncwarp();
+        uint32_t before = 0;
+        if (lane == 0) before = atomicAdd(join.arrived + slice, 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before + 1 != (uint32_t)work.parts) continue;
+        __threadfence();
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) out[i] = 0.f;
+        for (int p = 0; p < work.parts; ++p) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) out[i] += __ldcg(to + p * stride + 32 * i);
+        }
+      }
+      epi(row0, col, out, box);
+    }
+    if (Epi::kBoxes && lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+  }
+  if (broken) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    atomicOr(status, BAKRON_DEV_TIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+}
+
+// Rows of C as they are stored, in whole lines: 16-bit results whose rows
+// start on 16 bytes by TMA, others row by row.
+template <class T>
+struct F8Rows {
+  static constexpr bool kBoxes = true;
+  CUtensorMap map;
+  int64_t m, n;
+  const float* bias;  // n, or null
+  T* y;               // m x n
+  bool tma;           // then n is a multiple of 8, and the bias starts on 16 bytes
+  __device__ __forceinline__ int64_t rows() const { return m; }
+  __device__ __forceinline__ int64_t cols() const { return n; }
+  template <int kCols>
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const PairBox& box) const {
+    if (row0 >= m || col >= n) return;
+    if constexpr (sizeof(T) == 2) {
+      if (tma) {
+        box.open();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 8) {
+          float b[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) b[i] = 0.f;
+          if (bias && col + c < n) load_vec<float, 8>(bias + col + c, b);
+          box.put(c / 8, pack2<T>(v[c] + b[0], v[c + 1] + b[1]), pack2<T>(v[c + 2] + b[2], v[c + 3] + b[3]),
+                  pack2<T>(v[c + 4] + b[4], v[c + 5] + b[5]), pack2<T>(v[c + 6] + b[6], v[c + 7] + b[7]));
+        }
+        box.send(&map, (int)col, (int)row0);
+        return;
+      }
+    }
+    const int here = (int)(m - row0 < 32 ? m - row0 : 32);
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32) {
+      if (col + c >= n) break;
+      float w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = v[c + i];
+      const int64_t o = col + c + box.lane;
+      const bool in = o < n;
+      const float b = in && bias ? bias[o] : 0.f;
+      T* to = y + row0 * n + o;
+      box.by_row(w, here, in, [&](int r, float x) { to[r * n] = from_f32<T>(x + b); });
+    }
+  }
+};
+
+// Columns of C as the stored rows: lanes hold neighbours of a stored row.
+template <class T>
+struct F8Columns {
+  static constexpr bool kBoxes = false;
+  int64_t m, n;
+  const float* bias;  // m, or null
+  T* y;               // n x m
+  __device__ __forceinline__ int64_t rows() const { return m; }
+  __device__ __forceinline__ int64_t cols() const { return n; }
+  template <int kCols>
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const PairBox& box) const {
+    const int64_t o = row0 + box.lane;
+    const bool in = o < m;
+    const int here = in ? (int)(n - col < kCols ? n - col : kCols) : 0;  // may be negative
+    const float b = in && bias ? bias[o] : 0.f;
+    T* to = y + col * m + o;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i, to += m) store_if(i < here, to, v[i] + b);
+  }
+};
+
+struct F8Operand {
+  const void* p;
+  int64_t rows, ld;  // with K contiguous rows x K; else K x rows
+};
+
+// early: the kernel before may still run when this one starts.
+template <bool kARows, bool kBRows, int kN, bool kColumns, bool kWeightsA, class Epi>
+cudaError_t fp8_pair_launch(F8Operand a, F8Operand b, int64_t K, const PairWork& work, const F8Scales& sc, const F8Join& join,
+                            const Epi& epi, bool early, int32_t* status, cudaStream_t stream, int32_t first_status) {
+  using Shape = F8Shape<kN, kColumns, Epi::kBoxes>;
+  CUtensorMap ma, mb;
+  const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  cudaError_t e = make_tensor_map(&ma, kARows ? TileMap{a.p, type, K, a.rows, a.ld, kF8K, 128, true}
+                                              : TileMap{a.p, type, a.rows, K, a.ld, 128, kF8K, true});
+  if (e == cudaSuccess)
+    e = make_tensor_map(&mb, kBRows ? TileMap{b.p, type, K, b.rows, b.ld, kF8K, kN / 2, true}
+                                    : TileMap{b.p, type, b.rows, K, b.ld, kN / 2, kF8K, true});
+  auto kernel = fp8_pair_kernel<kARows, kBRows, kN, kColumns, kWeightsA, Epi>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)std::min(work.units(), pair_count()));
+  cfg.blockDim = dim3(kF8Threads);
+  cfg.dynamicSmemBytes = Shape::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, work, sc, join, epi, status, first_status);
+}
+
+}  // namespace bakron

@@ -75,23 +75,6 @@ struct Prepare {
   int32_t* status;
 };
 
-// The 16 codes at v, of which `bytes` are there, zeros for the others.  Rows
-// may start anywhere: the codes come in the 32-bit words that hold them,
-// shifted into place.
-__device__ __forceinline__ uint4 load_codes(const int8_t* v, int bytes) {
-  const int off = (int)(reinterpret_cast<uintptr_t>(v) & 3);
-  const uint32_t* word = reinterpret_cast<const uint32_t*>(v - off);
-  uint32_t f[5], e[4];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) f[i] = 4 * i < off + bytes ? word[i] : 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    e[i] = __funnelshift_r(f[i], f[i + 1], 8 * off);
-    const int here = bytes - 4 * i;
-    if (here < 4) e[i] = here <= 0 ? 0u : e[i] & ((1u << (8 * here)) - 1u);
-  }
-  return make_uint4(e[0], e[1], e[2], e[3]);
-}
 __device__ __forceinline__ void store_codes(void* to, int64_t at, bool f16, const uint4& u) {
   if (f16) {
     uint32_t h[8];

@@ -152,20 +152,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[30]), "r"(v[31])
       : "memory");
 }
-// A store and an integer sum to memory under a predicate: as a branch for each
-// value they cost a warp 150 cycles a value.
-__device__ __forceinline__ void store_if(bool p, float* to, float x) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p st.global.f32 [%0], %1;\n}\n" ::"l"(to), "f"(x), "r"((int)p)
-               : "memory");
-}
-template <class T>
-__device__ __forceinline__ void store_if(bool p, T* to, float x) {
-  const T v = from_f32<T>(x);
-  uint16_t bits;
-  memcpy(&bits, &v, 2);
-  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p st.global.b16 [%0], %1;\n}\n" ::"l"(to), "h"(bits), "r"((int)p)
-               : "memory");
-}
+// An integer sum to memory under a predicate (see store_if).
 __device__ __forceinline__ void add_if(bool p, int32_t* to, int x) {
   asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p red.global.add.s32 [%0], %1;\n}\n" ::"l"(to), "r"(x), "r"((int)p)
                : "memory");

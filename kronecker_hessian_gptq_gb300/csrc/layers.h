@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "bakron.h"
+
 namespace bakron {
 
 // Element types: the values of BAKRON_F32 / F16 / BF16 in bakron.h.
@@ -86,5 +88,96 @@ struct CrossEntropy {
 size_t cross_entropy_workspace_bytes(int64_t T, int64_t D, int64_t V, bool grad, bool copies);
 bool cross_entropy_needs_copies(const CrossEntropy& p);
 cudaError_t cross_entropy_launch(const CrossEntropy& p, void* ws, int32_t* status_dev, cudaStream_t stream);
+
+// head_norm.cu
+struct HeadSide {  // queries or keys
+  const void* x;   // T x heads x D
+  int64_t x_token, x_head;  // strides in elements
+  const void* dy;  // backward: the result's gradient
+  int64_t dy_token, dy_head;
+  const float* w;  // D, or null: no norm
+  void* y;         // T x heads x D, dense: the result, or the gradient of x
+  float* dw;       // D, or null
+  int heads;       // 0: not there
+};
+struct HeadNorm {
+  HeadSide side[2];
+  const int64_t* positions;  // T
+  const double* freqs;       // half
+  int half;                  // pairs that are turned
+  int neighbours;
+  float eps;
+  int dtype;
+  int64_t T;
+  int D;
+};
+constexpr int kHeadMaxD = 1024;
+cudaError_t head_norm_launch(const HeadNorm& p, cudaStream_t stream);
+size_t head_norm_backward_workspace_bytes(int64_t T, int64_t D);
+cudaError_t head_norm_backward_launch(const HeadNorm& p, void* ws, cudaStream_t stream);
+
+// adamw.cu
+struct Adamw {
+  bool eight;
+  double lr, scale, b1, b2, eps, decay;
+  int64_t step;
+  const float *lr_dev, *scale_dev;  // null: the numbers above
+  const int64_t* step_dev;
+  const int32_t* skip;  // or null
+  uint64_t seed;
+};
+size_t adamw_workspace_bytes();
+cudaError_t adamw_launch(const Adamw& a, const bakron_adamw_tensor* tensors, int64_t count, void* ws, int32_t* status,
+                         cudaStream_t stream);
+
+// fp8_quantize.cu
+struct Fp8Codes {
+  const void* X;  // rows x cols
+  int dtype;
+  int64_t rows, cols, ldx;
+  // Codes with a scale for each 128 of a row, of a column, or 128 x 128; null: not wanted.
+  uint8_t *along, *down, *whole;
+  int64_t ld_along, ld_down, ld_whole;
+  float *along_scales, *down_scales, *whole_scales;
+  int64_t along_row, along_col;  // strides of along_scales
+  int64_t down_pitch, whole_row;
+  float* sums;  // of the columns of each 128 rows, rows of down_pitch; or null
+  void* clear;  // words set to 0 by the same launch
+  int64_t clear_words;
+};
+cudaError_t fp8_codes_launch(const Fp8Codes& q, cudaStream_t stream);
+cudaError_t fp8_column_sums_launch(const float* parts, int64_t rows, int64_t pitch, int64_t cols, float* out, cudaStream_t stream);
+
+// fp8_matmul.cu
+struct Fp8Matmul {
+  const void* X;          // T x K values of x_dtype, or e4m3 codes with x_scales
+  const float* x_scales;  // T x ceil(K / 128), or null
+  int x_dtype;
+  int64_t ldx;
+  const uint8_t* V;  // N x K codes
+  int64_t ldv;
+  const float* scales;  // ceil(N / 128) x ceil(K / 128)
+  const float* bias;    // N, or null
+  int64_t T, K, N;
+  void* Y;
+  int y_dtype;
+};
+size_t fp8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool values, bool copies);
+bool fp8_matmul_needs_copies(const Fp8Matmul& p);
+cudaError_t fp8_matmul_launch(const Fp8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream);
+struct Fp8Backward {
+  const void *dY, *X;  // T x N, T x K
+  int64_t lddy, ldx;
+  int dtype;
+  const uint8_t* V;
+  int64_t ldv;
+  const float* scales;
+  int64_t T, K, N;
+  void *dX, *dW;  // T x K, N x K; or null
+  float* dbias;   // N, or null
+};
+size_t fp8_backward_workspace_bytes(int64_t T, int64_t K, int64_t N, bool dX, bool dW, bool dbias, bool copies);
+bool fp8_backward_needs_copies(const Fp8Backward& p);
+cudaError_t fp8_backward_launch(const Fp8Backward& p, void* ws, int32_t* status_dev, cudaStream_t stream);
 
 }  // namespace bakron
