@@ -185,7 +185,7 @@ int bakron_quantize_blocks(const void* X, int dtype, int64_t T, int64_t K, int64
 size_t bakron_fp8_matmul_workspace_size(int64_t T, int64_t K, int64_t N, int x_dtype, int copies) {
   if (T < 1 || T > kMaxFp8T || K < 1 || K > kMaxFp8 || N < 1 || N > kMaxFp8 || (x_dtype != BAKRON_E4M3 && !float_type(x_dtype)))
     return 0;
-  return bakron::fp8_matmul_workspace_bytes(T, K, N, x_dtype != BAKRON_E4M3, copies != 0);
+  return bakron::fp8_matmul_workspace_bytes(T, K, N, copies != 0);
 }
 
 int bakron_fp8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_scales, const uint8_t* codes, int64_t ldc,
@@ -199,7 +199,7 @@ int bakron_fp8_matmul(const void* X, int x_dtype, int64_t ldx, const float* x_sc
   if (!float_type(y_dtype) || !on_element(Y, y_dtype) || Y == X || Y == (const void*)codes) return BAKRON_ERR_INVALID_ARG;
   const bakron::Fp8Matmul p{X, x_scales, x_dtype, ldx, codes, ldc, scales, bias, T, K, N, Y, y_dtype};
   const bool copies = bakron::fp8_matmul_needs_copies(p);
-  if (!workspace_ok(ws, ws_bytes, bakron::fp8_matmul_workspace_bytes(T, K, N, !x_scales, copies))) return BAKRON_ERR_WORKSPACE;
+  if (!workspace_ok(ws, ws_bytes, bakron::fp8_matmul_workspace_bytes(T, K, N, copies))) return BAKRON_ERR_WORKSPACE;
   return from_cuda(bakron::fp8_matmul_launch(p, ws, status_dev, (cudaStream_t)stream));
 }
 

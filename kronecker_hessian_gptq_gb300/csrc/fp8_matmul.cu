@@ -45,8 +45,11 @@ PairWork plan(int64_t rows, int64_t cols, int kN, int64_t K) {
   w.parts = tiles < kPlanPairs ? (int)std::max<int64_t>(1, std::min<int64_t>(kPlanPairs / tiles, w.ksteps / 2)) : 1;
   return w;
 }
+// A slice is what one epilogue warp holds of a tile; the parts' sums are whole tiles.
 int64_t slices(const PairWork& w) { return (int64_t)w.tiles_m * w.tiles_n * 2 * kF8Warps; }
-size_t join_bytes(const PairWork& w, int kN) { return w.parts > 1 ? (size_t)w.parts * slices(w) * 32 * (kN / 4) * 4 : 0; }
+size_t join_bytes(const PairWork& w, int kN) {
+  return w.parts > 1 ? (size_t)w.parts * w.tiles_m * w.tiles_n * 256 * kN * sizeof(float) : 0;
+}
 size_t arrived_bytes(const PairWork& w) { return w.parts > 1 ? (size_t)slices(w) * 4 : 0; }
 
 // ------------------------------------------------------------ forward
@@ -55,18 +58,18 @@ struct Forward {
   bool columns;  // tokens as columns
   int kN;
   PairWork work;
-  int64_t pitch;  // columns: of the scales
+  int64_t pitch;  // of the tokens' scales, a row for each block of K
   size_t codes, scales, arrived, sums, weights, bytes;
 };
-Forward forward_plan(int64_t T, int64_t K, int64_t N, bool values, bool copies) {
+Forward forward_plan(int64_t T, int64_t K, int64_t N, bool copies) {
   Forward f = {};
   f.columns = T <= kColumnTokens;
   f.kN = !f.columns ? 256 : T <= 64 ? 64 : 128;
   f.work = f.columns ? plan(N, T, f.kN, K) : plan(T, N, f.kN, K);
-  f.pitch = (int64_t)f.work.tiles_n * f.kN;
+  f.pitch = f.columns ? (int64_t)f.work.tiles_n * f.kN : (int64_t)f.work.tiles_m * 256;
   Room room;
   f.codes = room.take(T * up16(K));
-  f.scales = room.take((f.columns ? f.pitch : values ? T : 0) * blocks_of(K) * 4);
+  f.scales = room.take(f.pitch * blocks_of(K) * 4);
   f.arrived = room.take(arrived_bytes(f.work));
   f.sums = room.take(join_bytes(f.work, f.kN));
   if (copies) f.weights = room.take(N * up16(K));
@@ -92,22 +95,21 @@ void copy_codes(const void* from, int64_t ld, int64_t rows, int64_t cols, void* 
 __global__ void __launch_bounds__(256) turn_scales_kernel(const float* from, int64_t T, int64_t blocks, float* to, int64_t pitch,
                                                           uint32_t* word, int64_t words) {
   const int64_t step = (int64_t)gridDim.x * 256, first = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (to)
-    for (int64_t i = first; i < T * blocks; i += step) {
-      const int64_t t = i / blocks;
-      to[(i - t * blocks) * pitch + t] = from[i];
-    }
+  for (int64_t i = first; i < T * blocks; i += step) {
+    const int64_t t = i / blocks;
+    to[(i - t * blocks) * pitch + t] = from[i];
+  }
   for (int64_t i = first; i < words; i += step) word[i] = 0;
 }
 
 template <class T>
 cudaError_t forward(const Fp8Matmul& p, char* ws, int32_t* status, cudaStream_t stream) {
   const bool values = !p.x_scales, copy = !on_16(p.V, p.ldv);
-  const Forward f = forward_plan(p.T, p.K, p.N, values, copy);
+  const Forward f = forward_plan(p.T, p.K, p.N, copy);
   const int64_t blocks = blocks_of(p.K);
   const void* codes = ws + f.codes;
   int64_t ldc = up16(p.K);
-  const float* scales = reinterpret_cast<float*>(ws + f.scales);
+  float* scales = reinterpret_cast<float*>(ws + f.scales);
   uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + f.arrived);
   const int64_t words = (int64_t)arrived_bytes(f.work) / 4;
   const void* V = p.V;
@@ -122,8 +124,8 @@ cudaError_t forward(const Fp8Matmul& p, char* ws, int32_t* status, cudaStream_t 
     Fp8Codes q = {};
     q.X = p.X, q.dtype = p.x_dtype, q.rows = p.T, q.cols = p.K, q.ldx = p.ldx;
     q.along = reinterpret_cast<uint8_t*>(ws + f.codes), q.ld_along = ldc;
-    q.along_scales = reinterpret_cast<float*>(ws + f.scales);
-    q.along_row = f.columns ? 1 : blocks, q.along_col = f.columns ? f.pitch : 1;
+    q.along_scales = scales;
+    q.along_row = 1, q.along_col = f.pitch;
     q.clear = arrived, q.clear_words = words;
     e = fp8_codes_launch(q, stream);
   } else {
@@ -131,12 +133,9 @@ cudaError_t forward(const Fp8Matmul& p, char* ws, int32_t* status, cudaStream_t 
       codes = p.X, ldc = p.ldx;
     else
       copy_codes(p.X, p.ldx, p.T, p.K, ws + f.codes, stream);
-    if (f.columns || words) {
-      const int64_t all = std::max<int64_t>(f.columns ? p.T * blocks : 0, words);
-      turn_scales_kernel<<<(unsigned)std::min<int64_t>((all + 255) / 256, 152 * 8), 256, 0, stream>>>(
-          p.x_scales, p.T, blocks, f.columns ? reinterpret_cast<float*>(ws + f.scales) : nullptr, f.pitch, arrived, words);
-    }
-    if (!f.columns) scales = p.x_scales;
+    const int64_t all = std::max<int64_t>(p.T * blocks, words);
+    turn_scales_kernel<<<(unsigned)std::min<int64_t>((all + 255) / 256, 152 * 8), 256, 0, stream>>>(
+        p.x_scales, p.T, blocks, scales, f.pitch, arrived, words);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
@@ -144,38 +143,38 @@ cudaError_t forward(const Fp8Matmul& p, char* ws, int32_t* status, cudaStream_t 
   const F8Operand x{codes, p.T, ldc}, v{V, p.N, ldv};
   const bool early = values && !copy;
   if (f.columns) {
-    const F8Scales sc{p.scales, blocks, 1, p.N, 7, scales, 0, f.pitch, p.T};
+    const F8Scales sc{p.scales, scales, 1, f.pitch, blocks, p.N};
     const F8Columns<T> epi{p.N, p.T, p.bias, static_cast<T*>(p.Y)};
     if (f.kN == 64)
-      return fp8_pair_launch<false, false, 64, true, true>(v, x, p.K, f.work, sc, join, epi, early, status, stream, 0);
-    return fp8_pair_launch<false, false, 128, true, true>(v, x, p.K, f.work, sc, join, epi, early, status, stream, 0);
+      return fp8_pair_launch<false, false, 64, 1>(v, x, p.K, f.work, sc, join, epi, early, status, stream, 0);
+    return fp8_pair_launch<false, false, 128, 1>(v, x, p.K, f.work, sc, join, epi, early, status, stream, 0);
   }
-  const F8Scales sc{scales, blocks, 1, p.T, 0, p.scales, blocks, 1, p.N};
+  const F8Scales sc{scales, p.scales, f.pitch, 1, blocks, p.N};
   F8Rows<T> epi{{}, p.T, p.N, p.bias, static_cast<T*>(p.Y), false};
   epi.tma = sizeof(T) == 2 && p.N % 8 == 0 && aligned_to(p.Y, 16) && aligned_to(p.bias, 16);
   if (epi.tma)
     e = make_tensor_map(&epi.map, TileMap{p.Y, p.y_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                                           p.T, p.N, p.N, 32, 64, true});
   if (e != cudaSuccess) return e;
-  return fp8_pair_launch<false, false, 256, false, false>(x, v, p.K, f.work, sc, join, epi, early, status, stream, 0);
+  return fp8_pair_launch<false, false, 256, 2>(x, v, p.K, f.work, sc, join, epi, early, status, stream, 0);
 }
 
 // ------------------------------------------------------------ backward
 
 struct Backward {
   PairWork dx, dw;
-  int64_t pitch_n, pitch_k;  // of the columns' scales
+  int64_t pitch_t, pitch_n, pitch_k;  // of scales, a row for each block of what is summed
   size_t along, along_scales, down_y, down_y_scales, down_x, down_x_scales, sums, arrived, arrived_words, join, weights, bytes;
 };
 Backward backward_plan(int64_t T, int64_t K, int64_t N, bool dX, bool dW, bool dbias, bool copies) {
   Backward b = {};
   b.dx = plan(T, K, 256, N);
   b.dw = plan(N, K, 256, T);
-  b.pitch_n = (N + 255) / 256 * 256, b.pitch_k = (K + 255) / 256 * 256;
+  b.pitch_t = (T + 255) / 256 * 256, b.pitch_n = (N + 255) / 256 * 256, b.pitch_k = (K + 255) / 256 * 256;
   Room room;
   if (dX) {
     b.along = room.take(T * up16(N));
-    b.along_scales = room.take(T * blocks_of(N) * 4);
+    b.along_scales = room.take(b.pitch_t * blocks_of(N) * 4);
     if (copies) b.weights = room.take(N * up16(K));
   }
   if (dW) {
@@ -203,7 +202,7 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
   uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + b.arrived);
   Fp8Codes q = {};
   q.X = p.dY, q.dtype = p.dtype, q.rows = p.T, q.cols = p.N, q.ldx = p.lddy;
-  if (p.dX) q.along = at(b.along), q.ld_along = up16(p.N), q.along_scales = floats(b.along_scales), q.along_row = blocks_of(p.N), q.along_col = 1;
+  if (p.dX) q.along = at(b.along), q.ld_along = up16(p.N), q.along_scales = floats(b.along_scales), q.along_row = 1, q.along_col = b.pitch_t;
   if (p.dW) q.down = at(b.down_y), q.ld_down = up16(p.N), q.down_scales = floats(b.down_y_scales);
   q.down_pitch = b.pitch_n;
   if (p.dbias) q.sums = floats(b.sums);
@@ -224,10 +223,10 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
       V = at(b.weights), ldv = up16(p.K);
       e = cudaGetLastError();
     }
-    const F8Scales sc{q.along_scales, blocks_of(p.N), 1, p.T, 0, p.scales, 1, blocks_of(p.K), p.K};
+    const F8Scales sc{q.along_scales, p.scales, b.pitch_t, blocks_of(p.K), 1, p.K};
     const F8Rows<T> epi = rows(p.dX, p.T, p.K);
     if (e == cudaSuccess)
-      e = fp8_pair_launch<false, true, 256, false, false>(F8Operand{q.along, p.T, q.ld_along}, F8Operand{V, p.K, ldv}, p.N, b.dx,
+      e = fp8_pair_launch<false, true, 256, 2>(F8Operand{q.along, p.T, q.ld_along}, F8Operand{V, p.K, ldv}, p.N, b.dx,
                                                           sc, F8Join{floats(b.join), arrived}, epi, false, status, stream, 0);
   }
   if (e == cudaSuccess && p.dW) {
@@ -235,11 +234,11 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
     x.X = p.X, x.dtype = p.dtype, x.rows = p.T, x.cols = p.K, x.ldx = p.ldx;
     x.down = at(b.down_x), x.ld_down = up16(p.K), x.down_scales = floats(b.down_x_scales), x.down_pitch = b.pitch_k;
     e = fp8_codes_launch(x, stream);
-    const F8Scales sc{q.down_scales, 1, b.pitch_n, p.N, 0, x.down_scales, 0, b.pitch_k, p.K};
+    const F8Scales sc{q.down_scales, x.down_scales, b.pitch_n, b.pitch_k, 0, 0};
     const F8Rows<T> epi = rows(p.dW, p.N, p.K);
     if (p.dX) arrived += arrived_bytes(b.dx) / 4;
     if (e == cudaSuccess)
-      e = fp8_pair_launch<true, true, 256, true, false>(F8Operand{q.down, p.N, q.ld_down}, F8Operand{x.down, p.K, x.ld_down}, p.T,
+      e = fp8_pair_launch<true, true, 256, 0>(F8Operand{q.down, p.N, q.ld_down}, F8Operand{x.down, p.K, x.ld_down}, p.T,
                                                         b.dw, sc, F8Join{floats(b.join), arrived}, epi, false, status, stream,
                                                         p.dX ? -1 : 0);
   }
@@ -248,8 +247,8 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
 
 }  // namespace
 
-size_t fp8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool values, bool copies) {
-  return forward_plan(T, K, N, values, copies).bytes;
+size_t fp8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies) {
+  return forward_plan(T, K, N, copies).bytes;
 }
 bool fp8_matmul_needs_copies(const Fp8Matmul& p) { return !on_16(p.V, p.ldv); }
 cudaError_t fp8_matmul_launch(const Fp8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream) {

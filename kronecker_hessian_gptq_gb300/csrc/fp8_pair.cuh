@@ -30,34 +30,35 @@
 namespace bakron {
 
 constexpr int kF8K = 128;  // K of a stage, and of a scale
-constexpr int kF8Warps = 16;
+constexpr int kF8Warps = 16;  // of the epilogue
 constexpr int kF8Threads = 128 + 32 * kF8Warps;
 constexpr int kF8MostStages = 10;
-constexpr int kF8Ring = 4;  // columns' scales on their way
+constexpr int kF8Ring = 2;  // batches of scales on their way
 constexpr int kF8Smem = 226 * 1024;
 
-// Shared memory of a variant: stages, boxes for results in whole lines, scales.
-template <int kN, bool kColumns, bool kBoxes>
+// Shared memory of a variant: stages, boxes for results in whole lines, scales
+// (of the columns, of the block's 128 rows).
+template <int kN, bool kColumns, bool kRows, bool kBoxes>
 struct F8Shape {
   static constexpr int kA = 128 * kF8K, kB = kN / 2 * kF8K, kStage = kA + kB;
+  static constexpr int kHalves = kN > 128 ? 2 : 1;  // products of half the columns each
   static constexpr int kBufs = kN > 128 ? 2 : 4;
-  static constexpr int kCols = kN / 4;  // of a thread
-  static constexpr int kScales = kColumns ? kF8Ring * kN * 4 : 0;
-  static constexpr int kOther = (kBoxes ? kF8Warps * kPairBox : 0) + kScales + 1024;
+  static constexpr int kCols = kN / (kF8Warps / 4);  // of a thread
+  static constexpr int kScales = ((kColumns ? kN : 0) + (kRows ? 128 : 0)) * 4;  // of a block of K
+  static constexpr int kBatch = kColumns && kN > 64 ? 4 : 8;  // blocks whose scales come together
+  static constexpr int kOther = (kBoxes ? kF8Warps * kPairBox : 0) + kF8Ring * kBatch * kScales + 1024;
   static constexpr int kFit = (kF8Smem - kOther) / kStage;
   static constexpr int kStages = kFit < kF8MostStages ? kFit : kF8MostStages;
   static constexpr int kBytes = kStages * kStage + kOther;
 };
 
+// Scales in block k of K.  Those of activations differ from row to row: the
+// one of row (or column) i is p[k step + i], step a multiple of 4 and at least
+// what the tiles cover.  Those of weights are one for 128: p[(i >> 7) each + k step].
 struct F8Scales {
-  // of row r in block b: a[(r >> a_shift) a_row + b a_k]
-  const float* a;
-  int64_t a_row, a_k, rows;
-  int a_shift;
-  // of column c: one for 128 columns, b[(c >> 7) b_col + b b_k]; kColumns: b[b b_k + c],
-  // b_k a multiple of 4 and at least the columns of all tiles
-  const float* b;
-  int64_t b_col, b_k, cols;
+  const float *a, *b;
+  int64_t a_step, b_step, each;
+  int64_t weights;  // rows or columns that weights have
 };
 struct F8Join {
   float* sums;        // a tile's parts: [part][tile][block of the pair][warp][column][lane]
@@ -92,14 +93,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// kWeightsA: A is what no kernel before writes (the weights), else B.
-template <bool kARows, bool kBRows, int kN, bool kColumns, bool kWeightsA, class Epi>
+// kWeights: which operand the weights are, 1 for A, 2 for B, 0 for neither
+// (then both have a scale for each row).  No kernel before writes them.
+template <bool kARows, bool kBRows, int kN, int kWeights, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairWork work,
                     F8Scales sc, F8Join join, const __grid_constant__ Epi epi, int32_t* status, int32_t first_status) {
-  using Shape = F8Shape<kN, kColumns, Epi::kBoxes>;
-  constexpr int kStages = Shape::kStages, kBufs = Shape::kBufs, kCols = Shape::kCols;
-  constexpr int kChunk = kCols < 32 ? kCols : 32;
+  constexpr bool kColumns = kWeights != 2, kRows = kWeights != 1;  // have scales of their own
+  using Shape = F8Shape<kN, kColumns, kRows, Epi::kBoxes>;
+  static_assert(2 * kF8Warps * 32 * Shape::kCols == 256 * kN, "the slices make up a tile");
+  constexpr int kStages = Shape::kStages, kBufs = Shape::kBufs, kHalves = Shape::kHalves, kCols = Shape::kCols;
   extern __shared__ unsigned char f8_smem_raw[];
   const uint32_t base = (smem_u32(f8_smem_raw) + 1023u) & ~1023u;
   const uint32_t boxes = base + kStages * Shape::kStage;
@@ -116,8 +119,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     auto init = [](uint64_t* b, int n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n));
     };
-    for (int i = 0; i < kStages; ++i) init(&bar.full[i], 1), init(&bar.empty[i], 1);
-    for (int i = 0; i < kBufs; ++i) init(&bar.sum_full[i], 1), init(&bar.sum_empty[i], 2 * kF8Warps);
+    for (int i = 0; i < kStages; ++i) init(&bar.full[i], 1), init(&bar.empty[i], kHalves);
+    for (int i = 0; i < kBufs * kHalves; ++i) init(&bar.sum_full[i], 1), init(&bar.sum_empty[i], 2 * kF8Warps / kHalves);
     for (int i = 0; i < kF8Ring; ++i) init(&bar.scale_full[i], 1), init(&bar.scale_empty[i], kF8Warps);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -130,16 +133,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-
-  if (warp == 0 || warp == 3) {  // copies: warp 0 the weights' side, warp 3 the other
-    const bool is_a = (warp == 0) == kWeightsA;
+  // 640 threads start with 96 registers each; the first four warps hand 32 of
+  // theirs on, 8 to each of the other 16 (128 x 64 + 512 x 104 = 640 x 96).
+  constexpr bool kHandOn = kCols == 64;
+  if (warp < 4) {
+  if (kHandOn) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+  if (warp == 0 || warp == 3) {  // copies: warp 0 the weights' side, warp 3 the other and the scales
+    const bool is_a = (warp == 0) == (kWeights == 1);
     if (warp == 3) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    Ring ring;
+    auto fetch = [&](uint32_t to, const float* from, uint32_t bytes, uint32_t full) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(to),
+                   "l"(from), "r"(bytes), "r"(full)
+                   : "memory");
+    };
+    Ring ring, batch;
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = pair_unit(work, u);
       const int row = is_a ? q.tm * 256 + (int)rank * 128 : q.tn * kN + (int)rank * (kN / 2);
       for (int k = q.k0; k < q.k1; ++k, ring.next(kStages)) {
         const int slot = ring.slot;
+        if (warp == 3 && (k - q.k0) % Shape::kBatch == 0) {
+          if (batch.round) warp_wait(&bar.scale_empty[batch.slot], batch.turn ^ 1u, broken);
+          if (broken) break;
+          if (elect_one()) {
+            const uint32_t full = smem_u32(&bar.scale_full[batch.slot]);
+            const int here = q.k1 - k < Shape::kBatch ? q.k1 - k : Shape::kBatch;
+            uint32_t to = scales + (uint32_t)(batch.slot * Shape::kBatch * Shape::kScales);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full), "r"(here * Shape::kScales)
+                         : "memory");
+            for (int j = 0; j < here; ++j, to += Shape::kScales) {
+              if (kColumns) fetch(to, sc.b + (k + j) * sc.b_step + (int64_t)q.tn * kN, kN * 4, full);
+              if (kRows)
+                fetch(to + (kColumns ? kN * 4 : 0), sc.a + (k + j) * sc.a_step + (int64_t)q.tm * 256 + rank * 128, 512, full);
+            }
+          }
+          __syncwarp();
+          batch.next(kF8Ring);
+        }
         if (ring.round) warp_wait(&bar.empty[slot], ring.turn ^ 1u, broken);
         if (broken) break;
         const uint32_t full = in_even_block(&bar.full[slot]);
@@ -167,147 +197,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
       else if (rank == 0)
         warp_wait(&bar.full[ring.slot], ring.turn ^ 1u, late);
     }
-  } else if (warp == 1 && rank == 0) {  // products
-    // fp32 sums of e4m3 products, which operands have their rows contiguous, N = kN, M = 256
-    constexpr uint32_t idesc = (1u << 4) | ((kARows ? 1u : 0u) << 15) | ((kBRows ? 1u : 0u) << 16) | ((uint32_t)(kN >> 3) << 17) |
-                               ((256u >> 4) << 24);
+    for (int i = 0; warp == 3 && i < kF8Ring; ++i, batch.next(kF8Ring)) {
+      bool late = false;
+      if (batch.round) warp_wait(&bar.scale_full[batch.slot], batch.turn ^ 1u, late);
+    }
+  } else if (rank == 0 && warp - 1 < kHalves) {  // products, a warp for each half of the columns
+    // fp32 sums of e4m3 products, which operands have their rows contiguous, N, M = 256
+    constexpr uint32_t idesc = (1u << 4) | ((kARows ? 1u : 0u) << 15) | ((kBRows ? 1u : 0u) << 16) |
+                               ((uint32_t)((kN / kHalves) >> 3) << 17) | ((256u >> 4) << 24);
+    const int half = warp - 1;
+    // Rows of B: with K contiguous 64 rows are 8 KB on, else 64 bytes of each.
+    const uint32_t b_half = (uint32_t)half * (kBRows ? 64u >> 4 : 8192u >> 4);
     int sums = 0;
     Ring ring;
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = pair_unit(work, u);
       for (int k = q.k0; k < q.k1; ++k, ring.next(kStages), ++sums) {
-        const int buf = sums % kBufs;
-        if (sums >= kBufs) warp_wait(&bar.sum_empty[buf], (uint32_t)(sums / kBufs - 1) & 1u, broken);
+        const int buf = sums % kBufs, sum = buf * kHalves + half;
         warp_wait(&bar.full[ring.slot], ring.turn, broken);
+        if (sums >= kBufs) warp_wait(&bar.sum_empty[sum], (uint32_t)(sums / kBufs - 1) & 1u, broken);
         if (broken) break;
         tc_fence_after();
-        const uint32_t at = base + (uint32_t)ring.slot * Shape::kStage, acc = tmem + (uint32_t)(buf * kN);
-        const uint32_t a = pair_desc_low<kARows>(at), b = pair_desc_low<kBRows>(at + Shape::kA);
+        const uint32_t at = base + (uint32_t)ring.slot * Shape::kStage, acc = tmem + (uint32_t)(sum * (kN / kHalves));
+        const uint32_t a = pair_desc_low<kARows>(at), b = pair_desc_low<kBRows>(at + Shape::kA) + b_half;
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < kF8K / 32; ++j) pair_mma_f8(acc, a + j * f8_kstep<kARows>(), b + j * f8_kstep<kBRows>(), idesc, j > 0);
+          pair_commit(&bar.sum_full[sum]);
           pair_commit(&bar.empty[ring.slot]);
-          pair_commit(&bar.sum_full[buf]);
         }
         __syncwarp();
       }
     }
-  } else if (warp == 2 && kColumns) {  // the columns' scales
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    Ring ring;
-    for (int u = mine; u < units && !broken; u += pairs) {
-      const PairUnit q = pair_unit(work, u);
-      for (int k = q.k0; k < q.k1; ++k, ring.next(kF8Ring)) {
-        if (ring.round) warp_wait(&bar.scale_empty[ring.slot], ring.turn ^ 1u, broken);
-        if (broken) break;
-        if (elect_one()) {
-          const uint32_t full = smem_u32(&bar.scale_full[ring.slot]);
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full), "r"(kN * 4) : "memory");
-          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                           scales + (uint32_t)(ring.slot * kN * 4)),
-                       "l"(sc.b + k * sc.b_k + (int64_t)q.tn * kN), "r"(kN * 4), "r"(full)
-                       : "memory");
-        }
-        __syncwarp();
-      }
-    }
-    for (int i = 0; i < kF8Ring; ++i, ring.next(kF8Ring)) {
-      bool late = false;
-      if (ring.round) warp_wait(&bar.scale_full[ring.slot], ring.turn ^ 1u, late);
-    }
-  } else if (warp >= 4) {  // epilogue: 32 rows of the block and kCols columns for each warp
+  }
+  } else {  // epilogue: 32 rows of the block and kCols columns for each warp
+    if (kHandOn) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
     const int quarter = warp & 3, part = (warp - 4) >> 2;
-    const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)(part * kCols);
+    // A half's products have 64 columns of the even block's rows of B, then 64 of the odd block's.
+    const int half = kHalves > 1 ? part & 1 : 0;
+    const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)((kHalves > 1 ? part >> 1 : part) * kCols);
+    const int first = part * kCols;  // of the thread's columns in the tile
     const PairBox box{boxes + (uint32_t)(warp - 4) * kPairBox, lane};
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    // The weights' scales are the whole warp's: a lane reads that of one block,
+    // 32 blocks at a time, and those of the next unit while this one is at hand.
+    auto shared_scale = [&](const PairUnit& q, int k) {
+      if (kWeights == 0 || k >= q.k1) return 0.f;
+      int64_t at = kWeights == 1 ? (int64_t)q.tm * 256 + rank * 128 : (int64_t)q.tn * kN + first;
+      at = at < sc.weights ? at : sc.weights - 1;  // beyond the matrix, where sums are 0, the last
+      return kWeights == 1 ? sc.a[(at >> 7) * sc.each + k * sc.a_step] : sc.b[(at >> 7) * sc.each + k * sc.b_step];
+    };
+    auto arrive = [&](uint64_t* b) {
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+    };
     int sums = 0;
     Ring ring;
+    PairUnit next = pair_unit(work, mine);
+    float ahead = shared_scale(next, next.k0 + lane);
     for (int u = mine; u < units && !broken; u += pairs) {
-      const PairUnit q = pair_unit(work, u);
-      const int64_t row0 = (int64_t)q.tm * 256 + rank * 128 + 32 * quarter, col = (int64_t)q.tn * kN + part * kCols;
-      // Beyond the matrix the last row's and column's scales: sums are 0 there.
-      const int64_t row = row0 + lane < sc.rows ? row0 + lane : sc.rows - 1;
-      const float* sa = sc.a + (row >> sc.a_shift) * sc.a_row;
-      const float* sb = kColumns ? nullptr : sc.b + ((col < sc.cols ? col : sc.cols - 1) >> 7) * sc.b_col;
+      const PairUnit q = next;
+      float of_32 = ahead;
+      if (u + pairs < units) {
+        next = pair_unit(work, u + pairs);
+        ahead = shared_scale(next, next.k0 + lane);
+      }
+      const int64_t row0 = (int64_t)q.tm * 256 + rank * 128 + 32 * quarter, col = (int64_t)q.tn * kN + first;
       F2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = f2(0.f);
-      float a_next = sa[q.k0 * sc.a_k], b_next = kColumns ? 1.f : sb[q.k0 * sc.b_k];
       for (int k = q.k0; k < q.k1; ++k, ++sums) {
-        const int buf = sums % kBufs;
-        const float a = a_next, b = b_next;
-        if (k + 1 < q.k1) {
-          a_next = sa[(k + 1) * sc.a_k];
-          if (!kColumns) b_next = sb[(k + 1) * sc.b_k];
+        const int sum = sums % kBufs * kHalves + half, in = k - q.k0, in_batch = in % Shape::kBatch;
+        if (kWeights && (in & 31) == 0 && in > 0) of_32 = shared_scale(q, k + lane);
+        if (in_batch == 0) {
+          if (in > 0) {
+            arrive(&bar.scale_empty[ring.slot]);
+            ring.next(kF8Ring);
+          }
+          warp_wait(&bar.scale_full[ring.slot], ring.turn, broken);
         }
-        if (kColumns) warp_wait(&bar.scale_full[ring.slot], ring.turn, broken);
-        warp_wait(&bar.sum_full[buf], (uint32_t)(sums / kBufs) & 1u, broken);
+        const uint32_t from = scales + (uint32_t)((ring.slot * Shape::kBatch + in_batch) * Shape::kScales);
+        float r = 1.f;
+        if (kRows)
+          asm volatile("ld.shared.f32 %0, [%1];\n"
+                       : "=f"(r)
+                       : "r"(from + (uint32_t)((kColumns ? kN : 0) + 32 * quarter + lane) * 4u)
+                       : "memory");
+        const F2 scale = f2(kWeights ? r * __shfl_sync(0xffffffffu, of_32, in & 31) : r);
+        warp_wait(&bar.sum_full[sum], (uint32_t)(sums / kBufs) & 1u, broken);
         if (broken) break;
         tc_fence_after();
-        const F2 s = f2(a * b);
-        const uint32_t from = scales + (uint32_t)(ring.slot * kN + part * kCols) * 4u;
 #pragma unroll
-        for (int c = 0; c < kCols; c += kChunk) {
-          float v[kChunk];
-          if constexpr (kChunk == 16)
-            tmem_ld16(tmem + (uint32_t)(buf * kN + c) + lanes, v);
-          else
-            tmem_ld32(tmem + (uint32_t)(buf * kN + c) + lanes, v);
-          if (c + kChunk == kCols) {  // all read: the buffer may be filled again
+        for (int c = 0; c < kCols; c += 16) {
+          float v[16];
+          tmem_ld16(tmem + (uint32_t)(sum * (kN / kHalves) + c) + lanes, v);
+          if (c + 16 == kCols) {  // all read: the buffer may be filled again
             tc_fence_before();
-            __syncwarp();
+            // A release of cluster scope would stall the warp for half a
+            // microsecond; the tensor-memory loads are complete.
             if (lane == 0)
-              asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.sum_empty[buf]))
-                           : "memory");
+              asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.sum_empty[sum])) : "memory");
           }
 #pragma unroll
-          for (int i = 0; i < kChunk; i += 4) {
+          for (int i = 0; i < 16; i += 4) {
             F2 x = f2(v[i], v[i + 1]), y = f2(v[i + 2], v[i + 3]);
             if constexpr (kColumns) {
-              float w[4];
+              float f[4];
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
-                           : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3])
-                           : "r"(from + (uint32_t)(c + i) * 4u)
+                           : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                           : "r"(from + (uint32_t)(first + c + i) * 4u)
                            : "memory");
-              x = x * f2(w[0], w[1]);
-              y = y * f2(w[2], w[3]);
+              x = x * f2(f[0], f[1]);
+              y = y * f2(f[2], f[3]);
             }
-            acc[(c + i) / 2] = fma2(x, s, acc[(c + i) / 2]);
-            acc[(c + i) / 2 + 1] = fma2(y, s, acc[(c + i) / 2 + 1]);
+            acc[(c + i) / 2] = fma2(x, scale, acc[(c + i) / 2]);
+            acc[(c + i) / 2 + 1] = fma2(y, scale, acc[(c + i) / 2 + 1]);
           }
         }
-        if (kColumns) {
-          __syncwarp();
-          if (lane == 0)
-            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(&bar.scale_empty[ring.slot])) : "memory");
-          ring.next(kF8Ring);
-        }
+      }
+      if (!broken) {
+        arrive(&bar.scale_empty[ring.slot]);
+        ring.next(kF8Ring);
       }
       if (broken) break;
-      float out[kCols];
-#pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) split(acc[i], out[2 * i], out[2 * i + 1]);
+      bool last = true;
       if (work.parts > 1) {
         if (row0 >= epi.rows() || col >= epi.cols()) continue;  // for every part alike
         const int64_t tile = (int64_t)q.tm * work.tiles_n + q.tn, tiles = (int64_t)work.tiles_m * work.tiles_n;
         const int64_t slice = (tile * 2 + rank) * kF8Warps + (warp - 4), stride = tiles * 2 * kF8Warps * 32 * kCols;
-        float* to = join.sums + slice * (32 * kCols) + lane;
+        float2* to = reinterpret_cast<float2*>(join.sums + slice * (32 * kCols)) + lane;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) to[q.part * stride + 32 * i] = out[i];
+        for (int i = 0; i < kCols / 2; ++i) {
+          float2 x;
+          split(acc[i], x.x, x.y);
+          to[q.part * (stride / 2) + 32 * i] = x;
+        }
         __threadfence();
         __syncwarp();
         uint32_t before = 0;
         if (lane == 0) before = atomicAdd(join.arrived + slice, 1u);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before + 1 != (uint32_t)work.parts) continue;
-        __threadfence();
+        last = __shfl_sync(0xffffffffu, before, 0) + 1 == (uint32_t)work.parts;
+        if (last) {
+          __threadfence();
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) out[i] = 0.f;
-        for (int p = 0; p < work.parts; ++p) {
+          for (int i = 0; i < kCols / 2; ++i) acc[i] = f2(0.f);
+          for (int p = 0; p < work.parts; ++p) {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) out[i] += __ldcg(to + p * stride + 32 * i);
+            for (int i = 0; i < kCols / 2; ++i) {
+              const float2 x = __ldcg(to + p * (stride / 2) + 32 * i);
+              acc[i] = acc[i] + f2(x.x, x.y);
+            }
+          }
         }
       }
+      if (!last) continue;
+      float out[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) split(acc[i], out[2 * i], out[2 * i + 1]);
       epi(row0, col, out, box);
     }
     if (Epi::kBoxes && lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
@@ -398,10 +444,10 @@ struct F8Operand {
 };
 
 // early: the kernel before may still run when this one starts.
-template <bool kARows, bool kBRows, int kN, bool kColumns, bool kWeightsA, class Epi>
+template <bool kARows, bool kBRows, int kN, int kWeights, class Epi>
 cudaError_t fp8_pair_launch(F8Operand a, F8Operand b, int64_t K, const PairWork& work, const F8Scales& sc, const F8Join& join,
                             const Epi& epi, bool early, int32_t* status, cudaStream_t stream, int32_t first_status) {
-  using Shape = F8Shape<kN, kColumns, Epi::kBoxes>;
+  using Shape = F8Shape<kN, kWeights != 2, kWeights != 1, Epi::kBoxes>;
   CUtensorMap ma, mb;
   const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   cudaError_t e = make_tensor_map(&ma, kARows ? TileMap{a.p, type, K, a.rows, a.ld, kF8K, 128, true}
@@ -409,7 +455,7 @@ cudaError_t fp8_pair_launch(F8Operand a, F8Operand b, int64_t K, const PairWork&
   if (e == cudaSuccess)
     e = make_tensor_map(&mb, kBRows ? TileMap{b.p, type, K, b.rows, b.ld, kF8K, kN / 2, true}
                                     : TileMap{b.p, type, b.rows, K, b.ld, kN / 2, kF8K, true});
-  auto kernel = fp8_pair_kernel<kARows, kBRows, kN, kColumns, kWeightsA, Epi>;
+  auto kernel = fp8_pair_kernel<kARows, kBRows, kN, kWeights, Epi>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

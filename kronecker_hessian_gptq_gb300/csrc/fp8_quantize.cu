@@ -81,7 +81,7 @@ struct TileCodes {
   int64_t ld_along, ld_down, ld_whole;
   bool vec_along, vec_down, vec_whole;
   float *along_scales, *down_scales, *whole_scales;
-  int64_t along_row;   // along_scales: rows of this many floats, one for each 128 columns
+  int64_t along_row, along_col;  // strides of along_scales
   int64_t down_pitch;  // down_scales: a row of this many floats for each 128 rows
   int64_t whole_row;
   float* sums;  // a row of down_pitch floats for each 128 rows
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kCodeThreads) tile_codes_kernel(const T* X, co
       const int64_t r = r0 + 16 * i;
       if (r < p.rows && k < p.cols) {
         put_codes8(p.along + r * p.ld_along, k, p.cols, p.vec_along, fp8_codes8(v[i], inv));
-        if (part == 0) p.along_scales[r * p.along_row + tn] = scale;
+        if (part == 0) p.along_scales[r * p.along_row + tn * p.along_col] = scale;
       }
     }
   }
@@ -209,7 +209,7 @@ cudaError_t codes_typed(const Fp8Codes& q, cudaStream_t stream) {
   const int64_t tiles = (q.rows + 127) / 128 * ((q.cols + 127) / 128);
   const TileCodes p{q.rows, q.cols, q.ldx, vec, q.along, q.down, q.whole, q.ld_along, q.ld_down, q.ld_whole,
                     in8(q.along, q.ld_along), in8(q.down, q.ld_down), in8(q.whole, q.ld_whole), q.along_scales,
-                    q.down_scales, q.whole_scales, q.along_row, q.down_pitch, q.whole_row, q.sums, clear};
+                    q.down_scales, q.whole_scales, q.along_row, q.along_col, q.down_pitch, q.whole_row, q.sums, clear};
   tile_codes_kernel<T><<<(unsigned)tiles, kCodeThreads, 0, stream>>>(X, p);
   return cudaGetLastError();
 }

@@ -162,7 +162,7 @@ struct Fp8Matmul {
   void* Y;
   int y_dtype;
 };
-size_t fp8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool values, bool copies);
+size_t fp8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies);
 bool fp8_matmul_needs_copies(const Fp8Matmul& p);
 cudaError_t fp8_matmul_launch(const Fp8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream);
 struct Fp8Backward {
