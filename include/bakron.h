@@ -593,8 +593,8 @@ int bakron_fp8_matmul_backward(const void* dY, int64_t lddy, const void* X, int6
  * positions: T (any 64-bit numbers).  freqs: R / 2, fp64, radians for each
  * position.  R even, 0 (no rotation; positions and freqs NULL) to D; D in 1 ..
  * 1024; Hq, Hk in 0 .. 65535, Hq + Hk at least 1.
- * YQ, YK: T x heads x D, dense; rounded once.  Angles are exact to |p| 2^-54
- * turns before they are rounded to fp32.
+ * YQ, YK: T x heads x D, dense; rounded once.  Angles are exact to
+ * |p f| 2^-54 + |p| 2^-64 turns before they are rounded to fp32.
  */
 #define BAKRON_PAIRS_HALVES 0
 #define BAKRON_PAIRS_NEIGHBOURS 1

@@ -158,7 +158,7 @@ def _heads(t, name, dtypes, T, D, device):
     token, head, one = t.stride()
     if n != T or d != D or t.get_device() != device or heads > 65535:
         raise ValueError(f"{name} must have {T} tokens and at most 65535 heads of {D}, on cuda:{device}")
-    if one != 1 and d > 1:
+    if one != 1 and d > 1 and n * heads:
         raise ValueError(f"the values of a head of {name} must be contiguous")
     # A lone token or head may carry any stride.
     return t.data_ptr(), token if n > 1 else 0, head if heads > 1 else 0, heads

@@ -12,10 +12,17 @@
 // scale; blocks walk over units of 2048 values of all tensors, whose addresses
 // come in the kernel's parameters, so that a launch takes up to 128 tensors
 // and a captured one keeps them.  Statistics, sums and the update are fp32.
+// 235 million values: 1054 us in fp32 (6.2 TB/s), 660 us with 8-bit states, fp32
+// masters, bf16 gradients and copies (5.7 TB/s), which issues 72 instructions a
+// value, two thirds of the time: a value's hash takes 9, two codes cut at random
+// 16.  Sums and products go in pairs, conditions that hardly ever hold are
+// tested for eight values at once, and all loads are under way before the first is
+// converted (815 us before that, at 104 instructions).
 #include <cuda_fp8.h>
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "bakron.h"
 #include "elem.cuh"
@@ -28,9 +35,16 @@ constexpr int kAdamThreads = 256;
 constexpr int kAdamUnit = kAdamThreads * 8;
 constexpr int kAdamList = 128;  // tensors of a launch
 
+// Squares are kept 2^48 times as large where states have 8 bits: none is then
+// subnormal, which the approximate square root would take for 0, and those that
+// overflow go the way of values that are not finite.
+constexpr float kLarger = 281474976710656.f, kRootLarger = 16777216.f;
+
 struct AdamConstants {
   float b1, c1, b2, c2, eps, root, rate, decay, grad;
   uint32_t key;  // of the seed and the step
+  // The same in pairs for 8-bit states, with squares kLarger times as large.
+  F2 pb1, pc1, pb2, pc2, peps, proot, prate, pdecay, pgrad;
 };
 struct AdamEntry {
   void* p;
@@ -48,24 +62,39 @@ struct AdamList {
   int count;
 };
 
-// 8 values from the i-th on, or fewer: up to n, then zeros.
-template <class T>
-__device__ __forceinline__ void get8(const T* p, int64_t i, int64_t n, bool vec, F2 (&v)[4]) {
-  Raw8<T> raw;
+// 8 values of 16 or 32 bits from the i-th on as they lie in memory, or fewer: up
+// to n, then zeros.  What they are is looked at after all loads are under way:
+// a conversion waits for its values.
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw get_raw(const void* p, bool wide, int64_t i, int64_t n, bool vec) {
+  Raw r = {};
   if (vec && i + 8 <= n) {
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
-      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p + i) + k);
-      raw.w[4 * k] = u.x, raw.w[4 * k + 1] = u.y, raw.w[4 * k + 2] = u.z, raw.w[4 * k + 3] = u.w;
-    }
-    open8<T>(raw, v);
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (wide ? 4 * i : 2 * i));
+    r.a = __ldcs(from);
+    if (wide) r.b = __ldcs(from + 1);
   } else {
-    float f[8];
+    uint32_t w[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = i + k < n ? to_f32<T>(p[i + k]) : 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = f2(f[2 * k], f[2 * k + 1]);
+    for (int k = 0; k < 8; ++k) {
+      w[k] = 0;
+      if (i + k < n) w[k] = wide ? static_cast<const uint32_t*>(p)[i + k] : static_cast<const uint16_t*>(p)[i + k];
+    }
+    if (wide)
+      r.a = make_uint4(w[0], w[1], w[2], w[3]), r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    else
+      r.a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
   }
+  return r;
+}
+__device__ __forceinline__ void open_raw(const Raw& r, int type, F2 (&v)[4]) {
+  if (type == kF32)
+    open8<float>(Raw8<float>{{r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w}}, v);
+  else if (type == kF16)
+    open8<__half>(Raw8<__half>{{r.a.x, r.a.y, r.a.z, r.a.w}}, v);
+  else
+    open8<__nv_bfloat16>(Raw8<__nv_bfloat16>{{r.a.x, r.a.y, r.a.z, r.a.w}}, v);
 }
 template <class T>
 __device__ __forceinline__ void put8(T* p, int64_t i, int64_t n, bool vec, const F2 (&v)[4]) {
@@ -84,14 +113,6 @@ __device__ __forceinline__ void put8(T* p, int64_t i, int64_t n, bool vec, const
       if (i + 2 * k + 1 < n) p[i + 2 * k + 1] = from_f32<T>(b);
     }
   }
-}
-__device__ __forceinline__ void get8(const void* p, int type, int64_t i, int64_t n, bool vec, F2 (&v)[4]) {
-  if (type == kF32)
-    get8(static_cast<const float*>(p), i, n, vec, v);
-  else if (type == kF16)
-    get8(static_cast<const __half*>(p), i, n, vec, v);
-  else
-    get8(static_cast<const __nv_bfloat16*>(p), i, n, vec, v);
 }
 __device__ __forceinline__ void put8(void* p, int type, int64_t i, int64_t n, bool vec, const F2 (&v)[4]) {
   if (type == kF32)
@@ -135,21 +156,35 @@ __device__ __forceinline__ void open_codes(const uint2& u, float scale, F2 (&v)[
 // golden ratio, then two rounds of a shift and a product with an odd number
 // (the fractions of the roots of 2 and 3).
 constexpr uint32_t kMixA = 0x9E3779B1u, kMixB = 0x6A09E667u, kMixC = 0xBB67AE85u;
+// The last step, x ^ x >> 16, is left to those who take the halves r of it, as
+// (1 + r) / 8.
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x = (x ^ (x >> 16)) * kMixB;
-  x = (x ^ (x >> 15)) * kMixC;
-  return x ^ (x >> 16);
+  return (x ^ (x >> 15)) * kMixC;
+}
+__device__ __forceinline__ float more_of_upper(uint32_t x) { return __uint_as_float(((x >> 9) & 0x7fff80u) | 0x3e000000u); }
+__device__ __forceinline__ float more_of_lower(uint32_t x) {
+  return __uint_as_float((((x << 7) ^ (x >> 9)) & 0x7fff80u) | 0x3e000000u);
 }
 
-// 0 <= q <= 448 on the numbers of e4m3 at or below q plus `bits` / 2^16 of a
-// step: q + step + bits step / 2^16 is cut to whole steps by adding a power of
-// two whose own last place is a step, towards zero; then that power and the
-// one step are taken off again.
-__device__ __forceinline__ float cut_at_random(float q, uint32_t bits) {
-  const uint32_t e = max(__float_as_uint(q) & 0x7f800000u, 121u << 23);  // at least 2^-6
-  const float step = __uint_as_float(e - (3u << 23)), big = __uint_as_float(e + (20u << 23));
-  const float t = fmaf(__uint_as_float(0x3f800000u | (bits << 7)), step, q);
-  return __fadd_rz(t, big) - (big + step);
+// Two values |q| <= 448 on the numbers of e4m3 at or below |q| + r step, r the
+// random 16 bits as a fraction, with q's sign.  With e the power of two below q,
+// at least 2^-6, a step is e / 8: q + (1 + r) step is cut to whole steps by adding
+// e 2^20, whose last place is a step, towards zero; then that and the one step
+// are taken off again.  more: (1 + r) / 8.
+template <bool kSigned>
+__device__ __forceinline__ F2 cut_at_random(F2 q, F2 more) {
+  float x[2], e[2];
+  split(q, x[0], x[1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u = __float_as_uint(x[h]), least = max(u & 0x7f800000u, 0x3c800000u);
+    e[h] = __uint_as_float(kSigned ? least | (u & 0x80000000u) : least);
+  }
+  const F2 each = f2(e[0], e[1]), t = fma2(each, more, q), up = f2(1048576.f);
+  F2 s;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;\n" : "=l"(s.v) : "l"(each.v), "l"(up.v), "l"(t.v));
+  return fma2(each, f2(-1048576.125f), s);
 }
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -162,12 +197,109 @@ __device__ __forceinline__ void group_scale(float top, float& scale, float& inv)
   if (inv == 0.f) scale = 0.f;
 }
 
-template <bool k8>
+// New moment, square and parameter of one value.  One whose gradient or its
+// square is not finite stays what it is (false).
+__device__ __forceinline__ bool step_of(const AdamConstants& c, float g, float& p, float& m, float& v, float& root) {
+  g *= c.grad;
+  const float x = fmaf(g, c.c1, m * c.b1), y = fmaf(g * g, c.c2, v * c.b2);
+  if (!(fabsf(x) < INFINITY && y < INFINITY)) return false;
+  float over;
+  asm("sqrt.approx.f32 %0, %1;\n" : "=f"(root) : "f"(y));
+  asm("rcp.approx.f32 %0, %1;\n" : "=f"(over) : "f"(fmaf(root, c.root, c.eps)));
+  p = fmaf(x * over, -c.rate, p * c.decay);
+  m = x, v = y;
+  return true;
+}
+// The codes of a thread's eight values of the warp's group, and lane 0 the scales.
+// mt, rt: the largest |m| and root (kRootLarger times as large) of the thread.
+__device__ __forceinline__ void put_states(const AdamConstants& c, const AdamEntry& e, int64_t i, float mt, float rt, const F2 (&m)[4],
+                                           const F2 (&root)[4]) {
+  constexpr float kLeast = 0.001953125f;  // of e4m3
+  float ms, vs, mi, vi, least = 1.f;
+  group_scale(mt, ms, mi);
+  group_scale(rt * (1 / kRootLarger), vs, vi);
+  vi *= 1 / kRootLarger;
+  if ((threadIdx.x & 31) == 0) e.ms[i >> 8] = ms, e.vs[i >> 8] = vs;
+  const uint32_t key = c.key + e.place * kMixC + (uint32_t)i * kMixA + (uint32_t)(i >> 32) * kMixC;
+  uint32_t mw[2], vw[2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t h0 = mix(key + (uint32_t)(2 * k) * kMixA), h1 = mix(key + (uint32_t)(2 * k + 1) * kMixA);
+    float z[2], q[2], r[2];
+    split(cut_at_random<true>(m[k] * f2(mi), f2(more_of_upper(h0), more_of_upper(h1))), z[0], z[1]);
+    // A root that is there stays there: nothing is divided by a lost one.
+    split(root[k] * f2(vi), q[0], q[1]);
+    least = fminf(least, fminf(q[0], q[1]));
+    split(cut_at_random<false>(f2(fmaxf(q[0], kLeast), fmaxf(q[1], kLeast)), f2(more_of_lower(h0), more_of_lower(h1))), r[0], r[1]);
+    const uint32_t a = e4m3_pair(z[0], z[1]), b = e4m3_pair(r[0], r[1]);
+    mw[k >> 1] = k & 1 ? mw[k >> 1] | (a << 16) : a;
+    vw[k >> 1] = k & 1 ? vw[k >> 1] | (b << 16) : b;
+  }
+  if (least == 0.f) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float r[2];
+      split(root[k], r[0], r[1]);
+      if (r[0] * vi == 0.f) vw[k >> 1] &= ~(0xffu << (16 * (k & 1)));
+      if (r[1] * vi == 0.f) vw[k >> 1] &= ~(0xff00u << (16 * (k & 1)));
+    }
+  }
+  put_codes(e.m, i, e.n, e.vec, mw);
+  put_codes(e.v, i, e.n, e.vec, vw);
+}
+__device__ __forceinline__ void put_params(const AdamEntry& e, int64_t i, const F2 (&p)[4]) {
+  put8(e.p, e.p_type, i, e.n, e.vec, p);
+  if (!e.copy) return;
+  if (e.copy_type == kF16)
+    put8(static_cast<__half*>(e.copy), i, e.n, e.vec, p);
+  else
+    put8(static_cast<__nv_bfloat16*>(e.copy), i, e.n, e.vec, p);
+}
+// A warp's 256 values with 8-bit states, of which some are not finite or their
+// squares too large for the fast way.  Returns whether a gradient is not finite.
+__device__ __noinline__ bool step_of_group(const AdamConstants& c, const AdamEntry& e, int64_t i) {
+  const int64_t n = e.n;
+  const bool vec = e.vec;
+  F2 p[4], g[4], m[4], root[4];
+  open_codes(get_codes(e.m, i, n, vec), e.ms[i >> 8], m);
+  open_codes(get_codes(e.v, i, n, vec), e.vs[i >> 8], root);
+  open_raw(get_raw(e.p, e.p_type == kF32, i, n, vec), e.p_type, p);
+  open_raw(get_raw(e.g, e.g_type == kF32, i, n, vec), e.g_type, g);
+  __syncwarp();  // the scales are written below
+  bool bad = false;
+  float mt = 0.f, rt = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float gs[2], ps[2], ms[2], rs[2];
+    split(g[k], gs[0], gs[1]);
+    split(p[k], ps[0], ps[1]);
+    split(m[k], ms[0], ms[1]);
+    split(root[k], rs[0], rs[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v = rs[h] * rs[h];
+      if (!step_of(c, gs[h], ps[h], ms[h], v, rs[h])) {
+        bad = true;
+        if (!(fabsf(ms[h]) < INFINITY)) ms[h] = 0.f;
+        if (!(rs[h] < INFINITY)) rs[h] = 0.f;
+      }
+      rs[h] *= kRootLarger;
+      mt = fmaxf(mt, fabsf(ms[h])), rt = fmaxf(rt, rs[h]);
+    }
+    p[k] = f2(ps[0], ps[1]), m[k] = f2(ms[0], ms[1]), root[k] = f2(rs[0], rs[1]);
+  }
+  put_params(e, i, p);
+  put_states(c, e, i, mt, rt, m, root);
+  return bad;
+}
+
+// kMade: the constants come from device memory.
+template <bool k8, bool kMade>
 __global__ void __launch_bounds__(kAdamThreads, k8 ? 4 : 3)
     adamw_kernel(const __grid_constant__ AdamList list, const __grid_constant__ AdamConstants given, const AdamConstants* made,
                  const int32_t* skip, int32_t* status) {
   if (skip && *skip) return;
-  const AdamConstants c = made ? *made : given;
+  const AdamConstants c = kMade ? *made : given;
   const int lane = threadIdx.x & 31;
   bool bad = false;
   int at = 0;
@@ -188,112 +320,87 @@ __global__ void __launch_bounds__(kAdamThreads, k8 ? 4 : 3)
     const int64_t n = e.n, i = (u - list.first[at]) * kAdamUnit + threadIdx.x * 8;
     const bool vec = e.vec;
     if (i - lane * 8 >= n) continue;  // the whole warp's
-    F2 p[4], g[4], m[4], v[4];
-    float ms = 0.f, vs = 0.f;
-    if constexpr (k8) {
-      const uint2 mc = get_codes(e.m, i, n, vec), vc = get_codes(e.v, i, n, vec);
-      ms = e.ms[i >> 8], vs = e.vs[i >> 8];
-      get8(e.p, e.p_type, i, n, vec, p);
-      get8(e.g, e.g_type, i, n, vec, g);
-      open_codes(mc, ms, m);
-      open_codes(vc, vs, v);  // the root
-    } else {
-      get8(static_cast<const float*>(e.m), i, n, vec, m);
-      get8(static_cast<const float*>(e.v), i, n, vec, v);
-      get8(e.p, e.p_type, i, n, vec, p);
-      get8(e.g, e.g_type, i, n, vec, g);
-    }
-    float mt = 0.f, rt = 0.f;
-    F2 root[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const F2 gk = g[k] * f2(c.grad);
-      const F2 m0 = m[k], v0 = k8 ? v[k] * v[k] : v[k];
-      const F2 m1 = fma2(gk, f2(c.c1), m0 * f2(c.b1)), v1 = fma2(gk * gk, f2(c.c2), v0 * f2(c.b2));
-      float x[2], y[2], q[2], r[2], old[2], mo[2], vo[2];
-      split(m1, x[0], x[1]);
-      split(v1, y[0], y[1]);
-      split(p[k], q[0], q[1]);
-      split(m0, mo[0], mo[1]);
-      split(v0, vo[0], vo[1]);
-      if (k8) split(v[k], old[0], old[1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        asm("sqrt.approx.f32 %0, %1;\n" : "=f"(r[h]) : "f"(y[h]));
-        float d = fmaf(r[h], c.root, c.eps), over;
-        asm("rcp.approx.f32 %0, %1;\n" : "=f"(over) : "f"(d));
-        const float step = x[h] == 0.f ? 0.f : x[h] * over * c.rate;
-        // A value whose gradient (or its square) is not finite stays what it is.
-        const bool fine = fabsf(x[h]) < INFINITY && y[h] < INFINITY;
-        const float moved = fmaf(q[h], c.decay, -step);
-        if (fine) {
-          q[h] = moved;
-        } else {
-          bad = true;
-          x[h] = mo[h], y[h] = vo[h];
-          if (k8) {
-            x[h] = fabsf(x[h]) < INFINITY ? x[h] : 0.f;
-            r[h] = fabsf(old[h]) < INFINITY ? old[h] : 0.f;
-          }
-        }
-        if (k8) mt = fmaxf(mt, fabsf(x[h])), rt = fmaxf(rt, r[h]);
-      }
-      p[k] = f2(q[0], q[1]);
-      m[k] = f2(x[0], x[1]);
-      v[k] = f2(y[0], y[1]);
-      root[k] = f2(r[0], r[1]);
-    }
-    put8(e.p, e.p_type, i, n, vec, p);
-    if (e.copy) {
-      if (e.copy_type == kF16)
-        put8(static_cast<__half*>(e.copy), i, n, vec, p);
-      else
-        put8(static_cast<__nv_bfloat16*>(e.copy), i, n, vec, p);
-    }
-    if constexpr (k8) {
-      float mi, vi;
-      group_scale(mt, ms, mi);
-      group_scale(rt, vs, vi);
-      if (lane == 0) e.ms[i >> 8] = ms, e.vs[i >> 8] = vs;
-      const uint32_t key = c.key + e.place * kMixC + (uint32_t)i * kMixA + (uint32_t)(i >> 32) * kMixC;
-      uint32_t mc[2], vc[2];
+    F2 p[4], g[4];
+    if constexpr (!k8) {
+      F2 m[4], v[4];
+      const Raw mr = get_raw(e.m, true, i, n, vec), vr = get_raw(e.v, true, i, n, vec);
+      const Raw pr = get_raw(e.p, e.p_type == kF32, i, n, vec), gr = get_raw(e.g, e.g_type == kF32, i, n, vec);
+      open_raw(mr, kF32, m);
+      open_raw(vr, kF32, v);
+      open_raw(pr, e.p_type, p);
+      open_raw(gr, e.g_type, g);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float x[2], r[2];
-        split(m[k], x[0], x[1]);
-        split(root[k], r[0], r[1]);
+        float gs[2], ps[2], ms[2], vs[2], root;
+        split(g[k], gs[0], gs[1]);
+        split(p[k], ps[0], ps[1]);
+        split(m[k], ms[0], ms[1]);
+        split(v[k], vs[0], vs[1]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t bits = mix(key + (uint32_t)(2 * k + h) * kMixA);
-          x[h] = copysignf(cut_at_random(fabsf(x[h]) * mi, bits >> 16), x[h]);
-          const float q = r[h] * vi, z = cut_at_random(q, bits & 0xffffu);
-          // A root that is there stays there: nothing is divided by a lost one.
-          r[h] = q > 0.f ? fmaxf(z, 0.001953125f) : 0.f;
-        }
-        const uint32_t a = e4m3_pair(x[0], x[1]), b = e4m3_pair(r[0], r[1]);
-        mc[k >> 1] = k & 1 ? mc[k >> 1] | (a << 16) : a;
-        vc[k >> 1] = k & 1 ? vc[k >> 1] | (b << 16) : b;
+        for (int h = 0; h < 2; ++h) bad |= !step_of(c, gs[h], ps[h], ms[h], vs[h], root);
+        p[k] = f2(ps[0], ps[1]), m[k] = f2(ms[0], ms[1]), v[k] = f2(vs[0], vs[1]);
       }
-      put_codes(e.m, i, n, vec, mc);
-      put_codes(e.v, i, n, vec, vc);
-    } else {
       put8(static_cast<float*>(e.m), i, n, vec, m);
       put8(static_cast<float*>(e.v), i, n, vec, v);
+      put_params(e, i, p);
+    } else {
+      const uint2 mc = get_codes(e.m, i, n, vec), vc = get_codes(e.v, i, n, vec);
+      const float ms = e.ms[i >> 8], vs = e.vs[i >> 8];
+      const Raw pr = get_raw(e.p, e.p_type == kF32, i, n, vec), gr = get_raw(e.g, e.g_type == kF32, i, n, vec);
+      open_raw(pr, e.p_type, p);
+      open_raw(gr, e.g_type, g);
+      F2 m[4], root[4], odd = f2(0.f);
+      open_codes(mc, ms, m);
+      open_codes(vc, vs, root);
+      float mt = 0.f, rt = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const F2 gk = g[k] * c.pgrad;
+        m[k] = fma2(gk, c.pc1, m[k] * c.pb1);
+        float y[2], r[2], d[2], o[2], x[2];
+        split(fma2(gk * gk, c.pc2, root[k] * root[k] * c.pb2), y[0], y[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) asm("sqrt.approx.ftz.f32 %0, %1;\n" : "=f"(r[h]) : "f"(y[h]));
+        root[k] = f2(r[0], r[1]);
+        split(fma2(root[k], c.proot, c.peps), d[0], d[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(o[h]) : "f"(d[h]));
+        p[k] = fma2(m[k] * f2(o[0], o[1]), c.prate, p[k] * c.pdecay);
+        odd = fma2(m[k], f2(0.f), odd);  // not 0 where one is not finite
+        split(m[k], x[0], x[1]);
+        mt = fmaxf(mt, fmaxf(fabsf(x[0]), fabsf(x[1])));
+        rt = fmaxf(rt, fmaxf(r[0], r[1]));
+      }
+      if (__any_sync(0xffffffffu, !(sum(odd) == 0.f && rt < INFINITY))) {
+        bad |= step_of_group(c, e, i);
+      } else {
+        put_params(e, i, p);
+        put_states(c, e, i, mt, rt, m, root);
+      }
     }
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(status, BAKRON_DEV_NONFINITE_GRAD);
 }
 
+__host__ __device__ inline F2 both(float x) {
+  uint32_t u;
+  memcpy(&u, &x, 4);
+  return F2{(unsigned long long)u << 32 | u};
+}
 __host__ __device__ inline AdamConstants constants(double lr, double step, double scale, double b1, double b2, double eps,
                                                    double decay, uint64_t seed) {
   AdamConstants c;
   c.b1 = (float)b1, c.c1 = (float)(1 - b1), c.b2 = (float)b2, c.c2 = (float)(1 - b2);
-  c.eps = (float)eps;
+  // At least the smallest normal number, too small to change a sum with any root
+  // that is not 0: what is divided by is never 0.
+  c.eps = eps > 1.1754943508222875e-38 ? (float)eps : 1.17549435e-38f;
   c.root = (float)(1 / sqrt(1 - pow(b2, step)));
   c.rate = (float)(lr / (1 - pow(b1, step)));
   c.decay = (float)(1 - lr * decay);
   c.grad = (float)scale;
   c.key = (uint32_t)seed * kMixA + (uint32_t)(uint64_t)step * kMixB;
+  c.pb1 = both(c.b1), c.pc1 = both(c.c1), c.pb2 = both(c.b2 * kLarger), c.pc2 = both(c.c2 * kLarger), c.peps = both(c.eps);
+  c.proot = both(c.root / kRootLarger), c.prate = both(-c.rate), c.pdecay = both(c.decay), c.pgrad = both(c.grad);
   return c;
 }
 // Where the step or a factor is on the device.
@@ -325,6 +432,8 @@ cudaError_t adamw_launch(const Adamw& a, const bakron_adamw_tensor* tensors, int
     given = constants(a.lr, (double)a.step, a.scale, a.b1, a.b2, a.eps, a.decay, a.seed);
   }
   const int64_t most = (int64_t)sm_count() * (a.eight ? 4 : 3);
+  auto kernel = a.eight ? (made ? adamw_kernel<true, true> : adamw_kernel<true, false>)
+                        : (made ? adamw_kernel<false, true> : adamw_kernel<false, false>);
   for (int64_t from = 0; from < count && e == cudaSuccess;) {
     AdamList list;
     list.count = 0;
@@ -341,10 +450,7 @@ cudaError_t adamw_launch(const Adamw& a, const bakron_adamw_tensor* tensors, int
     }
     if (list.count == 0) break;
     const unsigned grid = (unsigned)std::min<int64_t>(list.first[list.count], most);
-    if (a.eight)
-      adamw_kernel<true><<<grid, kAdamThreads, 0, stream>>>(list, given, made, a.skip, status);
-    else
-      adamw_kernel<false><<<grid, kAdamThreads, 0, stream>>>(list, given, made, a.skip, status);
+    kernel<<<grid, kAdamThreads, 0, stream>>>(list, given, made, a.skip, status);
     e = cudaGetLastError();
   }
   return e;

@@ -16,7 +16,7 @@
 // token are computed once, into shared memory, for its 40 or so heads.
 //
 // An angle is kept as a share of a turn in 64-bit fixed point: p f / 2 pi
-// modulo 1 is then one integer product, exact to p 2^-54 turns for any
+// modulo 1 is then one integer product, exact to |p f| 2^-54 turns for any
 // position, where fp32 would be off by a tenth of a turn from 10^6 on and fp64
 // runs at 1/64 of the fp32 rate.
 #include <algorithm>
@@ -33,9 +33,10 @@ constexpr int kHeadBlocks = 4 * 152;  // of the backward pass: four on each SM
 
 // The frequency f as a share of a turn for each position, 2^-64 of it.
 __device__ __forceinline__ uint64_t turn_of(double f) {
-  const double t = f * 0.15915494309189533577;  // 1 / 2 pi
-  const double part = t - floor(t);             // in [0, 1], 1 by rounding where t is just below a whole number
-  return part < 1.0 ? (uint64_t)(part * 18446744073709551616.0) : 0ull;
+  const double t = fabs(f) * 0.15915494309189533577;  // 1 / 2 pi
+  const double part = t - floor(t);                   // exact
+  const uint64_t share = part < 1.0 ? (uint64_t)(part * 18446744073709551616.0) : 0ull;  // 0 for a NaN
+  return f < 0.0 ? 0ull - share : share;
 }
 // cos and sin of 2 pi times the share: the nearest quarter turn is taken off
 // in integers, so that what is converted to fp32 is at most an eighth of a turn.
