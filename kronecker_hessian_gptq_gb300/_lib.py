@@ -98,6 +98,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_marshal = None
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -122,6 +123,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def load_marshal():
+    """The helper that reads lists of torch tensors (torch has to be imported first), loaded once.  Its calls hold
+    the interpreter's lock."""
+    global _marshal
+    if _marshal is None:
+        path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_marshal.so not found at {path}: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        lib = ctypes.PyDLL(path)
+        lib.bakron_py_adamw_tensors.restype = _int
+        lib.bakron_py_adamw_tensors.argtypes = [ctypes.py_object] * 7 + [_i64, _int, _vp]
+        _marshal = lib
+    return _marshal
 
 
 def check(status: int, what: str) -> None:

@@ -15,6 +15,7 @@ import struct
 
 import torch
 
+from . import _lib
 from ._layers import (_BYTES, _CODES, _F32, _call, _empty, _entry, _like, _matrix, _names, _on, _stream_on, _vector)
 
 _E4M3 = torch.float8_e4m3fn
@@ -303,6 +304,27 @@ def _number(x, name, dtype, device):
     return 1, x.data_ptr()
 
 
+def _pack(packed, params, lists, eight, device):
+    """The tensors' list for the C ABI, one attribute after another, with what is wrong with them."""
+    for name, l in lists.items():
+        if len(l) != len(params):
+            raise ValueError(f"{name} must have {len(params)} tensors, as params")
+    kinds = (_E4M3,) if eight else (_F32,)
+    for i, p in enumerate(params):
+        pp = _dense(p, "params", i, _CODES, p.numel() if isinstance(p, torch.Tensor) else 0, device)
+        n = p.numel()
+        g = lists["grads"][i]
+        gp = _dense(g, "grads", i, _CODES, n, device)
+        mp, vp = (_dense(lists[k][i], k, i, kinds, n, device) for k in "mv")
+        ms = vs = cp = ct = 0
+        if eight:
+            ms, vs = (_dense(lists[k][i], k, i, (_F32,), _ceil(n, _GROUP), device) for k in ("m_scales", "v_scales"))
+        c = lists["copies"][i] if "copies" in lists else None
+        if c is not None:
+            cp, ct = _dense(c, "copies", i, (torch.float16, torch.bfloat16), n, device), _CODES[c.dtype]
+        _TENSOR.pack_into(packed, i * _TENSOR.size, pp, gp, mp, vp, ms, vs, cp, n, _CODES[p.dtype], _CODES[g.dtype], ct)
+
+
 def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=1.0,
           copies=None, skip=None, seed=0, stream=None):
     """One AdamW step over all of params, in place (bakron_adamw).
@@ -329,32 +351,15 @@ def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, we
     if not params or not isinstance(params[0], torch.Tensor) or not params[0].is_cuda:
         raise ValueError("params must be CUDA tensors, at least one")
     device, at = params[0].get_device(), params[0].device
-    m, v = states["m"], states["v"]
+    lists = {"grads": grads, **{k: list(l) for k, l in states.items()}}
+    if copies is not None:
+        lists["copies"] = list(copies)
     count = len(params)
     eight = "m_scales" in states
-    kinds = (_E4M3,) if eight else (_F32,)
-    lists = {"grads": grads, **states}
-    if copies is not None:
-        lists["copies"] = copies
-    for name, l in lists.items():
-        if len(l) != count:
-            raise ValueError(f"{name} must have {count} tensors, as params")
-    packed = bytearray(count * _TENSOR.size)
-    for i in range(count):
-        p, g = params[i], grads[i]
-        n = p.numel()
-        pp = _dense(p, "params", i, _CODES, n, device)
-        gp = _dense(g, "grads", i, _CODES, n, device)
-        mp, vp = _dense(m[i], "m", i, kinds, n, device), _dense(v[i], "v", i, kinds, n, device)
-        ms = vs = cp = ct = 0
-        if eight:
-            groups = _ceil(n, _GROUP)
-            ms = _dense(states["m_scales"][i], "m_scales", i, (_F32,), groups, device)
-            vs = _dense(states["v_scales"][i], "v_scales", i, (_F32,), groups, device)
-        if copies is not None and copies[i] is not None:
-            cp = _dense(copies[i], "copies", i, (torch.float16, torch.bfloat16), n, device)
-            ct = _CODES[copies[i].dtype]
-        _TENSOR.pack_into(packed, i * _TENSOR.size, pp, gp, mp, vp, ms, vs, cp, n, _CODES[p.dtype], _CODES[g.dtype], ct)
+    packed = ctypes.create_string_buffer(count * _TENSOR.size)
+    if _lib.load_marshal().bakron_py_adamw_tensors(params, grads, lists["m"], lists["v"], lists.get("m_scales"), lists.get("v_scales"),
+                                                   lists.get("copies"), count, device, packed):
+        _pack(packed, params, lists, eight, device)
     rate, rate_dev = _number(lr, "lr", _F32, device)
     number, step_dev = _number(step, "step", torch.int64, device)
     scale, scale_dev = _number(grad_scale, "grad_scale", _F32, device)
@@ -366,7 +371,7 @@ def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, we
     status = _empty(1, dtype=torch.int32, device=at)
     nbytes = _entry("bakron_adamw_workspace_size")()
     ws = _empty(nbytes, dtype=torch.uint8, device=at)
-    _call("bakron_adamw", (ctypes.c_char * len(packed)).from_buffer(packed), count, 8 if eight else 32, rate, rate_dev, number,
+    _call("bakron_adamw", packed, count, 8 if eight else 32, rate, rate_dev, number,
           step_dev, betas[0], betas[1], eps, weight_decay, scale, scale_dev, stop, seed & 0xFFFFFFFFFFFFFFFF, ws.data_ptr(),
           nbytes, status.data_ptr(), _stream_on(device))
     return status

@@ -2,16 +2,20 @@
 
 The translation units under csrc/ compile in parallel to objects in
 _build/, then link into kronecker_hessian_gptq_gb300/libbakron.so.  A build
-is skipped when the library is newer than every source and header.
+is skipped when the library is newer than every source and header.  Beside it
+_marshal.so (csrc/marshal.cpp, g++, against torch's own headers) turns lists of
+torch tensors into what the C ABI takes.
 """
 
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbakron.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
@@ -36,15 +41,23 @@ def sources() -> list:
 
 
 def _inputs() -> list:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (sources() + [os.path.join(CSRC, "marshal.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + [os.path.join(INCLUDE, "bakron.h"), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _marshal_command(out: str) -> list:
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    return [cxx, "-O1", "-std=c++17", "-shared", "-fPIC", os.path.join(CSRC, "marshal.cpp"), "-o", out, "-I", INCLUDE,
+            "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -63,6 +76,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    procs.append((MARSHAL, subprocess.Popen(_marshal_command(MARSHAL + ".tmp"), stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                            text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -71,9 +86,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB + ".tmp"
     subprocess.run([nvcc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"], check=True)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     os.replace(tmp, LIB)
     return LIB
 

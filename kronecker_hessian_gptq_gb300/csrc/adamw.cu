@@ -10,7 +10,7 @@
 // read once (28 bytes a value in fp32; 16 with 8-bit states, 16-bit gradients
 // and 16-bit copies).  A thread takes 8 values, a warp the 256 that share a
 // scale; blocks walk over units of 2048 values of all tensors, whose addresses
-// come in the kernel's parameters, so that a launch takes up to 128 tensors
+// come in the kernel's parameters, so that a launch takes up to 384 tensors
 // and a captured one keeps them.  Statistics, sums and the update are fp32.
 // 235 million values: 1054 us in fp32 (6.2 TB/s), 660 us with 8-bit states, fp32
 // masters, bf16 gradients and copies (5.7 TB/s), which issues 72 instructions a
@@ -23,6 +23,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "bakron.h"
 #include "elem.cuh"
@@ -33,7 +35,8 @@ namespace {
 
 constexpr int kAdamThreads = 256;
 constexpr int kAdamUnit = kAdamThreads * 8;
-constexpr int kAdamList = 128;  // tensors of a launch
+// Tensors of a launch: a short list, or as many as a kernel's parameters have room for.
+constexpr int kAdamShort = 24, kAdamLong = 384;
 
 // Squares are kept 2^48 times as large where states have 8 bits: none is then
 // subnormal, which the approximate square root would take for 0, and those that
@@ -56,9 +59,10 @@ struct AdamEntry {
   uint8_t p_type, g_type, copy_type, vec;
   uint32_t place;  // in the call's list
 };
+template <int kMost>
 struct AdamList {
-  AdamEntry e[kAdamList];
-  int64_t first[kAdamList + 1];  // units before each tensor
+  AdamEntry e[kMost];
+  int64_t first[kMost + 1];  // units before each tensor
   int count;
 };
 
@@ -294,9 +298,9 @@ __device__ __noinline__ bool step_of_group(const AdamConstants& c, const AdamEnt
 }
 
 // kMade: the constants come from device memory.
-template <bool k8, bool kMade>
+template <bool k8, bool kMade, int kMost>
 __global__ void __launch_bounds__(kAdamThreads, k8 ? 4 : 3)
-    adamw_kernel(const __grid_constant__ AdamList list, const __grid_constant__ AdamConstants given, const AdamConstants* made,
+    adamw_kernel(const __grid_constant__ AdamList<kMost> list, const __grid_constant__ AdamConstants given, const AdamConstants* made,
                  const int32_t* skip, int32_t* status) {
   if (skip && *skip) return;
   const AdamConstants c = kMade ? *made : given;
@@ -420,25 +424,33 @@ int sm_count() {
 
 size_t adamw_workspace_bytes() { return 256; }
 
-cudaError_t adamw_launch(const Adamw& a, const bakron_adamw_tensor* tensors, int64_t count, void* ws, int32_t* status,
-                         cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(status, 0, 4, stream);
-  AdamConstants* made = nullptr;
-  AdamConstants given = {};
-  if (a.lr_dev || a.step_dev || a.scale_dev) {
-    made = static_cast<AdamConstants*>(ws);
-    if (e == cudaSuccess) adamw_constants_kernel<<<1, 1, 0, stream>>>(a, made);
-  } else {
-    given = constants(a.lr, (double)a.step, a.scale, a.b1, a.b2, a.eps, a.decay, a.seed);
+bool adamw_all_different(const bakron_adamw_tensor* tensors, int64_t count) {
+  std::unique_ptr<const void*[]> all(new (std::nothrow) const void*[4 * count + 1]);
+  if (!all) return false;
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const bakron_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    all[n++] = t.param, all[n++] = t.m, all[n++] = t.v;
+    if (t.copy) all[n++] = t.copy;
   }
+  std::sort(all.get(), all.get() + n);
+  return std::adjacent_find(all.get(), all.get() + n) == all.get() + n;
+}
+
+namespace {
+
+template <int kMost>
+cudaError_t launch_lists(const Adamw& a, const bakron_adamw_tensor* tensors, int64_t count, const AdamConstants& given,
+                         const AdamConstants* made, int32_t* status, cudaStream_t stream) {
   const int64_t most = (int64_t)sm_count() * (a.eight ? 4 : 3);
-  auto kernel = a.eight ? (made ? adamw_kernel<true, true> : adamw_kernel<true, false>)
-                        : (made ? adamw_kernel<false, true> : adamw_kernel<false, false>);
-  for (int64_t from = 0; from < count && e == cudaSuccess;) {
-    AdamList list;
+  auto kernel = a.eight ? (made ? adamw_kernel<true, true, kMost> : adamw_kernel<true, false, kMost>)
+                        : (made ? adamw_kernel<false, true, kMost> : adamw_kernel<false, false, kMost>);
+  for (int64_t from = 0; from < count;) {
+    AdamList<kMost> list;
     list.count = 0;
     list.first[0] = 0;
-    for (; from < count && list.count < kAdamList; ++from) {
+    for (; from < count && list.count < kMost; ++from) {
       const bakron_adamw_tensor& t = tensors[from];
       if (t.n == 0) continue;
       bool vec = true;
@@ -451,9 +463,30 @@ cudaError_t adamw_launch(const Adamw& a, const bakron_adamw_tensor* tensors, int
     if (list.count == 0) break;
     const unsigned grid = (unsigned)std::min<int64_t>(list.first[list.count], most);
     kernel<<<grid, kAdamThreads, 0, stream>>>(list, given, made, a.skip, status);
-    e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
   }
-  return e;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t adamw_launch(const Adamw& a, const bakron_adamw_tensor* tensors, int64_t count, void* ws, int32_t* status,
+                         cudaStream_t stream) {
+  cudaError_t e = cudaMemsetAsync(status, 0, 4, stream);
+  if (e != cudaSuccess) return e;
+  AdamConstants* made = nullptr;
+  AdamConstants given = {};
+  if (a.lr_dev || a.step_dev || a.scale_dev) {
+    made = static_cast<AdamConstants*>(ws);
+    adamw_constants_kernel<<<1, 1, 0, stream>>>(a, made);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  } else {
+    given = constants(a.lr, (double)a.step, a.scale, a.b1, a.b2, a.eps, a.decay, a.seed);
+  }
+  return count <= kAdamShort ? launch_lists<kAdamShort>(a, tensors, count, given, made, status, stream)
+                             : launch_lists<kAdamLong>(a, tensors, count, given, made, status, stream);
 }
 
 }  // namespace bakron

@@ -12,8 +12,12 @@
 // once.  A team of D / 16 lanes (rounded up to a power of two) holds a head,
 // 16 values a lane in two runs of 8, so that both values of a pair are the
 // same lane's, and a head's sums take three exchanges for D = 128.  A block
-// takes a tile of up to eight tokens with all their heads: the angles of a
-// token are computed once, into shared memory, for its 40 or so heads.
+// takes a tile of tokens: their angles are computed once, into shared memory, for
+// the 40 or so heads, and a team keeps to one token and goes from head to head.
+// The next heads' values are on their way meanwhile.  bf16, 32 and 8 heads of 128:
+// 16384 tokens take 64 us (5.2 TB/s), backward 116 us (4.3 TB/s; with three blocks on
+// an SM in place of two, and so 80 registers and spills, 136).  What
+// is not in such runs, or not on 16 bytes, takes a warp a head.
 //
 // An angle is kept as a share of a turn in 64-bit fixed point: p f / 2 pi
 // modulo 1 is then one integer product, exact to |p f| 2^-54 turns for any
@@ -29,7 +33,9 @@ namespace {
 
 constexpr int kHeadThreads = 256;
 constexpr int kHeadTile = 8;  // tokens of a tile at most, a power of two
-constexpr int kHeadBlocks = 4 * 152;  // of the backward pass: four on each SM
+constexpr int kHeadBlocks = 4 * 152;  // forward: four on each SM
+constexpr int kBackBlocks = 4 * 152;  // backward: at most
+constexpr int kBackTile = 32;
 
 // The frequency f as a share of a turn for each position, 2^-64 of it.
 __device__ __forceinline__ uint64_t turn_of(double f) {
@@ -57,25 +63,34 @@ struct Angles {
   float *cos, *sin;
   int pitch;
   static __host__ __device__ int pitch_of(int half) { return (half + 7) / 8 * 8; }
-  static __host__ __device__ size_t bytes(int half) { return (size_t)pitch_of(half) * (8 + 2 * 4 * kHeadTile); }
-  __device__ explicit Angles(unsigned char* smem, int half) : pitch(pitch_of(half)) {
+  static __host__ __device__ size_t bytes(int half, int tile) { return (size_t)pitch_of(half) * (8 + 2 * 4 * tile); }
+  // Where the angle of frequency k lies in its row: the first four of each eight,
+  // then the last four of each, so that neighbouring lanes' 16 bytes are neighbours.
+  __device__ __forceinline__ int place(int k) const { return (k >> 2 & 1) * (pitch / 2) + (k >> 3) * 4 + (k & 3); }
+  __device__ Angles(unsigned char* smem, int half, int tile) : pitch(pitch_of(half)) {
     turn = reinterpret_cast<uint64_t*>(smem);
     cos = reinterpret_cast<float*>(smem + 8 * pitch);
-    sin = cos + pitch * kHeadTile;
+    sin = cos + pitch * tile;
   }
 };
-// A frequency that is not finite turns nothing into numbers.
+// A frequency that is not finite turns nothing into numbers.  A thread keeps to
+// one frequency, or a few, and walks over the tokens.
 __device__ __forceinline__ void fill_turns(const HeadNorm& p, const Angles& a) {
   for (int i = threadIdx.x; i < p.half; i += kHeadThreads) a.turn[i] = turn_of(p.freqs[i]);
 }
 __device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, int64_t t0, int tokens) {
-  for (int i = threadIdx.x; i < tokens * p.half; i += kHeadThreads) {
-    const int t = i / p.half, k = i - t * p.half;
-    float c, s;
-    cos_sin((uint64_t)p.positions[t0 + t] * a.turn[k], c, s);
-    if (!isfinite(p.freqs[k])) c = s = __int_as_float(0x7fffffff);
-    a.cos[t * a.pitch + k] = c;
-    a.sin[t * a.pitch + k] = s;
+  const int wide = p.half < kHeadThreads ? p.half : kHeadThreads, rows = kHeadThreads / wide;
+  const int row = threadIdx.x / wide, col = threadIdx.x - row * wide;
+  if (row >= rows) return;
+  for (int k = col; k < p.half; k += wide) {
+    const uint64_t turn = a.turn[k];
+    const bool finite = isfinite(p.freqs[k]);
+    for (int t = row; t < tokens; t += rows) {
+      float c, s;
+      cos_sin((uint64_t)p.positions[t0 + t] * turn, c, s);
+      a.cos[t * a.pitch + a.place(k)] = finite ? c : __int_as_float(0x7fffffff);
+      a.sin[t * a.pitch + a.place(k)] = finite ? s : __int_as_float(0x7fffffff);
+    }
   }
 }
 
@@ -115,36 +130,44 @@ __device__ __forceinline__ Place place_of(int j, int rotated) {
   return Place{16 * j, 16 * j + 8, 8 * j};
 }
 
+// Eight angles' cosines or sines from a row of Angles, from the first of an eight on.
+__device__ __forceinline__ void load_angles(const float* row, int angle, int pitch, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(row + angle / 2), b = *reinterpret_cast<const float4*>(row + angle / 2 + pitch / 2);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
 // Turns a lane's pairs by their angles, or back (kBack).
 template <bool kNeighbours, bool kBack>
-__device__ __forceinline__ void turn_pairs(F2 (&a)[4], F2 (&b)[4], const float* cos, const float* sin, int angle, int half) {
+__device__ __forceinline__ void turn_pairs(F2 (&a)[4], F2 (&b)[4], const float* cos, const float* sin, int angle, int half, int pitch) {
+  if (angle >= half) return;
+  float c[8], s[8];
+  load_angles(cos, angle, pitch, c);
+  load_angles(sin, angle, pitch, s);
   if (!kNeighbours) {
-    if (angle >= half) return;
-    F2 c[4], s[4];
-    load_f2(cos + angle, c);
-    load_f2(sin + angle, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const F2 minus = f2(-1.f) * s[i];
+      const F2 cc = f2(c[2 * i], c[2 * i + 1]), ss = f2(s[2 * i], s[2 * i + 1]), minus = f2(-s[2 * i], -s[2 * i + 1]);
       const F2 x = a[i], y = b[i];
-      a[i] = fma2(y, kBack ? s[i] : minus, x * c[i]);
-      b[i] = fma2(x, kBack ? minus : s[i], y * c[i]);
+      a[i] = fma2(y, kBack ? ss : minus, x * cc);
+      b[i] = fma2(x, kBack ? minus : ss, y * cc);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (angle + i >= half) break;
-      const float c = cos[angle + i], s = kBack ? -sin[angle + i] : sin[angle + i];
       F2& v = i < 4 ? a[i & 3] : b[i & 3];
       float x, y;
       split(v, x, y);
-      v = f2(fmaf(-y, s, x * c), fmaf(x, s, y * c));
+      v = kBack ? f2(fmaf(y, s[i], x * c[i]), fmaf(-x, s[i], y * c[i])) : f2(fmaf(-y, s[i], x * c[i]), fmaf(x, s[i], y * c[i]));
     }
   }
 }
 
 __device__ __forceinline__ float team_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    if (o >= lanes) break;
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
 }
 __device__ __forceinline__ float squares(const F2 (&a)[4], const F2 (&b)[4]) {
@@ -156,82 +179,75 @@ __device__ __forceinline__ float squares(const F2 (&a)[4], const F2 (&b)[4]) {
   return sum(q);
 }
 
-// Two heads of a team are on their way at a time.
+// A team takes one token of the tile and every `step`-th of its heads, so that
+// it goes from head to head by adding strides; two heads are on their way at a time.
 template <class T, bool kNeighbours>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_kernel(const __grid_constant__ HeadNorm p, int tile, int lanes) {
+__global__ void __launch_bounds__(kHeadThreads, sizeof(T) == 2 ? 4 : 3)
+    head_norm_kernel(const __grid_constant__ HeadNorm p, int tile_log, int lanes) {
   extern __shared__ __align__(16) unsigned char head_smem[];
-  const Angles angles(head_smem, p.half);
-  const int64_t t0 = (int64_t)blockIdx.x * tile;
+  const int tile = 1 << tile_log;
+  const Angles angles(head_smem, p.half, tile);
+  const int64_t t0 = (int64_t)blockIdx.x << tile_log;
   const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
-  const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, teams = kHeadThreads / lanes;
-  const bool mine = 16 * j < p.D;
+  const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, each = (kHeadThreads / lanes) >> tile_log;
+  const int t = team & (tile - 1), slot = team >> tile_log, step = each * gridDim.y;
+  const bool live = 16 * j < p.D && t < tokens;
   const Place at = place_of<kNeighbours>(j, 2 * p.half);
-  const float each = 1.f / (float)p.D;
-  const int units = (p.side[0].heads + p.side[1].heads) * tile, step = teams * gridDim.y;
-  Raw8<T> lo[2], hi[2];
-  auto side_of = [&](int u, int& h) {
-    h = u / tile;  // a power of two
-    const int k = h >= p.side[0].heads;
-    if (k) h -= p.side[0].heads;
-    return k;
+  const float share = 1.f / (float)p.D;
+  const int queries = p.side[0].heads, heads = queries + p.side[1].heads;
+  const T* xq = static_cast<const T*>(p.side[0].x) + (t0 + t) * p.side[0].x_token;
+  const T* xk = static_cast<const T*>(p.side[1].x) + (t0 + t) * p.side[1].x_token;
+  T* yq = static_cast<T*>(p.side[0].y) + (t0 + t) * queries * p.D;
+  T* yk = static_cast<T*>(p.side[1].y) + (t0 + t) * (heads - queries) * p.D;
+  Raw8<T> lo[2] = {}, hi[2] = {};
+  auto fetch = [&](int h, int n) {
+    if (!live || h >= heads) return;  // what is there is not used, or zeros behind a head's end
+    const T* x = h < queries ? xq + h * p.side[0].x_head : xk + (h - queries) * p.side[1].x_head;
+    load8(x + at.lo, lo[n]);
+    load8(x + at.hi, hi[n]);
   };
-  auto fetch = [&](int u, int n) {
-    const int t = u & (tile - 1);
-    if (u < units && t < tokens && mine) {
-      int h;
-      const int k = side_of(u, h);
-      const HeadSide& s = p.side[k];
-      const T* x = static_cast<const T*>(s.x) + (t0 + t) * s.x_token + h * s.x_head;
-      load8(x + at.lo, lo[n]);
-      load8(x + at.hi, hi[n]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2 * (int)sizeof(T); ++i) lo[n].w[i] = hi[n].w[i] = 0;
-    }
-  };
-  int u = (int)blockIdx.y * teams + team;
-  fetch(u, 0);
-  fetch(u + step, 1);
+  int h = (int)blockIdx.y * each + slot;
+  fetch(h, 0);
+  fetch(h + step, 1);
   if (p.half) {
     fill_turns(p, angles);
     __syncthreads();
     fill_angles(p, angles, t0, tokens);
     __syncthreads();
   }
+  const float *cos = angles.cos + t * angles.pitch, *sin = angles.sin + t * angles.pitch;
   // All teams take the same number of turns: the exchanges are the whole warp's.
-  for (int base = (int)blockIdx.y * teams; base < units; base += 2 * step, u += 2 * step) {
+  for (int base = (int)blockIdx.y * each; base < heads; base += 2 * step, h += 2 * step) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const int v = u + n * step;
+      const int here = h + n * step;
       F2 a[4], b[4];
       open8<T>(lo[n], a);
       open8<T>(hi[n], b);
-      fetch(v + 2 * step, n);
-      const int t = v & (tile - 1);
-      int h;
-      const int k = side_of(v, h);
-      const HeadSide& s = p.side[k];
-      const float r = __frsqrt_rn(fmaf(team_sum(squares(a, b), lanes), each, p.eps));
-      if (v >= units || t >= tokens || !mine) continue;
-      if (s.w) {
+      fetch(here + 2 * step, n);
+      const bool query = here < queries;
+      const float* weight = query ? p.side[0].w : p.side[1].w;
+      const float r = rsqrtf(fmaf(team_sum(squares(a, b), lanes), share, p.eps));
+      if (!live || here >= heads) continue;
+      if (weight) {
         F2 w[4];
-        load_f2(s.w + at.lo, w);
+        load_f2(weight + at.lo, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = a[i] * f2(r) * w[i];
-        load_f2(s.w + at.hi, w);
+        load_f2(weight + at.hi, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) b[i] = b[i] * f2(r) * w[i];
       }
-      turn_pairs<kNeighbours, false>(a, b, angles.cos + t * angles.pitch, angles.sin + t * angles.pitch, at.angle, p.half);
-      T* y = static_cast<T*>(s.y) + ((t0 + t) * s.heads + h) * p.D;
+      turn_pairs<kNeighbours, false>(a, b, cos, sin, at.angle, p.half, angles.pitch);
+      T* y = query ? yq + here * p.D : yk + (here - queries) * p.D;
       store8(y + at.lo, a);
       store8(y + at.hi, b);
     }
   }
 }
 
-// Any sizes, strides and alignment: a warp for each head, which reads it
-// twice.  Pair i of the head (i < half), then its single values.
+// Any sizes, strides and alignment: a warp for each head.  Pair i of the head
+// (i < half), then its single values.
 __device__ __forceinline__ void pair_at(const HeadNorm& p, int i, int& a, int& b) {
   if (i >= p.half) {
     a = b = p.half + i;
@@ -242,49 +258,86 @@ __device__ __forceinline__ void pair_at(const HeadNorm& p, int i, int& a, int& b
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_any_kernel(const __grid_constant__ HeadNorm p, int tile) {
+// kN: a lane holds its kN pairs (there are 32 kN at most), and the next head's
+// are on their way; 0: it reads them again.
+template <class T, int kN>
+__global__ void __launch_bounds__(kHeadThreads) head_norm_any_kernel(const __grid_constant__ HeadNorm p, int tile_log) {
   extern __shared__ __align__(16) unsigned char head_smem[];
-  const Angles angles(head_smem, p.half);
-  const int64_t t0 = (int64_t)blockIdx.x * tile;
+  const int tile = 1 << tile_log;
+  const Angles angles(head_smem, p.half, tile);
+  const int64_t t0 = (int64_t)blockIdx.x << tile_log;
   const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, queries = p.side[0].heads, heads = queries + p.side[1].heads;
+  const int t = warp & (tile - 1), each = (kHeadThreads / 32) >> tile_log, step = each * gridDim.y, D = p.D, pairs = D - p.half;
+  auto input = [&](int h) {
+    const HeadSide& s = p.side[h >= queries];
+    return static_cast<const T*>(s.x) + (t0 + t) * s.x_token + (h < queries ? h : h - queries) * s.x_head;
+  };
+  constexpr int kRoom = kN ? kN : 1;
+  T na[kRoom], nb[kRoom];
+  auto fetch = [&](int h) {
+    if (t >= tokens || h >= heads) return;
+    const T* x = input(h);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int i = lane + 32 * n;
+      int a, b;
+      pair_at(p, i, a, b);
+      na[n] = i < pairs ? x[a] : from_f32<T>(0.f);
+      nb[n] = i < p.half ? x[b] : from_f32<T>(0.f);
+    }
+  };
+  int h = (int)blockIdx.y * each + (warp >> tile_log);
+  if (kN) fetch(h);
   if (p.half) {
     fill_turns(p, angles);
     __syncthreads();
     fill_angles(p, angles, t0, tokens);
     __syncthreads();
   }
-  const int lane = threadIdx.x & 31, heads = p.side[0].heads + p.side[1].heads, D = p.D, pairs = D - p.half;
-  const int warps = kHeadThreads / 32;
-  for (int u = (int)blockIdx.y * warps + (threadIdx.x >> 5); u < heads * tile; u += warps * gridDim.y) {
-    const int t = u & (tile - 1);
-    int h = u / tile;
-    if (t >= tokens) continue;
-    const int k = h >= p.side[0].heads;
-    if (k) h -= p.side[0].heads;
-    const HeadSide& s = p.side[k];
-    const T* x = static_cast<const T*>(s.x) + (t0 + t) * s.x_token + h * s.x_head;
-    T* y = static_cast<T*>(s.y) + ((t0 + t) * s.heads + h) * D;
-    float r = 1.f;
-    if (s.w) {
-      float q = 0.f;
-      for (int i = lane; i < D; i += 32) {
-        const float v = to_f32<T>(x[i]);
-        q = fmaf(v, v, q);
-      }
-      r = __frsqrt_rn(fmaf(warp_reduce(q, SumOp()), 1.f / (float)D, p.eps));
+  if (t >= tokens) return;
+  const float *cos = angles.cos + t * angles.pitch, *sin = angles.sin + t * angles.pitch;
+  auto write = [&](T* y, int i, float va, float vb, float r, const float* w) {
+    int a, b;
+    pair_at(p, i, a, b);
+    if (w) va = va * r * w[a], vb = vb * r * w[b];
+    if (i < p.half) {
+      const float c = cos[angles.place(i)], z = sin[angles.place(i)];
+      y[a] = from_f32<T>(fmaf(-vb, z, va * c));
+      y[b] = from_f32<T>(fmaf(va, z, vb * c));
+    } else {
+      y[a] = from_f32<T>(va);
     }
-    for (int i = lane; i < pairs; i += 32) {
-      int a, b;
-      pair_at(p, i, a, b);
-      float va = to_f32<T>(x[a]), vb = to_f32<T>(x[b]);
-      if (s.w) va = va * r * s.w[a], vb = vb * r * s.w[b];
-      if (i < p.half) {
-        const float c = angles.cos[t * angles.pitch + i], z = angles.sin[t * angles.pitch + i];
-        y[a] = from_f32<T>(fmaf(-vb, z, va * c));
-        y[b] = from_f32<T>(fmaf(va, z, vb * c));
-      } else {
-        y[a] = from_f32<T>(va);
+  };
+  for (; h < heads; h += step) {
+    const HeadSide& s = p.side[h >= queries];
+    T* y = static_cast<T*>(s.y) + ((t0 + t) * s.heads + (h < queries ? h : h - queries)) * D;
+    float r = 1.f, q = 0.f;
+    if constexpr (kN > 0) {
+      float va[kN], vb[kN];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        va[n] = to_f32<T>(na[n]), vb[n] = to_f32<T>(nb[n]);
+        q = fmaf(va[n], va[n], fmaf(vb[n], vb[n], q));
+      }
+      fetch(h + step);
+      if (s.w) r = rsqrtf(fmaf(warp_reduce(q, SumOp()), 1.f / (float)D, p.eps));
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+        if (lane + 32 * n < pairs) write(y, lane + 32 * n, va[n], vb[n], r, s.w);
+    } else {
+      const T* x = input(h);
+      if (s.w) {
+        for (int i = lane; i < D; i += 32) {
+          const float v = to_f32<T>(x[i]);
+          q = fmaf(v, v, q);
+        }
+        r = rsqrtf(fmaf(warp_reduce(q, SumOp()), 1.f / (float)D, p.eps));
+      }
+      for (int i = lane; i < pairs; i += 32) {
+        int a, b;
+        pair_at(p, i, a, b);
+        write(y, i, to_f32<T>(x[a]), to_f32<T>(x[b]), r, s.w);
       }
     }
   }
@@ -292,212 +345,298 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_any_kernel(const __gri
 
 // ------------------------------------------------------------ backward
 
-// Weight gradients of a block: D floats for queries, D for keys, in `parts`.
+// The blocks are shared out between queries and keys: the first blocks[0] walk
+// over the queries' tiles, the others over the keys', which have tiles of their
+// own.  So a block sums one weight's gradient, in registers, and leaves D
+// floats in `parts`.
+struct HeadPlan {
+  int tile_log[2], blocks[2];
+  int64_t tiles[2];
+};
+
 template <class T, bool kNeighbours>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_backward_kernel(const __grid_constant__ HeadNorm p, int tile, int lanes,
-                                                                          int64_t tiles, float* parts) {
+__global__ void __launch_bounds__(kHeadThreads, 2)
+    head_norm_backward_kernel(const __grid_constant__ HeadNorm p, const __grid_constant__ HeadPlan plan, int lanes, float* parts) {
   extern __shared__ __align__(16) unsigned char head_smem[];
-  const Angles angles(head_smem, p.half);
-  const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, teams = kHeadThreads / lanes;
-  const bool mine = 16 * j < p.D;
+  const int k = (int)blockIdx.x >= plan.blocks[0], tile_log = plan.tile_log[k], tile = 1 << tile_log;
+  const HeadSide& s = p.side[k];
+  const Angles angles(head_smem, p.half, tile);
+  const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, step = (kHeadThreads / lanes) >> tile_log;
+  const int t = team & (tile - 1), slot = team >> tile_log, heads = s.heads;
+  const bool mine = 16 * j < p.D, normed = s.w;
   const Place at = place_of<kNeighbours>(j, 2 * p.half);
-  const float each = 1.f / (float)p.D;
-  F2 dw[2][8];
+  const float share = 1.f / (float)p.D;
+  const int64_t tiles = plan.tiles[k];
+  const int stride = plan.blocks[k];
+  int64_t q = k ? (int)blockIdx.x - plan.blocks[0] : (int)blockIdx.x;
+  const T *dy = static_cast<const T*>(s.dy), *xs = static_cast<const T*>(s.x);
+  Raw8<T> raw[4] = {};
+  auto fetch = [&](int64_t q, int h) {
+    const int64_t token = (q << tile_log) + t;
+    if (!mine || token >= p.T || h >= heads) return;  // what is there is not used, or zeros behind a head's end
+    const T* d = dy + token * s.dy_token + h * s.dy_head;
+    load8(d + at.lo, raw[0]);
+    load8(d + at.hi, raw[1]);
+    if (normed) {
+      const T* v = xs + token * s.x_token + h * s.x_head;
+      load8(v + at.lo, raw[2]);
+      load8(v + at.hi, raw[3]);
+    }
+  };
+  F2 dw[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dw[i >> 3][i & 7] = f2(0.f);
+  for (int i = 0; i < 8; ++i) dw[i] = f2(0.f);
+  fetch(q, slot);
   if (p.half) fill_turns(p, angles);
-  for (int64_t q = blockIdx.x; q < tiles; q += gridDim.x) {
-    const int64_t t0 = q * tile;
+  const float *cos = angles.cos + t * angles.pitch, *sin = angles.sin + t * angles.pitch;
+  for (; q < tiles; q += stride) {
+    const int64_t t0 = q << tile_log;
     const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
     if (p.half) {
       __syncthreads();
       fill_angles(p, angles, t0, tokens);
       __syncthreads();
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const HeadSide& s = p.side[k];
-      const int units = s.heads * tile;
-      for (int base = 0; base < units; base += teams) {
-        const int u = base + team, t = u & (tile - 1), h = u / tile;
-        const bool live = u < units && t < tokens && mine;
-        F2 g[8], x[8];
-        F2(&ga)[4] = *reinterpret_cast<F2(*)[4]>(g), (&gb)[4] = *reinterpret_cast<F2(*)[4]>(g + 4);
-        F2(&xa)[4] = *reinterpret_cast<F2(*)[4]>(x), (&xb)[4] = *reinterpret_cast<F2(*)[4]>(x + 4);
-        if (live) {
-          const T* d = static_cast<const T*>(s.dy) + (t0 + t) * s.dy_token + h * s.dy_head;
-          Raw8<T> raw[4];
-          load8(d + at.lo, raw[0]);
-          load8(d + at.hi, raw[1]);
-          if (s.w) {
-            const T* v = static_cast<const T*>(s.x) + (t0 + t) * s.x_token + h * s.x_head;
-            load8(v + at.lo, raw[2]);
-            load8(v + at.hi, raw[3]);
-            open8<T>(raw[2], xa);
-            open8<T>(raw[3], xb);
-          }
-          open8<T>(raw[0], ga);
-          open8<T>(raw[1], gb);
-          turn_pairs<kNeighbours, true>(ga, gb, angles.cos + t * angles.pitch, angles.sin + t * angles.pitch, at.angle, p.half);
-        }
-        if (!live || !s.w) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = f2(0.f);
-            if (!live) g[i] = f2(0.f);
-          }
-        }
-        if (s.w) {
-          const float r = __frsqrt_rn(fmaf(team_sum(squares(xa, xb), lanes), each, p.eps));
+    T* out = static_cast<T*>(s.y) + (t0 + t) * heads * p.D;
+    for (int base = 0; base < heads; base += step) {
+      const int h = base + slot;
+      const bool live = t < tokens && h < heads;
+      F2 g[8], x[8];
+      F2(&ga)[4] = *reinterpret_cast<F2(*)[4]>(g), (&gb)[4] = *reinterpret_cast<F2(*)[4]>(g + 4);
+      F2(&xa)[4] = *reinterpret_cast<F2(*)[4]>(x), (&xb)[4] = *reinterpret_cast<F2(*)[4]>(x + 4);
+      open8<T>(raw[0], ga);
+      open8<T>(raw[1], gb);
+      open8<T>(raw[2], xa);
+      open8<T>(raw[3], xb);
+      if (base + step < heads)
+        fetch(q, h + step);
+      else
+        fetch(q + stride, slot);
+      if (mine) turn_pairs<kNeighbours, true>(ga, gb, cos, sin, at.angle, p.half, angles.pitch);
+      if (normed) {
+        const float r = rsqrtf(fmaf(team_sum(squares(xa, xb), lanes), share, p.eps));
+        F2 dot = f2(0.f);
+        if (mine) {
+          F2 w[8];
+          load_f2(s.w + at.lo, *reinterpret_cast<F2(*)[4]>(w));
+          load_f2(s.w + at.hi, *reinterpret_cast<F2(*)[4]>(w + 4));
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             x[i] = x[i] * f2(r);
-            dw[k][i] = fma2(g[i], x[i], dw[k][i]);
+            if (live) dw[i] = fma2(g[i], x[i], dw[i]);
+            g[i] = g[i] * w[i];
+            dot = fma2(g[i], x[i], dot);
           }
-          F2 dot = f2(0.f);
-          if (mine) {
-            F2 w[4];
-            load_f2(s.w + at.lo, w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = g[i] * w[i];
-            load_f2(s.w + at.hi, w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[4 + i] = g[4 + i] * w[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fma2(g[i], x[i], dot);
-          const float c = -team_sum(sum(dot), lanes) * each;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = fma2(x[i], f2(c), g[i]) * f2(r);
         }
-        if (live) {
-          T* y = static_cast<T*>(s.y) + ((t0 + t) * s.heads + h) * p.D;
-          store8(y + at.lo, ga);
-          store8(y + at.hi, gb);
-        }
+        const float c = -team_sum(sum(dot), lanes) * share;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = fma2(x[i], f2(c), g[i]) * f2(r);
+      }
+      if (live && mine) {
+        T* y = out + h * p.D;
+        store8(y + at.lo, ga);
+        store8(y + at.hi, gb);
       }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;\n");
   if (!parts) return;
   // The teams' sums one after another, in their order.
   __syncthreads();
   float* all = reinterpret_cast<float*>(head_smem);  // teams x D
-  for (int k = 0; k < 2; ++k) {
-    if (mine) {
+  if (mine) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float a, b;
-        split(k ? dw[1][i] : dw[0][i], a, b);
-        const int e = (i < 4 ? at.lo : at.hi) + 2 * (i & 3);
-        all[team * p.D + e] = a;
-        all[team * p.D + e + 1] = b;
-      }
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      split(dw[i], a, b);
+      const int e = (i < 4 ? at.lo : at.hi) + 2 * (i & 3);
+      all[team * p.D + e] = a;
+      all[team * p.D + e + 1] = b;
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.D; e += kHeadThreads) {
-      float v = 0.f;
-      for (int i = 0; i < teams; ++i) v += all[i * p.D + e];
-      parts[((int64_t)blockIdx.x * 2 + k) * p.D + e] = v;
-    }
-    __syncthreads();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.D; e += kHeadThreads) {
+    float v = 0.f;
+    for (int i = 0; i < kHeadThreads / lanes; ++i) v += all[i * p.D + e];
+    parts[(int64_t)blockIdx.x * p.D + e] = v;
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_backward_any_kernel(const __grid_constant__ HeadNorm p, int tile,
-                                                                              int64_t tiles, float* parts) {
+// As forward: a lane holds its kN pairs, with the next head's on their way, or
+// (0) reads them again and keeps the weight's gradient in shared memory.
+template <class T, int kN>
+__global__ void __launch_bounds__(kHeadThreads) head_norm_backward_any_kernel(const __grid_constant__ HeadNorm p,
+                                                                              const __grid_constant__ HeadPlan plan, float* parts) {
   extern __shared__ __align__(16) unsigned char head_smem[];
-  const Angles angles(head_smem, p.half);
+  const int k = (int)blockIdx.x >= plan.blocks[0], tile_log = plan.tile_log[k], tile = 1 << tile_log;
+  const HeadSide& s = p.side[k];
+  const Angles angles(head_smem, p.half, tile);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kHeadThreads / 32, D = p.D, pairs = D - p.half;
-  // each warp's sums: 2 D floats
-  float* own = reinterpret_cast<float*>(head_smem + Angles::bytes(p.half)) + warp * 2 * D;
-  for (int i = lane; i < 2 * D; i += 32) own[i] = 0.f;
+  const int t = warp & (tile - 1), slot = warp >> tile_log, step = warps >> tile_log, heads = s.heads;
+  // each warp's sums: D floats
+  float* own = reinterpret_cast<float*>(head_smem + Angles::bytes(p.half, tile)) + warp * D;
+  for (int i = lane; i < D; i += 32) own[i] = 0.f;
+  constexpr int kRoom = kN ? kN : 1;
+  T da[kRoom], db[kRoom], xa[kRoom], xb[kRoom];
+  float wa[kRoom], wb[kRoom];
+#pragma unroll
+  for (int n = 0; n < kRoom; ++n) wa[n] = wb[n] = 0.f;
+  const int64_t tiles = plan.tiles[k];
+  const int stride = plan.blocks[k];
+  int64_t q = k ? (int)blockIdx.x - plan.blocks[0] : (int)blockIdx.x;
+  auto gradient = [&](int64_t token, int h) { return static_cast<const T*>(s.dy) + token * s.dy_token + h * s.dy_head; };
+  auto input = [&](int64_t token, int h) { return static_cast<const T*>(s.x) + token * s.x_token + h * s.x_head; };
+  auto fetch = [&](int64_t q, int h) {
+    const int64_t token = (q << tile_log) + t;
+    if (token >= p.T || h >= heads) return;
+    const T *d = gradient(token, h), *x = s.w ? input(token, h) : d;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int i = lane + 32 * n;
+      int a, b;
+      pair_at(p, i, a, b);
+      const bool in = i < pairs, two = i < p.half;
+      da[n] = in ? d[a] : from_f32<T>(0.f), db[n] = two ? d[b] : from_f32<T>(0.f);
+      xa[n] = in ? x[a] : from_f32<T>(0.f), xb[n] = two ? x[b] : from_f32<T>(0.f);
+    }
+  };
+  if (kN) fetch(q, slot);
   if (p.half) fill_turns(p, angles);
-  for (int64_t q = blockIdx.x; q < tiles; q += gridDim.x) {
-    const int64_t t0 = q * tile;
+  const float *cos = angles.cos + t * angles.pitch, *sin = angles.sin + t * angles.pitch;
+  auto back = [&](int i, float& ga, float& gb) {
+    if (i >= p.half) return;
+    const float d = ga, c = cos[angles.place(i)], z = sin[angles.place(i)];
+    ga = fmaf(gb, z, d * c);
+    gb = fmaf(-d, z, gb * c);
+  };
+  for (; q < tiles; q += stride) {
+    const int64_t t0 = q << tile_log;
     const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
     if (p.half) {
       __syncthreads();
       fill_angles(p, angles, t0, tokens);
       __syncthreads();
     }
-    for (int u = warp; u < (p.side[0].heads + p.side[1].heads) * tile; u += warps) {
-      const int t = u & (tile - 1);
-      int h = u / tile;
-      if (t >= tokens) continue;
-      const int k = h >= p.side[0].heads;
-      if (k) h -= p.side[0].heads;
-      const HeadSide& s = p.side[k];
-      const T* x = static_cast<const T*>(s.x) + (t0 + t) * s.x_token + h * s.x_head;
-      const T* d = static_cast<const T*>(s.dy) + (t0 + t) * s.dy_token + h * s.dy_head;
-      T* y = static_cast<T*>(s.y) + ((t0 + t) * s.heads + h) * D;
-      const float *cos = angles.cos + t * angles.pitch, *sin = angles.sin + t * angles.pitch;
-      auto turned = [&](int i, int a, int b, float& ga, float& gb) {
-        ga = to_f32<T>(d[a]), gb = to_f32<T>(d[b]);
-        if (i < p.half) {
-          const float da = ga, c = cos[i], z = sin[i];
-          ga = fmaf(gb, z, da * c);
-          gb = fmaf(-da, z, gb * c);
+    for (int h = slot; h < heads; h += step) {
+      T* y = static_cast<T*>(s.y) + ((t0 + t) * heads + h) * D;
+      if constexpr (kN > 0) {
+        float ga[kN], gb[kN], ua[kN], ub[kN], sq = 0.f, dot = 0.f;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          ga[n] = to_f32<T>(da[n]), gb[n] = to_f32<T>(db[n]);
+          ua[n] = to_f32<T>(xa[n]), ub[n] = to_f32<T>(xb[n]);
         }
-      };
-      float r = 1.f, mean = 0.f;
-      if (s.w) {
-        float sq = 0.f, dot = 0.f;
+        if (h + step < heads)
+          fetch(q, h + step);
+        else
+          fetch(q + stride, slot);
+        if (t >= tokens) continue;
+        float r = 1.f, mean = 0.f;
+        if (s.w) {
+#pragma unroll
+          for (int n = 0; n < kN; ++n) sq = fmaf(ua[n], ua[n], fmaf(ub[n], ub[n], sq));
+          r = rsqrtf(fmaf(warp_reduce(sq, SumOp()), 1.f / (float)D, p.eps));
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const int i = lane + 32 * n;
+          if (i >= pairs) break;
+          back(i, ga[n], gb[n]);
+          if (!s.w) continue;
+          int a, b;
+          pair_at(p, i, a, b);
+          ua[n] *= r, ub[n] *= r;
+          wa[n] = fmaf(ga[n], ua[n], wa[n]), wb[n] = fmaf(gb[n], ub[n], wb[n]);
+          ga[n] *= s.w[a], gb[n] *= s.w[b];
+          dot = fmaf(ga[n], ua[n], fmaf(gb[n], ub[n], dot));
+        }
+        if (s.w) mean = warp_reduce(dot, SumOp()) * (1.f / (float)D);
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const int i = lane + 32 * n;
+          if (i >= pairs) break;
+          int a, b;
+          pair_at(p, i, a, b);
+          y[a] = from_f32<T>(s.w ? (ga[n] - ua[n] * mean) * r : ga[n]);
+          if (i < p.half) y[b] = from_f32<T>(s.w ? (gb[n] - ub[n] * mean) * r : gb[n]);
+        }
+      } else {
+        if (t >= tokens) continue;
+        const T *d = gradient(t0 + t, h), *x = s.w ? input(t0 + t, h) : d;
+        float r = 1.f, mean = 0.f;
+        if (s.w) {
+          float sq = 0.f, dot = 0.f;
+          for (int i = lane; i < pairs; i += 32) {
+            int a, b;
+            pair_at(p, i, a, b);
+            float ga = to_f32<T>(d[a]), gb = to_f32<T>(d[b]);
+            back(i, ga, gb);
+            const float va = to_f32<T>(x[a]), vb = i < p.half ? to_f32<T>(x[b]) : 0.f;
+            sq = fmaf(va, va, fmaf(vb, vb, sq));
+            dot = fmaf(ga * s.w[a], va, fmaf(gb * s.w[b], vb, dot));
+          }
+          r = rsqrtf(fmaf(warp_reduce(sq, SumOp()), 1.f / (float)D, p.eps));
+          mean = warp_reduce(dot, SumOp()) * r * (1.f / (float)D);
+        }
         for (int i = lane; i < pairs; i += 32) {
           int a, b;
           pair_at(p, i, a, b);
-          float ga, gb;
-          turned(i, a, b, ga, gb);
-          const float xa = to_f32<T>(x[a]), xb = i < p.half ? to_f32<T>(x[b]) : 0.f;
-          sq = fmaf(xa, xa, fmaf(xb, xb, sq));
-          dot = fmaf(ga * s.w[a], xa, fmaf(gb * s.w[b], xb, dot));
+          float ga = to_f32<T>(d[a]), gb = to_f32<T>(d[b]);
+          back(i, ga, gb);
+          if (s.w) {
+            const float va = to_f32<T>(x[a]) * r, vb = to_f32<T>(x[b]) * r;
+            own[a] += ga * va;
+            if (i < p.half) own[b] += gb * vb;
+            ga = (ga * s.w[a] - va * mean) * r;
+            gb = (gb * s.w[b] - vb * mean) * r;
+          }
+          y[a] = from_f32<T>(ga);
+          if (i < p.half) y[b] = from_f32<T>(gb);
         }
-        r = __frsqrt_rn(fmaf(warp_reduce(sq, SumOp()), 1.f / (float)D, p.eps));
-        mean = warp_reduce(dot, SumOp()) * r * (1.f / (float)D);
-      }
-      for (int i = lane; i < pairs; i += 32) {
-        int a, b;
-        pair_at(p, i, a, b);
-        float ga, gb;
-        turned(i, a, b, ga, gb);
-        if (s.w) {
-          const float ua = to_f32<T>(x[a]) * r, ub = to_f32<T>(x[b]) * r;
-          own[k * D + a] += ga * ua;
-          if (i < p.half) own[k * D + b] += gb * ub;
-          ga = (ga * s.w[a] - ua * mean) * r;
-          gb = (gb * s.w[b] - ub * mean) * r;
-        }
-        y[a] = from_f32<T>(ga);
-        if (i < p.half) y[b] = from_f32<T>(gb);
       }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;\n");
   if (!parts) return;
+  if constexpr (kN > 0) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int i = lane + 32 * n;
+      if (i >= pairs) break;
+      int a, b;
+      pair_at(p, i, a, b);
+      own[a] = wa[n];
+      if (i < p.half) own[b] = wb[n];
+    }
+  }
   __syncthreads();
-  own -= warp * 2 * D;
-  for (int i = threadIdx.x; i < 2 * D; i += kHeadThreads) {
+  own -= warp * D;
+  for (int i = threadIdx.x; i < D; i += kHeadThreads) {
     float v = 0.f;
-    for (int w = 0; w < warps; ++w) v += own[w * 2 * D + i];
-    parts[(int64_t)blockIdx.x * 2 * D + i] = v;
+    for (int w = 0; w < warps; ++w) v += own[w * D + i];
+    parts[(int64_t)blockIdx.x * D + i] = v;
   }
 }
 
-// The blocks' sums joined: 32 columns for each block, its warps each a share
-// of the rows in order, then the warps in order.
-__global__ void __launch_bounds__(1024) head_norm_join_kernel(const float* parts, int rows, int D, float* dq, float* dk) {
+// The blocks' sums joined: 32 columns of a side for each block, its warps each a
+// share of the rows in order, then the warps in order.
+__global__ void __launch_bounds__(1024) head_norm_join_kernel(const float* parts, int queries, int keys, int D, float* dq, float* dk) {
   __shared__ float red[32][33];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  const int rows = blockIdx.y ? keys : queries;
+  const float* from = parts + (blockIdx.y ? (int64_t)queries * D : 0);
   float v = 0.f;
-  if (col < 2 * D)
-    for (int r = warp; r < rows; r += 32) v += parts[(int64_t)r * 2 * D + col];
+  if (col < D) {
+#pragma unroll 8
+    for (int r = warp; r < rows; r += 32) v += from[(int64_t)r * D + col];
+  }
   red[warp][lane] = v;
   __syncthreads();
   v = warp_reduce(red[lane][warp], SumOp());
   const int out = blockIdx.x * 32 + warp;
-  if (lane == 0 && out < 2 * D) {
-    float* to = out < D ? dq : dk;
-    if (to) to[out < D ? out : out - D] = v;
-  }
+  float* to = blockIdx.y ? dk : dq;
+  if (lane == 0 && out < D && to) to[out] = v;
 }
 
 bool on_16(const void* p, int64_t token, int64_t head, int dtype) {
@@ -518,68 +657,115 @@ int lanes_of(int D) {
   while (16 * l < D) l *= 2;
   return l;
 }
-// Tokens of a tile: eight where that leaves a tile for each of `blocks`, else fewer.
-int tile_of(int64_t T, int64_t blocks) {
-  int tile = kHeadTile;
-  while (tile > 1 && (T + tile - 1) / tile < blocks) tile /= 2;
-  return tile;
+int log_of(int n) {
+  int l = 0;
+  while ((1 << (l + 1)) <= n) ++l;
+  return l;
 }
+// Tokens of a tile: eight where that leaves a tile for each of `blocks`, else fewer.
+int tile_log_of(int64_t T, int64_t blocks) {
+  int l = log_of(kHeadTile);
+  while (l && (T + (1 << l) - 1) >> l < blocks) --l;
+  return l;
+}
+int pairs_of(const HeadNorm& p) { return p.D - p.half; }
 
 template <class T>
 cudaError_t forward_typed(const HeadNorm& p, cudaStream_t stream) {
-  const int tile = tile_of(p.T, kHeadBlocks), heads = p.side[0].heads + p.side[1].heads;
-  const int64_t tiles = (p.T + tile - 1) / tile;
+  const int tile_log = tile_log_of(p.T, kHeadBlocks), heads = p.side[0].heads + p.side[1].heads;
+  const int64_t tiles = (p.T + (1 << tile_log) - 1) >> tile_log;
   const bool runs = in_runs(p);
-  const int lanes = runs ? lanes_of(p.D) : 32, teams = kHeadThreads / lanes;
+  const int lanes = runs ? lanes_of(p.D) : 32, each = (kHeadThreads / lanes) >> tile_log;
   // Few tokens: their heads over several blocks, which each compute the angles.
-  const int64_t rounds = ((int64_t)heads * tile + teams - 1) / teams;
-  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(rounds, kHeadBlocks / tiles));
+  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((heads + each - 1) / each, kHeadBlocks / tiles));
   const dim3 grid((unsigned)tiles, (unsigned)parts);
-  const size_t smem = Angles::bytes(p.half);
-  if (!runs)
-    head_norm_any_kernel<T><<<grid, kHeadThreads, smem, stream>>>(p, tile);
-  else if (p.neighbours)
-    head_norm_kernel<T, true><<<grid, kHeadThreads, smem, stream>>>(p, tile, lanes);
+  const size_t smem = Angles::bytes(p.half, 1 << tile_log);
+  const int pairs = pairs_of(p);
+  if (runs && p.neighbours)
+    head_norm_kernel<T, true><<<grid, kHeadThreads, smem, stream>>>(p, tile_log, lanes);
+  else if (runs)
+    head_norm_kernel<T, false><<<grid, kHeadThreads, smem, stream>>>(p, tile_log, lanes);
+  else if (pairs <= 32)
+    head_norm_any_kernel<T, 1><<<grid, kHeadThreads, smem, stream>>>(p, tile_log);
+  else if (pairs <= 64)
+    head_norm_any_kernel<T, 2><<<grid, kHeadThreads, smem, stream>>>(p, tile_log);
+  else if (pairs <= 128)
+    head_norm_any_kernel<T, 4><<<grid, kHeadThreads, smem, stream>>>(p, tile_log);
   else
-    head_norm_kernel<T, false><<<grid, kHeadThreads, smem, stream>>>(p, tile, lanes);
+    head_norm_any_kernel<T, 0><<<grid, kHeadThreads, smem, stream>>>(p, tile_log);
   return cudaGetLastError();
 }
 
-template <class K>
-cudaError_t room(K kernel, size_t smem) {
-  return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
+// A side's tiles: of so many tokens that a team, of which a block has `teams`, has eight heads
+// of one between two barriers, and fewer where there would be less than a tile for a third of its blocks.  A
+// block takes as many tiles as any other, or one less.
+void plan_side(HeadPlan& plan, int k, int64_t T, int heads, int teams, int blocks) {
+  if (heads == 0 || blocks == 0) return;
+  int l = 0;
+  while ((2 << l) <= std::min(teams, kBackTile) && ((int64_t)heads << (l + 1)) <= 8 * teams) ++l;
+  while (l && (T + (1 << l) - 1) >> l < (blocks + 2) / 3) --l;
+  plan.tile_log[k] = l;
+  plan.tiles[k] = (T + (1 << l) - 1) >> l;
+  const int64_t rounds = (plan.tiles[k] + blocks - 1) / blocks;
+  plan.blocks[k] = (int)((plan.tiles[k] + rounds - 1) / rounds);
+}
+HeadPlan backward_plan(const HeadNorm& p, int teams, int blocks) {
+  HeadPlan plan = {};
+  const int64_t hq = p.side[0].heads, hk = p.side[1].heads, share = (blocks * hq + (hq + hk) / 2) / (hq + hk);
+  const int queries = hk == 0 ? blocks : hq == 0 ? 0 : (int)std::min<int64_t>(blocks - 1, std::max<int64_t>(1, share));
+  plan_side(plan, 0, p.T, (int)hq, teams, queries);
+  plan_side(plan, 1, p.T, (int)hk, teams, blocks - queries);
+  return plan;
 }
 
 template <class T>
 cudaError_t backward_typed(const HeadNorm& p, float* parts, cudaStream_t stream) {
-  const int tile = tile_of(p.T, kHeadBlocks);
-  const int64_t tiles = (p.T + tile - 1) / tile;
-  const unsigned grid = (unsigned)std::min<int64_t>(tiles, kHeadBlocks);
+  const bool runs = in_runs(p);
+  const int lanes = runs ? lanes_of(p.D) : 32, teams = kHeadThreads / lanes;
+  const int pairs = pairs_of(p);
+  // As many blocks as fit on the SMs at a time: their registers decide.
+  const int on_sm = runs ? 2 : pairs > 64 && pairs <= 128 ? 2 : 4;
+  const HeadPlan plan = backward_plan(p, teams, 152 * on_sm);
+  const unsigned grid = (unsigned)(plan.blocks[0] + plan.blocks[1]);
   float* sums = p.side[0].dw || p.side[1].dw ? parts : nullptr;
+  const size_t angles = Angles::bytes(p.half, 1 << std::max(plan.tile_log[0], plan.tile_log[1]));
+  const size_t smem = runs ? std::max(angles, (size_t)teams * p.D * 4) : angles + (size_t)teams * p.D * 4;
   cudaError_t e = cudaSuccess;
-  if (!in_runs(p)) {
-    const size_t smem = Angles::bytes(p.half) + (size_t)(kHeadThreads / 32) * 2 * p.D * 4;
-    e = room(head_norm_backward_any_kernel<T>, smem);
-    if (e == cudaSuccess) head_norm_backward_any_kernel<T><<<grid, kHeadThreads, smem, stream>>>(p, tile, tiles, sums);
-  } else {
-    const int lanes = lanes_of(p.D);
-    const size_t smem = std::max(Angles::bytes(p.half), (size_t)(kHeadThreads / lanes) * p.D * 4);
-    if (p.neighbours)
-      head_norm_backward_kernel<T, true><<<grid, kHeadThreads, smem, stream>>>(p, tile, lanes, tiles, sums);
-    else
-      head_norm_backward_kernel<T, false><<<grid, kHeadThreads, smem, stream>>>(p, tile, lanes, tiles, sums);
-  }
-  if (e == cudaSuccess) e = cudaGetLastError();
+  auto go = [&](auto kernel, auto... more) {
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) kernel<<<grid, kHeadThreads, smem, stream>>>(p, plan, more..., sums);
+    if (e == cudaSuccess) e = cudaGetLastError();
+  };
+  if (runs && p.neighbours)
+    go(head_norm_backward_kernel<T, true>, lanes);
+  else if (runs)
+    go(head_norm_backward_kernel<T, false>, lanes);
+  else if (pairs <= 32)
+    go(head_norm_backward_any_kernel<T, 1>);
+  else if (pairs <= 64)
+    go(head_norm_backward_any_kernel<T, 2>);
+  else if (pairs <= 128)
+    go(head_norm_backward_any_kernel<T, 4>);
+  else
+    go(head_norm_backward_any_kernel<T, 0>);
   if (e != cudaSuccess || !sums) return e;
-  head_norm_join_kernel<<<(2 * p.D + 31) / 32, 1024, 0, stream>>>(parts, (int)grid, p.D, p.side[0].dw, p.side[1].dw);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.D + 31) / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, head_norm_join_kernel, (const float*)parts, plan.blocks[0], plan.blocks[1], p.D, p.side[0].dw,
+                            p.side[1].dw);
 }
 
 }  // namespace
 
 size_t head_norm_backward_workspace_bytes(int64_t T, int64_t D) {
-  const int tile = tile_of(T, kHeadBlocks);
-  return (size_t)std::min<int64_t>((T + tile - 1) / tile, kHeadBlocks) * 2 * D * 4;
+  return (size_t)std::min<int64_t>(2 * T, kBackBlocks) * D * 4;
 }
 
 cudaError_t head_norm_launch(const HeadNorm& p, cudaStream_t stream) {
