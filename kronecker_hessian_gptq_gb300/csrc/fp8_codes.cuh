@@ -27,6 +27,7 @@ __device__ __forceinline__ void block_scale(uint32_t top, float& scale, float& i
 }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t fp8_pair(float a, float b, float inv_a, float inv_b) {
+  // A block without a reciprocal may hold what is not finite, and 0 times that is no number.
   const float2 q = make_float2(inv_a > 0.f ? a * inv_a : 0.f, inv_b > 0.f ? b * inv_b : 0.f);
   return (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
 }

@@ -227,7 +227,7 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
     const F8Rows<T> epi = rows(p.dX, p.T, p.K);
     if (e == cudaSuccess)
       e = fp8_pair_launch<false, true, 256, 2>(F8Operand{q.along, p.T, q.ld_along}, F8Operand{V, p.K, ldv}, p.N, b.dx,
-                                                          sc, F8Join{floats(b.join), arrived}, epi, false, status, stream, 0);
+                                                          sc, F8Join{floats(b.join), arrived}, epi, !copy && !p.dbias, status, stream, 0);
   }
   if (e == cudaSuccess && p.dW) {
     Fp8Codes x = {};
@@ -239,7 +239,7 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
     if (p.dX) arrived += arrived_bytes(b.dx) / 4;
     if (e == cudaSuccess)
       e = fp8_pair_launch<true, true, 256, 0>(F8Operand{q.down, p.N, q.ld_down}, F8Operand{x.down, p.K, x.ld_down}, p.T,
-                                                        b.dw, sc, F8Join{floats(b.join), arrived}, epi, false, status, stream,
+                                                        b.dw, sc, F8Join{floats(b.join), arrived}, epi, true, status, stream,
                                                         p.dX ? -1 : 0);
   }
   return e;

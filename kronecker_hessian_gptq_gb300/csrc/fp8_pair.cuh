@@ -6,12 +6,16 @@
 // of K: 128 codes of 128 rows of A and of kN / 2 rows of B in each block of the
 // pair (TMA, 128-byte swizzle), four tcgen05.mma of kind::f8f6f4 with
 // cta_group::2.  The tensor cores sum one block of K alone; the sums (fp32, in
-// tensor memory, two or four in turn) are read by 16 epilogue warps, scaled and
-// added to sums in registers, a thread for a row and kN / 4 columns, while the
+// tensor memory, two or four in turn) are read by eight epilogue warps, scaled and
+// added to sums in registers, a thread for a row and kN / 2 columns, while the
 // next block is multiplied.  For kN = 256 the tensor cores take 512 cycles for a
-// block of K; the epilogue's 64 columns a thread are 64 scaled additions, at 128
-// a cycle 256 cycles, where the columns share a scale (weights: one for 128 x
-// 128), and twice as many where they do not (kColumns).
+// block of K, and the scaled additions as many where the columns share a scale
+// (weights: one for 128 x 128), for the packed ones go at half rate; twice as many
+// where they do not (kColumns).  Measured at 4096 x 4864 x 16384: 0.46 us a block
+// (950 cycles), of which the tensor cores and copies alone take 0.37 (the two
+// SMs fetch 64 KB for it, 13 TB/s over all of them); 4096 tokens 4096 x 14336
+// 218 us, quantized in the call (2.2 PFLOP/s).  16 epilogue warps with half the
+// columns each issue more for waits and scales (236 us).
 //
 // Either operand may be stored with K contiguous or with its rows contiguous
 // (a weight's gradient sums over tokens, a row each).  Where there are fewer
@@ -30,7 +34,7 @@
 namespace bakron {
 
 constexpr int kF8K = 128;  // K of a stage, and of a scale
-constexpr int kF8Warps = 16;  // of the epilogue
+constexpr int kF8Warps = 8;  // of the epilogue
 constexpr int kF8Threads = 128 + 32 * kF8Warps;
 constexpr int kF8MostStages = 10;
 constexpr int kF8Ring = 2;  // batches of scales on their way
@@ -46,7 +50,8 @@ struct F8Shape {
   static constexpr int kCols = kN / (kF8Warps / 4);  // of a thread
   static constexpr int kScales = ((kColumns ? kN : 0) + (kRows ? 128 : 0)) * 4;  // of a block of K
   static constexpr int kBatch = kColumns && kN > 64 ? 4 : 8;  // blocks whose scales come together
-  static constexpr int kOther = (kBoxes ? kF8Warps * kPairBox : 0) + kF8Ring * kBatch * kScales + 1024;
+  static constexpr int kBox = kBoxes ? kN / 128 * kPairBox : 0;  // of a warp: one for each run
+  static constexpr int kOther = kF8Warps * kBox + kF8Ring * kBatch * kScales + 1024;
   static constexpr int kFit = (kF8Smem - kOther) / kStage;
   static constexpr int kStages = kFit < kF8MostStages ? kFit : kF8MostStages;
   static constexpr int kBytes = kStages * kStage + kOther;
@@ -80,6 +85,7 @@ __device__ __forceinline__ void pair_mma_f8(uint32_t d, uint32_t a, uint32_t b, 
 // row, or 32 rows of 128 bytes.
 template <bool kRows>
 __host__ __device__ constexpr uint32_t f8_kstep() { return kRows ? 4096u >> 4 : 32u >> 4; }
+// 16 columns of the warp's 32 lanes of tensor memory.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
@@ -93,9 +99,61 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Whether the phase of a barrier, given by its address, is done, for a whole warp.
+__device__ __forceinline__ bool phase_done_at(uint32_t mbar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(done)
+               : "r"(mbar), "r"(parity)
+               : "memory");
+  return __all_sync(0xffffffffu, done) != 0;
+}
+__device__ __forceinline__ void warp_wait_at(uint32_t mbar, uint32_t parity, bool& broken) {
+  if (broken || phase_done_at(mbar, parity)) return;
+  const uint32_t t0 = clock();
+  while (!phase_done_at(mbar, parity)) {
+    if (__any_sync(0xffffffffu, clock() - t0 > (1u << 28))) {
+      broken = true;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void arrive_if(bool p, uint32_t mbar) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %1, 0;\n@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}\n" ::"r"(mbar),
+      "r"((uint32_t)p)
+      : "memory");
+}
+
+// A warp with a box for each of two runs: only the box before the last has to have been read.
+struct F8Box : PairBox {
+  __device__ __forceinline__ void open() const {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory");
+    __syncwarp();
+  }
+};
+// pair_unit without divisions where K is whole, and with few where it is not: they
+// would take an epilogue warp a thousand cycles of each tile.
+__device__ __forceinline__ PairUnit f8_unit(const PairWork& w, int u) {
+  PairUnit r;
+  const uint32_t tiles = (uint32_t)w.tiles_m * w.tiles_n, whole = (uint32_t)w.group * w.tiles_n;
+  uint32_t t = u;
+  r.part = 0, r.k0 = 0, r.k1 = w.ksteps;
+  if (w.parts > 1) {
+    r.part = t / tiles, t -= r.part * tiles;
+    r.k0 = (uint32_t)w.ksteps * r.part / w.parts;
+    r.k1 = (uint32_t)w.ksteps * (r.part + 1) / w.parts;
+  }
+  const uint32_t g = t / whole, first = g * w.group, in = t - g * whole;
+  const uint32_t rows = w.tiles_m - first < w.group ? w.tiles_m - first : w.group;
+  r.tn = in / rows;
+  r.tm = first + (in - r.tn * rows);
+  return r;
+}
+
 // kWeights: which operand the weights are, 1 for A, 2 for B, 0 for neither
 // (then both have a scale for each row).  No kernel before writes them.
-template <bool kARows, bool kBRows, int kN, int kWeights, class Epi>
+template <bool kARows, bool kBRows, int kN, int kWeights, bool kJoin, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairWork work,
                     F8Scales sc, F8Join join, const __grid_constant__ Epi epi, int32_t* status, int32_t first_status) {
@@ -106,7 +164,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   extern __shared__ unsigned char f8_smem_raw[];
   const uint32_t base = (smem_u32(f8_smem_raw) + 1023u) & ~1023u;
   const uint32_t boxes = base + kStages * Shape::kStage;
-  const uint32_t scales = boxes + (Epi::kBoxes ? kF8Warps * kPairBox : 0);
+  const uint32_t scales = boxes + kF8Warps * Shape::kBox;
   __shared__ F8Barriers bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -133,14 +191,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  // 640 threads start with 96 registers each; the first four warps hand 32 of
-  // theirs on, 8 to each of the other 16 (128 x 64 + 512 x 104 = 640 x 96).
-  constexpr bool kHandOn = kCols == 64;
+  // 384 threads start with 168 registers each.  Where that is not enough the first
+  // four warps hand 96 of theirs on, 48 to each of the other eight (128 x 72 +
+  // 256 x 216 = 384 x 168): with sums that meet in memory and with columns' scales.
+  // Where it is, the compiler does better without (220 us, with 230).
+  constexpr bool kHandOn = kCols == 128 && (kJoin || kWeights == 0);
   if (warp < 4) {
-  if (kHandOn) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+  if (kHandOn) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
   if (warp == 0 || warp == 3) {  // copies: warp 0 the weights' side, warp 3 the other and the scales
     const bool is_a = (warp == 0) == (kWeights == 1);
-    if (warp == 3) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (warp == 3 || kWeights == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
     auto fetch = [&](uint32_t to, const float* from, uint32_t bytes, uint32_t full) {
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(to),
                    "l"(from), "r"(bytes), "r"(full)
@@ -148,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     };
     Ring ring, batch;
     for (int u = mine; u < units && !broken; u += pairs) {
-      const PairUnit q = pair_unit(work, u);
+      const PairUnit q = f8_unit(work, u);
       const int row = is_a ? q.tm * 256 + (int)rank * 128 : q.tn * kN + (int)rank * (kN / 2);
       for (int k = q.k0; k < q.k1; ++k, ring.next(kStages)) {
         const int slot = ring.slot;
@@ -211,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     int sums = 0;
     Ring ring;
     for (int u = mine; u < units && !broken; u += pairs) {
-      const PairUnit q = pair_unit(work, u);
+      const PairUnit q = f8_unit(work, u);
       for (int k = q.k0; k < q.k1; ++k, ring.next(kStages), ++sums) {
         const int buf = sums % kBufs, sum = buf * kHalves + half;
         warp_wait(&bar.full[ring.slot], ring.turn, broken);
@@ -230,20 +290,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
       }
     }
   }
-  } else {  // epilogue: 32 rows of the block and kCols columns for each warp
-    if (kHandOn) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+  } else {  // epilogue: 32 rows of the block and kCols columns for each warp, in runs of at most 64
+    if (kHandOn) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     // A half's products have 64 columns of the even block's rows of B, then 64 of the odd block's.
-    const int half = kHalves > 1 ? part & 1 : 0;
-    const uint32_t lanes = ((uint32_t)(32 * quarter) << 16) + (uint32_t)((kHalves > 1 ? part >> 1 : part) * kCols);
-    const int first = part * kCols;  // of the thread's columns in the tile
-    const PairBox box{boxes + (uint32_t)(warp - 4) * kPairBox, lane};
+    constexpr int kRuns = kCols > 64 ? 2 : 1, kRun = kCols / kRuns;
+    static_assert(kRuns == kHalves, "a warp has one half's columns, or its share of them all");
+    const int half = kHalves > 1 ? part : 0, first = part * kRun;  // of the thread's columns in the tile; the second run is 128 on
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(kHalves > 1 ? half * (kN / 2) : part * kCols);
+    const uint32_t full_at = smem_u32(&bar.sum_full[half]), empty_at = in_even_block(&bar.sum_empty[half]);
+    const uint32_t row_at = (uint32_t)((kColumns ? kN : 0) + 32 * quarter + lane) * 4u, col_at = (uint32_t)first * 4u;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    // The weights' scales are the whole warp's: a lane reads that of one block,
+    // The weights' scales are the whole warp's: a lane reads those of one block,
     // 32 blocks at a time, and those of the next unit while this one is at hand.
-    auto shared_scale = [&](const PairUnit& q, int k) {
+    constexpr int kShared = kWeights == 2 ? kRuns : 1;
+    auto shared_scale = [&](const PairUnit& q, int k, int run) {
       if (kWeights == 0 || k >= q.k1) return 0.f;
-      int64_t at = kWeights == 1 ? (int64_t)q.tm * 256 + rank * 128 : (int64_t)q.tn * kN + first;
+      int64_t at = kWeights == 1 ? (int64_t)q.tm * 256 + rank * 128 : (int64_t)q.tn * kN + first + 128 * run;
       at = at < sc.weights ? at : sc.weights - 1;  // beyond the matrix, where sums are 0, the last
       return kWeights == 1 ? sc.a[(at >> 7) * sc.each + k * sc.a_step] : sc.b[(at >> 7) * sc.each + k * sc.b_step];
     };
@@ -251,53 +314,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
       __syncwarp();
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
     };
-    int sums = 0;
+    uint32_t buf = 0, turn = 0;
     Ring ring;
-    PairUnit next = pair_unit(work, mine);
-    float ahead = shared_scale(next, next.k0 + lane);
+    PairUnit next = f8_unit(work, mine);
+    float of_32[kShared], ahead[kShared];
+#pragma unroll
+    for (int i = 0; i < kShared; ++i) ahead[i] = shared_scale(next, next.k0 + lane, i);
     for (int u = mine; u < units && !broken; u += pairs) {
       const PairUnit q = next;
-      float of_32 = ahead;
+#pragma unroll
+      for (int i = 0; i < kShared; ++i) of_32[i] = ahead[i];
       if (u + pairs < units) {
-        next = pair_unit(work, u + pairs);
-        ahead = shared_scale(next, next.k0 + lane);
+        next = f8_unit(work, u + pairs);
+#pragma unroll
+        for (int i = 0; i < kShared; ++i) ahead[i] = shared_scale(next, next.k0 + lane, i);
       }
       const int64_t row0 = (int64_t)q.tm * 256 + rank * 128 + 32 * quarter, col = (int64_t)q.tn * kN + first;
       F2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = f2(0.f);
-      for (int k = q.k0; k < q.k1; ++k, ++sums) {
-        const int sum = sums % kBufs * kHalves + half, in = k - q.k0, in_batch = in % Shape::kBatch;
-        if (kWeights && (in & 31) == 0 && in > 0) of_32 = shared_scale(q, k + lane);
-        if (in_batch == 0) {
-          if (in > 0) {
-            arrive(&bar.scale_empty[ring.slot]);
-            ring.next(kF8Ring);
-          }
-          warp_wait(&bar.scale_full[ring.slot], ring.turn, broken);
+      const int blocks = q.k1 - q.k0;
+      for (int first_in = 0; first_in < blocks && !broken; first_in += Shape::kBatch) {
+        warp_wait_at(smem_u32(&bar.scale_full[ring.slot]), ring.turn, broken);
+        if (kWeights && first_in % 32 == 0 && first_in > 0) {  // 32 is a multiple of a batch
+#pragma unroll
+          for (int i = 0; i < kShared; ++i) of_32[i] = shared_scale(q, q.k0 + first_in + lane, i);
         }
-        const uint32_t from = scales + (uint32_t)((ring.slot * Shape::kBatch + in_batch) * Shape::kScales);
-        float r = 1.f;
-        if (kRows)
-          asm volatile("ld.shared.f32 %0, [%1];\n"
-                       : "=f"(r)
-                       : "r"(from + (uint32_t)((kColumns ? kN : 0) + 32 * quarter + lane) * 4u)
-                       : "memory");
-        const F2 scale = f2(kWeights ? r * __shfl_sync(0xffffffffu, of_32, in & 31) : r);
-        warp_wait(&bar.sum_full[sum], (uint32_t)(sums / kBufs) & 1u, broken);
+        const uint32_t batch = scales + (uint32_t)(ring.slot * Shape::kBatch * Shape::kScales);
+        const int here = blocks - first_in < Shape::kBatch ? blocks - first_in : Shape::kBatch;
+#pragma unroll 1
+        for (int j = 0; j < here; ++j) {
+        const uint32_t from = batch + (uint32_t)j * Shape::kScales;
+        float of_row = 1.f;
+        if (kRows) asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(of_row) : "r"(from + row_at) : "memory");
+        F2 scale[kShared];
+#pragma unroll
+        for (int i = 0; i < kShared; ++i) scale[i] = f2(of_row) * f2(kWeights ? __shfl_sync(0xffffffffu, of_32[i], (first_in + j) & 31) : 1.f);
+        warp_wait_at(full_at + buf * (kHalves * 8), turn, broken);
         if (broken) break;
         tc_fence_after();
+        const uint32_t at = lanes + buf * kN;
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
           float v[16];
-          tmem_ld16(tmem + (uint32_t)(sum * (kN / kHalves) + c) + lanes, v);
+          tmem_ld16(at + c, v);
           if (c + 16 == kCols) {  // all read: the buffer may be filled again
             tc_fence_before();
             // A release of cluster scope would stall the warp for half a
             // microsecond; the tensor-memory loads are complete.
-            if (lane == 0)
-              asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(in_even_block(&bar.sum_empty[sum])) : "memory");
+            arrive_if(lane == 0, empty_at + buf * (kHalves * 8));
           }
+          const F2 by = scale[kShared > 1 ? c / kRun : 0];
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             F2 x = f2(v[i], v[i + 1]), y = f2(v[i + 2], v[i + 3]);
@@ -305,23 +372,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
               float f[4];
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
                            : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
-                           : "r"(from + (uint32_t)(first + c + i) * 4u)
+                           : "r"(from + col_at + (uint32_t)(c + i + (c >= 64 ? 64 : 0)) * 4u)
                            : "memory");
               x = x * f2(f[0], f[1]);
               y = y * f2(f[2], f[3]);
             }
-            acc[(c + i) / 2] = fma2(x, scale, acc[(c + i) / 2]);
-            acc[(c + i) / 2 + 1] = fma2(y, scale, acc[(c + i) / 2 + 1]);
+            acc[(c + i) / 2] = fma2(x, by, acc[(c + i) / 2]);
+            acc[(c + i) / 2 + 1] = fma2(y, by, acc[(c + i) / 2 + 1]);
           }
         }
-      }
-      if (!broken) {
+        if (++buf == kBufs) buf = 0, turn ^= 1u;
+        }
+        if (broken) break;
         arrive(&bar.scale_empty[ring.slot]);
         ring.next(kF8Ring);
       }
       if (broken) break;
       bool last = true;
-      if (work.parts > 1) {
+      if (kJoin && work.parts > 1) {
         if (row0 >= epi.rows() || col >= epi.cols()) continue;  // for every part alike
         const int64_t tile = (int64_t)q.tm * work.tiles_n + q.tn, tiles = (int64_t)work.tiles_m * work.tiles_n;
         const int64_t slice = (tile * 2 + rank) * kF8Warps + (warp - 4), stride = tiles * 2 * kF8Warps * 32 * kCols;
@@ -351,10 +419,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         }
       }
       if (!last) continue;
-      float out[kCols];
 #pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) split(acc[i], out[2 * i], out[2 * i + 1]);
-      epi(row0, col, out, box);
+      for (int run = 0; run < kRuns; ++run) {
+        float out[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun / 2; ++i) split(acc[run * (kRun / 2) + i], out[2 * i], out[2 * i + 1]);
+        epi(row0, col + 128 * run, out, F8Box{{boxes + (uint32_t)((warp - 4) * Shape::kBox + run * kPairBox), lane}});
+      }
     }
     if (Epi::kBoxes && lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
@@ -383,7 +454,7 @@ struct F8Rows {
   __device__ __forceinline__ int64_t rows() const { return m; }
   __device__ __forceinline__ int64_t cols() const { return n; }
   template <int kCols>
-  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const PairBox& box) const {
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const F8Box& box) const {
     if (row0 >= m || col >= n) return;
     if constexpr (sizeof(T) == 2) {
       if (tma) {
@@ -427,7 +498,7 @@ struct F8Columns {
   __device__ __forceinline__ int64_t rows() const { return m; }
   __device__ __forceinline__ int64_t cols() const { return n; }
   template <int kCols>
-  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const PairBox& box) const {
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const F8Box& box) const {
     const int64_t o = row0 + box.lane;
     const bool in = o < m;
     const int here = in ? (int)(n - col < kCols ? n - col : kCols) : 0;  // may be negative
@@ -444,8 +515,8 @@ struct F8Operand {
 };
 
 // early: the kernel before may still run when this one starts.
-template <bool kARows, bool kBRows, int kN, int kWeights, class Epi>
-cudaError_t fp8_pair_launch(F8Operand a, F8Operand b, int64_t K, const PairWork& work, const F8Scales& sc, const F8Join& join,
+template <bool kARows, bool kBRows, int kN, int kWeights, bool kJoin, class Epi>
+cudaError_t fp8_pair_launch_as(F8Operand a, F8Operand b, int64_t K, const PairWork& work, const F8Scales& sc, const F8Join& join,
                             const Epi& epi, bool early, int32_t* status, cudaStream_t stream, int32_t first_status) {
   using Shape = F8Shape<kN, kWeights != 2, kWeights != 1, Epi::kBoxes>;
   CUtensorMap ma, mb;
@@ -455,7 +526,7 @@ cudaError_t fp8_pair_launch(F8Operand a, F8Operand b, int64_t K, const PairWork&
   if (e == cudaSuccess)
     e = make_tensor_map(&mb, kBRows ? TileMap{b.p, type, K, b.rows, b.ld, kF8K, kN / 2, true}
                                     : TileMap{b.p, type, b.rows, K, b.ld, kN / 2, kF8K, true});
-  auto kernel = fp8_pair_kernel<kARows, kBRows, kN, kWeights, Epi>;
+  auto kernel = fp8_pair_kernel<kARows, kBRows, kN, kWeights, kJoin, Epi>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -469,6 +540,13 @@ cudaError_t fp8_pair_launch(F8Operand a, F8Operand b, int64_t K, const PairWork&
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, ma, mb, work, sc, join, epi, status, first_status);
+}
+template <bool kARows, bool kBRows, int kN, int kWeights, class Epi>
+cudaError_t fp8_pair_launch(F8Operand a, F8Operand b, int64_t K, const PairWork& work, const F8Scales& sc, const F8Join& join,
+                            const Epi& epi, bool early, int32_t* status, cudaStream_t stream, int32_t first_status) {
+  if (kN == 256 && kWeights == 2 && work.parts == 1)
+    return fp8_pair_launch_as<kARows, kBRows, kN, kWeights, false>(a, b, K, work, sc, join, epi, early, status, stream, first_status);
+  return fp8_pair_launch_as<kARows, kBRows, kN, kWeights, true>(a, b, K, work, sc, join, epi, early, status, stream, first_status);
 }
 
 }  // namespace bakron

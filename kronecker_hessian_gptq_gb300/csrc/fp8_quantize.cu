@@ -2,7 +2,7 @@
 // 128 of a column, or block of 128 x 128 (see fp8_codes.cuh).
 //
 // Bound by memory: values are read once, into registers, their maxima taken
-// there, and the codes written.  Along rows a warp takes 256 values of a row.
+// there, and the codes written.  Along rows a warp takes 512 values of a row.
 // Otherwise a block takes 128 x 128 values, 8 x 8 a thread; one read of them
 // gives the codes along rows, the codes along columns and the columns' sums
 // (what the backward pass of a product needs of its output's gradient).
@@ -15,6 +15,7 @@ namespace bakron {
 namespace {
 
 constexpr int kCodeThreads = 256;
+constexpr int kTileThreads = 512;
 
 // 8 values from x[i] on, those past n as zeros.  Vectors where the rows allow.
 template <class T>
@@ -46,6 +47,9 @@ __device__ __forceinline__ void clear_words(const Clear& c) {
     c.word[i] = 0;
 }
 
+// A warp takes 512 values of a row, 16 a lane: the block's scale, two divisions,
+// is then computed for 16 values.  It goes from place to place by adding: a
+// division of 64 bits costs as much as the codes.
 template <class T>
 __global__ void __launch_bounds__(kCodeThreads) row_codes_kernel(const T* X, int64_t rows, int64_t cols, int64_t ldx, bool vec,
                                                                  uint8_t* codes, int64_t ldc, bool vec_codes, float* scales,
@@ -53,22 +57,36 @@ __global__ void __launch_bounds__(kCodeThreads) row_codes_kernel(const T* X, int
   asm volatile("griddepcontrol.launch_dependents;\n");
   clear_words(clear);
   const int lane = threadIdx.x & 31;
-  const int64_t per = (cols + 255) / 256, units = rows * per, step = (int64_t)gridDim.x * (kCodeThreads / 32);
-  for (int64_t u = (int64_t)blockIdx.x * (kCodeThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
-    const int64_t r = u / per, k = (u - r * per) * 256 + lane * 8;
-    float v[8];
-    values8(X + r * ldx, k, cols, vec, v);
+  const int64_t per = (cols + 511) / 512, first = (int64_t)blockIdx.x * (kCodeThreads / 32) + (threadIdx.x >> 5);
+  const int64_t step = (int64_t)gridDim.x * (kCodeThreads / 32);
+  auto over = [&](int64_t x) { return (x | per) >> 32 ? x / per : (int64_t)((uint32_t)x / (uint32_t)per); };
+  const int64_t step_rows = over(step), step_cols = step - step_rows * per;
+  int64_t row = over(first), col = first - row * per;
+  while (row < rows) {
+    const int64_t k = col * 512 + lane * 16;
+    float v[2][8];
+    values8(X + row * ldx, k, cols, vec, v[0]);
+    values8(X + row * ldx, k + 8, cols, vec, v[1]);
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[i]));
+    for (int i = 0; i < 16; ++i) top = max(top, magnitude(v[i / 8][i % 8]));
 #pragma unroll
-    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     float scale, inv;
     block_scale(top, scale, inv);
     if (k < cols) {
-      put_codes8(codes + r * ldc, k, cols, vec_codes, fp8_codes8(v, inv));
-      if ((lane & 15) == 0) scales[r * scale_row + (k >> 7) * scale_col] = scale;
+      uint8_t* to = codes + row * ldc;
+      const uint2 a = fp8_codes8(v[0], inv), b = fp8_codes8(v[1], inv);
+      if (vec_codes && k + 16 <= cols) {
+        *reinterpret_cast<uint4*>(to + k) = make_uint4(a.x, a.y, b.x, b.y);
+      } else {
+        put_codes8(to, k, cols, false, a);
+        put_codes8(to, k + 8, cols, false, b);
+      }
+      if ((lane & 7) == 0) scales[row * scale_row + (k >> 7) * scale_col] = scale;
     }
+    row += step_rows, col += step_cols;
+    if (col >= per) ++row, col -= per;
   }
 }
 
@@ -88,18 +106,20 @@ struct TileCodes {
   Clear clear;
 };
 template <class T>
-__global__ void __launch_bounds__(kCodeThreads) tile_codes_kernel(const T* X, const __grid_constant__ TileCodes p) {
-  __shared__ uint32_t tops[8][128];
-  __shared__ float sums[8][128];
+__global__ void __launch_bounds__(kTileThreads, 2) tile_codes_kernel(const T* X, const __grid_constant__ TileCodes p) {
+  constexpr int kWarps = kTileThreads / 32, kRows = 128 / (kTileThreads / 16), kEach = 128 / kRows;  // rows of a thread, kEach apart
+  __shared__ uint32_t tops[kWarps][128];
+  __shared__ float sums[kWarps][128];
   __shared__ float down_inv[128];
+  asm volatile("griddepcontrol.launch_dependents;\n");
   clear_words(p.clear);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane & 15;
   const int64_t tiles_n = (p.cols + 127) / 128, tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
-  const int64_t r0 = tm * 128 + (threadIdx.x >> 4), k = tn * 128 + part * 8;  // rows r0, r0 + 16, ..
-  float v[8][8];
+  const int64_t r0 = tm * 128 + (threadIdx.x >> 4), k = tn * 128 + part * 8;  // rows r0, r0 + kEach, ..
+  float v[kRows][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 16 * i;
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t r = r0 + kEach * i;
     if (r < p.rows) {
       values8(X + r * p.ldx, k, p.cols, p.vec, v[i]);
     } else {
@@ -110,7 +130,7 @@ __global__ void __launch_bounds__(kCodeThreads) tile_codes_kernel(const T* X, co
   uint32_t all = 0;
   if (p.along || p.whole) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[i][e]));
@@ -120,7 +140,7 @@ __global__ void __launch_bounds__(kCodeThreads) tile_codes_kernel(const T* X, co
       for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       float scale, inv;
       block_scale(top, scale, inv);
-      const int64_t r = r0 + 16 * i;
+      const int64_t r = r0 + kEach * i;
       if (r < p.rows && k < p.cols) {
         put_codes8(p.along + r * p.ld_along, k, p.cols, p.vec_along, fp8_codes8(v[i], inv));
         if (part == 0) p.along_scales[r * p.along_row + tn * p.along_col] = scale;
@@ -132,13 +152,13 @@ __global__ void __launch_bounds__(kCodeThreads) tile_codes_kernel(const T* X, co
     if (lane == 0) tops[0][warp] = all;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) all = max(all, tops[0][w]);
+    for (int w = 0; w < kWarps; ++w) all = max(all, tops[0][w]);
     float scale, inv;
     block_scale(all, scale, inv);
     if (threadIdx.x == 0) p.whole_scales[tm * p.whole_row + tn] = scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = r0 + 16 * i;
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = r0 + kEach * i;
       if (r < p.rows && k < p.cols) put_codes8(p.whole + r * p.ld_whole, k, p.cols, p.vec_whole, fp8_codes8(v[i], inv));
     }
     __syncthreads();
@@ -147,19 +167,27 @@ __global__ void __launch_bounds__(kCodeThreads) tile_codes_kernel(const T* X, co
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint32_t top = 0;
-    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[i][e])), s += v[i][e];
+    for (int i = 0; i < kRows; ++i) top = max(top, magnitude(v[i][e]));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    s += __shfl_xor_sync(0xffffffffu, s, 16);
-    if (lane < 16) tops[warp][part * 8 + e] = top, sums[warp][part * 8 + e] = s;
+    if (lane < 16) tops[warp][part * 8 + e] = top;
+    if (p.sums) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) s += v[i][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      if (lane < 16) sums[warp][part * 8 + e] = s;
+    }
   }
   __syncthreads();
   if (threadIdx.x < 128) {
     uint32_t top = 0;
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) top = max(top, tops[w][threadIdx.x]), s += sums[w][threadIdx.x];
+    for (int w = 0; w < kWarps; ++w) {
+      top = max(top, tops[w][threadIdx.x]);
+      if (p.sums) s += sums[w][threadIdx.x];
+    }
     float scale, inv;
     block_scale(top, scale, inv);
     down_inv[threadIdx.x] = inv;
@@ -175,8 +203,8 @@ __global__ void __launch_bounds__(kCodeThreads) tile_codes_kernel(const T* X, co
 #pragma unroll
   for (int e = 0; e < 8; ++e) inv[e] = down_inv[part * 8 + e];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 16 * i;
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t r = r0 + kEach * i;
     if (r < p.rows && k < p.cols)
       put_codes8(p.down + r * p.ld_down, k, p.cols, p.vec_down,
                  make_uint2(fp8_pair(v[i][0], v[i][1], inv[0], inv[1]) | (fp8_pair(v[i][2], v[i][3], inv[2], inv[3]) << 16),
@@ -200,17 +228,18 @@ cudaError_t codes_typed(const Fp8Codes& q, cudaStream_t stream) {
   auto in8 = [](const void* p, int64_t ld) { return aligned_to(p, 8) && ld % 8 == 0; };
   const Clear clear{static_cast<uint32_t*>(q.clear), (int)q.clear_words};
   if (q.along && !q.down && !q.whole && !q.sums) {
-    const int64_t units = q.rows * ((q.cols + 255) / 256);
-    const unsigned grid = (unsigned)std::min<int64_t>((units + kCodeThreads / 32 - 1) / (kCodeThreads / 32), 152 * 8 * 4);
+    const int64_t units = q.rows * ((q.cols + 511) / 512);
+    const unsigned grid = (unsigned)std::min<int64_t>((units + kCodeThreads / 32 - 1) / (kCodeThreads / 32), 1 << 20);
     row_codes_kernel<T><<<grid, kCodeThreads, 0, stream>>>(X, q.rows, q.cols, q.ldx, vec, q.along, q.ld_along,
-                                                          in8(q.along, q.ld_along), q.along_scales, q.along_row, q.along_col, clear);
+                                                          aligned_to(q.along, 16) && q.ld_along % 16 == 0, q.along_scales, q.along_row,
+                                                          q.along_col, clear);
     return cudaGetLastError();
   }
   const int64_t tiles = (q.rows + 127) / 128 * ((q.cols + 127) / 128);
   const TileCodes p{q.rows, q.cols, q.ldx, vec, q.along, q.down, q.whole, q.ld_along, q.ld_down, q.ld_whole,
                     in8(q.along, q.ld_along), in8(q.down, q.ld_down), in8(q.whole, q.ld_whole), q.along_scales,
                     q.down_scales, q.whole_scales, q.along_row, q.along_col, q.down_pitch, q.whole_row, q.sums, clear};
-  tile_codes_kernel<T><<<(unsigned)tiles, kCodeThreads, 0, stream>>>(X, p);
+  tile_codes_kernel<T><<<(unsigned)tiles, kTileThreads, 0, stream>>>(X, p);
   return cudaGetLastError();
 }
 
