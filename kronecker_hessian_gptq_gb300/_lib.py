@@ -126,18 +126,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def load_marshal():
-    """The helper that reads lists of torch tensors (torch has to be imported first), loaded once.  Its calls hold
-    the interpreter's lock."""
+    """The module that makes calls on torch tensors natively (torch has to be imported first), loaded once."""
     global _marshal
     if _marshal is None:
+        load()
         path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
         if not os.path.exists(path):
             raise RuntimeError(f"_marshal.so not found at {path}: build it first "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
-        lib = ctypes.PyDLL(path)
-        lib.bakron_py_adamw_tensors.restype = _int
-        lib.bakron_py_adamw_tensors.argtypes = [ctypes.py_object] * 7 + [_i64, _int, _vp]
-        _marshal = lib
+        from . import _marshal as module
+
+        if not module.bind(LIB_PATH):
+            raise RuntimeError(f"{path} finds no entry points in {LIB_PATH}: build them again")
+        _marshal = module
     return _marshal
 
 

@@ -6,6 +6,10 @@ and the AdamW step over many tensors.
 In the manner of the layer operators (_layers.py): torch tensors are marshalled
 into the C ABI, work is enqueued on the current stream (or stream=), no call is
 recorded by autograd, and zero tokens are allowed everywhere.
+
+The calls are made natively (csrc/marshal.cpp) where nothing is wrong with
+their arguments; what is not handled there comes back as None and goes through
+the checks here, which say what is wrong, and ctypes.
 """
 
 from __future__ import annotations
@@ -22,6 +26,15 @@ _E4M3 = torch.float8_e4m3fn
 _E4M3_CODE = 4
 _BLOCKS = ((1, 128), (128, 1), (128, 128))
 _GROUP = 256  # values that share a scale in 8-bit optimizer states
+
+
+_native = None
+
+
+def _fast():
+    global _native
+    _native = _lib.load_marshal()
+    return _native
 
 
 def _ceil(a, b):
@@ -84,6 +97,9 @@ def fp8_matmul(X, codes, scales, x_scales=None, bias=None, dtype=None, stream=No
     int32[1])."""
     if stream is not None:
         return _on(stream, fp8_matmul, X, codes, scales, x_scales, bias, dtype)
+    done = (_native or _fast()).fp8_matmul(X, codes, scales, x_scales, bias, -1 if dtype is None else _CODES.get(dtype, 9))
+    if done is not None:
+        return done
     T, K, ldx, device = _matrix(X, "X", _VALUES_OR_CODES)
     at = X.device
     p, ldc, w, N = _weights(codes, scales, K, None, device)
@@ -123,6 +139,9 @@ def fp8_matmul_backward(dY, X, codes, scales, bias=False, stream=None):
     bias=True; None for what there is no gradient of."""
     if stream is not None:
         return _on(stream, fp8_matmul_backward, dY, X, codes, scales, bias)
+    done = (_native or _fast()).fp8_matmul_backward(dY, X, codes, scales, bias)
+    if done is not None:
+        return done
     T, N, lddy, device = _matrix(dY, "dY", _CODES)
     at, dtype = dY.device, dY.dtype
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
@@ -205,6 +224,9 @@ def head_norm_rotary(Q, K, positions, freqs, q_weight=None, k_weight=None, eps=1
     "neighbours" (2 i, 2 i + 1).  Returns (YQ, YK), dense; YK None without K."""
     if stream is not None:
         return _on(stream, head_norm_rotary, Q, K, positions, freqs, q_weight, k_weight, eps, pairs)
+    done = (_native or _fast()).head_norm_rotary(Q, K, positions, freqs, q_weight, k_weight, eps, _PAIRS.get(pairs))
+    if done is not None:
+        return done
     T, D, device = _shape_of_heads(Q)
     dtype, at = Q.dtype, Q.device
     q, qt, qh, hq = _heads(Q, "Q", (dtype,), T, D, device)
@@ -230,6 +252,9 @@ def head_norm_rotary_backward(dYQ, dYK, Q, K, positions, freqs, q_weight=None, k
     there is no gradient of."""
     if stream is not None:
         return _on(stream, head_norm_rotary_backward, dYQ, dYK, Q, K, positions, freqs, q_weight, k_weight, eps, pairs)
+    done = (_native or _fast()).head_norm_rotary_backward(dYQ, dYK, Q, K, positions, freqs, q_weight, k_weight, eps, _PAIRS.get(pairs))
+    if done is not None:
+        return done
     T, D, device = _shape_of_heads(Q)
     dtype, at = Q.dtype, Q.device
     q, qt, qh, hq = _heads(Q, "Q", (dtype,), T, D, device)
@@ -357,8 +382,8 @@ def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, we
     count = len(params)
     eight = "m_scales" in states
     packed = ctypes.create_string_buffer(count * _TENSOR.size)
-    if _lib.load_marshal().bakron_py_adamw_tensors(params, grads, lists["m"], lists["v"], lists.get("m_scales"), lists.get("v_scales"),
-                                                   lists.get("copies"), count, device, packed):
+    if not (_native or _fast()).adamw_tensors(params, grads, lists["m"], lists["v"], lists.get("m_scales"), lists.get("v_scales"),
+                                              lists.get("copies"), device, ctypes.addressof(packed)):
         _pack(packed, params, lists, eight, device)
     rate, rate_dev = _number(lr, "lr", _F32, device)
     number, step_dev = _number(step, "step", torch.int64, device)

@@ -3,8 +3,8 @@
 The translation units under csrc/ compile in parallel to objects in
 _build/, then link into kronecker_hessian_gptq_gb300/libbakron.so.  A build
 is skipped when the library is newer than every source and header.  Beside it
-_marshal.so (csrc/marshal.cpp, g++, against torch's own headers) turns lists of
-torch tensors into what the C ABI takes.
+_marshal.so (csrc/marshal.cpp, g++, against torch's own headers) is the Python
+module that makes the calls for which ctypes is too slow.
 """
 
 from __future__ import annotations
@@ -57,7 +57,8 @@ def _marshal_command(out: str) -> list:
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     return [cxx, "-O1", "-std=c++17", "-shared", "-fPIC", os.path.join(CSRC, "marshal.cpp"), "-o", out, "-I", INCLUDE,
             "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-            "-I", sysconfig.get_paths()["include"], "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:

@@ -47,7 +47,7 @@ struct AdamConstants {
   float b1, c1, b2, c2, eps, root, rate, decay, grad;
   uint32_t key;  // of the seed and the step
   // The same in pairs for 8-bit states, with squares kLarger times as large.
-  F2 pb1, pc1, pb2, pc2, peps, proot, prate, pdecay, pgrad;
+  F2 pb1, pc1, pb2, pc2, peps, proot, prate, pdecay, pgrad, one;
 };
 struct AdamEntry {
   void* p;
@@ -171,11 +171,27 @@ __device__ __forceinline__ float more_of_lower(uint32_t x) {
   return __uint_as_float((((x << 7) ^ (x >> 9)) & 0x7fff80u) | 0x3e000000u);
 }
 
+__device__ __forceinline__ F2 fma2_rz(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// The roots of two numbers that are 0 or at least 2^-101: the approximate
+// reciprocal root and one step of Newton's method with the exact residual y - s^2,
+// which leaves the nearest number but for one in 10^5.  No number for an infinity.
+__device__ __forceinline__ F2 roots(F2 y) {
+  float a[2], r[2];
+  split(y, a[0], a[1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) asm("rsqrt.approx.ftz.f32 %0, %1;\n" : "=f"(r[h]) : "f"(fmaxf(a[h], 3.9443045e-31f)));
+  const F2 over = f2(r[0], r[1]), s = y * over;
+  return fma2(fma2(s, s, y * f2(-1.f)), over * f2(-0.5f), s);
+}
 // Two values |q| <= 448 on the numbers of e4m3 at or below |q| + r step, r the
 // random 16 bits as a fraction, with q's sign.  With e the power of two below q,
 // at least 2^-6, a step is e / 8: q + (1 + r) step is cut to whole steps by adding
-// e 2^20, whose last place is a step, towards zero; then that and the one step
-// are taken off again.  more: (1 + r) / 8.
+// e 2^20, whose last place is a step, towards zero (both sums: what is cut twice
+// is cut once); then that and the one step are taken off again.  more: (1 + r) / 8.
 template <bool kSigned>
 __device__ __forceinline__ F2 cut_at_random(F2 q, F2 more) {
   float x[2], e[2];
@@ -185,9 +201,7 @@ __device__ __forceinline__ F2 cut_at_random(F2 q, F2 more) {
     const uint32_t u = __float_as_uint(x[h]), least = max(u & 0x7f800000u, 0x3c800000u);
     e[h] = __uint_as_float(kSigned ? least | (u & 0x80000000u) : least);
   }
-  const F2 each = f2(e[0], e[1]), t = fma2(each, more, q), up = f2(1048576.f);
-  F2 s;
-  asm("fma.rz.f32x2 %0, %1, %2, %3;\n" : "=l"(s.v) : "l"(each.v), "l"(up.v), "l"(t.v));
+  const F2 each = f2(e[0], e[1]), s = fma2_rz(each, f2(1048576.f), fma2_rz(each, more, q));
   return fma2(each, f2(-1048576.125f), s);
 }
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
@@ -213,6 +227,15 @@ __device__ __forceinline__ bool step_of(const AdamConstants& c, float g, float& 
   p = fmaf(x * over, -c.rate, p * c.decay);
   m = x, v = y;
   return true;
+}
+// New moments and roots of two values, the roots kRootLarger times as large.  Each
+// product and sum is rounded by itself (a sum as x one + y, which the compiler
+// leaves alone), so that what a code is cut from is what the formula in elementary
+// fp32 operations gives: a code that is cut the other way, over one unit in the
+// last place, is off by a whole step of e4m3.
+__device__ __forceinline__ void moments(const AdamConstants& c, F2 g, F2& m, F2& root) {
+  m = fma2(m * c.pb1, c.one, g * c.pc1);
+  root = roots(fma2(root * root * c.pb2, c.one, g * g * c.pc2));
 }
 // The codes of a thread's eight values of the warp's group, and lane 0 the scales.
 // mt, rt: the largest |m| and root (kRootLarger times as large) of the thread.
@@ -272,22 +295,36 @@ __device__ __noinline__ bool step_of_group(const AdamConstants& c, const AdamEnt
   __syncwarp();  // the scales are written below
   bool bad = false;
   float mt = 0.f, rt = 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < 4; ++k) {
-    float gs[2], ps[2], ms[2], rs[2];
-    split(g[k], gs[0], gs[1]);
+    const F2 gk = g[k] * c.pgrad;
+    F2 m1 = m[k], r1 = root[k];
+    moments(c, gk, m1, r1);
+    float gs[2], ps[2], ms[2], rs[2], mn[2], rn[2];
+    split(gk, gs[0], gs[1]);
     split(p[k], ps[0], ps[1]);
     split(m[k], ms[0], ms[1]);
     split(root[k], rs[0], rs[1]);
+    split(m1, mn[0], mn[1]);
+    split(r1, rn[0], rn[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float v = rs[h] * rs[h];
-      if (!step_of(c, gs[h], ps[h], ms[h], v, rs[h])) {
+      // Squares that only the larger ones cannot hold: the root of the others.
+      const float y = __fadd_rn(__fmul_rn(__fmul_rn(rs[h], rs[h]), c.b2), __fmul_rn(__fmul_rn(gs[h], gs[h]), c.c2));
+      if (!(rn[h] < INFINITY)) rn[h] = sqrtf(y) * kRootLarger;
+      float d, over, n0, p0, p1, other;
+      split(fma2(f2(rn[h]), c.proot, c.peps), d, other);
+      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(over) : "f"(d));
+      split(c.prate, n0, other);
+      split(c.pdecay, p0, other);
+      p1 = fmaf(mn[h] * over, n0, ps[h] * p0);
+      if (fabsf(mn[h]) < INFINITY && y < INFINITY) {
+        ps[h] = p1, ms[h] = mn[h], rs[h] = rn[h];
+      } else {  // it stays what it is
         bad = true;
         if (!(fabsf(ms[h]) < INFINITY)) ms[h] = 0.f;
-        if (!(rs[h] < INFINITY)) rs[h] = 0.f;
+        rs[h] = rs[h] < INFINITY ? rs[h] * kRootLarger : 0.f;
       }
-      rs[h] *= kRootLarger;
       mt = fmaxf(mt, fabsf(ms[h])), rt = fmaxf(rt, rs[h]);
     }
     p[k] = f2(ps[0], ps[1]), m[k] = f2(ms[0], ms[1]), root[k] = f2(rs[0], rs[1]);
@@ -360,22 +397,19 @@ __global__ void __launch_bounds__(kAdamThreads, k8 ? 4 : 3)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const F2 gk = g[k] * c.pgrad;
-        m[k] = fma2(gk, c.pc1, m[k] * c.pb1);
-        float y[2], r[2], d[2], o[2], x[2];
-        split(fma2(gk * gk, c.pc2, root[k] * root[k] * c.pb2), y[0], y[1]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) asm("sqrt.approx.ftz.f32 %0, %1;\n" : "=f"(r[h]) : "f"(y[h]));
-        root[k] = f2(r[0], r[1]);
+        moments(c, gk, m[k], root[k]);
+        float r[2], d[2], o[2], x[2];
+        split(root[k], r[0], r[1]);
         split(fma2(root[k], c.proot, c.peps), d[0], d[1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(o[h]) : "f"(d[h]));
         p[k] = fma2(m[k] * f2(o[0], o[1]), c.prate, p[k] * c.pdecay);
-        odd = fma2(m[k], f2(0.f), odd);  // not 0 where one is not finite
+        odd = fma2(m[k], f2(0.f), fma2(root[k], f2(0.f), odd));  // not 0 where one is not finite
         split(m[k], x[0], x[1]);
         mt = fmaxf(mt, fmaxf(fabsf(x[0]), fabsf(x[1])));
         rt = fmaxf(rt, fmaxf(r[0], r[1]));
       }
-      if (__any_sync(0xffffffffu, !(sum(odd) == 0.f && rt < INFINITY))) {
+      if (__any_sync(0xffffffffu, sum(odd) != 0.f)) {
         bad |= step_of_group(c, e, i);
       } else {
         put_params(e, i, p);
@@ -405,6 +439,7 @@ __host__ __device__ inline AdamConstants constants(double lr, double step, doubl
   c.key = (uint32_t)seed * kMixA + (uint32_t)(uint64_t)step * kMixB;
   c.pb1 = both(c.b1), c.pc1 = both(c.c1), c.pb2 = both(c.b2 * kLarger), c.pc2 = both(c.c2 * kLarger), c.peps = both(c.eps);
   c.proot = both(c.root / kRootLarger), c.prate = both(-c.rate), c.pdecay = both(c.decay), c.pgrad = both(c.grad);
+  c.one = both(1.f);
   return c;
 }
 // Where the step or a factor is on the device.

@@ -1,76 +1,346 @@
-// marshal.cpp -- lists of torch tensors as the array of bakron_adamw_tensor that
-// bakron_adamw takes.  A step over 130 small tensors takes the GPU about ten
-// microseconds; reading five attributes of 520 tensors from Python takes 250.
+// marshal.cpp -- the calls of a projection in 8-bit floats from Python without
+// Python's price: checks of a dozen tensors, three allocations and a call with
+// twenty arguments take 18 us through ctypes, of which the GPU works 3 for one
+// token's heads; here about 6.  The same for the lists of AdamW: reading five
+// attributes of 520 tensors takes 250 us from Python, 10 here.
 //
-// Called with the interpreter's lock held (ctypes.PyDLL).  Nothing is raised here:
-// 0 when every tensor is what it has to be, else 1, and the caller's own
-// checks, in Python, say what is wrong.
+// Nothing is raised: a call that is not handled (an argument that is not what it
+// has to be, no tokens, an error) returns None, and the checks and the call
+// through ctypes, in _projection.py, follow and say what is wrong.
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
 
 #include "bakron.h"
 
 namespace {
 
-// Dense on the device, of `n` values; -1 for any number.
-const at::Tensor* dense(PyObject* o, int device, int64_t n) {
-  if (!THPVariable_Check(o)) return nullptr;
-  const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous() || (n >= 0 && t.numel() != n)) return nullptr;
-  return &t;
+// The library's entry points, as the caller has loaded them.
+struct Entries {
+  decltype(&bakron_fp8_matmul) fp8;
+  decltype(&bakron_fp8_matmul_workspace_size) fp8_size;
+  decltype(&bakron_fp8_matmul_backward) fp8_back;
+  decltype(&bakron_fp8_matmul_backward_workspace_size) fp8_back_size;
+  decltype(&bakron_head_norm_rotary) heads;
+  decltype(&bakron_head_norm_rotary_backward) heads_back;
+  decltype(&bakron_head_norm_rotary_backward_workspace_size) heads_back_size;
+} lib;
+bool bound = false;
+
+template <class F>
+bool find(void* handle, const char* name, F& f) {
+  f = reinterpret_cast<F>(dlsym(handle, name));
+  return f != nullptr;
 }
-int float_code(const at::Tensor& t) {
+
+constexpr int kE4M3 = BAKRON_E4M3;
+// 0, 1, 2 for the float types, 4 for e4m3, -1 for others.
+int code_of(const at::Tensor& t) {
   switch (t.scalar_type()) {
     case at::kFloat: return BAKRON_F32;
     case at::kHalf: return BAKRON_F16;
     case at::kBFloat16: return BAKRON_BF16;
+    case at::kFloat8_e4m3fn: return kE4M3;
     default: return -1;
   }
 }
+at::ScalarType type_of(int code) { return code == BAKRON_F32 ? at::kFloat : code == BAKRON_F16 ? at::kHalf : at::kBFloat16; }
+bool is_float(int code) { return code >= 0 && code <= 2; }
 
-int pack(PyObject* const* lists, Py_ssize_t count, int device, bakron_adamw_tensor* out) {
-  enum { kParams, kGrads, kM, kV, kMScales, kVScales, kCopies, kLists };
-  for (int l = 0; l < kLists; ++l) {
-    if (lists[l] == Py_None) continue;
-    if (!PyList_Check(lists[l]) || PyList_GET_SIZE(lists[l]) != count) return 1;
+const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+// Dense on the device, of `n` values; -1 for any number.
+const at::Tensor* dense(PyObject* o, int device, int64_t n) {
+  const at::Tensor* t = tensor(o);
+  if (!t || !t->is_cuda() || t->get_device() != device || !t->is_contiguous() || (n >= 0 && t->numel() != n)) return nullptr;
+  return t;
+}
+// A matrix with contiguous rows; its row stride (that of a lone row is its length).
+struct Matrix {
+  const at::Tensor* t = nullptr;
+  int64_t rows = 0, cols = 0, ld = 0;
+  void* p = nullptr;
+};
+bool matrix(PyObject* o, Matrix& m) {
+  m.t = tensor(o);
+  if (!m.t || !m.t->is_cuda() || m.t->dim() != 2) return false;
+  m.rows = m.t->size(0), m.cols = m.t->size(1);
+  if (m.rows < 1 || m.cols < 1 || (m.cols > 1 && m.t->stride(1) != 1)) return false;
+  m.ld = m.rows > 1 ? m.t->stride(0) : m.cols;
+  m.p = m.t->data_ptr();
+  return m.ld >= m.cols;
+}
+// A dense vector or matrix of n values of a type, or None (null).
+bool values(PyObject* o, at::ScalarType type, int64_t dim, int64_t first, int64_t n, int device, const void** p) {
+  *p = nullptr;
+  if (o == Py_None) return true;
+  const at::Tensor* t = dense(o, device, n);
+  if (!t || t->scalar_type() != type || t->dim() != dim || t->size(0) != first) return false;
+  *p = t->data_ptr();
+  return true;
+}
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+at::Tensor room(at::IntArrayRef size, at::ScalarType type, int device) {
+  return at::detail::empty_cuda(size, type, at::Device(at::kCUDA, device), std::nullopt);
+}
+void* stream_on(int device) { return c10::cuda::getCurrentCUDAStream(device).stream(); }
+bool ready(int device) { return bound && c10::cuda::current_device() == device; }
+PyObject* wrap(const at::Tensor& t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+// A tuple or a value of a dict; takes the references.
+PyObject* pair(PyObject* a, PyObject* b) {
+  PyObject* r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return r;
+}
+bool put(PyObject* dict, const char* key, const at::Tensor& t) {
+  PyObject* v = wrap(t);
+  const bool ok = v && PyDict_SetItemString(dict, key, v) == 0;
+  Py_XDECREF(v);
+  return ok;
+}
+
+// Weights in e4m3 or bytes with a scale for each 128 x 128.
+struct Weights {
+  Matrix codes;
+  const void* scales = nullptr;
+  int copies = 0;
+};
+bool weights(PyObject* codes, PyObject* scales, int64_t K, int device, Weights& w) {
+  if (!matrix(codes, w.codes) || w.codes.cols != K || w.codes.t->get_device() != device) return false;
+  const at::ScalarType type = w.codes.t->scalar_type();
+  if (type != at::kFloat8_e4m3fn && type != at::kChar && type != at::kByte) return false;
+  if (scales == Py_None || !values(scales, at::kFloat, 2, blocks(w.codes.rows), blocks(w.codes.rows) * blocks(K), device, &w.scales))
+    return false;
+  w.copies = reinterpret_cast<uintptr_t>(w.codes.p) % 16 || w.codes.ld % 16;
+  return true;
+}
+
+// (X, codes, scales, x_scales, bias, type of Y or -1)
+PyObject* fp8_matmul(PyObject* const* a) {
+  Matrix x;
+  Weights w;
+  const long want = PyLong_AsLong(a[5]);
+  if (!matrix(a[0], x)) return nullptr;
+  const int device = x.t->get_device(), kind = code_of(*x.t);
+  if (kind < 0 || want > 2 || !ready(device) || !weights(a[1], a[2], x.cols, device, w)) return nullptr;
+  const int64_t T = x.rows, K = x.cols, N = w.codes.rows;
+  const void *xs, *bias;
+  if ((kind == kE4M3) == (a[3] == Py_None) || !values(a[3], at::kFloat, 2, T, T * blocks(K), device, &xs) ||
+      !values(a[4], at::kFloat, 1, N, N, device, &bias))
+    return nullptr;
+  const int out = want >= 0 ? (int)want : kind == kE4M3 ? BAKRON_F32 : kind;
+  const at::Tensor y = room({T, N}, type_of(out), device), status = room({1}, at::kInt, device);
+  const size_t bytes = lib.fp8_size(T, K, N, kind, w.copies);
+  if (!bytes) return nullptr;
+  const at::Tensor ws = room({(int64_t)bytes}, at::kByte, device);
+  if (lib.fp8(x.p, kind, x.ld, static_cast<const float*>(xs), static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
+              static_cast<const float*>(w.scales), static_cast<const float*>(bias), T, K, N, y.data_ptr(), out, ws.data_ptr(), bytes,
+              static_cast<int32_t*>(status.data_ptr()), stream_on(device)))
+    return nullptr;
+  return pair(wrap(y), wrap(status));
+}
+
+// (dY, X, codes, scales, bias)
+PyObject* fp8_matmul_backward(PyObject* const* a) {
+  Matrix dy, x;
+  Weights w;
+  if (!matrix(a[0], dy)) return nullptr;
+  const int device = dy.t->get_device(), kind = code_of(*dy.t);
+  const at::Tensor* codes = tensor(a[2]);
+  if (!is_float(kind) || !ready(device) || !codes || codes->dim() != 2) return nullptr;
+  const int64_t T = dy.rows, N = dy.cols, K = codes->size(1);
+  if (!weights(a[2], a[3], K, device, w) || w.codes.rows != N) return nullptr;
+  const bool has_x = a[1] != Py_None, has_bias = PyObject_IsTrue(a[4]) == 1;
+  if (has_x && (!matrix(a[1], x) || x.rows != T || x.cols != K || x.t->get_device() != device || code_of(*x.t) != kind)) return nullptr;
+  const at::Tensor dx = room({T, K}, type_of(kind), device), status = room({1}, at::kInt, device);
+  at::Tensor dw, dbias;
+  if (has_x) dw = room({N, K}, type_of(kind), device);
+  if (has_bias) dbias = room({N}, at::kFloat, device);
+  const size_t bytes = lib.fp8_back_size(T, K, N, 1 + 2 * has_x + 4 * has_bias, w.copies);
+  if (!bytes) return nullptr;
+  const at::Tensor ws = room({(int64_t)bytes}, at::kByte, device);
+  if (lib.fp8_back(dy.p, dy.ld, x.p, x.ld, kind, static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
+                   static_cast<const float*>(w.scales), T, K, N, dx.data_ptr(), has_x ? dw.data_ptr() : nullptr,
+                   has_bias ? static_cast<float*>(dbias.data_ptr()) : nullptr, ws.data_ptr(), bytes,
+                   static_cast<int32_t*>(status.data_ptr()), stream_on(device)))
+    return nullptr;
+  PyObject* d = PyDict_New();
+  if (!d || !put(d, "X", dx) || !put(d, "W", dw) || !put(d, "bias", dbias)) {
+    Py_XDECREF(d);
+    return nullptr;
   }
-  const bool eight = lists[kMScales] != Py_None;
+  return pair(d, wrap(status));
+}
+
+// T x heads x D with contiguous values; the strides of a lone token or head do not count.
+struct Heads {
+  void* p = nullptr;
+  int64_t T = 0, heads = 0, D = 0, token = 0, head = 0;
+};
+bool heads_of(PyObject* o, at::ScalarType type, int device, Heads& h) {
+  const at::Tensor* t = tensor(o);
+  if (!t || !t->is_cuda() || t->dim() != 3 || t->scalar_type() != type || t->get_device() != device) return false;
+  h = {t->data_ptr(), t->size(0), t->size(1), t->size(2), 0, 0};
+  if (h.T < 1 || h.heads < 1 || h.D < 1 || (h.D > 1 && t->stride(2) != 1)) return false;
+  h.token = h.T > 1 ? t->stride(0) : 0, h.head = h.heads > 1 ? t->stride(1) : 0;
+  return true;
+}
+// What both directions take: (Q, K, positions, freqs, q_weight, k_weight, eps, pairs).
+struct Norm {
+  Heads q, k;
+  const void *qw, *kw, *positions, *freqs;
+  int64_t R = 0;
+  float eps;
+  int pairs, kind, device;
+  at::ScalarType type;
+};
+bool norm_of(PyObject* const* a, Norm& n) {
+  const at::Tensor* q = tensor(a[0]);
+  if (!q || !q->is_cuda()) return false;
+  n.kind = code_of(*q), n.device = q->get_device(), n.type = q->scalar_type();
+  if (!is_float(n.kind) || !ready(n.device) || !heads_of(a[0], n.type, n.device, n.q)) return false;
+  if (a[1] != Py_None && (!heads_of(a[1], n.type, n.device, n.k) || n.k.T != n.q.T || n.k.D != n.q.D)) return false;
+  if (a[1] == Py_None && a[5] != Py_None) return false;
+  if ((a[2] == Py_None) != (a[3] == Py_None)) return false;
+  if (a[3] != Py_None) {
+    const at::Tensor* f = tensor(a[3]);
+    if (!f || f->dim() != 1) return false;
+    n.R = 2 * f->size(0);
+  }
+  const int64_t D = n.q.D;
+  const double eps = PyFloat_AsDouble(a[6]);
+  n.eps = (float)eps, n.pairs = (int)PyLong_AsLong(a[7]);
+  return n.R <= D && !PyErr_Occurred() && values(a[2], at::kLong, 1, n.q.T, n.q.T, n.device, &n.positions) &&
+         values(a[3], at::kDouble, 1, n.R / 2, n.R / 2, n.device, &n.freqs) && values(a[4], at::kFloat, 1, D, D, n.device, &n.qw) &&
+         values(a[5], at::kFloat, 1, D, D, n.device, &n.kw);
+}
+PyObject* head_norm_rotary(PyObject* const* a) {
+  Norm n;
+  if (!norm_of(a, n)) return nullptr;
+  const at::Tensor yq = room({n.q.T, n.q.heads, n.q.D}, n.type, n.device);
+  at::Tensor yk;
+  if (n.k.p) yk = room({n.k.T, n.k.heads, n.k.D}, n.type, n.device);
+  if (lib.heads(n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token, n.k.head, n.k.heads, static_cast<const float*>(n.qw),
+                static_cast<const float*>(n.kw), static_cast<const int64_t*>(n.positions), static_cast<const double*>(n.freqs), n.R,
+                n.pairs, n.eps, n.kind, n.q.T, n.q.D, yq.data_ptr(), n.k.p ? yk.data_ptr() : nullptr, stream_on(n.device)))
+    return nullptr;
+  return pair(wrap(yq), wrap(yk));
+}
+// (dYQ, dYK, then as above)
+PyObject* head_norm_rotary_backward(PyObject* const* a) {
+  Norm n;
+  Heads dq, dk;
+  if (!norm_of(a + 2, n) || !heads_of(a[0], n.type, n.device, dq) || dq.T != n.q.T || dq.heads != n.q.heads || dq.D != n.q.D)
+    return nullptr;
+  if ((a[1] == Py_None) != (n.k.p == nullptr)) return nullptr;
+  if (n.k.p && (!heads_of(a[1], n.type, n.device, dk) || dk.T != n.k.T || dk.heads != n.k.heads || dk.D != n.k.D)) return nullptr;
+  const at::Tensor gq = room({n.q.T, n.q.heads, n.q.D}, n.type, n.device);
+  at::Tensor gk, gqw, gkw;
+  if (n.k.p) gk = room({n.k.T, n.k.heads, n.k.D}, n.type, n.device);
+  if (n.qw) gqw = room({n.q.D}, at::kFloat, n.device);
+  if (n.kw) gkw = room({n.q.D}, at::kFloat, n.device);
+  const size_t bytes = lib.heads_back_size(n.q.T, n.q.D);
+  if (!bytes) return nullptr;
+  const at::Tensor ws = room({(int64_t)bytes}, at::kByte, n.device);
+  auto at = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  if (lib.heads_back(dq.p, dq.token, dq.head, dk.p, dk.token, dk.head, n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token,
+                     n.k.head, n.k.heads, static_cast<const float*>(n.qw), static_cast<const float*>(n.kw),
+                     static_cast<const int64_t*>(n.positions), static_cast<const double*>(n.freqs), n.R, n.pairs, n.eps, n.kind, n.q.T,
+                     n.q.D, at(gq), at(gk), static_cast<float*>(at(gqw)), static_cast<float*>(at(gkw)), ws.data_ptr(), bytes,
+                     stream_on(n.device)))
+    return nullptr;
+  PyObject* d = PyDict_New();
+  if (!d || !put(d, "Q", gq) || !put(d, "K", gk) || !put(d, "q_weight", gqw) || !put(d, "k_weight", gkw)) {
+    Py_XDECREF(d);
+    return nullptr;
+  }
+  return d;
+}
+
+// (params, grads, m, v, m_scales, v_scales, copies, device, address): the array of
+// bakron_adamw_tensor at the address; the three before the device may be None.
+PyObject* adamw_tensors(PyObject* const* a) {
+  enum { kParams, kGrads, kM, kV, kMScales, kVScales, kCopies, kLists };
+  if (!PyList_Check(a[kParams])) return nullptr;
+  const Py_ssize_t count = PyList_GET_SIZE(a[kParams]);
+  for (int l = 1; l < kLists; ++l)
+    if (a[l] != Py_None && (!PyList_Check(a[l]) || PyList_GET_SIZE(a[l]) != count)) return nullptr;
+  const int device = (int)PyLong_AsLong(a[kLists]);
+  auto* out = static_cast<bakron_adamw_tensor*>(PyLong_AsVoidPtr(a[kLists + 1]));
+  const bool eight = a[kMScales] != Py_None;
+  if (!out || eight != (a[kVScales] != Py_None)) return nullptr;
   const at::ScalarType state = eight ? at::kFloat8_e4m3fn : at::kFloat;
   for (Py_ssize_t i = 0; i < count; ++i) {
-    auto item = [&](int l) { return PyList_GET_ITEM(lists[l], i); };
+    auto item = [&](int l) { return PyList_GET_ITEM(a[l], i); };
     bakron_adamw_tensor& e = out[i];
     e = {};
     const at::Tensor* p = dense(item(kParams), device, -1);
-    if (!p) return 1;
+    if (!p) return nullptr;
     e.n = p->numel();
     const at::Tensor *g = dense(item(kGrads), device, e.n), *m = dense(item(kM), device, e.n), *v = dense(item(kV), device, e.n);
-    if (!g || !m || !v || m->scalar_type() != state || v->scalar_type() != state) return 1;
-    e.param_dtype = float_code(*p), e.grad_dtype = float_code(*g);
-    if (e.param_dtype < 0 || e.grad_dtype < 0) return 1;
+    if (!g || !m || !v || m->scalar_type() != state || v->scalar_type() != state) return nullptr;
+    e.param_dtype = code_of(*p), e.grad_dtype = code_of(*g);
+    if (!is_float(e.param_dtype) || !is_float(e.grad_dtype)) return nullptr;
     e.param = p->data_ptr(), e.grad = g->data_ptr(), e.m = m->data_ptr(), e.v = v->data_ptr();
     if (eight) {
       const int64_t groups = (e.n + 255) / 256;
       const at::Tensor *ms = dense(item(kMScales), device, groups), *vs = dense(item(kVScales), device, groups);
-      if (!ms || !vs || ms->scalar_type() != at::kFloat || vs->scalar_type() != at::kFloat) return 1;
+      if (!ms || !vs || ms->scalar_type() != at::kFloat || vs->scalar_type() != at::kFloat) return nullptr;
       e.m_scales = static_cast<float*>(ms->data_ptr()), e.v_scales = static_cast<float*>(vs->data_ptr());
     }
-    if (lists[kCopies] != Py_None && item(kCopies) != Py_None) {
+    if (a[kCopies] != Py_None && item(kCopies) != Py_None) {
       const at::Tensor* c = dense(item(kCopies), device, e.n);
-      if (!c || float_code(*c) <= BAKRON_F32) return 1;
-      e.copy = c->data_ptr(), e.copy_dtype = float_code(*c);
+      if (!c || code_of(*c) < 1 || code_of(*c) > 2) return nullptr;
+      e.copy = c->data_ptr(), e.copy_dtype = code_of(*c);
     }
   }
-  return 0;
+  Py_RETURN_TRUE;
 }
+
+template <PyObject* (*kCall)(PyObject* const*), int kArgs>
+PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  PyObject* r = nullptr;
+  try {
+    if (n == kArgs) r = kCall(args);
+  } catch (...) {
+    r = nullptr;
+  }
+  if (r) return r;
+  PyErr_Clear();
+  Py_RETURN_NONE;
+}
+
+// The path of the library that the entry points are taken from.
+PyObject* bind(PyObject*, PyObject* path) {
+  const char* p = PyUnicode_AsUTF8(path);
+  if (!p) return nullptr;
+  void* h = dlopen(p, RTLD_NOW | RTLD_LOCAL);
+  bound = h && find(h, "bakron_fp8_matmul", lib.fp8) && find(h, "bakron_fp8_matmul_workspace_size", lib.fp8_size) &&
+          find(h, "bakron_fp8_matmul_backward", lib.fp8_back) &&
+          find(h, "bakron_fp8_matmul_backward_workspace_size", lib.fp8_back_size) && find(h, "bakron_head_norm_rotary", lib.heads) &&
+          find(h, "bakron_head_norm_rotary_backward", lib.heads_back) &&
+          find(h, "bakron_head_norm_rotary_backward_workspace_size", lib.heads_back_size);
+  return PyBool_FromLong(bound);
+}
+
+#define CALL(name, args) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(guarded<name, args>)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
+                         CALL(fp8_matmul, 6),
+                         CALL(fp8_matmul_backward, 5),
+                         CALL(head_norm_rotary, 8),
+                         CALL(head_norm_rotary_backward, 10),
+                         CALL(adamw_tensors, 9),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-// lists: params, grads, m, v, m_scales, v_scales, copies; the last three may be None.
-extern "C" int bakron_py_adamw_tensors(PyObject* params, PyObject* grads, PyObject* m, PyObject* v, PyObject* m_scales,
-                                       PyObject* v_scales, PyObject* copies, int64_t count, int device, void* out) {
-  PyObject* const lists[] = {params, grads, m, v, m_scales, v_scales, copies};
-  try {
-    return pack(lists, count, device, static_cast<bakron_adamw_tensor*>(out));
-  } catch (...) {
-    return 1;
-  }
-}
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__marshal(void) { return PyModule_Create(&module); }

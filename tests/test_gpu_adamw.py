@@ -380,3 +380,36 @@ def test_refusals(bk):  # noqa: F811
     with pytest.raises(RuntimeError):  # the parameter as its own gradient
         bk.adamw(p, p, s32, 1)
     assert bool((p[0] == 1).all())
+
+
+def test_codes_are_those_of_elementary_operations(bk):  # noqa: F811
+    """Four million values against torch's fp32 products, sums, root and quotients, each rounded by itself.  At most one
+    root in 10^5 is a neighbour of the nearest number, and a cut notices a last place in one of 10^5 at most (16 steps of
+    2^-24 of a value): fewer than one code here, and four scales."""
+    import torch
+
+    n = 1 << 22
+    gen = torch.Generator("cuda").manual_seed(3)
+    rand = lambda: torch.randn(n, generator=gen, device="cuda")  # noqa: E731
+    p, g = [0.02 * rand()], [(1e-3 * torch.exp(rand()) * rand()).bfloat16()]
+    states = bk.adamw_states(p, 8)
+    (b1, b2), t = ARGS["betas"], ARGS["step"]
+    for turn in range(2):
+        m = states["m"][0].float().view(-1, GROUP) * states["m_scales"][0][:, None]
+        v = (states["v"][0].float().view(-1, GROUP) * states["v_scales"][0][:, None]).square()
+        x = g[0].float().view(-1, GROUP) * ARGS["grad_scale"]
+        m = m * b1 + x * (1 - b1)
+        root = (v * b2 + x * x * (1 - b2)).sqrt()
+        bk.adamw(p, g, states, seed=turn, **ARGS)
+        bits = _bits(torch.arange(n, device="cuda"), turn, t, 0).view(-1, GROUP)
+        for name, y, b in (("m", m, bits >> 16), ("v", root, bits & 0xFFFF)):
+            top = y.abs().amax(1)
+            scale = top / torch.full_like(top, 448.0)
+            q = (y.abs() * (1 / scale)[:, None])
+            u = q.view(torch.int32)
+            code = torch.where(q >= 2.0 ** -6, ((u + (b.int() << 4)) >> 20) - 960, (q * 512 + b.float() * 2.0 ** -16).int()).clamp(max=126)
+            code = torch.where((q > 0) & (code == 0), 1, code) if name == "v" else code
+            got = states[name][0].view(torch.uint8).view(-1, GROUP)
+            assert int((states[name + "_scales"][0] != scale).sum()) <= 4
+            assert int(((got & 127) != code).sum()) <= 4
+        g[0].mul_(-0.5)
