@@ -373,18 +373,20 @@ def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, we
                 t.record_stream(stream)
         with torch.cuda.stream(stream):
             return adamw(params, grads, states, step, lr, betas, eps, weight_decay, grad_scale, copies, skip, seed)
-    if not params or not isinstance(params[0], torch.Tensor) or not params[0].is_cuda:
-        raise ValueError("params must be CUDA tensors, at least one")
-    device, at = params[0].get_device(), params[0].device
     lists = {"grads": grads, **{k: list(l) for k, l in states.items()}}
     if copies is not None:
         lists["copies"] = list(copies)
-    count = len(params)
     eight = "m_scales" in states
+    done = (_native or _fast()).adamw(params, grads, lists["m"], lists["v"], lists.get("m_scales"), lists.get("v_scales"),
+                                      lists.get("copies"), step, lr, betas[0], betas[1], eps, weight_decay, grad_scale, skip, seed)
+    if done is not None:
+        return done
+    if not params or not isinstance(params[0], torch.Tensor) or not params[0].is_cuda:
+        raise ValueError("params must be CUDA tensors, at least one")
+    device, at = params[0].get_device(), params[0].device
+    count = len(params)
     packed = ctypes.create_string_buffer(count * _TENSOR.size)
-    if not (_native or _fast()).adamw_tensors(params, grads, lists["m"], lists["v"], lists.get("m_scales"), lists.get("v_scales"),
-                                              lists.get("copies"), device, ctypes.addressof(packed)):
-        _pack(packed, params, lists, eight, device)
+    _pack(packed, params, lists, eight, device)
     rate, rate_dev = _number(lr, "lr", _F32, device)
     number, step_dev = _number(step, "step", torch.int64, device)
     scale, scale_dev = _number(grad_scale, "grad_scale", _F32, device)

@@ -179,7 +179,7 @@ int bakron_quantize_blocks(const void* X, int dtype, int64_t T, int64_t K, int64
     q.down = codes, q.ld_down = ldc, q.down_scales = scales, q.down_pitch = K;
   else
     return BAKRON_ERR_INVALID_ARG;
-  return from_cuda(bakron::fp8_codes_launch(q, (cudaStream_t)stream));
+  return from_cuda(bakron::fp8_codes_launch(q, nullptr, (cudaStream_t)stream));
 }
 
 size_t bakron_fp8_matmul_workspace_size(int64_t T, int64_t K, int64_t N, int x_dtype, int copies) {

@@ -460,17 +460,24 @@ int sm_count() {
 size_t adamw_workspace_bytes() { return 256; }
 
 bool adamw_all_different(const bakron_adamw_tensor* tensors, int64_t count) {
-  std::unique_ptr<const void*[]> all(new (std::nothrow) const void*[4 * count + 1]);
-  if (!all) return false;
-  int64_t n = 0;
+  // A table of at least twice as many places as addresses; an address goes to the next free one.
+  uint64_t size = 64;
+  while (size < (uint64_t)count * 8) size *= 2;
+  std::unique_ptr<const void*[]> seen(new (std::nothrow) const void*[size]());
+  if (!seen) return false;
+  auto fresh = [&](const void* p) {
+    if (!p) return true;
+    uint64_t i = (reinterpret_cast<uintptr_t>(p) >> 4) * 0x9E3779B97F4A7C15ull >> 20 & (size - 1);
+    for (; seen[i]; i = (i + 1) & (size - 1))
+      if (seen[i] == p) return false;
+    seen[i] = p;
+    return true;
+  };
   for (int64_t i = 0; i < count; ++i) {
     const bakron_adamw_tensor& t = tensors[i];
-    if (t.n == 0) continue;
-    all[n++] = t.param, all[n++] = t.m, all[n++] = t.v;
-    if (t.copy) all[n++] = t.copy;
+    if (t.n && !(fresh(t.param) && fresh(t.m) && fresh(t.v) && fresh(t.copy))) return false;
   }
-  std::sort(all.get(), all.get() + n);
-  return std::adjacent_find(all.get(), all.get() + n) == all.get() + n;
+  return true;
 }
 
 namespace {

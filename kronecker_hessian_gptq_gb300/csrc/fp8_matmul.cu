@@ -127,7 +127,7 @@ cudaError_t forward(const Fp8Matmul& p, char* ws, int32_t* status, cudaStream_t 
     q.along_scales = scales;
     q.along_row = 1, q.along_col = f.pitch;
     q.clear = arrived, q.clear_words = words;
-    e = fp8_codes_launch(q, stream);
+    e = fp8_codes_launch(q, nullptr, stream);
   } else {
     if (on_16(p.X, p.ldx))
       codes = p.X, ldc = p.ldx;
@@ -207,7 +207,10 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
   q.down_pitch = b.pitch_n;
   if (p.dbias) q.sums = floats(b.sums);
   q.clear = arrived, q.clear_words = (int64_t)b.arrived_words;
-  cudaError_t e = fp8_codes_launch(q, stream);
+  Fp8Codes x = {};
+  x.X = p.X, x.dtype = p.dtype, x.rows = p.T, x.cols = p.K, x.ldx = p.ldx;
+  if (p.dW) x.down = at(b.down_x), x.ld_down = up16(p.K), x.down_scales = floats(b.down_x_scales), x.down_pitch = b.pitch_k;
+  cudaError_t e = fp8_codes_launch(q, p.dW ? &x : nullptr, stream);
   if (e == cudaSuccess && p.dbias) e = fp8_column_sums_launch(floats(b.sums), blocks_of(p.T), b.pitch_n, p.N, p.dbias, stream);
   auto rows = [&](void* y, int64_t m, int64_t n) {
     F8Rows<T> epi{{}, m, n, nullptr, static_cast<T*>(y), false};
@@ -230,10 +233,6 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
                                                           sc, F8Join{floats(b.join), arrived}, epi, !copy && !p.dbias, status, stream, 0);
   }
   if (e == cudaSuccess && p.dW) {
-    Fp8Codes x = {};
-    x.X = p.X, x.dtype = p.dtype, x.rows = p.T, x.cols = p.K, x.ldx = p.ldx;
-    x.down = at(b.down_x), x.ld_down = up16(p.K), x.down_scales = floats(b.down_x_scales), x.down_pitch = b.pitch_k;
-    e = fp8_codes_launch(x, stream);
     const F8Scales sc{q.down_scales, x.down_scales, b.pitch_n, b.pitch_k, 0, 0};
     const F8Rows<T> epi = rows(p.dW, p.N, p.K);
     if (p.dX) arrived += arrived_bytes(b.dx) / 4;

@@ -171,6 +171,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   const int pairs = gridDim.x / 2, mine = blockIdx.x / 2, units = work.units();
   bool broken = false;
 
+  // Blocks of a kernel that may start early take the SMs that this one's leave.
+  asm volatile("griddepcontrol.launch_dependents;\n");
   // This early nothing can have been reported.
   if (first_status >= 0 && blockIdx.x == 0 && threadIdx.x == 0) *status = first_status;
   if (threadIdx.x == 0) {

@@ -106,15 +106,20 @@ struct TileCodes {
   Clear clear;
 };
 template <class T>
-__global__ void __launch_bounds__(kTileThreads, 2) tile_codes_kernel(const T* X, const __grid_constant__ TileCodes p) {
+__global__ void __launch_bounds__(kTileThreads, 2) tile_codes_kernel(const T* X, const __grid_constant__ TileCodes first, const T* second_X,
+                                                                      const __grid_constant__ TileCodes second, int64_t split) {
+  // The tiles of one matrix, then those of the other.
+  const bool other = blockIdx.x >= split;
+  const TileCodes& p = other ? second : first;
+  if (other) X = second_X;
   constexpr int kWarps = kTileThreads / 32, kRows = 128 / (kTileThreads / 16), kEach = 128 / kRows;  // rows of a thread, kEach apart
   __shared__ uint32_t tops[kWarps][128];
   __shared__ float sums[kWarps][128];
   __shared__ float down_inv[128];
   asm volatile("griddepcontrol.launch_dependents;\n");
-  clear_words(p.clear);
+  clear_words(first.clear);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane & 15;
-  const int64_t tiles_n = (p.cols + 127) / 128, tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
+  const int64_t tile = (int64_t)blockIdx.x - (other ? split : 0), tiles_n = (p.cols + 127) / 128, tm = tile / tiles_n, tn = tile - tm * tiles_n;
   const int64_t r0 = tm * 128 + (threadIdx.x >> 4), k = tn * 128 + part * 8;  // rows r0, r0 + kEach, ..
   float v[kRows][8];
 #pragma unroll
@@ -222,34 +227,39 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* parts, in
 }
 
 template <class T>
-cudaError_t codes_typed(const Fp8Codes& q, cudaStream_t stream) {
-  const T* X = static_cast<const T*>(q.X);
-  const bool vec = aligned_to(q.X, 16) && q.ldx % (16 / (int64_t)sizeof(T)) == 0;
+TileCodes tile_codes(const Fp8Codes& q) {
   auto in8 = [](const void* p, int64_t ld) { return aligned_to(p, 8) && ld % 8 == 0; };
-  const Clear clear{static_cast<uint32_t*>(q.clear), (int)q.clear_words};
-  if (q.along && !q.down && !q.whole && !q.sums) {
+  return TileCodes{q.rows, q.cols, q.ldx, aligned_to(q.X, 16) && q.ldx % (16 / (int64_t)sizeof(T)) == 0, q.along, q.down, q.whole,
+                   q.ld_along, q.ld_down, q.ld_whole, in8(q.along, q.ld_along), in8(q.down, q.ld_down), in8(q.whole, q.ld_whole),
+                   q.along_scales, q.down_scales, q.whole_scales, q.along_row, q.along_col, q.down_pitch, q.whole_row, q.sums,
+                   Clear{static_cast<uint32_t*>(q.clear), (int)q.clear_words}};
+}
+int64_t tiles_of(const Fp8Codes& q) { return (q.rows + 127) / 128 * ((q.cols + 127) / 128); }
+template <class T>
+cudaError_t codes_typed(const Fp8Codes& q, const Fp8Codes* other, cudaStream_t stream) {
+  const T* X = static_cast<const T*>(q.X);
+  if (!other && q.along && !q.down && !q.whole && !q.sums) {
     const int64_t units = q.rows * ((q.cols + 511) / 512);
     const unsigned grid = (unsigned)std::min<int64_t>((units + kCodeThreads / 32 - 1) / (kCodeThreads / 32), 1 << 20);
-    row_codes_kernel<T><<<grid, kCodeThreads, 0, stream>>>(X, q.rows, q.cols, q.ldx, vec, q.along, q.ld_along,
-                                                          aligned_to(q.along, 16) && q.ld_along % 16 == 0, q.along_scales, q.along_row,
-                                                          q.along_col, clear);
+    row_codes_kernel<T><<<grid, kCodeThreads, 0, stream>>>(
+        X, q.rows, q.cols, q.ldx, aligned_to(q.X, 16) && q.ldx % (16 / (int64_t)sizeof(T)) == 0, q.along, q.ld_along,
+        aligned_to(q.along, 16) && q.ld_along % 16 == 0, q.along_scales, q.along_row, q.along_col,
+        Clear{static_cast<uint32_t*>(q.clear), (int)q.clear_words});
     return cudaGetLastError();
   }
-  const int64_t tiles = (q.rows + 127) / 128 * ((q.cols + 127) / 128);
-  const TileCodes p{q.rows, q.cols, q.ldx, vec, q.along, q.down, q.whole, q.ld_along, q.ld_down, q.ld_whole,
-                    in8(q.along, q.ld_along), in8(q.down, q.ld_down), in8(q.whole, q.ld_whole), q.along_scales,
-                    q.down_scales, q.whole_scales, q.along_row, q.along_col, q.down_pitch, q.whole_row, q.sums, clear};
-  tile_codes_kernel<T><<<(unsigned)tiles, kTileThreads, 0, stream>>>(X, p);
+  const int64_t split = tiles_of(q), tiles = split + (other ? tiles_of(*other) : 0);
+  tile_codes_kernel<T><<<(unsigned)tiles, kTileThreads, 0, stream>>>(X, tile_codes<T>(q), other ? static_cast<const T*>(other->X) : X,
+                                                                     tile_codes<T>(other ? *other : q), split);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t fp8_codes_launch(const Fp8Codes& q, cudaStream_t stream) {
+cudaError_t fp8_codes_launch(const Fp8Codes& q, const Fp8Codes* other, cudaStream_t stream) {
   switch (q.dtype) {
-    case kF32: return codes_typed<float>(q, stream);
-    case kF16: return codes_typed<__half>(q, stream);
-    default: return codes_typed<__nv_bfloat16>(q, stream);
+    case kF32: return codes_typed<float>(q, other, stream);
+    case kF16: return codes_typed<__half>(q, other, stream);
+    default: return codes_typed<__nv_bfloat16>(q, other, stream);
   }
 }
 

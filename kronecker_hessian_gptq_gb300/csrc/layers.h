@@ -147,7 +147,8 @@ struct Fp8Codes {
   void* clear;  // words set to 0 by the same launch
   int64_t clear_words;
 };
-cudaError_t fp8_codes_launch(const Fp8Codes& q, cudaStream_t stream);
+// other: a second matrix of the same type in the same launch, or null.
+cudaError_t fp8_codes_launch(const Fp8Codes& q, const Fp8Codes* other, cudaStream_t stream);
 cudaError_t fp8_column_sums_launch(const float* parts, int64_t rows, int64_t pitch, int64_t cols, float* out, cudaStream_t stream);
 
 // fp8_matmul.cu

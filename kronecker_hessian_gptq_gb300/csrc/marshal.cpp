@@ -13,6 +13,7 @@
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <memory>
 #include <optional>
 
 #include "bakron.h"
@@ -28,6 +29,8 @@ struct Entries {
   decltype(&bakron_head_norm_rotary) heads;
   decltype(&bakron_head_norm_rotary_backward) heads_back;
   decltype(&bakron_head_norm_rotary_backward_workspace_size) heads_back_size;
+  decltype(&bakron_adamw) adamw;
+  decltype(&bakron_adamw_workspace_size) adamw_size;
 } lib;
 bool bound = false;
 
@@ -265,18 +268,49 @@ PyObject* head_norm_rotary_backward(PyObject* const* a) {
   return d;
 }
 
-// (params, grads, m, v, m_scales, v_scales, copies, device, address): the array of
-// bakron_adamw_tensor at the address; the three before the device may be None.
-PyObject* adamw_tensors(PyObject* const* a) {
+// A number, or a tensor of one value of the type (then its address).
+bool number(PyObject* o, at::ScalarType type, int device, double* value, const void** p) {
+  *p = nullptr, *value = 1;
+  if (const at::Tensor* t = tensor(o)) {
+    if (!t->is_cuda() || t->get_device() != device || t->scalar_type() != type || t->numel() != 1) return false;
+    *p = t->data_ptr();
+    return true;
+  }
+  *value = PyFloat_AsDouble(o);
+  return !PyErr_Occurred();
+}
+
+// (params, grads, m, v, m_scales, v_scales, copies, step, lr, beta1, beta2, eps, weight_decay, grad_scale, skip, seed);
+// the last three lists and skip may be None.
+PyObject* adamw(PyObject* const* a) {
   enum { kParams, kGrads, kM, kV, kMScales, kVScales, kCopies, kLists };
-  if (!PyList_Check(a[kParams])) return nullptr;
+  if (!PyList_Check(a[kParams]) || PyList_GET_SIZE(a[kParams]) < 1) return nullptr;
   const Py_ssize_t count = PyList_GET_SIZE(a[kParams]);
   for (int l = 1; l < kLists; ++l)
     if (a[l] != Py_None && (!PyList_Check(a[l]) || PyList_GET_SIZE(a[l]) != count)) return nullptr;
-  const int device = (int)PyLong_AsLong(a[kLists]);
-  auto* out = static_cast<bakron_adamw_tensor*>(PyLong_AsVoidPtr(a[kLists + 1]));
+  const at::Tensor* lead = tensor(PyList_GET_ITEM(a[kParams], 0));
+  if (!lead || !lead->is_cuda()) return nullptr;
+  const int device = lead->get_device();
   const bool eight = a[kMScales] != Py_None;
-  if (!out || eight != (a[kVScales] != Py_None)) return nullptr;
+  if (!ready(device) || eight != (a[kVScales] != Py_None)) return nullptr;
+  // The step as an integer: a double holds fewer.
+  PyObject* const* n = a + kLists;
+  double rate, scale, none;
+  const void *step_dev, *rate_dev, *scale_dev, *skip = nullptr;
+  long long step = 1;
+  if (tensor(n[0])) {
+    if (!number(n[0], at::kLong, device, &none, &step_dev)) return nullptr;
+  } else {
+    step_dev = nullptr, step = PyLong_AsLongLong(n[0]);
+  }
+  if (PyErr_Occurred() || step < 1 || !number(n[1], at::kFloat, device, &rate, &rate_dev) ||
+      !number(n[6], at::kFloat, device, &scale, &scale_dev) ||
+      (n[7] != Py_None && (!tensor(n[7]) || !number(n[7], at::kInt, device, &none, &skip))))
+    return nullptr;
+  const double b1 = PyFloat_AsDouble(n[2]), b2 = PyFloat_AsDouble(n[3]), eps = PyFloat_AsDouble(n[4]), decay = PyFloat_AsDouble(n[5]);
+  const uint64_t seed = PyLong_AsUnsignedLongLongMask(n[8]);
+  if (PyErr_Occurred()) return nullptr;
+  std::unique_ptr<bakron_adamw_tensor[]> out(new bakron_adamw_tensor[count]);
   const at::ScalarType state = eight ? at::kFloat8_e4m3fn : at::kFloat;
   for (Py_ssize_t i = 0; i < count; ++i) {
     auto item = [&](int l) { return PyList_GET_ITEM(a[l], i); };
@@ -302,7 +336,12 @@ PyObject* adamw_tensors(PyObject* const* a) {
       e.copy = c->data_ptr(), e.copy_dtype = code_of(*c);
     }
   }
-  Py_RETURN_TRUE;
+  const at::Tensor status = room({1}, at::kInt, device), ws = room({(int64_t)lib.adamw_size()}, at::kByte, device);
+  if (lib.adamw(out.get(), count, eight ? 8 : 32, rate, static_cast<const float*>(rate_dev), step, static_cast<const int64_t*>(step_dev),
+                b1, b2, eps, decay, scale, static_cast<const float*>(scale_dev), static_cast<const int32_t*>(skip), seed, ws.data_ptr(),
+                ws.numel(), static_cast<int32_t*>(status.data_ptr()), stream_on(device)))
+    return nullptr;
+  return wrap(status);
 }
 
 template <PyObject* (*kCall)(PyObject* const*), int kArgs>
@@ -327,7 +366,8 @@ PyObject* bind(PyObject*, PyObject* path) {
           find(h, "bakron_fp8_matmul_backward", lib.fp8_back) &&
           find(h, "bakron_fp8_matmul_backward_workspace_size", lib.fp8_back_size) && find(h, "bakron_head_norm_rotary", lib.heads) &&
           find(h, "bakron_head_norm_rotary_backward", lib.heads_back) &&
-          find(h, "bakron_head_norm_rotary_backward_workspace_size", lib.heads_back_size);
+          find(h, "bakron_head_norm_rotary_backward_workspace_size", lib.heads_back_size) && find(h, "bakron_adamw", lib.adamw) &&
+          find(h, "bakron_adamw_workspace_size", lib.adamw_size);
   return PyBool_FromLong(bound);
 }
 
@@ -337,7 +377,7 @@ PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
                          CALL(fp8_matmul_backward, 5),
                          CALL(head_norm_rotary, 8),
                          CALL(head_norm_rotary_backward, 10),
-                         CALL(adamw_tensors, 9),
+                         CALL(adamw, 16),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
