@@ -247,10 +247,11 @@ cudaError_t backward(const Fp8Backward& p, char* ws, int32_t* status, cudaStream
 }  // namespace
 
 size_t fp8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies) {
-  return forward_plan(T, K, N, copies).bytes;
+  return fp8_few_tokens(T, K, N) ? 256 : forward_plan(T, K, N, copies).bytes;
 }
 bool fp8_matmul_needs_copies(const Fp8Matmul& p) { return !on_16(p.V, p.ldv); }
 cudaError_t fp8_matmul_launch(const Fp8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream) {
+  if (fp8_few_tokens(p.T, p.K, p.N)) return fp8_rows(p, status_dev, stream);
   char* at = static_cast<char*>(ws);
   switch (p.y_dtype) {
     case kF32: return forward<float>(p, at, status_dev, stream);

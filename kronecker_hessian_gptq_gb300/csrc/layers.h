@@ -165,6 +165,10 @@ struct Fp8Matmul {
   void* Y;
   int y_dtype;
 };
+// fp8_rows.cu: few tokens, without a workspace.
+bool fp8_few_tokens(int64_t T, int64_t K, int64_t N);
+cudaError_t fp8_rows(const Fp8Matmul& p, int32_t* status_dev, cudaStream_t stream);
+
 size_t fp8_matmul_workspace_bytes(int64_t T, int64_t K, int64_t N, bool copies);
 bool fp8_matmul_needs_copies(const Fp8Matmul& p);
 cudaError_t fp8_matmul_launch(const Fp8Matmul& p, void* ws, int32_t* status_dev, cudaStream_t stream);
