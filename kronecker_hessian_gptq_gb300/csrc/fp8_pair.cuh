@@ -42,9 +42,11 @@ constexpr int kF8Smem = 226 * 1024;
 
 // Shared memory of a variant: stages, boxes for results in whole lines, scales
 // (of the columns, of the block's 128 rows).
-template <int kN, bool kColumns, bool kRows, bool kBoxes>
+template <int kN, bool kBRows, bool kColumns, bool kRows, bool kBoxes>
 struct F8Shape {
-  static constexpr int kA = 128 * kF8K, kB = kN / 2 * kF8K, kStage = kA + kB;
+  // Rows of B that a block copies: with its rows contiguous whole lines of 128, of which 64 may count.
+  static constexpr int kCopied = kBRows && kN < 256 ? 128 : kN / 2;
+  static constexpr int kA = 128 * kF8K, kB = kCopied * kF8K, kStage = kA + kB;
   static constexpr int kHalves = kN > 128 ? 2 : 1;  // products of half the columns each
   static constexpr int kBufs = kN > 128 ? 2 : 4;
   static constexpr int kCols = kN / (kF8Warps / 4);  // of a thread
@@ -125,10 +127,11 @@ __device__ __forceinline__ void arrive_if(bool p, uint32_t mbar) {
       : "memory");
 }
 
-// A warp with a box for each of two runs: only the box before the last has to have been read.
+// A warp's box for one of kRuns runs: only those before the last kRuns - 1 copies have to have been read.
+template <int kRuns>
 struct F8Box : PairBox {
   __device__ __forceinline__ void open() const {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(kRuns - 1) : "memory");
     __syncwarp();
   }
 };
@@ -158,7 +161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, PairWork work,
                     F8Scales sc, F8Join join, const __grid_constant__ Epi epi, int32_t* status, int32_t first_status) {
   constexpr bool kColumns = kWeights != 2, kRows = kWeights != 1;  // have scales of their own
-  using Shape = F8Shape<kN, kColumns, kRows, Epi::kBoxes>;
+  using Shape = F8Shape<kN, kBRows, kColumns, kRows, Epi::kBoxes>;
   static_assert(2 * kF8Warps * 32 * Shape::kCols == 256 * kN, "the slices make up a tile");
   constexpr int kStages = Shape::kStages, kBufs = Shape::kBufs, kHalves = Shape::kHalves, kCols = Shape::kCols;
   extern __shared__ unsigned char f8_smem_raw[];
@@ -426,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         float out[kRun];
 #pragma unroll
         for (int i = 0; i < kRun / 2; ++i) split(acc[run * (kRun / 2) + i], out[2 * i], out[2 * i + 1]);
-        epi(row0, col + 128 * run, out, F8Box{{boxes + (uint32_t)((warp - 4) * Shape::kBox + run * kPairBox), lane}});
+        epi(row0, col + 128 * run, out, F8Box<kRuns>{{boxes + (uint32_t)((warp - 4) * Shape::kBox + run * kPairBox), lane}});
       }
     }
     if (Epi::kBoxes && lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
@@ -455,8 +458,8 @@ struct F8Rows {
   bool tma;           // then n is a multiple of 8, and the bias starts on 16 bytes
   __device__ __forceinline__ int64_t rows() const { return m; }
   __device__ __forceinline__ int64_t cols() const { return n; }
-  template <int kCols>
-  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const F8Box& box) const {
+  template <int kCols, int kRuns>
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const F8Box<kRuns>& box) const {
     if (row0 >= m || col >= n) return;
     if constexpr (sizeof(T) == 2) {
       if (tma) {
@@ -499,8 +502,8 @@ struct F8Columns {
   T* y;               // n x m
   __device__ __forceinline__ int64_t rows() const { return m; }
   __device__ __forceinline__ int64_t cols() const { return n; }
-  template <int kCols>
-  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const F8Box& box) const {
+  template <int kCols, int kRuns>
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const F8Box<kRuns>& box) const {
     const int64_t o = row0 + box.lane;
     const bool in = o < m;
     const int here = in ? (int)(n - col < kCols ? n - col : kCols) : 0;  // may be negative
@@ -520,13 +523,13 @@ struct F8Operand {
 template <bool kARows, bool kBRows, int kN, int kWeights, bool kJoin, class Epi>
 cudaError_t fp8_pair_launch_as(F8Operand a, F8Operand b, int64_t K, const PairWork& work, const F8Scales& sc, const F8Join& join,
                             const Epi& epi, bool early, int32_t* status, cudaStream_t stream, int32_t first_status) {
-  using Shape = F8Shape<kN, kWeights != 2, kWeights != 1, Epi::kBoxes>;
+  using Shape = F8Shape<kN, kBRows, kWeights != 2, kWeights != 1, Epi::kBoxes>;
   CUtensorMap ma, mb;
   const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   cudaError_t e = make_tensor_map(&ma, kARows ? TileMap{a.p, type, K, a.rows, a.ld, kF8K, 128, true}
                                               : TileMap{a.p, type, a.rows, K, a.ld, 128, kF8K, true});
   if (e == cudaSuccess)
-    e = make_tensor_map(&mb, kBRows ? TileMap{b.p, type, K, b.rows, b.ld, kF8K, kN / 2, true}
+    e = make_tensor_map(&mb, kBRows ? TileMap{b.p, type, K, b.rows, b.ld, kF8K, Shape::kCopied, true}
                                     : TileMap{b.p, type, b.rows, K, b.ld, kN / 2, kF8K, true});
   auto kernel = fp8_pair_kernel<kARows, kBRows, kN, kWeights, kJoin, Epi>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes);
