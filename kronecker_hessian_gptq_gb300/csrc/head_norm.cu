@@ -78,7 +78,8 @@ struct Angles {
 __device__ __forceinline__ void fill_turns(const HeadNorm& p, const Angles& a) {
   for (int i = threadIdx.x; i < p.half; i += kHeadThreads) a.turn[i] = turn_of(p.freqs[i]);
 }
-__device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, int64_t t0, int tokens) {
+// The angles of so many tokens into the rows from `to` on.
+__device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, int64_t t0, int tokens, int to = 0) {
   const int wide = p.half < kHeadThreads ? p.half : kHeadThreads, rows = kHeadThreads / wide;
   const int row = threadIdx.x / wide, col = threadIdx.x - row * wide;
   if (row >= rows) return;
@@ -88,8 +89,8 @@ __device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, 
     for (int t = row; t < tokens; t += rows) {
       float c, s;
       cos_sin((uint64_t)p.positions[t0 + t] * turn, c, s);
-      a.cos[t * a.pitch + a.place(k)] = finite ? c : __int_as_float(0x7fffffff);
-      a.sin[t * a.pitch + a.place(k)] = finite ? s : __int_as_float(0x7fffffff);
+      a.cos[(to + t) * a.pitch + a.place(k)] = finite ? c : __int_as_float(0x7fffffff);
+      a.sin[(to + t) * a.pitch + a.place(k)] = finite ? s : __int_as_float(0x7fffffff);
     }
   }
 }
@@ -179,69 +180,84 @@ __device__ __forceinline__ float squares(const F2 (&a)[4], const F2 (&b)[4]) {
   return sum(q);
 }
 
-// A team takes one token of the tile and every `step`-th of its heads, so that
-// it goes from head to head by adding strides; two heads are on their way at a time.
+// A team takes one token of a tile and every `step`-th of its heads; two heads are
+// on their way at a time, from one tile into the next, and so are the next tile's
+// angles.
 template <class T, bool kNeighbours>
 __global__ void __launch_bounds__(kHeadThreads, sizeof(T) == 2 ? 4 : 3)
-    head_norm_kernel(const __grid_constant__ HeadNorm p, int tile_log, int lanes) {
+    head_norm_kernel(const __grid_constant__ HeadNorm p, int tile_log, int lanes, int tiles) {
   extern __shared__ __align__(16) unsigned char head_smem[];
   const int tile = 1 << tile_log;
-  const Angles angles(head_smem, p.half, tile);
-  const int64_t t0 = (int64_t)blockIdx.x << tile_log;
-  const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
+  const Angles angles(head_smem, p.half, 2 * tile);  // of two tiles in turn
   const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, each = (kHeadThreads / lanes) >> tile_log;
-  const int t = team & (tile - 1), slot = team >> tile_log, step = each * gridDim.y;
-  const bool live = 16 * j < p.D && t < tokens;
+  const int t = team & (tile - 1), slot = team >> tile_log, first = (int)blockIdx.y * each, step = each * gridDim.y;
+  const bool mine = 16 * j < p.D;
   const Place at = place_of<kNeighbours>(j, 2 * p.half);
   const float share = 1.f / (float)p.D;
   const int queries = p.side[0].heads, heads = queries + p.side[1].heads;
-  const T* xq = static_cast<const T*>(p.side[0].x) + (t0 + t) * p.side[0].x_token;
-  const T* xk = static_cast<const T*>(p.side[1].x) + (t0 + t) * p.side[1].x_token;
-  T* yq = static_cast<T*>(p.side[0].y) + (t0 + t) * queries * p.D;
-  T* yk = static_cast<T*>(p.side[1].y) + (t0 + t) * (heads - queries) * p.D;
   Raw8<T> lo[2] = {}, hi[2] = {};
-  auto fetch = [&](int h, int n) {
-    if (!live || h >= heads) return;  // what is there is not used, or zeros behind a head's end
-    const T* x = h < queries ? xq + h * p.side[0].x_head : xk + (h - queries) * p.side[1].x_head;
-    load8(x + at.lo, lo[n]);
-    load8(x + at.hi, hi[n]);
+  int ahead_q = blockIdx.x, ahead = first;  // what is fetched next
+  auto fetch = [&](int n) {
+    const int64_t token = ((int64_t)ahead_q << tile_log) + t;
+    const int h = ahead + slot;
+    if (mine && token < p.T && h < heads) {  // else what is there is not used, or zeros behind a head's end
+      const HeadSide& s = p.side[h >= queries];
+      const T* x = static_cast<const T*>(s.x) + token * s.x_token + (h < queries ? h : h - queries) * s.x_head;
+      load8(x + at.lo, lo[n]);
+      load8(x + at.hi, hi[n]);
+    }
+    ahead += step;
+    if (ahead >= heads) ahead = first, ahead_q += gridDim.x;
   };
-  int h = (int)blockIdx.y * each + slot;
-  fetch(h, 0);
-  fetch(h + step, 1);
+  auto fill = [&](int q, int buf) {
+    if (!p.half || q >= tiles) return;
+    const int64_t t0 = (int64_t)q << tile_log;
+    const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
+    fill_angles(p, angles, t0, tokens, buf * tile);
+  };
+  int q = blockIdx.x, base = first, buf = 0;
+  fetch(0);
+  if (ahead_q < tiles) fetch(1);
   if (p.half) {
     fill_turns(p, angles);
     __syncthreads();
-    fill_angles(p, angles, t0, tokens);
-    __syncthreads();
+    fill(q, 0);
   }
-  const float *cos = angles.cos + t * angles.pitch, *sin = angles.sin + t * angles.pitch;
   // All teams take the same number of turns: the exchanges are the whole warp's.
-  for (int base = (int)blockIdx.y * each; base < heads; base += 2 * step, h += 2 * step) {
+  while (q < tiles) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const int here = h + n * step;
+      if (q >= tiles) break;
+      if (base == first && p.half) {
+        __syncthreads();  // this tile's angles are there, the one's before are read
+        fill(q + gridDim.x, buf ^ 1);
+      }
       F2 a[4], b[4];
       open8<T>(lo[n], a);
       open8<T>(hi[n], b);
-      fetch(here + 2 * step, n);
-      const bool query = here < queries;
-      const float* weight = query ? p.side[0].w : p.side[1].w;
+      if (ahead_q < tiles) fetch(n);
+      const int64_t token = ((int64_t)q << tile_log) + t;
+      const int h = base + slot;
+      const HeadSide& s = p.side[h >= queries];
       const float r = rsqrtf(fmaf(team_sum(squares(a, b), lanes), share, p.eps));
-      if (!live || here >= heads) continue;
-      if (weight) {
-        F2 w[4];
-        load_f2(weight + at.lo, w);
+      if (mine && token < p.T && h < heads) {
+        if (s.w) {
+          F2 w[4];
+          load_f2(s.w + at.lo, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = a[i] * f2(r) * w[i];
-        load_f2(weight + at.hi, w);
+          for (int i = 0; i < 4; ++i) a[i] = a[i] * f2(r) * w[i];
+          load_f2(s.w + at.hi, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = b[i] * f2(r) * w[i];
+          for (int i = 0; i < 4; ++i) b[i] = b[i] * f2(r) * w[i];
+        }
+        const int row = (buf * tile + t) * angles.pitch;
+        turn_pairs<kNeighbours, false>(a, b, angles.cos + row, angles.sin + row, at.angle, p.half, angles.pitch);
+        T* y = static_cast<T*>(s.y) + (token * s.heads + (h < queries ? h : h - queries)) * p.D;
+        store8(y + at.lo, a);
+        store8(y + at.hi, b);
       }
-      turn_pairs<kNeighbours, false>(a, b, cos, sin, at.angle, p.half, angles.pitch);
-      T* y = query ? yq + here * p.D : yk + (here - queries) * p.D;
-      store8(y + at.lo, a);
-      store8(y + at.hi, b);
+      base += step;
+      if (base >= heads) base = first, q += gridDim.x, buf ^= 1;
     }
   }
 }
@@ -680,11 +696,18 @@ cudaError_t forward_typed(const HeadNorm& p, cudaStream_t stream) {
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((heads + each - 1) / each, kHeadBlocks / tiles));
   const dim3 grid((unsigned)tiles, (unsigned)parts);
   const size_t smem = Angles::bytes(p.half, 1 << tile_log);
+  // In runs, with fewer than eight heads for a team: no more blocks than the SMs hold at a time, each with as many
+  // tiles as any other or one less, so that one's start is behind another's heads (16384 tokens, 2 heads of 64: 9.4 us,
+  // else 11.5).  With more a tile is a block, and the SMs share them out (16384 tokens, 40 heads of 128: 64 us, else 75).
+  const bool few = runs && heads < 8 * each;
+  const int64_t most = few ? 152 * (sizeof(T) == 2 ? 4 : 3) : tiles, rounds = (tiles + most - 1) / most;
+  const dim3 walk((unsigned)((tiles + rounds - 1) / rounds), (unsigned)parts);
+  const size_t both = Angles::bytes(p.half, 2 << tile_log);
   const int pairs = pairs_of(p);
   if (runs && p.neighbours)
-    head_norm_kernel<T, true><<<grid, kHeadThreads, smem, stream>>>(p, tile_log, lanes);
+    head_norm_kernel<T, true><<<walk, kHeadThreads, both, stream>>>(p, tile_log, lanes, (int)tiles);
   else if (runs)
-    head_norm_kernel<T, false><<<grid, kHeadThreads, smem, stream>>>(p, tile_log, lanes);
+    head_norm_kernel<T, false><<<walk, kHeadThreads, both, stream>>>(p, tile_log, lanes, (int)tiles);
   else if (pairs <= 32)
     head_norm_any_kernel<T, 1><<<grid, kHeadThreads, smem, stream>>>(p, tile_log);
   else if (pairs <= 64)
