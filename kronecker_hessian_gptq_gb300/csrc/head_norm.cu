@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_any_kernel(const __gri
 // The blocks are shared out between queries and keys: the first blocks[0] walk
 // over the queries' tiles, the others over the keys', which have tiles of their
 // own.  So a block sums one weight's gradient, in registers, and leaves D
-// floats in `parts`.
+// floats in `parts`.  In runs the next tile's angles are computed behind this one's heads.
 struct HeadPlan {
   int tile_log[2], blocks[2];
   int64_t tiles[2];
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   extern __shared__ __align__(16) unsigned char head_smem[];
   const int k = (int)blockIdx.x >= plan.blocks[0], tile_log = plan.tile_log[k], tile = 1 << tile_log;
   const HeadSide& s = p.side[k];
-  const Angles angles(head_smem, p.half, tile);
+  const Angles angles(head_smem, p.half, 2 * tile);  // of two tiles in turn
   const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, step = (kHeadThreads / lanes) >> tile_log;
   const int t = team & (tile - 1), slot = team >> tile_log, heads = s.heads;
   const bool mine = 16 * j < p.D, normed = s.w;
@@ -402,17 +402,21 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   F2 dw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = f2(0.f);
+  auto tokens_of = [&](int64_t q) { return (int)(p.T - (q << tile_log) < tile ? p.T - (q << tile_log) : tile); };
   fetch(q, slot);
-  if (p.half) fill_turns(p, angles);
-  const float *cos = angles.cos + t * angles.pitch, *sin = angles.sin + t * angles.pitch;
-  for (; q < tiles; q += stride) {
+  if (p.half) {
+    fill_turns(p, angles);
+    __syncthreads();
+    if (q < tiles) fill_angles(p, angles, q << tile_log, tokens_of(q));
+  }
+  for (int buf = 0; q < tiles; q += stride, buf ^= 1) {
     const int64_t t0 = q << tile_log;
-    const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
+    const int tokens = tokens_of(q);
     if (p.half) {
-      __syncthreads();
-      fill_angles(p, angles, t0, tokens);
-      __syncthreads();
+      __syncthreads();  // this tile's angles are there, the one's before are read
+      if (q + stride < tiles) fill_angles(p, angles, (q + stride) << tile_log, tokens_of(q + stride), (buf ^ 1) * tile);
     }
+    const float *cos = angles.cos + (buf * tile + t) * angles.pitch, *sin = angles.sin + (buf * tile + t) * angles.pitch;
     T* out = static_cast<T*>(s.y) + (t0 + t) * heads * p.D;
     for (int base = 0; base < heads; base += step) {
       const int h = base + slot;
@@ -719,13 +723,13 @@ cudaError_t forward_typed(const HeadNorm& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// A side's tiles: of so many tokens that a team, of which a block has `teams`, has eight heads
+// A side's tiles: of so many tokens that a team, of which a block has `teams`, has four heads
 // of one between two barriers, and fewer where there would be less than a tile for a third of its blocks.  A
 // block takes as many tiles as any other, or one less.
 void plan_side(HeadPlan& plan, int k, int64_t T, int heads, int teams, int blocks) {
   if (heads == 0 || blocks == 0) return;
   int l = 0;
-  while ((2 << l) <= std::min(teams, kBackTile) && ((int64_t)heads << (l + 1)) <= 8 * teams) ++l;
+  while ((2 << l) <= std::min(teams, kBackTile) && ((int64_t)heads << (l + 1)) <= 4 * teams) ++l;
   while (l && (T + (1 << l) - 1) >> l < (blocks + 2) / 3) --l;
   plan.tile_log[k] = l;
   plan.tiles[k] = (T + (1 << l) - 1) >> l;
@@ -751,7 +755,7 @@ cudaError_t backward_typed(const HeadNorm& p, float* parts, cudaStream_t stream)
   const HeadPlan plan = backward_plan(p, teams, 152 * on_sm);
   const unsigned grid = (unsigned)(plan.blocks[0] + plan.blocks[1]);
   float* sums = p.side[0].dw || p.side[1].dw ? parts : nullptr;
-  const size_t angles = Angles::bytes(p.half, 1 << std::max(plan.tile_log[0], plan.tile_log[1]));
+  const size_t angles = Angles::bytes(p.half, (runs ? 2 : 1) << std::max(plan.tile_log[0], plan.tile_log[1]));
   const size_t smem = runs ? std::max(angles, (size_t)teams * p.D * 4) : angles + (size_t)teams * p.D * 4;
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel, auto... more) {
