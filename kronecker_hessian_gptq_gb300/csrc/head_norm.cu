@@ -15,8 +15,8 @@
 // takes a tile of tokens: their angles are computed once, into shared memory, for
 // the 40 or so heads, and a team keeps to one token and goes from head to head.
 // The next heads' values are on their way meanwhile.  bf16, 32 and 8 heads of 128:
-// 16384 tokens take 64 us (5.2 TB/s), backward 116 us (4.3 TB/s; with three blocks on
-// an SM in place of two, and so 80 registers and spills, 136).  What
+// 16384 tokens take 63 us (5.3 TB/s), backward 105 us (4.8 TB/s; with three blocks on
+// an SM in place of two, and so 80 registers and spills, 20 us more).  What
 // is not in such runs, or not on 16 bytes, takes a warp a head.
 //
 // An angle is kept as a share of a turn in 64-bit fixed point: p f / 2 pi
@@ -45,15 +45,16 @@ __device__ __forceinline__ uint64_t turn_of(double f) {
   return f < 0.0 ? 0ull - share : share;
 }
 // cos and sin of 2 pi times the share: the nearest quarter turn is taken off
-// in integers, so that what is converted to fp32 is at most an eighth of a turn.
+// in integers, and for the at most an eighth of a turn that is left, x, Taylor's
+// series to x^10, whose next terms are below 2^-29.
 __device__ __forceinline__ void cos_sin(uint64_t share, float& c, float& s) {
-  const uint32_t v = (uint32_t)(share >> 32);
-  const uint32_t quarter = (v + 0x20000000u) >> 30;
-  const int rest = (int)(v - (quarter << 30));
-  float a, b;
-  sincospif((float)rest * 4.656612873077393e-10f, &b, &a);  // 2^-31: in half turns
-  c = quarter & 1 ? (quarter & 2 ? b : -b) : (quarter & 2 ? -a : a);
-  s = quarter & 1 ? (quarter & 2 ? -a : a) : (quarter & 2 ? -b : b);
+  const uint32_t v = (uint32_t)(share >> 32), quarter = (v + 0x20000000u) >> 30;
+  const float x = (float)(int)(v - (quarter << 30)) * 1.4629180792671596e-9f, y = x * x;  // 2 pi 2^-32
+  const float b = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+  const float a = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+  const uint32_t cos = __float_as_uint(quarter & 1 ? b : a), sin = __float_as_uint(quarter & 1 ? a : b);
+  c = __uint_as_float(cos ^ ((quarter + 1 & 2) << 30));
+  s = __uint_as_float(sin ^ ((quarter & 2) << 30));
 }
 
 // Shared memory of a block: the turns of each frequency, and cos and sin for
@@ -79,7 +80,7 @@ __device__ __forceinline__ void fill_turns(const HeadNorm& p, const Angles& a) {
   for (int i = threadIdx.x; i < p.half; i += kHeadThreads) a.turn[i] = turn_of(p.freqs[i]);
 }
 // The angles of so many tokens into the rows from `to` on.
-__device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, int64_t t0, int tokens, int to = 0) {
+__device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, const int64_t* positions, int tokens, int to = 0) {
   const int wide = p.half < kHeadThreads ? p.half : kHeadThreads, rows = kHeadThreads / wide;
   const int row = threadIdx.x / wide, col = threadIdx.x - row * wide;
   if (row >= rows) return;
@@ -88,7 +89,7 @@ __device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, 
     const bool finite = isfinite(p.freqs[k]);
     for (int t = row; t < tokens; t += rows) {
       float c, s;
-      cos_sin((uint64_t)p.positions[t0 + t] * turn, c, s);
+      cos_sin((uint64_t)positions[t] * turn, c, s);
       a.cos[(to + t) * a.pitch + a.place(k)] = finite ? c : __int_as_float(0x7fffffff);
       a.sin[(to + t) * a.pitch + a.place(k)] = finite ? s : __int_as_float(0x7fffffff);
     }
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kHeadThreads, sizeof(T) == 2 ? 4 : 3)
     if (!p.half || q >= tiles) return;
     const int64_t t0 = (int64_t)q << tile_log;
     const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
-    fill_angles(p, angles, t0, tokens, buf * tile);
+    fill_angles(p, angles, p.positions + t0, tokens, buf * tile);
   };
   int q = blockIdx.x, base = first, buf = 0;
   fetch(0);
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_any_kernel(const __gri
   if (p.half) {
     fill_turns(p, angles);
     __syncthreads();
-    fill_angles(p, angles, t0, tokens);
+    fill_angles(p, angles, p.positions + t0, tokens);
     __syncthreads();
   }
   if (t >= tokens) return;
@@ -404,18 +405,26 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   for (int i = 0; i < 8; ++i) dw[i] = f2(0.f);
   auto tokens_of = [&](int64_t q) { return (int)(p.T - (q << tile_log) < tile ? p.T - (q << tile_log) : tile); };
   fetch(q, slot);
+  // Positions are read a tile before their angles are computed.
+  __shared__ int64_t positions[2][kBackTile];
+  auto position = [&](int64_t q) {
+    const int64_t token = (q << tile_log) + threadIdx.x;
+    return p.half && (int)threadIdx.x < tile && token < p.T ? p.positions[token] : 0;
+  };
   if (p.half) {
+    if ((int)threadIdx.x < tile) positions[0][threadIdx.x] = position(q), positions[1][threadIdx.x] = position(q + stride);
     fill_turns(p, angles);
     __syncthreads();
-    if (q < tiles) fill_angles(p, angles, q << tile_log, tokens_of(q));
+    if (q < tiles) fill_angles(p, angles, positions[0], tokens_of(q));
   }
   for (int buf = 0; q < tiles; q += stride, buf ^= 1) {
     const int64_t t0 = q << tile_log;
     const int tokens = tokens_of(q);
     if (p.half) {
       __syncthreads();  // this tile's angles are there, the one's before are read
-      if (q + stride < tiles) fill_angles(p, angles, (q + stride) << tile_log, tokens_of(q + stride), (buf ^ 1) * tile);
+      if (q + stride < tiles) fill_angles(p, angles, positions[buf ^ 1], tokens_of(q + stride), (buf ^ 1) * tile);
     }
+    const int64_t later = position(q + 2 * stride);
     const float *cos = angles.cos + (buf * tile + t) * angles.pitch, *sin = angles.sin + (buf * tile + t) * angles.pitch;
     T* out = static_cast<T*>(s.y) + (t0 + t) * heads * p.D;
     for (int base = 0; base < heads; base += step) {
@@ -458,6 +467,8 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
         store8(y + at.hi, gb);
       }
     }
+    // (All have read this tile's: its angles were computed before the barrier above.)
+    if (p.half && (int)threadIdx.x < tile) positions[buf][threadIdx.x] = later;
   }
   asm volatile("griddepcontrol.launch_dependents;\n");
   if (!parts) return;
@@ -534,7 +545,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_backward_any_kernel(co
     const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
     if (p.half) {
       __syncthreads();
-      fill_angles(p, angles, t0, tokens);
+      fill_angles(p, angles, p.positions + t0, tokens);
       __syncthreads();
     }
     for (int h = slot; h < heads; h += step) {
@@ -736,9 +747,11 @@ void plan_side(HeadPlan& plan, int k, int64_t T, int heads, int teams, int block
   const int64_t rounds = (plan.tiles[k] + blocks - 1) / blocks;
   plan.blocks[k] = (int)((plan.tiles[k] + rounds - 1) / rounds);
 }
-HeadPlan backward_plan(const HeadNorm& p, int teams, int blocks) {
+HeadPlan backward_plan(const HeadNorm& p, int teams, int blocks, bool runs) {
   HeadPlan plan = {};
-  const int64_t hq = p.side[0].heads, hk = p.side[1].heads, share = (blocks * hq + (hq + hk) / 2) / (hq + hk);
+  // A token's angles cost a side about as much as two of its heads.
+  const int64_t hq = p.side[0].heads, hk = p.side[1].heads, more = p.half && runs ? 2 : 0;
+  const int64_t share = (blocks * (hq + more) + (hq + hk) / 2 + more) / (hq + hk + 2 * more);
   const int queries = hk == 0 ? blocks : hq == 0 ? 0 : (int)std::min<int64_t>(blocks - 1, std::max<int64_t>(1, share));
   plan_side(plan, 0, p.T, (int)hq, teams, queries);
   plan_side(plan, 1, p.T, (int)hk, teams, blocks - queries);
@@ -752,7 +765,7 @@ cudaError_t backward_typed(const HeadNorm& p, float* parts, cudaStream_t stream)
   const int pairs = pairs_of(p);
   // As many blocks as fit on the SMs at a time: their registers decide.
   const int on_sm = runs ? 2 : pairs > 64 && pairs <= 128 ? 2 : 4;
-  const HeadPlan plan = backward_plan(p, teams, 152 * on_sm);
+  const HeadPlan plan = backward_plan(p, teams, 152 * on_sm, runs);
   const unsigned grid = (unsigned)(plan.blocks[0] + plan.blocks[1]);
   float* sums = p.side[0].dw || p.side[1].dw ? parts : nullptr;
   const size_t angles = Angles::bytes(p.half, (runs ? 2 : 1) << std::max(plan.tile_log[0], plan.tile_log[1]));
