@@ -620,7 +620,8 @@ int bakron_head_norm_rotary_backward(const void* dYQ, int64_t dq_token, int64_t 
  *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
  *     param = (1 - lr weight_decay) param
  *             - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * (0 where m is 0), computed in fp32 and rounded to the parameter's type;
+ * (0 where m is 0; what is divided by is at least 2^-126), computed in fp32 and
+ * rounded to the parameter's type;
  * copy, where given, gets the same value in its type.
  * bits = 32: m and v are fp32.  bits = 8: m and v hold e4m3 codes of m and of
  * sqrt(v) with a scale (max / 448) for each 256 values of the tensor, the last
@@ -630,7 +631,7 @@ int bakron_head_norm_rotary_backward(const void* dYQ, int64_t dq_token, int64_t 
  * A value whose gradient, or its square, is not finite in fp32 is left as it
  * is, and BAKRON_DEV_NONFINITE_GRAD is set.
  * tensors: host, read in the call.  Arrays are dense, start on their elements
- * and do not overlap; param: param_dtype (fp32, fp16, bf16), grad: grad_dtype,
+ * and do not overlap (a parameter, state or copy that is there twice is refused); param: param_dtype (fp32, fp16, bf16), grad: grad_dtype,
  * copy: copy_dtype (fp16 or bf16), or NULL.  n may be 0.
  * step: from 1 on.  lr_dev, step_dev, grad_scale_dev: device, in place of the
  * numbers, or NULL; skip: device, a number that is not 0 leaves everything as

@@ -96,6 +96,14 @@ PyObject* wrap(const at::Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
 }
+// A call of the library, with other threads free to run meanwhile: a launch may wait for room.
+template <class F>
+int unlocked(F call) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int r = call();
+  PyEval_RestoreThread(state);
+  return r;
+}
 // A tuple or a value of a dict; takes the references.
 PyObject* pair(PyObject* a, PyObject* b) {
   PyObject* r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
@@ -140,13 +148,16 @@ PyObject* fp8_matmul(PyObject* const* a) {
       !values(a[4], at::kFloat, 1, N, N, device, &bias))
     return nullptr;
   const int out = want >= 0 ? (int)want : kind == kE4M3 ? BAKRON_F32 : kind;
+  void* const stream = stream_on(device);
   const at::Tensor y = room({T, N}, type_of(out), device), status = room({1}, at::kInt, device);
   const size_t bytes = lib.fp8_size(T, K, N, kind, w.copies);
   if (!bytes) return nullptr;
   const at::Tensor ws = room({(int64_t)bytes}, at::kByte, device);
-  if (lib.fp8(x.p, kind, x.ld, static_cast<const float*>(xs), static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
+  if (unlocked([&] {
+        return lib.fp8(x.p, kind, x.ld, static_cast<const float*>(xs), static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
               static_cast<const float*>(w.scales), static_cast<const float*>(bias), T, K, N, y.data_ptr(), out, ws.data_ptr(), bytes,
-              static_cast<int32_t*>(status.data_ptr()), stream_on(device)))
+              static_cast<int32_t*>(status.data_ptr()), stream);
+      }))
     return nullptr;
   return pair(wrap(y), wrap(status));
 }
@@ -163,6 +174,7 @@ PyObject* fp8_matmul_backward(PyObject* const* a) {
   if (!weights(a[2], a[3], K, device, w) || w.codes.rows != N) return nullptr;
   const bool has_x = a[1] != Py_None, has_bias = PyObject_IsTrue(a[4]) == 1;
   if (has_x && (!matrix(a[1], x) || x.rows != T || x.cols != K || x.t->get_device() != device || code_of(*x.t) != kind)) return nullptr;
+  void* const stream = stream_on(device);
   const at::Tensor dx = room({T, K}, type_of(kind), device), status = room({1}, at::kInt, device);
   at::Tensor dw, dbias;
   if (has_x) dw = room({N, K}, type_of(kind), device);
@@ -170,10 +182,12 @@ PyObject* fp8_matmul_backward(PyObject* const* a) {
   const size_t bytes = lib.fp8_back_size(T, K, N, 1 + 2 * has_x + 4 * has_bias, w.copies);
   if (!bytes) return nullptr;
   const at::Tensor ws = room({(int64_t)bytes}, at::kByte, device);
-  if (lib.fp8_back(dy.p, dy.ld, x.p, x.ld, kind, static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
+  if (unlocked([&] {
+        return lib.fp8_back(dy.p, dy.ld, x.p, x.ld, kind, static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
                    static_cast<const float*>(w.scales), T, K, N, dx.data_ptr(), has_x ? dw.data_ptr() : nullptr,
                    has_bias ? static_cast<float*>(dbias.data_ptr()) : nullptr, ws.data_ptr(), bytes,
-                   static_cast<int32_t*>(status.data_ptr()), stream_on(device)))
+                   static_cast<int32_t*>(status.data_ptr()), stream);
+      }))
     return nullptr;
   PyObject* d = PyDict_New();
   if (!d || !put(d, "X", dx) || !put(d, "W", dw) || !put(d, "bias", dbias)) {
@@ -228,12 +242,15 @@ bool norm_of(PyObject* const* a, Norm& n) {
 PyObject* head_norm_rotary(PyObject* const* a) {
   Norm n;
   if (!norm_of(a, n)) return nullptr;
+  void* const stream = stream_on(n.device);
   const at::Tensor yq = room({n.q.T, n.q.heads, n.q.D}, n.type, n.device);
   at::Tensor yk;
   if (n.k.p) yk = room({n.k.T, n.k.heads, n.k.D}, n.type, n.device);
-  if (lib.heads(n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token, n.k.head, n.k.heads, static_cast<const float*>(n.qw),
+  if (unlocked([&] {
+        return lib.heads(n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token, n.k.head, n.k.heads, static_cast<const float*>(n.qw),
                 static_cast<const float*>(n.kw), static_cast<const int64_t*>(n.positions), static_cast<const double*>(n.freqs), n.R,
-                n.pairs, n.eps, n.kind, n.q.T, n.q.D, yq.data_ptr(), n.k.p ? yk.data_ptr() : nullptr, stream_on(n.device)))
+                n.pairs, n.eps, n.kind, n.q.T, n.q.D, yq.data_ptr(), n.k.p ? yk.data_ptr() : nullptr, stream);
+      }))
     return nullptr;
   return pair(wrap(yq), wrap(yk));
 }
@@ -245,6 +262,7 @@ PyObject* head_norm_rotary_backward(PyObject* const* a) {
     return nullptr;
   if ((a[1] == Py_None) != (n.k.p == nullptr)) return nullptr;
   if (n.k.p && (!heads_of(a[1], n.type, n.device, dk) || dk.T != n.k.T || dk.heads != n.k.heads || dk.D != n.k.D)) return nullptr;
+  void* const stream = stream_on(n.device);
   const at::Tensor gq = room({n.q.T, n.q.heads, n.q.D}, n.type, n.device);
   at::Tensor gk, gqw, gkw;
   if (n.k.p) gk = room({n.k.T, n.k.heads, n.k.D}, n.type, n.device);
@@ -254,11 +272,13 @@ PyObject* head_norm_rotary_backward(PyObject* const* a) {
   if (!bytes) return nullptr;
   const at::Tensor ws = room({(int64_t)bytes}, at::kByte, n.device);
   auto at = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-  if (lib.heads_back(dq.p, dq.token, dq.head, dk.p, dk.token, dk.head, n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token,
+  if (unlocked([&] {
+        return lib.heads_back(dq.p, dq.token, dq.head, dk.p, dk.token, dk.head, n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token,
                      n.k.head, n.k.heads, static_cast<const float*>(n.qw), static_cast<const float*>(n.kw),
                      static_cast<const int64_t*>(n.positions), static_cast<const double*>(n.freqs), n.R, n.pairs, n.eps, n.kind, n.q.T,
                      n.q.D, at(gq), at(gk), static_cast<float*>(at(gqw)), static_cast<float*>(at(gkw)), ws.data_ptr(), bytes,
-                     stream_on(n.device)))
+                     stream_on(n.device));
+      }))
     return nullptr;
   PyObject* d = PyDict_New();
   if (!d || !put(d, "Q", gq) || !put(d, "K", gk) || !put(d, "q_weight", gqw) || !put(d, "k_weight", gkw)) {
@@ -336,10 +356,13 @@ PyObject* adamw(PyObject* const* a) {
       e.copy = c->data_ptr(), e.copy_dtype = code_of(*c);
     }
   }
+  void* const stream = stream_on(device);
   const at::Tensor status = room({1}, at::kInt, device), ws = room({(int64_t)lib.adamw_size()}, at::kByte, device);
-  if (lib.adamw(out.get(), count, eight ? 8 : 32, rate, static_cast<const float*>(rate_dev), step, static_cast<const int64_t*>(step_dev),
+  if (unlocked([&] {
+        return lib.adamw(out.get(), count, eight ? 8 : 32, rate, static_cast<const float*>(rate_dev), step, static_cast<const int64_t*>(step_dev),
                 b1, b2, eps, decay, scale, static_cast<const float*>(scale_dev), static_cast<const int32_t*>(skip), seed, ws.data_ptr(),
-                ws.numel(), static_cast<int32_t*>(status.data_ptr()), stream_on(device)))
+                ws.numel(), static_cast<int32_t*>(status.data_ptr()), stream);
+      }))
     return nullptr;
   return wrap(status);
 }

@@ -211,6 +211,31 @@ def test_the_same_step_in_any_alignment_and_company(bk):  # noqa: F811
             assert all(torch.equal(s[k][0].view(torch.uint8), states[k][0].view(torch.uint8)) for k in s)
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_more_tensors_than_a_launch_takes(bk, bits):  # noqa: F811
+    import torch
+
+    rng = np.random.default_rng(11)
+    sizes = [int(n) for n in rng.integers(0, 600, 801)]
+    params, grads, states = _make(rng, sizes, "float32", "bfloat16", bits)
+    before, old = [p.clone() for p in params], _copy(states)
+    assert int(bk.adamw(params, grads, states, seed=4, **ARGS).item()) == 0
+    _check(before, grads, old, params, states, None, ARGS, seed=4)
+
+
+def test_the_same_tensor_twice(bk):  # noqa: F811
+    """Two steps of one parameter, or of one state, at once would race: refused, and nothing changes."""
+    import torch
+
+    params, grads, states = _make(np.random.default_rng(12), [300, 300], "float32", "float32", 32)
+    before = [p.clone() for p in params]
+    twice = {"m": [states["m"][0]] * 2, "v": states["v"]}
+    for p, s, c in (([params[0]] * 2, states, None), (params, twice, None), (params, states, [params[0].half()] * 2)):
+        with pytest.raises(RuntimeError):
+            bk.adamw(p, grads, s, copies=c, **ARGS)
+    assert all(torch.equal(a, b) for a, b in zip(params, before))
+
+
 def test_rounding_at_random_is_without_bias(bk):  # noqa: F811
     """Values between two codes, over many seeds: the mean is the value, within 6 standard deviations of the mean."""
     import torch

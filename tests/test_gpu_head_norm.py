@@ -313,6 +313,24 @@ def test_no_tokens_no_heads_and_another_stream(bk):  # noqa: F811
     assert torch.equal(there, want) and torch.equal(g2["Q"], g["Q"]) and torch.equal(g2["q_weight"], g["q_weight"])
 
 
+def test_keys_without_queries(bk):  # noqa: F811
+    import torch
+
+    rng = np.random.default_rng(8)
+    for d in (64, 50):
+        q, k = _inputs(rng, 70, 0, 3, d, "bfloat16")
+        p, f, (qw, kw) = _args(rng, 70, d, 32)
+        want = bk.head_norm_rotary(k, None, p, f, kw)[0]
+        none, y = bk.head_norm_rotary(q, k, p, f, qw, kw)
+        assert none.shape == (70, 0, d) and torch.equal(y, want)
+        g = bk.head_norm_rotary_backward(none, y, q, k, p, f, qw, kw)
+        h = bk.head_norm_rotary_backward(y, None, k, None, p, f, kw)
+        assert not g["q_weight"].any() and torch.equal(g["K"], h["Q"])
+        # other blocks sum the weight's gradient: in another order
+        size = _gradients(k, y, p, f, kw, 1e-6, "halves")[3]
+        assert bool(((g["k_weight"] - h["q_weight"]).abs().double() <= 2 * 128 * E * size).all())
+
+
 def test_offsets_beyond_32_bits(bk):  # noqa: F811
     """A token whose values lie more than 2^32 elements into the buffer."""
     import torch
