@@ -3,10 +3,11 @@
 //
 // Bound by memory: values are read once, into registers, their maxima taken
 // there, and the codes written.  Along rows a warp takes 512 values of a row.
-// Otherwise a block takes 128 x 128 values, 8 x 8 a thread; one read of them
+// Otherwise a block takes 128 x 128 values, 4 x 8 a thread; one read of them
 // gives the codes along rows, the codes along columns and the columns' sums
 // (what the backward pass of a product needs of its output's gradient).
 #include <algorithm>
+#include <cstring>
 
 #include "fp8_codes.cuh"
 #include "layers.h"
@@ -105,6 +106,90 @@ struct TileCodes {
   float* sums;  // a row of down_pitch floats for each 128 rows
   Clear clear;
 };
+// Eight values as they lie in registers: four words of two 16-bit ones, or eight.
+// Magnitudes of floats order as their bits do, with infinity and then NaN above
+// all, so maxima are taken of the bits, two 16-bit ones at a time.
+template <class T>
+struct Eight {
+  static constexpr bool kPairs = sizeof(T) == 2;
+  static constexpr int kWords = kPairs ? 4 : 8;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const T* x, int64_t i, int64_t n, bool vec) {
+    if (vec && i + 8 <= n) {
+#pragma unroll
+      for (int k = 0; k < kWords / 4; ++k) {
+        const uint4 u = reinterpret_cast<const uint4*>(x + i)[k];
+        w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+      }
+    } else if constexpr (kPairs) {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = (i + 2 * k < n ? (uint32_t)h[i + 2 * k] : 0u) | (i + 2 * k + 1 < n ? (uint32_t)h[i + 2 * k + 1] << 16 : 0u);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = i + k < n ? __float_as_uint(x[i + k]) : 0u;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = 0;
+  }
+  static __device__ __forceinline__ uint32_t size_of(uint32_t word) { return word & (kPairs ? 0x7fff7fffu : 0x7fffffffu); }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return kPairs ? __vmaxu2(a, b) : max(a, b); }
+  // The fp32 magnitude, in bits, of one 16-bit magnitude or of a word.
+  static __device__ __forceinline__ uint32_t as_fp32(uint32_t bits) {
+    if constexpr (kPairs) {
+      const uint16_t h = (uint16_t)bits;
+      T t;
+      memcpy(&t, &h, 2);
+      return __float_as_uint(to_f32<T>(t));
+    } else {
+      return bits;
+    }
+  }
+  // ... and of the larger one of a word.
+  static __device__ __forceinline__ uint32_t top_of(uint32_t word) { return as_fp32(kPairs ? max(word & 0xffffu, word >> 16) : word); }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = size_of(w[0]);
+#pragma unroll
+    for (int k = 1; k < kWords; ++k) t = larger(t, size_of(w[k]));
+    return t;
+  }
+  // The values, or zeros where `keep` (bits) is 0: a block without a reciprocal may hold what is not finite.
+  __device__ __forceinline__ void open(const uint32_t (&keep)[kWords], float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const uint32_t x = w[k] & keep[k];
+      if constexpr (kPairs) {
+        T t[2];
+        memcpy(t, &x, 4);
+        v[2 * k] = to_f32<T>(t[0]), v[2 * k + 1] = to_f32<T>(t[1]);
+      } else {
+        v[k] = __uint_as_float(x);
+      }
+    }
+  }
+  __device__ __forceinline__ void open(bool keep, float (&v)[8]) const {
+    uint32_t all[kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) all[k] = keep ? 0xffffffffu : 0u;
+    open(all, v);
+  }
+};
+__device__ __forceinline__ uint32_t codes2(float a, float b, float inv_a, float inv_b) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a * inv_a, b * inv_b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const float (&inv)[8]) {
+  return make_uint2(codes2(v[0], v[1], inv[0], inv[1]) | (codes2(v[2], v[3], inv[2], inv[3]) << 16),
+                    codes2(v[4], v[5], inv[4], inv[5]) | (codes2(v[6], v[7], inv[6], inv[7]) << 16));
+}
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+  return make_uint2(codes2(v[0], v[1], inv, inv) | (codes2(v[2], v[3], inv, inv) << 16),
+                    codes2(v[4], v[5], inv, inv) | (codes2(v[6], v[7], inv, inv) << 16));
+}
+
 template <class T>
 __global__ void __launch_bounds__(kTileThreads, 2) tile_codes_kernel(const T* X, const __grid_constant__ TileCodes first, const T* second_X,
                                                                       const __grid_constant__ TileCodes second, int64_t split) {
@@ -112,89 +197,101 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_codes_kernel(const T* X,
   const bool other = blockIdx.x >= split;
   const TileCodes& p = other ? second : first;
   if (other) X = second_X;
+  using V = Eight<T>;
   constexpr int kWarps = kTileThreads / 32, kRows = 128 / (kTileThreads / 16), kEach = 128 / kRows;  // rows of a thread, kEach apart
-  __shared__ uint32_t tops[kWarps][128];
-  __shared__ float sums[kWarps][128];
-  __shared__ float down_inv[128];
+  constexpr int kWords = V::kWords;
+  __shared__ __align__(16) uint32_t tops[kWarps][16 * kWords];
+  __shared__ __align__(16) float sums[kWarps][128];
+  __shared__ __align__(16) float down_inv[128];
   asm volatile("griddepcontrol.launch_dependents;\n");
   clear_words(first.clear);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane & 15;
   const int64_t tile = (int64_t)blockIdx.x - (other ? split : 0), tiles_n = (p.cols + 127) / 128, tm = tile / tiles_n, tn = tile - tm * tiles_n;
   const int64_t r0 = tm * 128 + (threadIdx.x >> 4), k = tn * 128 + part * 8;  // rows r0, r0 + kEach, ..
-  float v[kRows][8];
+  V x[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int64_t r = r0 + kEach * i;
-    if (r < p.rows) {
-      values8(X + r * p.ldx, k, p.cols, p.vec, v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    }
+    if (r < p.rows)
+      x[i].load(X + r * p.ldx, k, p.cols, p.vec);
+    else
+      x[i].zero();
   }
+  float v[8], scale, inv;
   uint32_t all = 0;
   if (p.along || p.whole) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[i][e]));
-      all = max(all, top);
+      uint32_t top = x[i].top();
+      all = V::larger(all, top);
       if (!p.along) continue;
 #pragma unroll
-      for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float scale, inv;
-      block_scale(top, scale, inv);
+      for (int o = 8; o; o >>= 1) top = V::larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+      block_scale(V::top_of(top), scale, inv);
       const int64_t r = r0 + kEach * i;
       if (r < p.rows && k < p.cols) {
-        put_codes8(p.along + r * p.ld_along, k, p.cols, p.vec_along, fp8_codes8(v[i], inv));
+        x[i].open(inv > 0.f, v);
+        put_codes8(p.along + r * p.ld_along, k, p.cols, p.vec_along, codes8(v, inv));
         if (part == 0) p.along_scales[r * p.along_row + tn * p.along_col] = scale;
       }
     }
   }
   if (p.whole) {
-    all = __reduce_max_sync(0xffffffffu, all);
+    all = __reduce_max_sync(0xffffffffu, V::top_of(all));
     if (lane == 0) tops[0][warp] = all;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) all = max(all, tops[0][w]);
-    float scale, inv;
     block_scale(all, scale, inv);
     if (threadIdx.x == 0) p.whole_scales[tm * p.whole_row + tn] = scale;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int64_t r = r0 + kEach * i;
-      if (r < p.rows && k < p.cols) put_codes8(p.whole + r * p.ld_whole, k, p.cols, p.vec_whole, fp8_codes8(v[i], inv));
+      x[i].open(inv > 0.f, v);
+      if (r < p.rows && k < p.cols) put_codes8(p.whole + r * p.ld_whole, k, p.cols, p.vec_whole, codes8(v, inv));
     }
     __syncthreads();
   }
   if (!p.down && !p.sums) return;
+  uint32_t top[kWords];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    uint32_t top = 0;
+  for (int e = 0; e < kWords; ++e) {
+    top[e] = V::size_of(x[0].w[e]);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) top = max(top, magnitude(v[i][e]));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    if (lane < 16) tops[warp][part * 8 + e] = top;
-    if (p.sums) {
-      float s = 0.f;
+    for (int i = 1; i < kRows; ++i) top[e] = V::larger(top[e], V::size_of(x[i].w[e]));
+    top[e] = V::larger(top[e], __shfl_xor_sync(0xffffffffu, top[e], 16));
+  }
+  if (lane < 16) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) s += v[i][e];
-      s += __shfl_xor_sync(0xffffffffu, s, 16);
-      if (lane < 16) sums[warp][part * 8 + e] = s;
+    for (int e = 0; e < kWords; e += 4)
+      *reinterpret_cast<uint4*>(&tops[warp][part * kWords + e]) = make_uint4(top[e], top[e + 1], top[e + 2], top[e + 3]);
+  }
+  if (p.sums) {
+    float s[8] = {};
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      x[i].open(true, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += __shfl_xor_sync(0xffffffffu, s[e], 16);
+    if (lane < 16) {
+      *reinterpret_cast<float4*>(&sums[warp][part * 8]) = make_float4(s[0], s[1], s[2], s[3]);
+      *reinterpret_cast<float4*>(&sums[warp][part * 8 + 4]) = make_float4(s[4], s[5], s[6], s[7]);
     }
   }
   __syncthreads();
   if (threadIdx.x < 128) {
-    uint32_t top = 0;
+    uint32_t most = 0;
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      top = max(top, tops[w][threadIdx.x]);
+      const uint32_t word = tops[w][V::kPairs ? threadIdx.x / 2 : threadIdx.x];
+      most = max(most, V::kPairs ? (threadIdx.x & 1 ? word >> 16 : word & 0xffffu) : word);
       if (p.sums) s += sums[w][threadIdx.x];
     }
-    float scale, inv;
-    block_scale(top, scale, inv);
+    block_scale(V::as_fp32(most), scale, inv);
     down_inv[threadIdx.x] = inv;
     const int64_t c = tn * 128 + threadIdx.x;
     if (c < p.cols) {
@@ -204,16 +301,24 @@ __global__ void __launch_bounds__(kTileThreads, 2) tile_codes_kernel(const T* X,
   }
   if (!p.down) return;
   __syncthreads();
-  float inv[8];
+  float each[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) inv[e] = down_inv[part * 8 + e];
+  for (int e = 0; e < 8; e += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(&down_inv[part * 8 + e]);
+    each[e] = f.x, each[e + 1] = f.y, each[e + 2] = f.z, each[e + 3] = f.w;
+  }
+  uint32_t keep[kWords];
+#pragma unroll
+  for (int e = 0; e < kWords; ++e)
+    keep[e] = V::kPairs ? (each[2 * e & 7] > 0.f ? 0xffffu : 0u) | (each[(2 * e + 1) & 7] > 0.f ? 0xffff0000u : 0u)
+                        : (each[e] > 0.f ? 0xffffffffu : 0u);
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int64_t r = r0 + kEach * i;
-    if (r < p.rows && k < p.cols)
-      put_codes8(p.down + r * p.ld_down, k, p.cols, p.vec_down,
-                 make_uint2(fp8_pair(v[i][0], v[i][1], inv[0], inv[1]) | (fp8_pair(v[i][2], v[i][3], inv[2], inv[3]) << 16),
-                            fp8_pair(v[i][4], v[i][5], inv[4], inv[5]) | (fp8_pair(v[i][6], v[i][7], inv[6], inv[7]) << 16)));
+    if (r < p.rows && k < p.cols) {
+      x[i].open(keep, v);
+      put_codes8(p.down + r * p.ld_down, k, p.cols, p.vec_down, codes8(v, each));
+    }
   }
 }
 
