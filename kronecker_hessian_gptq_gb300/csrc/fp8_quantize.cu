@@ -18,16 +18,6 @@ namespace {
 constexpr int kCodeThreads = 256;
 constexpr int kTileThreads = 512;
 
-// 8 values from x[i] on, those past n as zeros.  Vectors where the rows allow.
-template <class T>
-__device__ __forceinline__ void values8(const T* x, int64_t i, int64_t n, bool vec, float (&v)[8]) {
-  if (vec && i + 8 <= n) {
-    load_vec<T, 8>(x + i, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = i + k < n ? to_f32<T>(x[i + k]) : 0.f;
-  }
-}
 __device__ __forceinline__ void put_codes8(uint8_t* c, int64_t i, int64_t n, bool vec, const uint2& w) {
   if (vec && i + 8 <= n) {
     *reinterpret_cast<uint2*>(c + i) = w;
@@ -48,64 +38,6 @@ __device__ __forceinline__ void clear_words(const Clear& c) {
     c.word[i] = 0;
 }
 
-// A warp takes 512 values of a row, 16 a lane: the block's scale, two divisions,
-// is then computed for 16 values.  It goes from place to place by adding: a
-// division of 64 bits costs as much as the codes.
-template <class T>
-__global__ void __launch_bounds__(kCodeThreads) row_codes_kernel(const T* X, int64_t rows, int64_t cols, int64_t ldx, bool vec,
-                                                                 uint8_t* codes, int64_t ldc, bool vec_codes, float* scales,
-                                                                 int64_t scale_row, int64_t scale_col, Clear clear) {
-  asm volatile("griddepcontrol.launch_dependents;\n");
-  clear_words(clear);
-  const int lane = threadIdx.x & 31;
-  const int64_t per = (cols + 511) / 512, first = (int64_t)blockIdx.x * (kCodeThreads / 32) + (threadIdx.x >> 5);
-  const int64_t step = (int64_t)gridDim.x * (kCodeThreads / 32);
-  auto over = [&](int64_t x) { return (x | per) >> 32 ? x / per : (int64_t)((uint32_t)x / (uint32_t)per); };
-  const int64_t step_rows = over(step), step_cols = step - step_rows * per;
-  int64_t row = over(first), col = first - row * per;
-  while (row < rows) {
-    const int64_t k = col * 512 + lane * 16;
-    float v[2][8];
-    values8(X + row * ldx, k, cols, vec, v[0]);
-    values8(X + row * ldx, k + 8, cols, vec, v[1]);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, magnitude(v[i / 8][i % 8]));
-#pragma unroll
-    for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float scale, inv;
-    block_scale(top, scale, inv);
-    if (k < cols) {
-      uint8_t* to = codes + row * ldc;
-      const uint2 a = fp8_codes8(v[0], inv), b = fp8_codes8(v[1], inv);
-      if (vec_codes && k + 16 <= cols) {
-        *reinterpret_cast<uint4*>(to + k) = make_uint4(a.x, a.y, b.x, b.y);
-      } else {
-        put_codes8(to, k, cols, false, a);
-        put_codes8(to, k + 8, cols, false, b);
-      }
-      if ((lane & 7) == 0) scales[row * scale_row + (k >> 7) * scale_col] = scale;
-    }
-    row += step_rows, col += step_cols;
-    if (col >= per) ++row, col -= per;
-  }
-}
-
-// A tile of 128 x 128 for each block: codes along rows, along columns, or one
-// scale for all, and the sums of the tile's columns.
-struct TileCodes {
-  int64_t rows, cols, ldx;
-  bool vec;
-  uint8_t *along, *down, *whole;  // null: not wanted
-  int64_t ld_along, ld_down, ld_whole;
-  bool vec_along, vec_down, vec_whole;
-  float *along_scales, *down_scales, *whole_scales;
-  int64_t along_row, along_col;  // strides of along_scales
-  int64_t down_pitch;  // down_scales: a row of this many floats for each 128 rows
-  int64_t whole_row;
-  float* sums;  // a row of down_pitch floats for each 128 rows
-  Clear clear;
-};
 // Eight values as they lie in registers: four words of two 16-bit ones, or eight.
 // Magnitudes of floats order as their bits do, with infinity and then NaN above
 // all, so maxima are taken of the bits, two 16-bit ones at a time.
@@ -190,6 +122,64 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
                     codes2(v[4], v[5], inv, inv) | (codes2(v[6], v[7], inv, inv) << 16));
 }
 
+// A warp takes 512 values of a row, 16 a lane: the block's scale, two divisions,
+// is then computed for 16 values.  It goes from place to place by adding: a
+// division of 64 bits costs as much as the codes.
+template <class T>
+__global__ void __launch_bounds__(kCodeThreads) row_codes_kernel(const T* X, int64_t rows, int64_t cols, int64_t ldx, bool vec,
+                                                                 uint8_t* codes, int64_t ldc, bool vec_codes, float* scales,
+                                                                 int64_t scale_row, int64_t scale_col, Clear clear) {
+  asm volatile("griddepcontrol.launch_dependents;\n");
+  clear_words(clear);
+  const int lane = threadIdx.x & 31;
+  const int64_t per = (cols + 511) / 512, first = (int64_t)blockIdx.x * (kCodeThreads / 32) + (threadIdx.x >> 5);
+  const int64_t step = (int64_t)gridDim.x * (kCodeThreads / 32);
+  auto over = [&](int64_t x) { return (x | per) >> 32 ? x / per : (int64_t)((uint32_t)x / (uint32_t)per); };
+  const int64_t step_rows = over(step), step_cols = step - step_rows * per;
+  int64_t row = over(first), col = first - row * per;
+  while (row < rows) {
+    const int64_t k = col * 512 + lane * 16;
+    Eight<T> x[2];
+    x[0].load(X + row * ldx, k, cols, vec);
+    x[1].load(X + row * ldx, k + 8, cols, vec);
+    uint32_t top = Eight<T>::larger(x[0].top(), x[1].top());
+#pragma unroll
+    for (int o = 4; o; o >>= 1) top = Eight<T>::larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float scale, inv, v[2][8];
+    block_scale(Eight<T>::top_of(top), scale, inv);
+    if (k < cols) {
+      uint8_t* to = codes + row * ldc;
+      x[0].open(inv > 0.f, v[0]);
+      x[1].open(inv > 0.f, v[1]);
+      const uint2 a = codes8(v[0], inv), b = codes8(v[1], inv);
+      if (vec_codes && k + 16 <= cols) {
+        *reinterpret_cast<uint4*>(to + k) = make_uint4(a.x, a.y, b.x, b.y);
+      } else {
+        put_codes8(to, k, cols, false, a);
+        put_codes8(to, k + 8, cols, false, b);
+      }
+      if ((lane & 7) == 0) scales[row * scale_row + (k >> 7) * scale_col] = scale;
+    }
+    row += step_rows, col += step_cols;
+    if (col >= per) ++row, col -= per;
+  }
+}
+
+// A tile of 128 x 128 for each block: codes along rows, along columns, or one
+// scale for all, and the sums of the tile's columns.
+struct TileCodes {
+  int64_t rows, cols, ldx;
+  bool vec;
+  uint8_t *along, *down, *whole;  // null: not wanted
+  int64_t ld_along, ld_down, ld_whole;
+  bool vec_along, vec_down, vec_whole;
+  float *along_scales, *down_scales, *whole_scales;
+  int64_t along_row, along_col;  // strides of along_scales
+  int64_t down_pitch;  // down_scales: a row of this many floats for each 128 rows
+  int64_t whole_row;
+  float* sums;  // a row of down_pitch floats for each 128 rows
+  Clear clear;
+};
 template <class T>
 __global__ void __launch_bounds__(kTileThreads, 2) tile_codes_kernel(const T* X, const __grid_constant__ TileCodes first, const T* second_X,
                                                                       const __grid_constant__ TileCodes second, int64_t split) {
