@@ -10,7 +10,7 @@
 //
 // Bound by memory: each value is read once (dy and x backward) and written
 // once.  A team of D / 16 lanes (rounded up to a power of two) holds a head,
-// 16 values a lane in two runs of 8, so that both values of a pair are the
+// 16 values a lane in two runs of 8 (or half as many in runs of 4), so that both values of a pair are the
 // same lane's, and a head's sums take three exchanges for D = 128.  A block
 // takes a tile of tokens: their angles are computed once, into shared memory, for
 // the 40 or so heads, and a team keeps to one token and goes from head to head.
@@ -65,10 +65,12 @@ struct Angles {
   int pitch;
   static __host__ __device__ int pitch_of(int half) { return (half + 7) / 8 * 8; }
   static __host__ __device__ size_t bytes(int half, int tile) { return (size_t)pitch_of(half) * (8 + 2 * 4 * tile); }
-  // Where the angle of frequency k lies in its row: the first four of each eight,
-  // then the last four of each, so that neighbouring lanes' 16 bytes are neighbours.
-  __device__ __forceinline__ int place(int k) const { return (k >> 2 & 1) * (pitch / 2) + (k >> 3) * 4 + (k & 3); }
-  __device__ Angles(unsigned char* smem, int half, int tile) : pitch(pitch_of(half)) {
+  bool eights;
+  // Where the angle of frequency k lies in its row: for lanes that read eight, the
+  // first four of each eight, then the last four of each, so that neighbouring
+  // lanes' 16 bytes are neighbours.
+  __device__ __forceinline__ int place(int k) const { return eights ? (k >> 2 & 1) * (pitch / 2) + (k >> 3) * 4 + (k & 3) : k; }
+  __device__ Angles(unsigned char* smem, int half, int tile, bool eights) : pitch(pitch_of(half)), eights(eights) {
     turn = reinterpret_cast<uint64_t*>(smem);
     cos = reinterpret_cast<float*>(smem + 8 * pitch);
     sin = cos + pitch * tile;
@@ -96,57 +98,97 @@ __device__ __forceinline__ void fill_angles(const HeadNorm& p, const Angles& a, 
   }
 }
 
-template <class T>
-__device__ __forceinline__ void load8(const T* p, Raw8<T>& raw) {
+// kRun consecutive values of a lane as they lie in memory: 8, 16 or 32 bytes.
+template <class T, int kRun>
+struct Run {
+  static constexpr int kWords = kRun * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 2) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x, w[1] = u.y;
+    } else {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
-    raw.w[4 * i] = u.x, raw.w[4 * i + 1] = u.y, raw.w[4 * i + 2] = u.z, raw.w[4 * i + 3] = u.w;
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[i / 4];
+        w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void open(F2 (&v)[kRun / 2]) const {
+#pragma unroll
+    for (int i = 0; i < kRun / 2; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      } else {
+        T e[2];
+        memcpy(e, &w[i], 4);
+        v[i] = f2(to_f32<T>(e[0]), to_f32<T>(e[1]));
+      }
+    }
+  }
+};
+template <class T, int kPairs>
+__device__ __forceinline__ void store_run(T* p, const F2 (&v)[kPairs]) {
+  constexpr int kWords = kPairs * (int)sizeof(T) / 2;
+  uint32_t w[kWords];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    float a, b;
+    split(v[i], a, b);
+    if constexpr (sizeof(T) == 4)
+      w[2 * i] = __float_as_uint(a), w[2 * i + 1] = __float_as_uint(b);
+    else
+      w[i] = pack2<T>(a, b);
+  }
+  if constexpr (kWords == 2) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
   }
 }
-template <class T>
-__device__ __forceinline__ void store8(T* p, const F2 (&v)[4]) {
-  Raw8<T> raw;
-  close8<T>(v, raw);
+template <int kPairs>
+__device__ __forceinline__ void load_f2(const float* p, F2 (&v)[kPairs]) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(raw.w[4 * i], raw.w[4 * i + 1], raw.w[4 * i + 2], raw.w[4 * i + 3]);
-}
-__device__ __forceinline__ void load_f2(const float* p, F2 (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 f = reinterpret_cast<const float4*>(p)[i];
-    v[2 * i] = f2(f.x, f.y), v[2 * i + 1] = f2(f.z, f.w);
+  for (int i = 0; i < kPairs; i += 2) {
+    const float4 f = reinterpret_cast<const float4*>(p)[i / 2];
+    v[i] = f2(f.x, f.y), v[i + 1] = f2(f.z, f.w);
   }
 }
 
-// A lane's 16 values: two runs of 8, from lo and from hi on.
+// A lane's values: two runs, from lo and from hi on.
 struct Place {
   int lo, hi;
   int angle;  // of lo's first pair
 };
-template <bool kNeighbours>
+template <bool kNeighbours, int kRun>
 __device__ __forceinline__ Place place_of(int j, int rotated) {
-  if (kNeighbours) return Place{16 * j, 16 * j + 8, 8 * j};
-  if (16 * j < rotated) return Place{8 * j, rotated / 2 + 8 * j, 8 * j};
-  return Place{16 * j, 16 * j + 8, 8 * j};
+  if (!kNeighbours && 2 * kRun * j < rotated) return Place{kRun * j, rotated / 2 + kRun * j, kRun * j};
+  return Place{2 * kRun * j, 2 * kRun * j + kRun, kRun * j};
 }
 
-// Eight angles' cosines or sines from a row of Angles, from the first of an eight on.
-__device__ __forceinline__ void load_angles(const float* row, int angle, int pitch, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(row + angle / 2), b = *reinterpret_cast<const float4*>(row + angle / 2 + pitch / 2);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// kRun angles' cosines or sines from a row of Angles, from the first of such a run on.
+template <int kRun>
+__device__ __forceinline__ void load_angles(const float* row, int angle, int pitch, float (&v)[kRun]) {
+#pragma unroll
+  for (int i = 0; i < kRun; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(row + (kRun == 8 ? angle / 2 + i / 4 * (pitch / 2) : angle));
+    v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+  }
 }
 // Turns a lane's pairs by their angles, or back (kBack).
-template <bool kNeighbours, bool kBack>
-__device__ __forceinline__ void turn_pairs(F2 (&a)[4], F2 (&b)[4], const float* cos, const float* sin, int angle, int half, int pitch) {
+template <bool kNeighbours, bool kBack, int kPairs>
+__device__ __forceinline__ void turn_pairs(F2 (&a)[kPairs], F2 (&b)[kPairs], const float* cos, const float* sin, int angle, int half,
+                                           int pitch) {
+  constexpr int kRun = 2 * kPairs;
   if (angle >= half) return;
-  float c[8], s[8];
-  load_angles(cos, angle, pitch, c);
-  load_angles(sin, angle, pitch, s);
+  float c[kRun], s[kRun];
+  load_angles<kRun>(cos, angle, pitch, c);
+  load_angles<kRun>(sin, angle, pitch, s);
   if (!kNeighbours) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       const F2 cc = f2(c[2 * i], c[2 * i + 1]), ss = f2(s[2 * i], s[2 * i + 1]), minus = f2(-s[2 * i], -s[2 * i + 1]);
       const F2 x = a[i], y = b[i];
       a[i] = fma2(y, kBack ? ss : minus, x * cc);
@@ -154,9 +196,9 @@ __device__ __forceinline__ void turn_pairs(F2 (&a)[4], F2 (&b)[4], const float* 
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kRun; ++i) {
       if (angle + i >= half) break;
-      F2& v = i < 4 ? a[i & 3] : b[i & 3];
+      F2& v = i < kPairs ? a[i % kPairs] : b[i % kPairs];
       float x, y;
       split(v, x, y);
       v = kBack ? f2(fmaf(y, s[i], x * c[i]), fmaf(-x, s[i], y * c[i])) : f2(fmaf(-y, s[i], x * c[i]), fmaf(x, s[i], y * c[i]));
@@ -172,31 +214,38 @@ __device__ __forceinline__ float team_sum(float v, int lanes) {
   }
   return v;
 }
-__device__ __forceinline__ float squares(const F2 (&a)[4], const F2 (&b)[4]) {
+template <int kPairs>
+__device__ __forceinline__ float squares(const F2 (&a)[kPairs], const F2 (&b)[kPairs]) {
   F2 q = a[0] * a[0];
 #pragma unroll
-  for (int i = 1; i < 4; ++i) q = fma2(a[i], a[i], q);
+  for (int i = 1; i < kPairs; ++i) q = fma2(a[i], a[i], q);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q = fma2(b[i], b[i], q);
+  for (int i = 0; i < kPairs; ++i) q = fma2(b[i], b[i], q);
   return sum(q);
 }
+
+// Blocks of a variant that an SM holds at a time.
+template <class T, int kRun>
+__host__ __device__ constexpr int forward_on_sm() { return kRun == 4 ? (sizeof(T) == 2 ? 5 : 4) : sizeof(T) == 2 ? 4 : 3; }
+template <class T, int kRun>
+__host__ __device__ constexpr int backward_on_sm() { return kRun == 4 ? (sizeof(T) == 2 ? 4 : 3) : 2; }
 
 // A team takes one token of a tile and every `step`-th of its heads; two heads are
 // on their way at a time, from one tile into the next, and so are the next tile's
 // angles.
-template <class T, bool kNeighbours>
-__global__ void __launch_bounds__(kHeadThreads, sizeof(T) == 2 ? 4 : 3)
+template <class T, bool kNeighbours, int kRun>
+__global__ void __launch_bounds__(kHeadThreads, forward_on_sm<T, kRun>())
     head_norm_kernel(const __grid_constant__ HeadNorm p, int tile_log, int lanes, int tiles) {
   extern __shared__ __align__(16) unsigned char head_smem[];
   const int tile = 1 << tile_log;
-  const Angles angles(head_smem, p.half, 2 * tile);  // of two tiles in turn
+  const Angles angles(head_smem, p.half, 2 * tile, kRun == 8);  // of two tiles in turn
   const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, each = (kHeadThreads / lanes) >> tile_log;
   const int t = team & (tile - 1), slot = team >> tile_log, first = (int)blockIdx.y * each, step = each * gridDim.y;
-  const bool mine = 16 * j < p.D;
-  const Place at = place_of<kNeighbours>(j, 2 * p.half);
+  const bool mine = 2 * kRun * j < p.D;
+  const Place at = place_of<kNeighbours, kRun>(j, 2 * p.half);
   const float share = 1.f / (float)p.D;
   const int queries = p.side[0].heads, heads = queries + p.side[1].heads;
-  Raw8<T> lo[2] = {}, hi[2] = {};
+  Run<T, kRun> lo[2] = {}, hi[2] = {};
   int ahead_q = blockIdx.x, ahead = first;  // what is fetched next
   auto fetch = [&](int n) {
     const int64_t token = ((int64_t)ahead_q << tile_log) + t;
@@ -204,8 +253,8 @@ __global__ void __launch_bounds__(kHeadThreads, sizeof(T) == 2 ? 4 : 3)
     if (mine && token < p.T && h < heads) {  // else what is there is not used, or zeros behind a head's end
       const HeadSide& s = p.side[h >= queries];
       const T* x = static_cast<const T*>(s.x) + token * s.x_token + (h < queries ? h : h - queries) * s.x_head;
-      load8(x + at.lo, lo[n]);
-      load8(x + at.hi, hi[n]);
+      lo[n].load(x + at.lo);
+      hi[n].load(x + at.hi);
     }
     ahead += step;
     if (ahead >= heads) ahead = first, ahead_q += gridDim.x;
@@ -233,9 +282,9 @@ __global__ void __launch_bounds__(kHeadThreads, sizeof(T) == 2 ? 4 : 3)
         __syncthreads();  // this tile's angles are there, the one's before are read
         fill(q + gridDim.x, buf ^ 1);
       }
-      F2 a[4], b[4];
-      open8<T>(lo[n], a);
-      open8<T>(hi[n], b);
+      F2 a[kRun / 2], b[kRun / 2];
+      lo[n].open(a);
+      hi[n].open(b);
       if (ahead_q < tiles) fetch(n);
       const int64_t token = ((int64_t)q << tile_log) + t;
       const int h = base + slot;
@@ -243,19 +292,19 @@ __global__ void __launch_bounds__(kHeadThreads, sizeof(T) == 2 ? 4 : 3)
       const float r = rsqrtf(fmaf(team_sum(squares(a, b), lanes), share, p.eps));
       if (mine && token < p.T && h < heads) {
         if (s.w) {
-          F2 w[4];
+          F2 w[kRun / 2];
           load_f2(s.w + at.lo, w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = a[i] * f2(r) * w[i];
+          for (int i = 0; i < kRun / 2; ++i) a[i] = a[i] * f2(r) * w[i];
           load_f2(s.w + at.hi, w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) b[i] = b[i] * f2(r) * w[i];
+          for (int i = 0; i < kRun / 2; ++i) b[i] = b[i] * f2(r) * w[i];
         }
         const int row = (buf * tile + t) * angles.pitch;
         turn_pairs<kNeighbours, false>(a, b, angles.cos + row, angles.sin + row, at.angle, p.half, angles.pitch);
         T* y = static_cast<T*>(s.y) + (token * s.heads + (h < queries ? h : h - queries)) * p.D;
-        store8(y + at.lo, a);
-        store8(y + at.hi, b);
+        store_run(y + at.lo, a);
+        store_run(y + at.hi, b);
       }
       base += step;
       if (base >= heads) base = first, q += gridDim.x, buf ^= 1;
@@ -281,7 +330,7 @@ template <class T, int kN>
 __global__ void __launch_bounds__(kHeadThreads) head_norm_any_kernel(const __grid_constant__ HeadNorm p, int tile_log) {
   extern __shared__ __align__(16) unsigned char head_smem[];
   const int tile = 1 << tile_log;
-  const Angles angles(head_smem, p.half, tile);
+  const Angles angles(head_smem, p.half, tile, false);
   const int64_t t0 = (int64_t)blockIdx.x << tile_log;
   const int tokens = (int)(p.T - t0 < tile ? p.T - t0 : tile);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, queries = p.side[0].heads, heads = queries + p.side[1].heads;
@@ -371,38 +420,38 @@ struct HeadPlan {
   int64_t tiles[2];
 };
 
-template <class T, bool kNeighbours>
-__global__ void __launch_bounds__(kHeadThreads, 2)
+template <class T, bool kNeighbours, int kRun>
+__global__ void __launch_bounds__(kHeadThreads, backward_on_sm<T, kRun>())
     head_norm_backward_kernel(const __grid_constant__ HeadNorm p, const __grid_constant__ HeadPlan plan, int lanes, float* parts) {
   extern __shared__ __align__(16) unsigned char head_smem[];
   const int k = (int)blockIdx.x >= plan.blocks[0], tile_log = plan.tile_log[k], tile = 1 << tile_log;
   const HeadSide& s = p.side[k];
-  const Angles angles(head_smem, p.half, 2 * tile);  // of two tiles in turn
+  const Angles angles(head_smem, p.half, 2 * tile, kRun == 8);  // of two tiles in turn
   const int j = threadIdx.x & (lanes - 1), team = threadIdx.x / lanes, step = (kHeadThreads / lanes) >> tile_log;
   const int t = team & (tile - 1), slot = team >> tile_log, heads = s.heads;
-  const bool mine = 16 * j < p.D, normed = s.w;
-  const Place at = place_of<kNeighbours>(j, 2 * p.half);
+  const bool mine = 2 * kRun * j < p.D, normed = s.w;
+  const Place at = place_of<kNeighbours, kRun>(j, 2 * p.half);
   const float share = 1.f / (float)p.D;
   const int64_t tiles = plan.tiles[k];
   const int stride = plan.blocks[k];
   int64_t q = k ? (int)blockIdx.x - plan.blocks[0] : (int)blockIdx.x;
   const T *dy = static_cast<const T*>(s.dy), *xs = static_cast<const T*>(s.x);
-  Raw8<T> raw[4] = {};
+  Run<T, kRun> raw[4] = {};
   auto fetch = [&](int64_t q, int h) {
     const int64_t token = (q << tile_log) + t;
     if (!mine || token >= p.T || h >= heads) return;  // what is there is not used, or zeros behind a head's end
     const T* d = dy + token * s.dy_token + h * s.dy_head;
-    load8(d + at.lo, raw[0]);
-    load8(d + at.hi, raw[1]);
+    raw[0].load(d + at.lo);
+    raw[1].load(d + at.hi);
     if (normed) {
       const T* v = xs + token * s.x_token + h * s.x_head;
-      load8(v + at.lo, raw[2]);
-      load8(v + at.hi, raw[3]);
+      raw[2].load(v + at.lo);
+      raw[3].load(v + at.hi);
     }
   };
-  F2 dw[8];
+  F2 dw[kRun];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = f2(0.f);
+  for (int i = 0; i < kRun; ++i) dw[i] = f2(0.f);
   auto tokens_of = [&](int64_t q) { return (int)(p.T - (q << tile_log) < tile ? p.T - (q << tile_log) : tile); };
   fetch(q, slot);
   // Positions are read a tile before their angles are computed.
@@ -430,13 +479,14 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
     for (int base = 0; base < heads; base += step) {
       const int h = base + slot;
       const bool live = t < tokens && h < heads;
-      F2 g[8], x[8];
-      F2(&ga)[4] = *reinterpret_cast<F2(*)[4]>(g), (&gb)[4] = *reinterpret_cast<F2(*)[4]>(g + 4);
-      F2(&xa)[4] = *reinterpret_cast<F2(*)[4]>(x), (&xb)[4] = *reinterpret_cast<F2(*)[4]>(x + 4);
-      open8<T>(raw[0], ga);
-      open8<T>(raw[1], gb);
-      open8<T>(raw[2], xa);
-      open8<T>(raw[3], xb);
+      F2 g[kRun], x[kRun];
+      constexpr int kPairs = kRun / 2;
+      F2(&ga)[kPairs] = *reinterpret_cast<F2(*)[kPairs]>(g), (&gb)[kPairs] = *reinterpret_cast<F2(*)[kPairs]>(g + kPairs);
+      F2(&xa)[kPairs] = *reinterpret_cast<F2(*)[kPairs]>(x), (&xb)[kPairs] = *reinterpret_cast<F2(*)[kPairs]>(x + kPairs);
+      raw[0].open(ga);
+      raw[1].open(gb);
+      raw[2].open(xa);
+      raw[3].open(xb);
       if (base + step < heads)
         fetch(q, h + step);
       else
@@ -446,11 +496,11 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
         const float r = rsqrtf(fmaf(team_sum(squares(xa, xb), lanes), share, p.eps));
         F2 dot = f2(0.f);
         if (mine) {
-          F2 w[8];
-          load_f2(s.w + at.lo, *reinterpret_cast<F2(*)[4]>(w));
-          load_f2(s.w + at.hi, *reinterpret_cast<F2(*)[4]>(w + 4));
+          F2 w[kRun];
+          load_f2(s.w + at.lo, *reinterpret_cast<F2(*)[kPairs]>(w));
+          load_f2(s.w + at.hi, *reinterpret_cast<F2(*)[kPairs]>(w + kPairs));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kRun; ++i) {
             x[i] = x[i] * f2(r);
             if (live) dw[i] = fma2(g[i], x[i], dw[i]);
             g[i] = g[i] * w[i];
@@ -459,12 +509,12 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
         }
         const float c = -team_sum(sum(dot), lanes) * share;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = fma2(x[i], f2(c), g[i]) * f2(r);
+        for (int i = 0; i < kRun; ++i) g[i] = fma2(x[i], f2(c), g[i]) * f2(r);
       }
       if (live && mine) {
         T* y = out + h * p.D;
-        store8(y + at.lo, ga);
-        store8(y + at.hi, gb);
+        store_run(y + at.lo, ga);
+        store_run(y + at.hi, gb);
       }
     }
     // (All have read this tile's: its angles were computed before the barrier above.)
@@ -477,10 +527,10 @@ __global__ void __launch_bounds__(kHeadThreads, 2)
   float* all = reinterpret_cast<float*>(head_smem);  // teams x D
   if (mine) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kRun; ++i) {
       float a, b;
       split(dw[i], a, b);
-      const int e = (i < 4 ? at.lo : at.hi) + 2 * (i & 3);
+      const int e = (i < kRun / 2 ? at.lo : at.hi) + 2 * (i % (kRun / 2));
       all[team * p.D + e] = a;
       all[team * p.D + e + 1] = b;
     }
@@ -501,7 +551,7 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_backward_any_kernel(co
   extern __shared__ __align__(16) unsigned char head_smem[];
   const int k = (int)blockIdx.x >= plan.blocks[0], tile_log = plan.tile_log[k], tile = 1 << tile_log;
   const HeadSide& s = p.side[k];
-  const Angles angles(head_smem, p.half, tile);
+  const Angles angles(head_smem, p.half, tile, false);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kHeadThreads / 32, D = p.D, pairs = D - p.half;
   const int t = warp & (tile - 1), slot = warp >> tile_log, step = warps >> tile_log, heads = s.heads;
   // each warp's sums: D floats
@@ -670,22 +720,28 @@ __global__ void __launch_bounds__(1024) head_norm_join_kernel(const float* parts
   if (lane == 0 && out < D && to) to[out] = v;
 }
 
-bool on_16(const void* p, int64_t token, int64_t head, int dtype) {
-  const int64_t per = 16 / (int64_t)elem_size(dtype);
-  return aligned_to(p, 16) && token % per == 0 && head % per == 0;
+bool on_run(const void* p, int64_t token, int64_t head, int dtype, int run) {
+  const int64_t bytes = std::min<int64_t>(16, run * (int64_t)elem_size(dtype)), per = bytes / (int64_t)elem_size(dtype);
+  return aligned_to(p, bytes) && token % per == 0 && head % per == 0;
 }
-// Runs of 8 values of both values of each pair, on 16 bytes everywhere.
-bool in_runs(const HeadNorm& p) {
-  if (p.D % 16 || p.D > 512 || (!p.neighbours && (2 * p.half) % 16)) return false;
+// Runs of so many values of both values of each pair, at addresses that allow them.
+bool in_runs(const HeadNorm& p, int run) {
+  if (p.D % (2 * run) || p.D > 64 * run || (!p.neighbours && p.half % run)) return false;
   for (const HeadSide& s : p.side)
-    if (s.heads && (!on_16(s.x, s.x_token, s.x_head, p.dtype) || !on_16(s.dy, s.dy_token, s.dy_head, p.dtype) ||
-                    !aligned_to(s.y, 16) || !aligned_to(s.w, 16)))
+    if (s.heads && (!on_run(s.x, s.x_token, s.x_head, p.dtype, run) || !on_run(s.dy, s.dy_token, s.dy_head, p.dtype, run) ||
+                    !on_run(s.y, 0, 0, p.dtype, run) || !aligned_to(s.w, 16)))
       return false;
   return true;
 }
-int lanes_of(int D) {
+// Runs of 8 or 4 values, or 0: none.  In 16 bits 8 where they fit, 16 bytes a lane (with 4 the heads of 8192 tokens take 61 us
+// for 34, their gradients 85 for 56); in fp32 4 are 16 bytes (4096 tokens, 12 heads of 256: 21.6 us for 24.8, gradients 31.7 for 32.7).
+int run_of(const HeadNorm& p) {
+  const int first = p.dtype == kF32 ? 4 : 8;
+  return in_runs(p, first) ? first : in_runs(p, 12 - first) ? 12 - first : 0;
+}
+int lanes_of(int D, int run) {
   int l = 1;
-  while (16 * l < D) l *= 2;
+  while (2 * run * l < D) l *= 2;
   return l;
 }
 int log_of(int n) {
@@ -705,8 +761,9 @@ template <class T>
 cudaError_t forward_typed(const HeadNorm& p, cudaStream_t stream) {
   const int tile_log = tile_log_of(p.T, kHeadBlocks), heads = p.side[0].heads + p.side[1].heads;
   const int64_t tiles = (p.T + (1 << tile_log) - 1) >> tile_log;
-  const bool runs = in_runs(p);
-  const int lanes = runs ? lanes_of(p.D) : 32, each = (kHeadThreads / lanes) >> tile_log;
+  const int run = run_of(p);
+  const bool runs = run != 0;
+  const int lanes = runs ? lanes_of(p.D, run) : 32, each = (kHeadThreads / lanes) >> tile_log;
   // Few tokens: their heads over several blocks, which each compute the angles.
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((heads + each - 1) / each, kHeadBlocks / tiles));
   const dim3 grid((unsigned)tiles, (unsigned)parts);
@@ -715,14 +772,15 @@ cudaError_t forward_typed(const HeadNorm& p, cudaStream_t stream) {
   // tiles as any other or one less, so that one's start is behind another's heads (16384 tokens, 2 heads of 64: 9.4 us,
   // else 11.5).  With more a tile is a block, and the SMs share them out (16384 tokens, 40 heads of 128: 64 us, else 75).
   const bool few = runs && heads < 8 * each;
-  const int64_t most = few ? 152 * (sizeof(T) == 2 ? 4 : 3) : tiles, rounds = (tiles + most - 1) / most;
+  const int64_t most = few ? 152 * (run == 4 ? forward_on_sm<T, 4>() : forward_on_sm<T, 8>()) : tiles, rounds = (tiles + most - 1) / most;
   const dim3 walk((unsigned)((tiles + rounds - 1) / rounds), (unsigned)parts);
   const size_t both = Angles::bytes(p.half, 2 << tile_log);
   const int pairs = pairs_of(p);
-  if (runs && p.neighbours)
-    head_norm_kernel<T, true><<<walk, kHeadThreads, both, stream>>>(p, tile_log, lanes, (int)tiles);
-  else if (runs)
-    head_norm_kernel<T, false><<<walk, kHeadThreads, both, stream>>>(p, tile_log, lanes, (int)tiles);
+  auto go = [&](auto kernel) { kernel<<<walk, kHeadThreads, both, stream>>>(p, tile_log, lanes, (int)tiles); };
+  if (run == 8)
+    p.neighbours ? go(head_norm_kernel<T, true, 8>) : go(head_norm_kernel<T, false, 8>);
+  else if (run == 4)
+    p.neighbours ? go(head_norm_kernel<T, true, 4>) : go(head_norm_kernel<T, false, 4>);
   else if (pairs <= 32)
     head_norm_any_kernel<T, 1><<<grid, kHeadThreads, smem, stream>>>(p, tile_log);
   else if (pairs <= 64)
@@ -760,11 +818,12 @@ HeadPlan backward_plan(const HeadNorm& p, int teams, int blocks, bool runs) {
 
 template <class T>
 cudaError_t backward_typed(const HeadNorm& p, float* parts, cudaStream_t stream) {
-  const bool runs = in_runs(p);
-  const int lanes = runs ? lanes_of(p.D) : 32, teams = kHeadThreads / lanes;
+  const int run = run_of(p);
+  const bool runs = run != 0;
+  const int lanes = runs ? lanes_of(p.D, run) : 32, teams = kHeadThreads / lanes;
   const int pairs = pairs_of(p);
   // As many blocks as fit on the SMs at a time: their registers decide.
-  const int on_sm = runs ? 2 : pairs > 64 && pairs <= 128 ? 2 : 4;
+  const int on_sm = run == 8 ? backward_on_sm<T, 8>() : run == 4 ? backward_on_sm<T, 4>() : pairs > 64 && pairs <= 128 ? 2 : 4;
   const HeadPlan plan = backward_plan(p, teams, 152 * on_sm, runs);
   const unsigned grid = (unsigned)(plan.blocks[0] + plan.blocks[1]);
   float* sums = p.side[0].dw || p.side[1].dw ? parts : nullptr;
@@ -776,10 +835,10 @@ cudaError_t backward_typed(const HeadNorm& p, float* parts, cudaStream_t stream)
     if (e == cudaSuccess) kernel<<<grid, kHeadThreads, smem, stream>>>(p, plan, more..., sums);
     if (e == cudaSuccess) e = cudaGetLastError();
   };
-  if (runs && p.neighbours)
-    go(head_norm_backward_kernel<T, true>, lanes);
-  else if (runs)
-    go(head_norm_backward_kernel<T, false>, lanes);
+  if (run == 8)
+    p.neighbours ? go(head_norm_backward_kernel<T, true, 8>, lanes) : go(head_norm_backward_kernel<T, false, 8>, lanes);
+  else if (run == 4)
+    p.neighbours ? go(head_norm_backward_kernel<T, true, 4>, lanes) : go(head_norm_backward_kernel<T, false, 4>, lanes);
   else if (pairs <= 32)
     go(head_norm_backward_any_kernel<T, 1>);
   else if (pairs <= 64)

@@ -97,7 +97,8 @@ def _check(bk, q, k, p, f, qw, kw, pairs, dtype, eps=1e-6):  # noqa: F811
 
 SHAPES = [(1, 1, 1, 2, 2), (1, 32, 8, 128, 128), (3, 4, 1, 64, 64), (17, 7, 3, 80, 20), (33, 5, 2, 96, 48), (9, 3, 1, 77, 76),
           (130, 2, 2, 256, 64), (1000, 8, 2, 128, 128), (41, 2, 1, 512, 512), (11, 2, 1, 1024, 1024), (5, 3, 2, 1, 0),
-          (700, 12, 4, 48, 16), (2600, 6, 2, 64, 32), (64, 1, 1, 400, 100), (21, 9, 9, 16, 16), (8, 2, 1, 513, 512)]
+          (700, 12, 4, 48, 16), (2600, 6, 2, 64, 32), (64, 1, 1, 400, 100), (21, 9, 9, 16, 16), (8, 2, 1, 513, 512), (13, 4, 2, 80, 40), (9, 3, 1, 96, 72), (7, 2, 2, 24, 8),
+          (130, 3, 1, 72, 64)]
 
 
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
