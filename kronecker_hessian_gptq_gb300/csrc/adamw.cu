@@ -12,12 +12,13 @@
 // scale; blocks walk over units of 2048 values of all tensors, whose addresses
 // come in the kernel's parameters, so that a launch takes up to 384 tensors
 // and a captured one keeps them.  Statistics, sums and the update are fp32.
-// 235 million values: 1054 us in fp32 (6.2 TB/s), 660 us with 8-bit states, fp32
-// masters, bf16 gradients and copies (5.7 TB/s), which issues 72 instructions a
-// value, two thirds of the time: a value's hash takes 9, two codes cut at random
-// 16.  Sums and products go in pairs, conditions that hardly ever hold are
-// tested for eight values at once, and all loads are under way before the first is
-// converted (815 us before that, at 104 instructions).
+// 235 million values: 1054 us in fp32 (6.2 TB/s), 696 us with 8-bit states, fp32
+// masters, bf16 gradients and copies (5.4 TB/s), which issues 82 instructions a
+// value, 70% of the time: a value's hash takes 9, two codes cut at random 16,
+// products, sums and the root each rounded by themselves 10 (without that 660 us,
+// but codes that fall elsewhere).  Sums and products go in pairs, conditions that
+// hardly ever hold are tested for eight values at once, and all loads are under
+// way before the first is converted (815 us before that, at 104 instructions).
 #include <cuda_fp8.h>
 
 #include <algorithm>

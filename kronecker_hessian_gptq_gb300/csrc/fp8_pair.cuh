@@ -14,7 +14,7 @@
 // where they do not (kColumns).  Measured at 4096 x 4864 x 16384: 0.46 us a block
 // (950 cycles), of which the tensor cores and copies alone take 0.37 (the two
 // SMs fetch 64 KB for it, 13 TB/s over all of them); 4096 tokens 4096 x 14336
-// 218 us, quantized in the call (2.2 PFLOP/s).  16 epilogue warps with half the
+// 216 us, quantized in the call (2.2 PFLOP/s).  16 epilogue warps with half the
 // columns each issue more for waits and scales (236 us).
 //
 // Either operand may be stored with K contiguous or with its rows contiguous

@@ -6,6 +6,8 @@
 // Otherwise a block takes 128 x 128 values, 4 x 8 a thread; one read of them
 // gives the codes along rows, the codes along columns and the columns' sums
 // (what the backward pass of a product needs of its output's gradient).
+// 4096 x 4096 in bf16: 12.9 us along rows, 15.0 along columns, 14.2 in blocks (3.4
+// to 3.9 TB/s); with maxima of single fp32 magnitudes 14.3, 22 and 20.5.
 #include <algorithm>
 #include <cstring>
 

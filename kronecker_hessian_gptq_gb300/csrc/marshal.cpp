@@ -172,7 +172,9 @@ PyObject* fp8_matmul_backward(PyObject* const* a) {
   if (!is_float(kind) || !ready(device) || !codes || codes->dim() != 2) return nullptr;
   const int64_t T = dy.rows, N = dy.cols, K = codes->size(1);
   if (!weights(a[2], a[3], K, device, w) || w.codes.rows != N) return nullptr;
-  const bool has_x = a[1] != Py_None, has_bias = PyObject_IsTrue(a[4]) == 1;
+  const int wanted = PyObject_IsTrue(a[4]);
+  if (wanted < 0) return nullptr;
+  const bool has_x = a[1] != Py_None, has_bias = wanted;
   if (has_x && (!matrix(a[1], x) || x.rows != T || x.cols != K || x.t->get_device() != device || code_of(*x.t) != kind)) return nullptr;
   void* const stream = stream_on(device);
   const at::Tensor dx = room({T, K}, type_of(kind), device), status = room({1}, at::kInt, device);
