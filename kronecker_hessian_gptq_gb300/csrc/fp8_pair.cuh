@@ -127,12 +127,18 @@ __device__ __forceinline__ void arrive_if(bool p, uint32_t mbar) {
       : "memory");
 }
 
-// A warp's box for one of kRuns runs: only those before the last kRuns - 1 copies have to have been read.
+// A warp's box for one of kRuns runs: only those before the last kRuns - 1 groups of
+// copies have to have been read.  So every run is a group, in turn: one that lies
+// outside the matrix commits an empty one (skip), without which the next tile's first
+// run would take its own box's copy for the other's.
 template <int kRuns>
 struct F8Box : PairBox {
   __device__ __forceinline__ void open() const {
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(kRuns - 1) : "memory");
     __syncwarp();
+  }
+  __device__ __forceinline__ void skip() const {
+    if (lane == 0) asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
   }
 };
 // pair_unit without divisions where K is whole, and with few where it is not: they
@@ -460,7 +466,10 @@ struct F8Rows {
   __device__ __forceinline__ int64_t cols() const { return n; }
   template <int kCols, int kRuns>
   __device__ __forceinline__ void operator()(int64_t row0, int64_t col, float (&v)[kCols], const F8Box<kRuns>& box) const {
-    if (row0 >= m || col >= n) return;
+    if (row0 >= m || col >= n) {
+      if (sizeof(T) == 2 && tma) box.skip();
+      return;
+    }
     if constexpr (sizeof(T) == 2) {
       if (tma) {
         box.open();
