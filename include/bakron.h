@@ -637,6 +637,8 @@ int bakron_head_norm_rotary_backward(const void* dYQ, int64_t dq_token, int64_t 
  * numbers, or NULL; skip: device, a number that is not 0 leaves everything as
  * it is, or NULL.  (A captured call reads these when it is replayed.)
  * 0 <= beta < 1; eps >= 0.  ws: 256 bytes, device.  status_dev: device.
+ * A refusal (an argument, the workspace) changes nothing; after an error of
+ * CUDA itself some of the tensors may have taken the step.
  */
 typedef struct {
   void* param;

@@ -46,7 +46,12 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int from_cuda(cudaError_t e) { return e == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA; }
+// An error is reported once: what is left of it would be the next launch's.
+int from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return BAKRON_OK;
+  (void)cudaGetLastError();
+  return BAKRON_ERR_CUDA;
+}
 
 constexpr int64_t kMaxElems = (int64_t)1 << 31;  // m * n and d * d limit (int indexing)
 

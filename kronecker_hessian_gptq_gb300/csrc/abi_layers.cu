@@ -11,7 +11,12 @@ namespace {
 
 using bakron::aligned_to;
 
-int from_cuda(cudaError_t e) { return e == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA; }
+// An error is reported once: what is left of it would be the next launch's.
+int from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return BAKRON_OK;
+  (void)cudaGetLastError();
+  return BAKRON_ERR_CUDA;
+}
 bool float_type(int dtype) { return dtype == BAKRON_F32 || dtype == BAKRON_F16 || dtype == BAKRON_BF16; }
 bool on_element(const void* p, int dtype) { return aligned_to(p, bakron::elem_size(dtype)); }
 // Arrays of 32-bit elements (null: not there).

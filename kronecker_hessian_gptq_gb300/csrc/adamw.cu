@@ -505,8 +505,10 @@ cudaError_t launch_lists(const Adamw& a, const bakron_adamw_tensor* tensors, int
     }
     if (list.count == 0) break;
     const unsigned grid = (unsigned)std::min<int64_t>(list.first[list.count], most);
-    kernel<<<grid, kAdamThreads, 0, stream>>>(list, given, made, a.skip, status);
-    const cudaError_t e = cudaGetLastError();
+    // The launch's own error, not one that is left from before: a step that was made is never reported as failed.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kAdamThreads), cfg.stream = stream;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, list, given, made, a.skip, status);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

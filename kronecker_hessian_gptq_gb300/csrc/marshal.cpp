@@ -4,9 +4,11 @@
 // token's heads; here about 6.  The same for the lists of AdamW: reading five
 // attributes of 520 tensors takes 250 us from Python, 10 here.
 //
-// Nothing is raised: a call that is not handled (an argument that is not what it
-// has to be, no tokens, an error) returns None, and the checks and the call
-// through ctypes, in _projection.py, follow and say what is wrong.
+// A call that is not handled (an argument that is not what it has to be, no
+// tokens, a refusal by the library) returns None, and the checks and the call
+// through ctypes, in _projection.py, follow and say what is wrong.  An error of
+// the library that may have enqueued something is raised: made again, an AdamW
+// step would be two.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -31,6 +33,7 @@ struct Entries {
   decltype(&bakron_head_norm_rotary_backward_workspace_size) heads_back_size;
   decltype(&bakron_adamw) adamw;
   decltype(&bakron_adamw_workspace_size) adamw_size;
+  decltype(&bakron_status_string) text;
 } lib;
 bool bound = false;
 
@@ -96,13 +99,19 @@ PyObject* wrap(const at::Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
 }
-// A call of the library, with other threads free to run meanwhile: a launch may wait for room.
+// Whether the present call of this thread has enqueued work, or may have.
+thread_local bool enqueued = false;
+// A call of the library, with other threads free to run meanwhile: a launch may
+// wait for room.  Whether it succeeded; if not, and it was no refusal, with the error set.
 template <class F>
-int unlocked(F call) {
+bool launched(const char* name, F call) {
   PyThreadState* state = PyEval_SaveThread();
   const int r = call();
   PyEval_RestoreThread(state);
-  return r;
+  if (r == BAKRON_ERR_INVALID_ARG || r == BAKRON_ERR_WORKSPACE) return false;
+  enqueued = true;
+  if (r != BAKRON_OK) PyErr_Format(PyExc_RuntimeError, "%s failed: %s", name, lib.text(r));
+  return r == BAKRON_OK;
 }
 // A tuple or a value of a dict; takes the references.
 PyObject* pair(PyObject* a, PyObject* b) {
@@ -153,7 +162,7 @@ PyObject* fp8_matmul(PyObject* const* a) {
   const size_t bytes = lib.fp8_size(T, K, N, kind, w.copies);
   if (!bytes) return nullptr;
   const at::Tensor ws = room({(int64_t)bytes}, at::kByte, device);
-  if (unlocked([&] {
+  if (!launched("bakron_fp8_matmul", [&] {
         return lib.fp8(x.p, kind, x.ld, static_cast<const float*>(xs), static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
               static_cast<const float*>(w.scales), static_cast<const float*>(bias), T, K, N, y.data_ptr(), out, ws.data_ptr(), bytes,
               static_cast<int32_t*>(status.data_ptr()), stream);
@@ -184,7 +193,7 @@ PyObject* fp8_matmul_backward(PyObject* const* a) {
   const size_t bytes = lib.fp8_back_size(T, K, N, 1 + 2 * has_x + 4 * has_bias, w.copies);
   if (!bytes) return nullptr;
   const at::Tensor ws = room({(int64_t)bytes}, at::kByte, device);
-  if (unlocked([&] {
+  if (!launched("bakron_fp8_matmul_backward", [&] {
         return lib.fp8_back(dy.p, dy.ld, x.p, x.ld, kind, static_cast<const uint8_t*>(w.codes.p), w.codes.ld,
                    static_cast<const float*>(w.scales), T, K, N, dx.data_ptr(), has_x ? dw.data_ptr() : nullptr,
                    has_bias ? static_cast<float*>(dbias.data_ptr()) : nullptr, ws.data_ptr(), bytes,
@@ -248,7 +257,7 @@ PyObject* head_norm_rotary(PyObject* const* a) {
   const at::Tensor yq = room({n.q.T, n.q.heads, n.q.D}, n.type, n.device);
   at::Tensor yk;
   if (n.k.p) yk = room({n.k.T, n.k.heads, n.k.D}, n.type, n.device);
-  if (unlocked([&] {
+  if (!launched("bakron_head_norm_rotary", [&] {
         return lib.heads(n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token, n.k.head, n.k.heads, static_cast<const float*>(n.qw),
                 static_cast<const float*>(n.kw), static_cast<const int64_t*>(n.positions), static_cast<const double*>(n.freqs), n.R,
                 n.pairs, n.eps, n.kind, n.q.T, n.q.D, yq.data_ptr(), n.k.p ? yk.data_ptr() : nullptr, stream);
@@ -274,7 +283,7 @@ PyObject* head_norm_rotary_backward(PyObject* const* a) {
   if (!bytes) return nullptr;
   const at::Tensor ws = room({(int64_t)bytes}, at::kByte, n.device);
   auto at = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-  if (unlocked([&] {
+  if (!launched("bakron_head_norm_rotary_backward", [&] {
         return lib.heads_back(dq.p, dq.token, dq.head, dk.p, dk.token, dk.head, n.q.p, n.q.token, n.q.head, n.q.heads, n.k.p, n.k.token,
                      n.k.head, n.k.heads, static_cast<const float*>(n.qw), static_cast<const float*>(n.kw),
                      static_cast<const int64_t*>(n.positions), static_cast<const double*>(n.freqs), n.R, n.pairs, n.eps, n.kind, n.q.T,
@@ -360,7 +369,7 @@ PyObject* adamw(PyObject* const* a) {
   }
   void* const stream = stream_on(device);
   const at::Tensor status = room({1}, at::kInt, device), ws = room({(int64_t)lib.adamw_size()}, at::kByte, device);
-  if (unlocked([&] {
+  if (!launched("bakron_adamw", [&] {
         return lib.adamw(out.get(), count, eight ? 8 : 32, rate, static_cast<const float*>(rate_dev), step, static_cast<const int64_t*>(step_dev),
                 b1, b2, eps, decay, scale, static_cast<const float*>(scale_dev), static_cast<const int32_t*>(skip), seed, ws.data_ptr(),
                 ws.numel(), static_cast<int32_t*>(status.data_ptr()), stream);
@@ -372,12 +381,17 @@ PyObject* adamw(PyObject* const* a) {
 template <PyObject* (*kCall)(PyObject* const*), int kArgs>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
   PyObject* r = nullptr;
+  enqueued = false;
   try {
     if (n == kArgs) r = kCall(args);
   } catch (...) {
     r = nullptr;
   }
   if (r) return r;
+  if (enqueued) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "the call was made, but its results cannot be handed out");
+    return nullptr;
+  }
   PyErr_Clear();
   Py_RETURN_NONE;
 }
@@ -392,7 +406,7 @@ PyObject* bind(PyObject*, PyObject* path) {
           find(h, "bakron_fp8_matmul_backward_workspace_size", lib.fp8_back_size) && find(h, "bakron_head_norm_rotary", lib.heads) &&
           find(h, "bakron_head_norm_rotary_backward", lib.heads_back) &&
           find(h, "bakron_head_norm_rotary_backward_workspace_size", lib.heads_back_size) && find(h, "bakron_adamw", lib.adamw) &&
-          find(h, "bakron_adamw_workspace_size", lib.adamw_size);
+          find(h, "bakron_adamw_workspace_size", lib.adamw_size) && find(h, "bakron_status_string", lib.text);
   return PyBool_FromLong(bound);
 }
 
