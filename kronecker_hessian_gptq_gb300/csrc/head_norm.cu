@@ -36,6 +36,10 @@ constexpr int kHeadTile = 8;  // tokens of a tile at most, a power of two
 constexpr int kHeadBlocks = 4 * 152;  // forward: four on each SM
 constexpr int kBackBlocks = 4 * 152;  // backward: at most
 constexpr int kBackTile = 32;
+// Dynamic shared memory that a block of any kernel here may take.  The most is that
+// of the backward pass for any sizes, with 1024 values, all turned, in tiles of a
+// token a warp: 512 turns, 8 rows of 512 angles, and each warp's 1024 sums, 68 KB.
+constexpr size_t kHeadSmem = 68 * 1024;
 
 // The frequency f as a share of a turn for each position, 2^-64 of it.
 __device__ __forceinline__ uint64_t turn_of(double f) {
@@ -833,7 +837,8 @@ cudaError_t backward_typed(const HeadNorm& p, float* parts, cudaStream_t stream)
   const size_t smem = runs ? std::max(angles, (size_t)teams * p.D * 4) : angles + (size_t)teams * p.D * 4;
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel, auto... more) {
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // One bound for every call: it is the kernel's, and threads that set their own would lower each other's.
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHeadSmem);
     if (e == cudaSuccess) kernel<<<grid, kHeadThreads, smem, stream>>>(p, plan, more..., sums);
     if (e == cudaSuccess) e = cudaGetLastError();
   };
