@@ -354,6 +354,7 @@ cudaError_t norm_residual_typed(const NormResidual& p, cudaStream_t stream) {
 // Values a column keeps in a block: the weights pre, post and the gate's row,
 // the sums of their gradients; the same of the biases.
 constexpr int bwd_held(bool layer) { return layer ? 9 : 6; }
+constexpr int kBwdSharedBytes = 220 * 1024;  // of a block whose sums are in shared memory, at most
 constexpr int kBwdRegisterD = 4096;  // columns up to which they are in registers, 512 threads of 8
 constexpr int kBwdPerSm = 8;         // blocks of an SM at most
 // Rows on their way in shared memory: of 32-bit elements, whose 32 registers
@@ -379,7 +380,7 @@ BackwardPlan backward_plan(int64_t T, int64_t D, int64_t groups, bool layer, int
   b.shared = D > kBwdRegisterD;
   const int64_t each = T / b.groups;
   // columns of a block: 32 bytes of shared memory hold a value for 8 of them
-  const int64_t most_cols = !b.shared ? kBwdRegisterD : std::min(1024, 220 * 1024 / 32 / bwd_held(layer) / 32 * 32) * 8;
+  const int64_t most_cols = !b.shared ? kBwdRegisterD : std::min(1024, kBwdSharedBytes / 32 / bwd_held(layer) / 32 * 32) * 8;
   b.cluster = 1;
   while (b.cluster * most_cols < D) b.cluster *= 2;
   const int64_t per = (D + b.cluster - 1) / b.cluster;
@@ -817,7 +818,9 @@ cudaError_t norm_backward_typed(const NormBackward& p, float* part, cudaStream_t
   cfg.numAttrs = 1;
   auto kernel = plan.shared ? (p.layer ? norm_backward_kernel<T, VEC, true, true> : norm_backward_kernel<T, VEC, false, true>)
                             : (p.layer ? norm_backward_kernel<T, VEC, true, false> : norm_backward_kernel<T, VEC, false, false>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  // What the kernel may take at most, whatever the width: threads that set their own would lower each other's.
+  const int most = plan.shared ? kBwdSharedBytes : kBwdRegisterD / 8 * 32 * kBwdStages<T> * (int)sizeof(T);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   e = cudaLaunchKernelEx(&cfg, kernel, p, plan, part);
   if (e != cudaSuccess) return e;
