@@ -158,7 +158,8 @@ cudaError_t row_scales_launch(const float* W, int m, int n, int group, Alphabet 
   const bool staged = (size_t)group * sizeof(float) <= kMaxStagedBytes;
   const size_t smem = staged ? (size_t)group * sizeof(float) : 0;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(row_scales_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // One bound for every call: threads that set their own would lower each other's.
+    cudaError_t e = cudaFuncSetAttribute(row_scales_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxStagedBytes);
     if (e != cudaSuccess) return e;
   }
   row_scales_kernel<<<(unsigned)((size_t)m * runs), kScaleThreads, smem, stream>>>(W, n, group, runs, al.lo, al.hi,

@@ -46,3 +46,11 @@ def test_norm_residual_backward(bk, widths):  # noqa: F811
         return [t for t in g.values() if t is not None]
 
     _at_once([lambda a=(rand(300, d), rand(300, d), rand(d)): call(*a) for d in widths], 60)
+
+
+def test_row_scales(bk):  # noqa: F811
+    import torch
+
+    gen = torch.Generator("cuda").manual_seed(2)
+    work = [torch.randn((8, n), generator=gen, device="cuda") for n in (13000, 20000, 32000, 48000)]
+    _at_once([lambda w=w: (bk.row_scales(w, -4, 3, grid=4),) for w in work], 60)
