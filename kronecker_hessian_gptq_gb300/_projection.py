@@ -360,9 +360,10 @@ def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, we
     step (from 1 on), lr and grad_scale: numbers, or CUDA tensors of one value
     (int64, float32, float32), which a captured call reads when it is replayed.
     skip: int32 CUDA tensor of one value; if it is not 0 everything stays as it
-    is.  seed: of the random rounding of 8-bit states.  Returns status
-    int32[1]: DEV_NONFINITE_GRAD where values with such gradients were left as
-    they are."""
+    is.  seed: of the random rounding of 8-bit states.  Autograd sees parameters
+    and copies change in place, as it does with an optimizer of torch: a graph
+    that kept one of them refuses to go backward.  Returns status int32[1]:
+    DEV_NONFINITE_GRAD where values with such gradients were left as they are."""
     params, grads = list(params), list(grads)
     if stream is not None:
         for t in (*grads, *(copies or ()), *(t for l in states.values() for t in l)):
@@ -401,4 +402,7 @@ def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, we
     _call("bakron_adamw", packed, count, 8 if eight else 32, rate, rate_dev, number,
           step_dev, betas[0], betas[1], eps, weight_decay, scale, scale_dev, stop, seed & 0xFFFFFFFFFFFFFFFF, ws.data_ptr(),
           nbytes, status.data_ptr(), _stream_on(device))
+    # A graph that kept one of them from before must not go backward with other values.
+    torch.autograd.graph.increment_version([t for t in (*params, *lists.get("copies", ())) if t is not None
+                                            and not t.is_inference()])
     return status
