@@ -126,18 +126,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def load_marshal():
-    """The module that makes calls on torch tensors natively (torch has to be imported first), loaded once."""
+    """The module that makes calls on torch tensors natively (torch has to be imported first), loaded once; None where
+    there is none for this torch and this Python: the same calls go through ctypes."""
     global _marshal
     if _marshal is None:
         load()
-        path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"_marshal.so not found at {path}: build it first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        import torch
+
+        from . import build
+
+        # Looked at before it is loaded: the code of another torch's headers may do anything.
+        if not build.marshal_fits(build.marshal_tag(torch.__version__)):
+            return None
         from . import _marshal as module
 
         if not module.bind(LIB_PATH):
-            raise RuntimeError(f"{path} finds no entry points in {LIB_PATH}: build them again")
+            return None
         _marshal = module
     return _marshal
 
