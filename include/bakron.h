@@ -631,8 +631,9 @@ int bakron_head_norm_rotary_backward(const void* dYQ, int64_t dq_token, int64_t 
  * A value whose gradient, or its square, is not finite in fp32 is left as it
  * is, and BAKRON_DEV_NONFINITE_GRAD is set.
  * tensors: host, read in the call.  Arrays are dense, start on their elements
- * and do not overlap (a parameter, state or copy that is there twice is refused); param: param_dtype (fp32, fp16, bf16), grad: grad_dtype,
- * copy: copy_dtype (fp16 or bf16), or NULL.  n may be 0.
+ * and do not overlap (a parameter, state, copy or, with bits = 8, array of scales
+ * that is there twice is refused); param: param_dtype (fp32, fp16, bf16), grad:
+ * grad_dtype, copy: copy_dtype (fp16 or bf16), or NULL.  n may be 0.
  * step: from 1 on.  lr_dev, step_dev, grad_scale_dev: device, in place of the
  * numbers, or NULL; skip: device, a number that is not 0 leaves everything as
  * it is, or NULL.  (A captured call reads these when it is replayed.)

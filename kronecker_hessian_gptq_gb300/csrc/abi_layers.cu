@@ -315,7 +315,7 @@ int bakron_adamw(const bakron_adamw_tensor* tensors, int64_t count, int bits, do
     if (t.param == t.grad || t.param == t.m || t.param == t.v || t.m == t.v || t.copy == t.param || t.grad == t.m || t.grad == t.v)
       return BAKRON_ERR_INVALID_ARG;
   }
-  if (!bakron::adamw_all_different(tensors, count)) return BAKRON_ERR_INVALID_ARG;
+  if (!bakron::adamw_all_different(tensors, count, bits == 8)) return BAKRON_ERR_INVALID_ARG;
   if (!workspace_ok(ws, ws_bytes, bakron::adamw_workspace_bytes())) return BAKRON_ERR_WORKSPACE;
   const bakron::Adamw a{bits == 8, lr, grad_scale, beta1, beta2, eps, weight_decay, step, lr_dev, grad_scale_dev, step_dev, skip, seed};
   return from_cuda(bakron::adamw_launch(a, tensors, count, ws, status_dev, (cudaStream_t)stream));

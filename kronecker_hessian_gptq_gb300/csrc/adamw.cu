@@ -460,10 +460,10 @@ int sm_count() {
 
 size_t adamw_workspace_bytes() { return 256; }
 
-bool adamw_all_different(const bakron_adamw_tensor* tensors, int64_t count) {
-  // A table of at least twice as many places as addresses; an address goes to the next free one.
+bool adamw_all_different(const bakron_adamw_tensor* tensors, int64_t count, bool eight) {
+  // A table of at least twice as many places as addresses (six of a tensor); an address goes to the next free one.
   uint64_t size = 64;
-  while (size < (uint64_t)count * 8) size *= 2;
+  while (size < (uint64_t)count * 12) size *= 2;
   std::unique_ptr<const void*[]> seen(new (std::nothrow) const void*[size]());
   if (!seen) return false;
   auto fresh = [&](const void* p) {
@@ -476,7 +476,8 @@ bool adamw_all_different(const bakron_adamw_tensor* tensors, int64_t count) {
   };
   for (int64_t i = 0; i < count; ++i) {
     const bakron_adamw_tensor& t = tensors[i];
-    if (t.n && !(fresh(t.param) && fresh(t.m) && fresh(t.v) && fresh(t.copy))) return false;
+    if (t.n && !(fresh(t.param) && fresh(t.m) && fresh(t.v) && fresh(t.copy) && (!eight || (fresh(t.m_scales) && fresh(t.v_scales)))))
+      return false;
   }
   return true;
 }

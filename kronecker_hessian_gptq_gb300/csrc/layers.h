@@ -127,8 +127,8 @@ struct Adamw {
   uint64_t seed;
 };
 size_t adamw_workspace_bytes();
-// Whether no parameter, and no state, is in the list twice.
-bool adamw_all_different(const bakron_adamw_tensor* tensors, int64_t count);
+// Whether nothing that is written, parameter, state, scales (of states in 8 bits) or copy, is in the list twice.
+bool adamw_all_different(const bakron_adamw_tensor* tensors, int64_t count, bool eight);
 cudaError_t adamw_launch(const Adamw& a, const bakron_adamw_tensor* tensors, int64_t count, void* ws, int32_t* status,
                          cudaStream_t stream);
 
