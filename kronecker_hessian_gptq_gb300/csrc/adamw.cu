@@ -159,11 +159,12 @@ __device__ __forceinline__ void open_codes(const uint2& u, float scale, F2 (&v)[
 
 // 32 random bits for the i-th value of a tensor: a product with 2^32 over the
 // golden ratio, then two rounds of a shift and a product with an odd number
-// (the fractions of the roots of 2 and 3).
+// (the fractions of the roots of 2 and 3).  A seed's upper half goes through the
+// same rounds before it is added to the lower one's.
 constexpr uint32_t kMixA = 0x9E3779B1u, kMixB = 0x6A09E667u, kMixC = 0xBB67AE85u;
 // The last step, x ^ x >> 16, is left to those who take the halves r of it, as
 // (1 + r) / 8.
-__device__ __forceinline__ uint32_t mix(uint32_t x) {
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x = (x ^ (x >> 16)) * kMixB;
   return (x ^ (x >> 15)) * kMixC;
 }
@@ -437,7 +438,7 @@ __host__ __device__ inline AdamConstants constants(double lr, double step, doubl
   c.rate = (float)(lr / (1 - pow(b1, step)));
   c.decay = (float)(1 - lr * decay);
   c.grad = (float)scale;
-  c.key = (uint32_t)seed * kMixA + (uint32_t)(uint64_t)step * kMixB;
+  c.key = (uint32_t)seed * kMixA + mix((uint32_t)(seed >> 32) * kMixA) + (uint32_t)(uint64_t)step * kMixB;
   c.pb1 = both(c.b1), c.pc1 = both(c.c1), c.pb2 = both(c.b2 * kLarger), c.pc2 = both(c.c2 * kLarger), c.peps = both(c.eps);
   c.proot = both(c.root / kRootLarger), c.prate = both(-c.rate), c.pdecay = both(c.decay), c.pgrad = both(c.grad);
   c.one = both(1.f);
