@@ -382,18 +382,16 @@ def adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, we
     that kept one of them refuses to go backward.  Returns status int32[1]:
     DEV_NONFINITE_GRAD where values with such gradients were left as they are."""
     params, grads = list(params), list(grads)
-    if stream is not None:
-        for t in (*grads, *(copies or ()), *(t for l in states.values() for t in l)):
-            if t is not None:
-                t.record_stream(stream)
-        for t in (*params, step, lr, grad_scale, skip):
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
-        with torch.cuda.stream(stream):
-            return adamw(params, grads, states, step, lr, betas, eps, weight_decay, grad_scale, copies, skip, seed)
     lists = {"grads": grads, **{k: list(l) for k, l in states.items()}}
     if copies is not None:
         lists["copies"] = list(copies)
+    if stream is not None:
+        for t in (*params, *(t for l in lists.values() for t in l), step, lr, grad_scale, skip):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        states = {k: l for k, l in lists.items() if k in states}
+        with torch.cuda.stream(stream):
+            return adamw(params, grads, states, step, lr, betas, eps, weight_decay, grad_scale, lists.get("copies"), skip, seed)
     eight = "m_scales" in states
     done = (_native or _fast()).adamw(params, grads, lists["m"], lists["v"], lists.get("m_scales"), lists.get("v_scales"),
                                       lists.get("copies"), step, lr, betas[0], betas[1], eps, weight_decay, grad_scale, skip, seed)
